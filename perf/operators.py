@@ -100,7 +100,7 @@ def work(case):
     if c["op"] == "select_bwd":
         b, n = _BYTES[c["dtype"]], c["T"] * c["E"]
         dense = c["prob"] or (c["kind"] == "softmax" and not c["renorm"])  # else only the chosen logits matter
-        return {"bytes": n * b + (n * b if dense else c["T"] * c["k"] * b) + 12 * c["T"] * c["k"], "flops": 8 * n}
+        return {"bytes": n * b + (n * b if dense else c["T"] * c["k"] * b) + 8 * c["T"] * c["k"], "flops": 8 * n}
     if c["op"] == "quantize":
         n = c["R"] * c["K"]
         return {"bytes": n * (_BYTES[c["dtype"]] + 2 + 0.5 + 1 / 32), "flops": 2 * n}
@@ -175,8 +175,8 @@ def prepare(case, seed):
             s["opts"] = moe.select_opts(kind, n_group=c["groups"], topk_group=c["keep"], group_top=c["top"],
                                         renorm=c["renorm"])
         if c["op"] == "select_bwd":
-            # what the forward pass and the layer above left
-            s["idx"], s["w"] = _select_plain(c, s["logits"], s["bias"])[:2]
+            # what the forward pass chose and what the layer above sends back
+            s["idx"] = _select_plain(c, s["logits"], s["bias"])[0]
             s["d_w"] = torch.randn((c["T"], c["k"]), generator=g, device="cuda")
             s["d_prob"] = torch.randn(c["E"], generator=g, device="cuda") if c["prob"] else None
         return s
@@ -232,7 +232,7 @@ def _select_plain(c, logits, bias):
 
 
 def _select_bwd_plain(c, s):
-    l, idx, w, dw = s["logits"].float(), s["idx"].long(), s["w"], s["d_w"]
+    l, idx, dw = s["logits"].float(), s["idx"].long(), s["d_w"]
     if c["kind"] == "softmax":
         key = l if s["bias"] is None else l + s["bias"]
         p = torch.exp(key - key.amax(dim=1, keepdim=True))
@@ -243,7 +243,9 @@ def _select_bwd_plain(c, s):
         q = score / total
     # the gradient for the chosen scores, then for every score
     if c["renorm"]:
-        d_chosen = (dw - (dw * w).sum(dim=1, keepdim=True)) / score.gather(1, idx).sum(dim=1, keepdim=True)
+        chosen = score.gather(1, idx)
+        total_chosen = chosen.sum(dim=1, keepdim=True)
+        d_chosen = (dw - (dw * chosen).sum(dim=1, keepdim=True) / total_chosen) / total_chosen
     else:
         d_chosen = dw
     d_score = torch.zeros_like(l).scatter_(1, idx, d_chosen)
@@ -314,7 +316,7 @@ def run(state):
         if not own:
             return _select_bwd_plain(c, s)
         want = s["bias"] is not None and c["kind"] == "softmax"
-        r = s["moe"].route_select_backward(s["logits"], s["idx"], s["w"], s["d_w"], s["opts"], bias=s["bias"],
+        r = s["moe"].route_select_backward(s["logits"], s["idx"], s["d_w"], s["opts"], bias=s["bias"],
                                            d_prob_sum=s["d_prob"], want_d_bias=want)
         return {"d_logits": r[0], "d_bias": r[1]} if want else {"d_logits": r}
     if c["op"] == "quantize":
