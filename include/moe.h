@@ -391,6 +391,145 @@ moe_status moe_layer_fwd_profiled(const void* x, const float* w_router, const fl
 moe_status moe_load_stats_noalloc(const int32_t* topk_idx, moe_dims d, int32_t* counts,
                                   int32_t* offsets, int32_t* device_status, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Router logits, selection from logits, and the selection's gradient.
+ *
+ * moe_route computes logits and chooses in one call and keeps the logits to
+ * itself.  A training step needs them again for the gradient, and rules with
+ * groups of experts choose in two stages; these calls take the pieces apart. */
+
+/* Element types of tensors whose type is an argument. */
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dtype;
+
+/* The projection of moe_route alone: logits[t, e] = the FP32 fused multiply-add
+ * chain over h of float(x[t,h]) * w_router[h,e], plus bias[e] if given (the same
+ * bits moe_route selects by).  x [T, H] bf16; logits [T, E] fp32 out.  d.k and d.I
+ * are not used beyond the limits. */
+moe_status moe_router_logits(const void* x, const float* w_router, const float* bias, moe_dims d,
+                             float* logits, void* stream);
+
+/* Selection rule.  For one token with logits l[e] and bias b[e] (0 if NULL):
+ *   kind MOE_ROUTER_SOFTMAX              key = l + b, score = softmax(key)
+ *   kind MOE_ROUTER_SIGMOID_BIAS_SELECT  score = sigmoid(l), key = score + b
+ * The experts form n_group groups of E / n_group consecutive ones.  A group's score
+ * is the sum of its group_top (1 or 2) largest keys; the topk_group groups with the
+ * largest scores stay (ties: lower group), and the k experts in them with the
+ * largest keys are chosen, in that order (ties: lower expert).  n_group = 1: no
+ * groups.
+ *   w_j = score_j, divided by the sum of the k chosen scores if renorm is nonzero.
+ * A logit (or key) of -inf or NaN masks its expert: key -inf, score 0, left out of
+ * group sums (a group of masked experts scores -inf); masked experts are chosen only
+ * when nothing else is left.  A row whose chosen scores are all 0 gets weights 0.
+ * +inf keys share the probability 1 among them for the first of the chosen.
+ * Sigmoid scores below FP32's range (logits below about -88) are 0. */
+typedef struct {
+  int32_t kind;        /* moe_router_kind */
+  int32_t n_group;     /* 1..32, divides E */
+  int32_t topk_group;  /* 1..n_group; k <= topk_group * E / n_group */
+  int32_t group_top;   /* 1 or 2 */
+  int32_t renorm;
+} moe_select_opts;
+
+/* Scratch of moe_route_select with prob_sum, and of moe_route_select_bwd with
+ * d_bias (0: dimensions outside the limits).  No status word; any contents. */
+size_t moe_select_workspace_bytes(int32_t T, int32_t E);
+
+/* Selection from logits (opts as above).
+ *   logits [T, E] of `dtype`, rows ld >= E elements apart (base aligned to 16 bytes;
+ *          rows that are not are read element by element)
+ *   bias [E] fp32 or NULL; topk_idx [T, k] int32 and topk_w [T, k] fp32 out
+ *   prob_sum [E] fp32 out or NULL: the sum over tokens of score[e] / (sum of all E
+ *          scores), what a load-balance loss is made of; needs the workspace
+ * 1 <= E <= 256, 1 <= k <= min(E, 16).  The routing scale belongs to the combine. */
+moe_status moe_route_select(const void* logits, int32_t dtype, int64_t ld, const float* bias,
+                            const moe_select_opts* opts, int32_t T, int32_t E, int32_t k,
+                            int32_t* topk_idx, float* topk_w, float* prob_sum, void* workspace,
+                            size_t ws_bytes, void* stream);
+
+/* Gradient of moe_route_select for the logits, the choice held fixed:
+ *   d_logits[t, :] = the gradient of sum_j d_topk_w[t,j] w[t,j] + sum_e d_prob_sum[e] *
+ *                    prob_sum[e]
+ * in `dtype`, rows ld_d elements apart; every element of [T, E] is written (masked
+ * experts and rows without a score get 0).
+ *   topk_idx [T, k] as moe_route_select wrote it (ids outside [0, E) contribute
+ *   nothing); d_topk_w [T, k] fp32; d_prob_sum [E] fp32 or NULL
+ *   d_bias [E] fp32 out or NULL, softmax kind only (its bias joins the logits): the
+ *   column sums of the gradient in FP32, in a fixed order; needs the workspace. */
+moe_status moe_route_select_bwd(const void* logits, int32_t dtype, int64_t ld, const float* bias,
+                                const moe_select_opts* opts, int32_t T, int32_t E, int32_t k,
+                                const int32_t* topk_idx, const float* d_topk_w,
+                                const float* d_prob_sum, void* d_logits, int64_t ld_d,
+                                float* d_bias, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (MXFP4) experts.
+ *
+ * A block is 32 consecutive values along K with one scale byte (2^(byte - 127);
+ * 255: the block is NaN); a value is a 4-bit code, sign and one of 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6; two codes a byte, the even index in the low half (OCP Microscaling
+ * Formats v1.0, E2M1 with E8M0 scales). */
+
+/* Quantises rows: scale = 2^(floor(log2 max|v|) - 2) of each block (clamped to
+ * 2^-127), codes = v / scale to nearest, ties to even, at most 6 in magnitude.  A
+ * block with an infinity or a NaN becomes NaN.
+ *   x [R, K] of `dtype`, rows ld >= K elements apart (ld * element size a multiple of
+ *     16); K a multiple of 32, at most 2^24
+ *   codes [R, K/2], scales [R, K/32] bytes and values [R, K] bf16 out (the values the
+ *     codes stand for, exact in bf16); each may be NULL */
+moe_status moe_mx4_quantize(const void* x, int32_t dtype, int64_t ld, int64_t R, int32_t K,
+                            void* codes, void* scales, void* values, void* stream);
+
+/* Bytes of a packed operand of E experts, K x N each (0: outside the limits: K and N
+ * multiples of 128, K <= 16384, N <= 32768, 1 <= E <= 256). */
+size_t moe_mx4_packed_bytes(int32_t E, int32_t K, int32_t N);
+
+/* One-time weight preparation from a quantised checkpoint: codes [E, N, K/2] and
+ * scales [E, N, K/32], row n the output column n over K. */
+moe_status moe_mx4_pack(const void* codes, const void* scales, int32_t E, int32_t K, int32_t N,
+                        void* packed, size_t packed_bytes, void* stream);
+
+/* The same from bf16 weights w [E, K, N] in the logical layout of
+ * moe_prepack_expert_weights (w_gate and w_up: K = H, N = I; w_down: K = I, N = H),
+ * quantised along K as moe_mx4_quantize does.  Writes the columns [col0, col0 + N) of
+ * a packed operand of N_total columns (all multiples of 128), so that gate and up
+ * share one: gate at 0 and up at I of N_total = 2 I. */
+moe_status moe_mx4_prepack(const void* w, int32_t E, int32_t K, int32_t N, int32_t col0,
+                           int32_t N_total, void* packed, size_t packed_bytes, void* stream);
+
+/* Workspace of moe_mx4_expert_product (0: outside the limits). */
+size_t moe_mx4_product_workspace_bytes(int32_t R, int32_t K, int32_t E);
+
+/* Grouped product: for each expert e and row r in [offsets[e], offsets[e+1]),
+ *   y[r, n] = sum over k of q(x[r])[k] * W_e[k, n]
+ * with q the block quantisation above and W_e the packed values; products exact,
+ * accumulated in FP32, rounded once if y is bf16.
+ *   x [R, K] of x_dtype, dense; offsets [E+1] int32 as moe_load_stats writes them; y
+ *   [R, N] of y_dtype (MOE_DTYPE_F32 or MOE_DTYPE_BF16)
+ * Offsets that are not a non-decreasing sequence from 0 to R are flagged
+ * (MOE_ERR_DEVICE_CHECK) and no row is written.  A row's result does not depend on
+ * the other rows.  Workspace as moe_workspace_bytes describes (status word first). */
+moe_status moe_mx4_expert_product(const void* x, int32_t x_dtype, const int32_t* offsets,
+                                  const void* packed, int32_t R, int32_t K, int32_t N, int32_t E,
+                                  void* y, int32_t y_dtype, void* workspace, size_t ws_bytes,
+                                  void* stream);
+
+/* Workspace of moe_mx4_layer_fwd (0: outside the limits). */
+size_t moe_mx4_layer_workspace_bytes(moe_dims d);
+
+/* The layer with microscaled 4-bit experts: moe_router_logits -> moe_route_select ->
+ * load stats -> stable ranks -> gate/up product -> silu(gate) * up quantised -> down
+ * product -> combine, enqueued on one stream.  The tokens are quantised as they are
+ * gathered (no permuted copy is kept); gate and up are rounded to bf16 once before
+ * the SwiGLU, whose own rounding is the 4-bit one; the down rows are FP32.
+ *   packed_gate_up: K = H, N = 2 I (gate columns first); packed_down: K = I, N = H
+ *   opts: the selection rule; bias as moe_route_select; route_scale as moe_combine_ex
+ *   topk_idx_out, topk_w_out, counts_out optional (NULL: workspace only) */
+moe_status moe_mx4_layer_fwd(const void* x, const float* w_router, const float* bias,
+                             const moe_select_opts* opts, float route_scale,
+                             const void* packed_gate_up, const void* packed_down, moe_dims d,
+                             void* out, int32_t* topk_idx_out, float* topk_w_out,
+                             int32_t* counts_out, void* workspace, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, returns the workspace status word in *status_out
  * (MOE_OK or the first device-side error recorded since the last read) and
  * clears it. */

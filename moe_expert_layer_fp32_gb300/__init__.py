@@ -39,7 +39,11 @@ ABI_SYMBOLS = ("moe_workspace_bytes", "moe_packed_weight_bytes", "moe_route", "m
                "moe_tree_reduce_bf16", "moe_shared_packed_bytes", "moe_prepack_shared_expert",
                "moe_shared_expert_workspace_bytes", "moe_shared_expert",
                "moe_sharded_workspace_bytes", "moe_layer_fwd_sharded",
-               "moe_layer_fwd_sharded_profiled", "moe_expert_ffn_form")
+               "moe_layer_fwd_sharded_profiled", "moe_expert_ffn_form",
+               "moe_router_logits", "moe_select_workspace_bytes", "moe_route_select",
+               "moe_route_select_bwd", "moe_mx4_quantize", "moe_mx4_packed_bytes",
+               "moe_mx4_pack", "moe_mx4_prepack", "moe_mx4_product_workspace_bytes",
+               "moe_mx4_expert_product", "moe_mx4_layer_workspace_bytes", "moe_mx4_layer_fwd")
 
 
 class moe_dims(ctypes.Structure):
@@ -66,11 +70,28 @@ def router_opts(kind=MOE_ROUTER_SOFTMAX, weights_bf16=False, route_scale=1.0) ->
     return moe_router_opts(int(kind), int(bool(weights_bf16)), float(route_scale))
 
 
+MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16 = 0, 1, 2
+_DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16,
+           torch.float16: MOE_DTYPE_F16}
+
+
+class moe_select_opts(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32)]
+
+
+def select_opts(kind=MOE_ROUTER_SOFTMAX, n_group=1, topk_group=1, group_top=1,
+                renorm=True) -> moe_select_opts:
+    return moe_select_opts(int(kind), int(n_group), int(topk_group), int(group_top),
+                           int(bool(renorm)))
+
+
 def _opts(o):
     return None if o is None else ctypes.byref(o)
 
 
-_vp, _sz, _i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32
+_vp, _sz, _i32, _i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
 _sig = {
     "moe_workspace_bytes": (_sz, [moe_dims]),
     "moe_packed_weight_bytes": (_sz, [moe_dims]),
@@ -114,6 +135,22 @@ _sig = {
     "moe_layer_fwd_sharded_profiled": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp,
                                                       _i32, moe_dims, _vp, _vp, _vp, _vp, _vp,
                                                       _sz, _vp, _vp, _i32]),
+    "moe_router_logits": (ctypes.c_int, [_vp, _vp, _vp, moe_dims, _vp, _vp]),
+    "moe_select_workspace_bytes": (_sz, [_i32, _i32]),
+    "moe_route_select": (ctypes.c_int, [_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp,
+                                        _vp, _sz, _vp]),
+    "moe_route_select_bwd": (ctypes.c_int, [_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _vp, _vp,
+                                            _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "moe_mx4_quantize": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "moe_mx4_packed_bytes": (_sz, [_i32, _i32, _i32]),
+    "moe_mx4_pack": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _sz, _vp]),
+    "moe_mx4_prepack": (ctypes.c_int, [_vp, _i32, _i32, _i32, _i32, _i32, _vp, _sz, _vp]),
+    "moe_mx4_product_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "moe_mx4_expert_product": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp,
+                                              _i32, _vp, _sz, _vp]),
+    "moe_mx4_layer_workspace_bytes": (_sz, [moe_dims]),
+    "moe_mx4_layer_fwd": (ctypes.c_int, [_vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, moe_dims,
+                                         _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -378,6 +415,84 @@ def moe_layer_fwd_profiled(x, w_router, bias, packed_weights, d, out, topk_idx_o
         len(events)))
 
 
+def moe_router_logits(x, w_router, bias, d, logits, stream=None):
+    _check("moe_router_logits", _lib.moe_router_logits(_ptr(x), _ptr(w_router), _ptr(bias), d,
+                                                       _ptr(logits), _stream(stream)))
+
+
+def moe_select_workspace_bytes(T, E) -> int:
+    return int(_lib.moe_select_workspace_bytes(int(T), int(E)))
+
+
+def _ws_or_none(ws):
+    return (None, 0) if ws is None else _ws(ws)
+
+
+def moe_route_select(logits, dtype, ld, bias, opts, T, E, k, topk_idx, topk_w, prob_sum=None,
+                     workspace=None, stream=None):
+    wp, wb = _ws_or_none(workspace)
+    _check("moe_route_select", _lib.moe_route_select(
+        _ptr(logits), int(dtype), int(ld), _ptr(bias), _opts(opts), int(T), int(E), int(k),
+        _ptr(topk_idx), _ptr(topk_w), _ptr(prob_sum), wp, wb, _stream(stream)))
+
+
+def moe_route_select_bwd(logits, dtype, ld, bias, opts, T, E, k, topk_idx, d_topk_w, d_prob_sum,
+                         d_logits, ld_d, d_bias=None, workspace=None, stream=None):
+    wp, wb = _ws_or_none(workspace)
+    _check("moe_route_select_bwd", _lib.moe_route_select_bwd(
+        _ptr(logits), int(dtype), int(ld), _ptr(bias), _opts(opts), int(T), int(E), int(k),
+        _ptr(topk_idx), _ptr(d_topk_w), _ptr(d_prob_sum), _ptr(d_logits), int(ld_d), _ptr(d_bias),
+        wp, wb, _stream(stream)))
+
+
+def moe_mx4_quantize(x, dtype, ld, R, K, codes, scales, values, stream=None):
+    _check("moe_mx4_quantize", _lib.moe_mx4_quantize(
+        _ptr(x), int(dtype), int(ld), int(R), int(K), _ptr(codes), _ptr(scales), _ptr(values),
+        _stream(stream)))
+
+
+def moe_mx4_packed_bytes(E, K, N) -> int:
+    return int(_lib.moe_mx4_packed_bytes(int(E), int(K), int(N)))
+
+
+def moe_mx4_pack(codes, scales, E, K, N, packed, stream=None):
+    nbytes = packed.numel() * packed.element_size() if isinstance(packed, torch.Tensor) else 1 << 62
+    _check("moe_mx4_pack", _lib.moe_mx4_pack(_ptr(codes), _ptr(scales), int(E), int(K), int(N),
+                                             _ptr(packed), nbytes, _stream(stream)))
+
+
+def moe_mx4_prepack(w, E, K, N, col0, N_total, packed, stream=None):
+    nbytes = packed.numel() * packed.element_size() if isinstance(packed, torch.Tensor) else 1 << 62
+    _check("moe_mx4_prepack", _lib.moe_mx4_prepack(_ptr(w), int(E), int(K), int(N), int(col0),
+                                                   int(N_total), _ptr(packed), nbytes,
+                                                   _stream(stream)))
+
+
+def moe_mx4_product_workspace_bytes(R, K, E) -> int:
+    return int(_lib.moe_mx4_product_workspace_bytes(int(R), int(K), int(E)))
+
+
+def moe_mx4_expert_product(x, x_dtype, offsets, packed, R, K, N, E, y, y_dtype, workspace,
+                           stream=None):
+    wp, wb = _ws(workspace)
+    _check("moe_mx4_expert_product", _lib.moe_mx4_expert_product(
+        _ptr(x), int(x_dtype), _ptr(offsets), _ptr(packed), int(R), int(K), int(N), int(E),
+        _ptr(y), int(y_dtype), wp, wb, _stream(stream)))
+
+
+def moe_mx4_layer_workspace_bytes(d: moe_dims) -> int:
+    return int(_lib.moe_mx4_layer_workspace_bytes(d))
+
+
+def moe_mx4_layer_fwd(x, w_router, bias, opts, route_scale, packed_gate_up, packed_down, d, out,
+                      topk_idx_out, topk_w_out, counts_out, workspace, stream=None):
+    wp, wb = _ws(workspace)
+    _check("moe_mx4_layer_fwd", _lib.moe_mx4_layer_fwd(
+        _ptr(x), _ptr(w_router), _ptr(bias), _opts(opts), float(route_scale),
+        _ptr(packed_gate_up), _ptr(packed_down), d, _ptr(out), _ptr(topk_idx_out),
+        _ptr(topk_w_out), _ptr(counts_out), wp, wb, _stream(stream)))
+
+
 def moe_set_wait_limit(cycles: int) -> None:
     """Diagnostics: bounded-wait limit of the GEMM kernels (<= 0: default)."""
     _check("moe_set_wait_limit", _lib.moe_set_wait_limit(int(cycles)))
@@ -420,6 +535,197 @@ def layer_forward(x, w_router, bias, packed, d, workspace, stream=None, want_rou
         w = torch.empty((d.T, d.k), dtype=torch.float32, device=dev)
         counts = torch.empty(d.E, dtype=torch.int32, device=dev)
     moe_layer_fwd_ex(x, w_router, bias, opts, packed, d, out, idx, w, counts, workspace, stream)
+    return (out, idx, w, counts) if want_routing else out
+
+
+def _dtype(name, t):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: float32, bfloat16 or float16, not {t.dtype}")
+    return code
+
+
+def _rows(name, t, cols=None):
+    """Row stride of a 2D tensor whose elements within a row are adjacent."""
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name}: a 2D tensor" + (f" of {cols} columns" if cols else "")
+                         + f", not {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent (stride {t.stride()})")
+    if t.shape[0] <= 1:
+        return t.shape[1]
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows must not overlap (stride {t.stride()})")
+    return t.stride(0)
+
+
+def _dense(name, t, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: a dense {dtype} tensor of shape {tuple(shape)}, not "
+                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()}")
+    return t
+
+
+def _on_device(*tensors):
+    """One device for all tensors, made current for the call's launches by the caller's
+    context; CPU tensors and mixed devices are refused."""
+    devs = {t.device for t in tensors if t is not None}
+    if any(d.type != "cuda" for d in devs):
+        raise ValueError("tensors must be on a CUDA device")
+    if len(devs) > 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+
+
+def route_select(logits, k, opts=None, bias=None, want_prob_sum=False, stream=None):
+    """(topk_idx [T, k] int32, topk_w [T, k] fp32[, prob_sum [E] fp32]) from logits [T, E]
+    (fp32, bf16 or fp16).  opts: a select_opts (default: softmax over all experts)."""
+    ld = _rows("logits", logits)
+    T, E = logits.shape
+    dt = _dtype("logits", logits)
+    if bias is not None:
+        _dense("bias", bias, torch.float32, (E,))
+    _on_device(logits, bias)
+    dev = logits.device
+    idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    prob = ws = None
+    if want_prob_sum:
+        prob = torch.empty(E, dtype=torch.float32, device=dev)
+        ws = torch.empty(moe_select_workspace_bytes(T, E), dtype=torch.uint8, device=dev)
+    moe_route_select(logits, dt, ld, bias, select_opts() if opts is None else opts, T, E, k, idx, w,
+                     prob, ws, stream)
+    return (idx, w, prob) if want_prob_sum else (idx, w)
+
+
+def route_select_backward(logits, topk_idx, d_topk_w, opts=None, bias=None, d_prob_sum=None,
+                          want_d_bias=False, stream=None):
+    """d_logits [T, E] in the logits' type (and d_bias [E] fp32 if want_d_bias, softmax only)
+    for d_topk_w [T, k] and, if given, d_prob_sum [E], both fp32; the choice stays fixed."""
+    ld = _rows("logits", logits)
+    T, E = logits.shape
+    dt = _dtype("logits", logits)
+    if topk_idx.dim() != 2:
+        raise ValueError(f"topk_idx: [T, k], not {tuple(topk_idx.shape)}")
+    k = topk_idx.shape[1]
+    _dense("topk_idx", topk_idx, torch.int32, (T, k))
+    _dense("d_topk_w", d_topk_w, torch.float32, (T, k))
+    for name, t in (("bias", bias), ("d_prob_sum", d_prob_sum)):
+        if t is not None:
+            _dense(name, t, torch.float32, (E,))
+    _on_device(logits, topk_idx, d_topk_w, bias, d_prob_sum)
+    d_logits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    d_bias = ws = None
+    if want_d_bias:
+        d_bias = torch.empty(E, dtype=torch.float32, device=logits.device)
+        ws = torch.empty(moe_select_workspace_bytes(T, E), dtype=torch.uint8, device=logits.device)
+    moe_route_select_bwd(logits, dt, ld, bias, select_opts() if opts is None else opts, T, E, k,
+                         topk_idx, d_topk_w, d_prob_sum, d_logits, E, d_bias, ws, stream)
+    return (d_logits, d_bias) if want_d_bias else d_logits
+
+
+def mx4_quantize(x, want_values=False, stream=None):
+    """(codes [R, K/2] uint8, scales [R, K/32] uint8[, values [R, K] bf16]) of rows x [R, K]
+    (fp32, bf16 or fp16), K a multiple of 32."""
+    ld = _rows("x", x)
+    dt = _dtype("x", x)
+    _on_device(x)
+    R, K = x.shape
+    codes = torch.empty((R, K // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((R, K // 32), dtype=torch.uint8, device=x.device)
+    values = torch.empty((R, K), dtype=torch.bfloat16, device=x.device) if want_values else None
+    moe_mx4_quantize(x, dt, ld, R, K, codes, scales, values, stream)
+    return (codes, scales, values) if want_values else (codes, scales)
+
+
+def mx4_pack(codes, scales, stream=None) -> torch.Tensor:
+    """Packed operand from checkpoint tensors codes [E, N, K/2] and scales [E, N, K/32]."""
+    if codes.dim() != 3:
+        raise ValueError(f"codes: [E, N, K/2], not {tuple(codes.shape)}")
+    E, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+    _dense("codes", codes, torch.uint8, (E, N, K // 2))
+    _dense("scales", scales, torch.uint8, (E, N, K // 32))
+    _on_device(codes, scales)
+    n = moe_mx4_packed_bytes(E, K, N)
+    if n == 0:
+        raise MoEError("moe_mx4_packed_bytes", 2)
+    packed = torch.empty(n, dtype=torch.uint8, device=codes.device)
+    moe_mx4_pack(codes, scales, E, K, N, packed, stream)
+    return packed
+
+
+def mx4_prepack(*weights, stream=None) -> torch.Tensor:
+    """Packed operand from bf16 weights [E, K, N_i] in the logical layout, quantised along K;
+    several (gate, up) lie side by side in one operand of sum(N_i) columns."""
+    if not weights or any(w.dim() != 3 for w in weights):
+        raise ValueError("weights: one or more [E, K, N] tensors")
+    E, K = weights[0].shape[:2]
+    N_total = sum(w.shape[2] for w in weights)
+    for w in weights:
+        _dense("weights", w, torch.bfloat16, (E, K, w.shape[2]))
+    _on_device(*weights)
+    n = moe_mx4_packed_bytes(E, K, N_total)
+    if n == 0:
+        raise MoEError("moe_mx4_packed_bytes", 2)
+    packed = torch.empty(n, dtype=torch.uint8, device=weights[0].device)
+    col = 0
+    for w in weights:
+        moe_mx4_prepack(w, E, K, w.shape[2], col, N_total, packed, stream)
+        col += w.shape[2]
+    return packed
+
+
+def _zeroed(n, name, device):
+    if n == 0:
+        raise MoEError(name, 2)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()  # the status word; the rest is scratch
+    return ws
+
+
+def mx4_new_workspace(R, K, N, E, device="cuda") -> torch.Tensor:
+    """Workspace of mx4_expert_product for up to R rows."""
+    return _zeroed(moe_mx4_product_workspace_bytes(R, K, E), "moe_mx4_product_workspace_bytes",
+                   device)
+
+
+def mx4_expert_product(x, offsets, packed, N, workspace, dtype=torch.bfloat16, stream=None):
+    """y [R, N] (bf16 or fp32): rows x [R, K] of each expert (offsets [E+1] int32) quantised to
+    microscaled 4 bits, times the expert's packed weights."""
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError(f"x: a dense [R, K] tensor, not {tuple(x.shape)} strides {x.stride()}")
+    dt = _dtype("x", x)
+    if offsets.dim() != 1:
+        raise ValueError(f"offsets: [E + 1], not {tuple(offsets.shape)}")
+    E, (R, K) = offsets.numel() - 1, x.shape
+    _dense("offsets", offsets, torch.int32, (E + 1,))
+    if packed.numel() * packed.element_size() != moe_mx4_packed_bytes(E, K, N):
+        raise ValueError(f"packed: {packed.numel() * packed.element_size()} bytes, not those of "
+                         f"{E} experts of {K} x {N}")
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"y: float32 or bfloat16, not {dtype}")
+    _on_device(x, offsets, packed, workspace)
+    y = torch.empty((R, N), dtype=dtype, device=x.device)
+    moe_mx4_expert_product(x, dt, offsets, packed, R, K, N, E, y, _DTYPES[dtype], workspace, stream)
+    return y
+
+
+def mx4_new_layer_workspace(d: moe_dims, device="cuda") -> torch.Tensor:
+    return _zeroed(moe_mx4_layer_workspace_bytes(d), "moe_mx4_layer_workspace_bytes", device)
+
+
+def mx4_layer_forward(x, w_router, bias, packed_gate_up, packed_down, d, workspace, opts=None,
+                      route_scale=1.0, want_routing=False, stream=None):
+    """out [T, H] bf16 (and topk_idx, topk_w, counts if want_routing) of the layer with
+    microscaled 4-bit experts."""
+    dev = x.device
+    out = torch.empty((d.T, d.H), dtype=torch.bfloat16, device=dev)
+    idx = w = counts = None
+    if want_routing:
+        idx = torch.empty((d.T, d.k), dtype=torch.int32, device=dev)
+        w = torch.empty((d.T, d.k), dtype=torch.float32, device=dev)
+        counts = torch.empty(d.E, dtype=torch.int32, device=dev)
+    moe_mx4_layer_fwd(x, w_router, bias, select_opts() if opts is None else opts, route_scale,
+                      packed_gate_up, packed_down, d, out, idx, w, counts, workspace, stream)
     return (out, idx, w, counts) if want_routing else out
 
 

@@ -151,6 +151,44 @@ cudaError_t launch_combine_sharded(const float* y, const float* topk_w, const in
 cudaError_t launch_tree_reduce(const void* partials, int G, long long N, void* out, bool vec,
                                cudaStream_t s);
 
+// ------------------------------------------- selection from router logits ---
+// (select.cu) dtype: moe_dtype of the logits and their gradient; ld: their row strides.
+// partial: select_partial_bytes(T, E) of scratch, used only with prob_sum / d_bias.
+size_t select_partial_bytes(int T, int E);
+cudaError_t launch_select(const void* logits, int dtype, long long ld, const float* bias,
+                          const moe_select_opts& o, int T, int E, int k, int32_t* topk_idx,
+                          float* topk_w, float* prob_sum, float* partial, cudaStream_t s);
+cudaError_t launch_select_bwd(const void* logits, int dtype, long long ld, const float* bias,
+                              const moe_select_opts& o, int T, int E, int k,
+                              const int32_t* topk_idx, const float* d_topk_w,
+                              const float* d_prob_sum, void* d_logits, long long ld_d,
+                              float* d_bias, float* partial, cudaStream_t s);
+
+// ------------------------------------------- microscaled 4-bit floating point ---
+// (mx4_quant.cu, mx4_gemm.cu; layouts in mx4.cuh)
+cudaError_t launch_mx4_quantize(const void* x, int dtype, long long ld, long long R, int K,
+                                void* codes, void* scales, void* values, cudaStream_t s);
+// An expert operand's row images.  src 0: x [R, K]; 1: row r is row row_of[r] / k of x [T, K]
+// bf16; 2: silu(gate) * up of x [R, 2K] bf16.
+cudaError_t launch_mx4_rows(const void* x, int dtype, int src, const int32_t* row_of, int k, int T,
+                            const int32_t* offsets, int E, int R, int K, void* codes, void* sf,
+                            int32_t* status, cudaStream_t s);
+cudaError_t launch_mx4_pack(const void* codes, const void* scales, int E, int K, int N,
+                            void* packed, cudaStream_t s);
+cudaError_t launch_mx4_prepack(const void* w, int E, int K, int N, int col0, int N_total,
+                               void* packed, cudaStream_t s);
+// y [R, N] (FP32 or bf16) = the row images times each expert's weight images
+cudaError_t launch_mx4_gemm(const void* packed, const void* codes, const void* sf,
+                            const int32_t* offsets, int E, int R, int K, int N, void* y,
+                            int y_dtype, int32_t* status, long long spin_limit, cudaStream_t s);
+
+// The limit of the GEMM kernels' bounded waits now in force (moe_set_wait_limit).
+long long wait_limit();
+
+// The router's projection alone: logits [T, E] = the FP32 chains plus the optional bias.
+cudaError_t launch_router_logits(const void* x, const float* w_router, const float* bias, int T,
+                                 int H, int E, float* logits, cudaStream_t s);
+
 // number of SMs of the current device (cached per device)
 int device_sm_count();
 

@@ -164,6 +164,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 moe_status validate_dims(const moe_dims& d) { return check_dims(d); }
 moe_status validate_ptr(const void* p) { return need(p); }
 moe_status validate_device() { return device_ok(); }
+long long wait_limit() { return g_wait_limit.load(); }
 
 bool GemmOperand::encode(CUtensorMap* m, uint32_t box_rows) const {
   auto fn = encode_fn();

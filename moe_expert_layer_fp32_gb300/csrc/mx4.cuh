@@ -1,0 +1,166 @@
+// Microscaled 4-bit floating point (MXFP4): the block format, and the layout in which
+// the grouped product streams its operands.
+//
+// A block is 32 consecutive values of a row over K.  Its scale is 2^(byte - 127), one byte
+// (255: NaN); each value is a 4-bit code, sign and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6.  Two
+// codes share a byte, the even one in the low half.  (OCP Microscaling Formats v1.0:
+// element E2M1, scale E8M0, block size 32.)
+//
+// Operand images.  The product reads shared-memory images that one bulk copy brings in:
+// rows of 128 bytes (256 codes, a k-block) whose 16-byte chunk c sits at c ^ (row & 7)
+// (the MMA's 128-byte swizzle), and the scales of 128 rows x 128 K as 512 bytes, row r's
+// four scales at (r % 32) * 16 + (r / 32) * 4 (the order in which tensor memory takes
+// them).
+//   weights  per (expert, 128 output columns, k-block): 16384 bytes of codes, then 1024 of
+//            scales (two halves of the k-block)
+//   rows     the rows of an expert in tiles of at most kMx4TileRows, evenly cut; an expert's
+//            rows are padded to 16, a tile's k-blocks follow one another (tile rows x 128
+//            bytes each); the scales of tile i and k-block b at slot (i * KB + b) of 2048
+//            bytes, [128-row half][half of the k-block][512]
+// Padding rows are never written; they only reach accumulator columns that are not stored.
+#pragma once
+
+#include <stdint.h>
+
+#include "common.cuh"
+#include "kernels.cuh"
+
+namespace moe {
+
+constexpr int kMx4KB = 256;           // values of a k-block: one 128-byte row of codes
+constexpr int kMx4TileRows = 224;     // rows of the largest tile (accumulator columns)
+constexpr int kMx4WTile = 128;        // output columns of a weight tile (accumulator lanes)
+constexpr int kMx4WBytes = kMx4WTile * 128 + 1024;  // image of a weight tile's k-block
+constexpr int kMx4SfSlot = 2048;      // scales of a row tile's k-block
+
+__host__ __device__ inline int mx4_kblocks(int K) { return (K + kMx4KB - 1) / kMx4KB; }
+
+// How an expert's m rows are cut: n tiles of `step` rows (a multiple of 16), the last shorter.
+struct Mx4Cut {
+  int n, step;
+};
+__host__ __device__ inline Mx4Cut mx4_cut(int m) {
+  Mx4Cut c;
+  c.n = (m + kMx4TileRows - 1) / kMx4TileRows;
+  c.step = c.n > 0 ? ((m + c.n - 1) / c.n + 15) / 16 * 16 : 16;
+  return c;
+}
+
+// Bounds over every split of R rows among E experts.
+inline long long mx4_max_padded_rows(long long R, int E) {
+  const long long with = R < E ? R : E;  // experts that can have rows
+  return R + 15 * with;
+}
+inline long long mx4_max_tiles(long long R, int E) {
+  const long long with = R < E ? R : E;
+  return R / kMx4TileRows + with;
+}
+
+// Prefix tables of a grouped operand in shared memory, from offsets [E+1]; every thread of
+// the block calls it (blockDim a multiple of 32, at least 32).  Returns false (and flags) if
+// the offsets are not 0 = o_0 <= ... <= o_E = R.
+struct Mx4Tables {
+  int off[kMaxE + 1];    // first row of each expert
+  int pad[kMaxE + 1];    // its first padded row, in units of 16
+  int tile[kMaxE + 1];   // its first row tile
+  int ok;
+};
+
+__device__ __forceinline__ bool mx4_build_tables(Mx4Tables& s, const int32_t* __restrict__ offsets,
+                                                 int E, int R, int32_t* status) {
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) s.off[e] = offsets[e];
+  __syncthreads();
+  if (threadIdx.x < 32) {  // one warp scans, 32 experts a step
+    const int lane = threadIdx.x;
+    int pad = 0, tile = 0;
+    bool ok = s.off[0] == 0 && s.off[E] == R;
+    for (int b = 0; b < E; b += 32) {
+      const int e = b + lane;
+      int m = 0;
+      if (e < E) {
+        const int lo = s.off[e], hi = s.off[e + 1];
+        if (lo < 0 || hi < lo || hi > R) ok = false;
+        else m = hi - lo;
+      }
+      int p = (m + 15) / 16, n = mx4_cut(m).n;
+      const int p0 = p, n0 = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int pu = __shfl_up_sync(0xFFFFFFFFu, p, o), nu = __shfl_up_sync(0xFFFFFFFFu, n, o);
+        if (lane >= o) {
+          p += pu;
+          n += nu;
+        }
+      }
+      if (e < E) {
+        s.pad[e] = pad + p - p0;
+        s.tile[e] = tile + n - n0;
+      }
+      pad += __shfl_sync(0xFFFFFFFFu, p, 31);
+      tile += __shfl_sync(0xFFFFFFFFu, n, 31);
+    }
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (lane == 0) {
+      s.pad[E] = pad;
+      s.tile[E] = tile;
+      s.ok = ok;
+      if (!ok) flag_error(status, MOE_ERR_DEVICE_CHECK);
+    }
+  }
+  __syncthreads();
+  return s.ok != 0;
+}
+
+// largest e in [0, E) with table[e] <= v (experts without entries share the next value)
+__device__ __forceinline__ int mx4_find(const int* table, int E, int v) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (table[mid] <= v) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Scale byte of a block whose largest magnitude has the FP32 bits `amax` (sign cleared):
+// the exponent of the block's largest value becomes the format's (4 = 2^2), clamped to the
+// smallest scale; infinities and NaN give 255.
+__device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t amax) {
+  const uint32_t e = amax >> 23;
+  return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+// 2^(127 - byte), which takes the block's values into the code's range (0 for a NaN block,
+// whose codes are then 0 or, for its NaNs, whatever the conversion gives: its scale decides)
+__device__ __forceinline__ float mx4_inverse_scale(uint32_t byte) {
+  if (byte == 255u) return 0.0f;
+  return __uint_as_float((254u - byte) << 23);
+}
+// 2^(byte - 127); 255: NaN
+__device__ __forceinline__ float mx4_scale(uint32_t byte) {
+  if (byte == 255u) return __uint_as_float(0x7FC00000u);
+  return byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+}
+
+// Eight values (already scaled) to eight codes, the first in the lowest four bits: to
+// nearest, ties to even, at most 6.
+__device__ __forceinline__ uint32_t mx4_encode8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// A code's magnitude and sign as a float.
+__device__ __forceinline__ float mx4_value(uint32_t code) {
+  // magnitudes in quarters of 2: 0 .5 1 1.5 2 3 4 6 as four-bit halves 0 1 2 3 4 6 8 12
+  const float m = 0.5f * (float)((0xC8643210u >> ((code & 7u) * 4u)) & 15u);
+  return (code & 8u) ? -m : m;
+}
+
+}  // namespace moe

@@ -1,0 +1,332 @@
+// Grouped product of microscaled 4-bit operands on the 5th-generation tensor cores.
+//
+//   y[r, n] = sum over k of q(x)[r, k] * q(W_e)[k, n]     for the rows r of expert e,
+//
+// each operand a code times its block's power-of-two scale (mx4.cuh), products exact and
+// accumulated in FP32 by tcgen05.mma kind::mxf4 (block scales from tensor memory).
+//
+// The weights take the MMA's M side: 128 output columns in the accumulator's lanes, a
+// tile of up to 224 rows of the expert in its columns (N is the tile's own row count, so
+// a short tile costs what it holds).  Persistent CTAs, one per SM, warp-specialised:
+//   warp 0   producer: three bulk copies a k-block of 256 (weights with their scales,
+//            rows, row scales) into a ring of STAGES shared-memory images
+//   warp 1   MMA issuer: the scales from shared into tensor memory, then four MMAs of
+//            K = 64.  The role runs in one elected lane for its whole loop: issued from a
+//            lane picked by its index instead, an MMA took 95 cycles of issue, the 224-row
+//            MMA itself 112.
+//   warps 2-5  epilogue: 32 lanes x 32 columns at a time from tensor memory; a warp writes
+//            32 consecutive output columns of one row per store
+// Tensor memory: two accumulators of 224 columns (a unit's epilogue runs under the next
+// one's main loop) and two sets of 24 scale columns, 496 of 512.
+//
+// Every wait is bounded and drains as in expert_gemm.cu.
+#include "common.cuh"
+#include "kernels.cuh"
+#include "mx4.cuh"
+#include "pdl.cuh"
+
+namespace moe {
+namespace {
+
+struct MxCfg {
+  static constexpr int STAGES = 4;
+  static constexpr int SF_OFF = kMx4WBytes;                  // row scales
+  static constexpr int ROW_OFF = SF_OFF + kMx4SfSlot;        // row codes (1024-byte aligned)
+  static constexpr int STAGE_BYTES = ROW_OFF + kMx4TileRows * 128;
+  static constexpr int NBAR = 2 * STAGES + 2 + 2 + 1;
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int ACC_COLS = kMx4TileRows;
+  static constexpr int SF_COL = 2 * ACC_COLS;                // first scale column
+  static constexpr int SMEM_BYTES =
+      1024 + STAGES * STAGE_BYTES + NBAR * 8 + 16 + (int)sizeof(Mx4Tables) + 16;
+  static_assert(ROW_OFF % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzled images: 1024 bytes");
+  static_assert(SF_COL + 48 <= TMEM_COLS, "scale columns");
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_u32(smem_dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// 32 rows of 16 bytes in shared memory to four columns of tensor memory, in each of its
+// four lane quarters
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)1u << 16;
+  d |= (uint64_t)(128u >> 4) << 32;  // next 8 rows
+  d |= (uint64_t)1u << 46;
+  return d;
+}
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+               : "memory");
+}
+
+// Instruction descriptor, kind::mxf4: E2M1 A and B (K-major), E8M0 scales, M = 128, N rows;
+// `id`: which two of a scale word's four bytes an MMA of K = 64 reads (0 or 2).
+__device__ __forceinline__ uint32_t idesc_mx4(int N, uint32_t id) {
+  return (id << 4)                       // B scale bytes
+         | (1u << 7) | (1u << 10)        // A, B: E2M1
+         | ((uint32_t)(N >> 3) << 17)    // N / 8
+         | (1u << 23)                    // scales: E8M0
+         | ((128u >> 4) << 24)           // M / 16
+         | (id << 29);                   // A scale bytes
+}
+__device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
+      "p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// One unit: a row tile of an expert times one weight tile.
+struct MxUnit {
+  int row0;              // first output row
+  int rows;              // rows of the tile
+  int rows16;            // padded to 16: N of its MMAs
+  int nt;                // weight tile of the expert
+  size_t w_img;          // byte offsets of k-block 0's images
+  size_t row_img;
+  size_t sf_img;
+};
+
+__device__ __forceinline__ MxUnit mx_unit(long long u, const Mx4Tables& tb, int E, int NT, int KB) {
+  const int tile = (int)(u / NT);
+  const int e = mx4_find(tb.tile, E, tile);
+  const int m = tb.off[e + 1] - tb.off[e];
+  const Mx4Cut cut = mx4_cut(m);
+  const int ti = tile - tb.tile[e];
+  MxUnit w;
+  w.nt = (int)(u - (long long)tile * NT);
+  w.row0 = tb.off[e] + ti * cut.step;
+  w.rows = min(cut.step, m - ti * cut.step);
+  w.rows16 = (w.rows + 15) / 16 * 16;
+  w.w_img = ((size_t)e * NT + w.nt) * KB * kMx4WBytes;
+  w.row_img = ((size_t)tb.pad[e] * 16 + (size_t)ti * cut.step) * KB * 128;
+  w.sf_img = (size_t)tile * KB * kMx4SfSlot;
+  return w;
+}
+
+template <typename Tout>
+__global__ void __launch_bounds__(192, 1)
+    mx4_gemm_kernel(const uint8_t* __restrict__ wimg, const uint8_t* __restrict__ rimg,
+                    const uint8_t* __restrict__ simg, const int32_t* __restrict__ offsets, int E,
+                    int R, int K, int N, Tout* __restrict__ y, int32_t* status,
+                    long long spin_limit) {
+  using C = MxCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::STAGES * C::STAGE_BYTES);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + C::STAGES;
+  uint64_t* tfull = bars + 2 * C::STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* mma_done = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Mx4Tables& tb = *reinterpret_cast<Mx4Tables*>(tmem_slot + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int NT = N / kMx4WTile;
+  const int KB = mx4_kblocks(K);
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 128);
+    }
+    mbar_init(mma_done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
+  const bool ok_tables = mx4_build_tables(tb, offsets, E, R, status);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const long long total = ok_tables ? (long long)tb.tile[E] * NT : 0;
+
+  if (warp == 0) {
+    if (elect_one()) {
+      // ------------------------------------------------------------ producer
+      int it = 0;
+      bool aborted = false;
+      for (long long u = blockIdx.x; u < total && !aborted; u += gridDim.x) {
+        const MxUnit w = mx_unit(u, tb, E, NT, KB);
+        const uint32_t row_bytes = (uint32_t)w.rows16 * 128u;
+        const uint32_t sf_bytes = w.rows16 > 128 ? 2048u : 1024u;
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const int s = it % C::STAGES;
+          const uint32_t ph = (it / C::STAGES) & 1;
+          if (!mbar_wait_bounded(&empty[s], ph ^ 1, abort_flag, status, spin_limit)) {
+            aborted = true;
+            break;
+          }
+          uint8_t* st = base + s * C::STAGE_BYTES;
+          mbar_arrive_expect_tx(&full[s], kMx4WBytes + row_bytes + sf_bytes);
+          bulk_load(st, wimg + w.w_img + (size_t)kb * kMx4WBytes, kMx4WBytes, &full[s]);
+          bulk_load(st + C::ROW_OFF, rimg + w.row_img + (size_t)kb * row_bytes, row_bytes, &full[s]);
+          bulk_load(st + C::SF_OFF, simg + w.sf_img + (size_t)kb * kMx4SfSlot, sf_bytes, &full[s]);
+        }
+      }
+      if (aborted) {
+        // the copies issued into the last STAGES slots may still be in flight
+        for (int i = (it > C::STAGES ? it - C::STAGES : 0); i < it; ++i)
+          wait_drain(&full[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (elect_one()) {
+      // ---------------------------------------------------------- MMA issuer
+      int it = 0, tcount = 0;
+      for (long long u = blockIdx.x; u < total; u += gridDim.x, ++tcount) {
+        const MxUnit w = mx_unit(u, tb, E, NT, KB);
+        const int acc = tcount & 1;
+        const uint32_t aph = (tcount >> 1) & 1;
+        if (!mbar_wait_bounded(&tempty[acc], aph ^ 1, abort_flag, status, spin_limit)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + acc * C::ACC_COLS;
+        const uint32_t id0 = idesc_mx4(w.rows16, 0), id1 = idesc_mx4(w.rows16, 2);
+        const bool two = w.rows16 > 128;
+        bool aborted = false;
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const int s = it % C::STAGES;
+          const uint32_t ph = (it / C::STAGES) & 1;
+          if (!mbar_wait_bounded(&full[s], ph, abort_flag, status, spin_limit)) {
+            aborted = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = smem_u32(base + s * C::STAGE_BYTES);
+          const uint64_t da = sdesc_k_major_sw128(st), db = sdesc_k_major_sw128(st + C::ROW_OFF);
+          const uint64_t fa = sdesc_scales(st + kMx4WTile * 128), fb = sdesc_scales(st + C::SF_OFF);
+          // scale columns: weights 4 per half k-block, rows 8 (two 128-row halves)
+          const uint32_t sfa = tmem_base + C::SF_COL + (it & 1) * 24, sfb = sfa + 8;
+          const bool whole = (kb + 1) * kMx4KB <= K;  // else the first half only
+          copy_scales(sfa, fa);
+          copy_scales(sfb, fb);
+          if (two) copy_scales(sfb + 4, fb + 64);
+          if (whole) {
+            copy_scales(sfa + 4, fa + 32);
+            copy_scales(sfb + 8, fb + 32);
+            if (two) copy_scales(sfb + 12, fb + 96);
+          }
+          mma_mx4(d, da, db, id0, sfa, sfb, kb > 0 ? 1u : 0u);
+          mma_mx4(d, da + 2, db + 2, id1, sfa, sfb, 1u);
+          if (whole) {
+            mma_mx4(d, da + 4, db + 4, id0, sfa + 4, sfb + 8, 1u);
+            mma_mx4(d, da + 6, db + 6, id1, sfa + 4, sfb + 8, 1u);
+          }
+          mma_commit(&empty[s]);
+        }
+        if (aborted) break;
+        mma_commit(&tfull[acc]);
+      }
+      // every MMA this thread issued completes before tensor memory is released
+      mma_commit(mma_done);
+      wait_drain(mma_done, 0, kSpinLimitCycles);
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int q = warp & 3;  // lane quarter of tensor memory this warp may access
+    int tcount = 0;
+    for (long long u = blockIdx.x; u < total; u += gridDim.x, ++tcount) {
+      const MxUnit w = mx_unit(u, tb, E, NT, KB);
+      const int acc = tcount & 1;
+      const uint32_t aph = (tcount >> 1) & 1;
+      int ok = 1;
+      if (lane == 0) ok = mbar_wait_bounded(&tfull[acc], aph, abort_flag, status, spin_limit);
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * C::ACC_COLS);
+      Tout* dst = y + (size_t)w.row0 * N + w.nt * kMx4WTile + q * 32 + lane;
+      for (int c0 = 0; c0 < w.rows; c0 += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(taddr + c0, v);
+        tmem_ld_wait();
+        const int n = min(32, w.rows - c0);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (i < n) {
+            const float f = __uint_as_float(v[i]);
+            if constexpr (sizeof(Tout) == 4) dst[(size_t)(c0 + i) * N] = f;
+            else dst[(size_t)(c0 + i) * N] = __float2bfloat16_rn(f);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&tempty[acc]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+template <typename Tout>
+cudaError_t go(const uint8_t* w, const uint8_t* r, const uint8_t* sf, const int32_t* offsets, int E,
+               int R, int K, int N, void* y, int32_t* status, long long limit, cudaStream_t s) {
+  static bool attr[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !attr[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(
+        mx4_gemm_kernel<Tout>, cudaFuncAttributeMaxDynamicSharedMemorySize, MxCfg::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr[dev] = true;
+  }
+  const long long units = mx4_max_tiles(R, E) * (N / kMx4WTile);
+  const int sms = device_sm_count();
+  const int grid = (int)(units < sms ? units : sms);
+  mx4_gemm_kernel<Tout><<<grid, 192, MxCfg::SMEM_BYTES, s>>>(w, r, sf, offsets, E, R, K, N,
+                                                            static_cast<Tout*>(y), status, limit);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_gemm(const void* packed, const void* codes, const void* sf,
+                            const int32_t* offsets, int E, int R, int K, int N, void* y,
+                            int y_dtype, int32_t* status, long long spin_limit, cudaStream_t s) {
+  if (R == 0) return cudaSuccess;
+  const uint8_t* w = static_cast<const uint8_t*>(packed);
+  const uint8_t* r = static_cast<const uint8_t*>(codes);
+  const uint8_t* f = static_cast<const uint8_t*>(sf);
+  if (y_dtype == MOE_DTYPE_F32)
+    return go<float>(w, r, f, offsets, E, R, K, N, y, status, spin_limit, s);
+  return go<__nv_bfloat16>(w, r, f, offsets, E, R, K, N, y, status, spin_limit, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,275 @@
+// Microscaled 4-bit quantisation: rows (moe_mx4_quantize), an expert operand's row tiles
+// (the first half of moe_mx4_expert_product), and weight images (moe_mx4_pack,
+// moe_mx4_prepack).  Format and layouts: mx4.cuh.
+//
+// Per block of 32 values v: a = max |v|, the scale 2^(floor(log2 a) - 2) (so that a lands
+// in [4, 8)), the codes v / scale rounded to nearest even and cut at 6.  A power of two
+// divides exactly, so the only rounding is the one to the code.
+//
+// Memory-bound: 8 values a lane (one or two 16-byte loads), four lanes a block whose
+// maximum meets in two shuffles; a warp covers one row's 256-value k-block.
+#include "common.cuh"
+#include "kernels.cuh"
+#include "mx4.cuh"
+#include "select_math.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kQThreads = 256;
+constexpr int kQWarps = kQThreads / 32;
+
+// The lane's eight values to codes; `byte`: the block's scale (the same in its four lanes).
+__device__ __forceinline__ uint32_t quantize8(const float (&v)[8], uint32_t& byte) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
+  a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+  byte = mx4_scale_byte(a);
+  const float inv = mx4_inverse_scale(byte);
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = (byte == 255u) ? 0.0f : v[i] * inv;
+  return mx4_encode8(q);
+}
+
+// ------------------------------------------------------------ logical rows ---
+// blocks of 32 values numbered row-major; four lanes a block
+template <typename Tin>
+__global__ void __launch_bounds__(kQThreads) quantize_kernel(const Tin* __restrict__ x, long long ld,
+                                                             long long R, int K,
+                                                             uint32_t* __restrict__ codes,
+                                                             uint8_t* __restrict__ scales,
+                                                             __nv_bfloat16* __restrict__ values) {
+  const int per_row = K / 8;  // lanes' pieces of a row
+  const long long n = R * per_row;
+  const long long stride = (long long)gridDim.x * kQThreads;
+  // whole warps stay together for the shuffles (n is a multiple of 4)
+  const long long n32 = (n + 31) / 32 * 32;
+  for (long long i = (long long)blockIdx.x * kQThreads + threadIdx.x; i < n32; i += stride) {
+    const bool in = i < n;
+    const long long row = in ? i / per_row : 0;
+    const int col = in ? (int)(i - row * per_row) * 8 : 0;
+    float v[8];
+    if (in) {
+      load_floats<Tin, 8>(x + row * ld + col, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    }
+    uint32_t byte;
+    const uint32_t c = quantize8(v, byte);
+    if (!in) continue;
+    if (codes != nullptr) codes[i] = c;
+    if (scales != nullptr && (i & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+    if (values != nullptr) {
+      const float sc = mx4_scale(byte);
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = mx4_value(c >> (4 * j)) * sc;
+      store_floats<__nv_bfloat16, 8>(values + i * 8, o);
+    }
+  }
+}
+
+// ------------------------------------------------------------ operand rows ---
+// SRC 0: rows of x.  SRC 1: row r of the operand is row row_of[r] / k of x (the gather of
+// the dispatch).  SRC 2: x holds [R, 2K] (gate | up), the operand is silu(gate) * up.
+template <typename Tin, int SRC>
+__global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(
+    const Tin* __restrict__ x, const int32_t* __restrict__ row_of, int k, int T,
+    const int32_t* __restrict__ offsets, int E, int R, int K, uint8_t* __restrict__ codes,
+    uint8_t* __restrict__ sf, int32_t* status) {
+  __shared__ Mx4Tables tb;
+  if (!mx4_build_tables(tb, offsets, E, R, status)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int KB = mx4_kblocks(K);
+  for (long long r = (long long)blockIdx.x * kQWarps + warp; r < R;
+       r += (long long)gridDim.x * kQWarps) {
+    const int e = mx4_find(tb.off, E, (int)r);
+    const int m = tb.off[e + 1] - tb.off[e];
+    const int local = (int)r - tb.off[e];
+    const Mx4Cut cut = mx4_cut(m);
+    const int ti = local / cut.step, rt = local - ti * cut.step;
+    const int rows = min(cut.step, (m - ti * cut.step + 15) / 16 * 16);  // padded tile rows
+    uint8_t* cdst = codes + ((size_t)tb.pad[e] * 16 + (size_t)ti * cut.step) * KB * 128 + rt * 128;
+    uint8_t* sdst = sf + (size_t)(tb.tile[e] + ti) * KB * kMx4SfSlot + (rt >> 7) * 1024 +
+                    (rt & 31) * 16 + ((rt >> 5) & 3) * 4;
+    long long src = r;
+    if constexpr (SRC == 1) {
+      const int slot = row_of[r];
+      src = slot >= 0 ? slot / k : T;
+      if (src >= T) {
+        if (lane == 0) flag_error(status, MOE_ERR_DEVICE_CHECK);
+        src = 0;
+      }
+    }
+    const Tin* row = x + (size_t)src * (SRC == 2 ? 2 * (size_t)K : (size_t)K);
+    for (int kb = 0; kb < KB; ++kb) {
+      const int col = kb * kMx4KB + lane * 8;
+      const bool in = col < K;  // K is a multiple of 128: whole half-warps
+      float v[8];
+      if (in) {
+        load_floats<Tin, 8>(row + col, v);
+        if constexpr (SRC == 2) {
+          float up[8];
+          load_floats<Tin, 8>(row + K + col, up);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(silu_f32(v[i]), up[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      }
+      uint32_t byte;
+      const uint32_t c = quantize8(v, byte);
+      // the four scales of each half of the k-block meet in its first lane
+      uint32_t w = byte;
+      w |= __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
+      w |= __shfl_down_sync(0xFFFFFFFFu, byte, 8) << 16;
+      w |= __shfl_down_sync(0xFFFFFFFFu, byte, 12) << 24;
+      if (in) {
+        *reinterpret_cast<uint32_t*>(cdst + (size_t)kb * rows * 128 +
+                                     (((lane >> 2) ^ (rt & 7)) * 16) + (lane & 3) * 4) = c;
+        if ((lane & 15) == 0)
+          *reinterpret_cast<uint32_t*>(sdst + (size_t)kb * kMx4SfSlot + (lane >> 4) * 512) = w;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------- weight images ---
+// codes [E, N, K/2], scales [E, N, K/32] -> images; one CTA per (k-block, weight tile)
+__global__ void __launch_bounds__(kQThreads) pack_kernel(const uint8_t* __restrict__ codes,
+                                                         const uint8_t* __restrict__ scales, int K,
+                                                         int N, uint8_t* __restrict__ packed) {
+  const int KB = mx4_kblocks(K);
+  const int kb = blockIdx.x;
+  const long long tile = blockIdx.y + (long long)blockIdx.z * (N / kMx4WTile);
+  uint8_t* dst = packed + (tile * KB + kb) * (size_t)kMx4WBytes;
+  const size_t row0 = (size_t)blockIdx.z * N + (size_t)blockIdx.y * kMx4WTile;
+  for (int i = threadIdx.x; i < kMx4WTile * 8; i += kQThreads) {
+    const int r = i >> 3, c = i & 7;
+    const int col = kb * 128 + c * 16;  // bytes
+    const uint4 v = col < K / 2 ? *reinterpret_cast<const uint4*>(codes + (row0 + r) * (K / 2) + col)
+                                : make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(dst + r * 128 + ((c ^ (r & 7)) * 16)) = v;
+  }
+  for (int i = threadIdx.x; i < kMx4WTile * 2; i += kQThreads) {
+    const int r = i >> 1, j = i & 1;
+    const int s = kb * 8 + j * 4;
+    const uint32_t w =
+        s < K / 32 ? *reinterpret_cast<const uint32_t*>(scales + (row0 + r) * (K / 32) + s) : 0u;
+    *reinterpret_cast<uint32_t*>(dst + kMx4WTile * 128 + j * 512 + (r & 31) * 16 + (r >> 5) * 4) = w;
+  }
+}
+
+// w [E, K, N] bf16 (row-major over K) -> images, quantised along K.  One CTA per (k-block,
+// weight tile, expert); the tile goes through shared memory 32 values of K at a time, a
+// thread quantising one output column's block.
+__global__ void __launch_bounds__(128) prepack_kernel(const __nv_bfloat16* __restrict__ w, int K,
+                                                      int N, int tile0, int tiles,
+                                                      uint8_t* __restrict__ packed) {
+  __shared__ __nv_bfloat16 s[32][128];
+  const int KB = mx4_kblocks(K);
+  const int kb = blockIdx.x, e = blockIdx.z;
+  const long long tile = tile0 + blockIdx.y + (long long)e * tiles;
+  uint8_t* dst = packed + (tile * KB + kb) * (size_t)kMx4WBytes;
+  const __nv_bfloat16* src = w + ((size_t)e * K + (size_t)kb * kMx4KB) * N + blockIdx.y * kMx4WTile;
+  const int r = threadIdx.x;
+  for (int c = 0; c < 8; ++c) {
+    const bool in = kb * kMx4KB + c * 32 < K;
+    __syncthreads();
+    if (in) {
+      for (int i = threadIdx.x; i < 32 * 16; i += 128) {
+        const int kk = i >> 4, q = i & 15;
+        *reinterpret_cast<uint4*>(&s[kk][q * 8]) =
+            *reinterpret_cast<const uint4*>(src + (size_t)(c * 32 + kk) * N + q * 8);
+      }
+    }
+    __syncthreads();
+    uint32_t byte = 0;
+    uint32_t out[4] = {0, 0, 0, 0};
+    if (in) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int kk = 0; kk < 32; ++kk)
+        a = max(a, __float_as_uint(__bfloat162float(s[kk][r])) & 0x7FFFFFFFu);
+      byte = mx4_scale_byte(a);
+      const float inv = mx4_inverse_scale(byte);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = byte == 255u ? 0.0f : __bfloat162float(s[q * 8 + i][r]) * inv;
+        out[q] = mx4_encode8(v);
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + r * 128 + ((c ^ (r & 7)) * 16)) =
+        make_uint4(out[0], out[1], out[2], out[3]);
+    dst[kMx4WTile * 128 + (c >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (c & 3)] = (uint8_t)byte;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_quantize(const void* x, int dtype, long long ld, long long R, int K,
+                                void* codes, void* scales, void* values, cudaStream_t s) {
+  const long long n = R * (K / 8);
+  if (n == 0) return cudaSuccess;
+  const long long need = (n + kQThreads - 1) / kQThreads;
+  const long long most = (long long)device_sm_count() * 8 * 4;
+  const int grid = (int)(need < most ? need : most);
+  uint32_t* c = static_cast<uint32_t*>(codes);
+  uint8_t* sc = static_cast<uint8_t*>(scales);
+  __nv_bfloat16* v = static_cast<__nv_bfloat16*>(values);
+  if (dtype == MOE_DTYPE_F32)
+    quantize_kernel<<<grid, kQThreads, 0, s>>>(static_cast<const float*>(x), ld, R, K, c, sc, v);
+  else if (dtype == MOE_DTYPE_BF16)
+    quantize_kernel<<<grid, kQThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(x), ld, R, K, c, sc, v);
+  else
+    quantize_kernel<<<grid, kQThreads, 0, s>>>(static_cast<const __half*>(x), ld, R, K, c, sc, v);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_mx4_rows(const void* x, int dtype, int src, const int32_t* row_of, int k, int T,
+                            const int32_t* offsets, int E, int R, int K, void* codes, void* sf,
+                            int32_t* status, cudaStream_t s) {
+  if (R == 0) return cudaSuccess;
+  const long long need = ((long long)R + kQWarps - 1) / kQWarps;
+  const long long most = (long long)device_sm_count() * 8;
+  const int grid = (int)(need < most ? need : most);
+  uint8_t* c = static_cast<uint8_t*>(codes);
+  uint8_t* f = static_cast<uint8_t*>(sf);
+  auto go = [&](auto kern, auto* p) {
+    kern<<<grid, kQThreads, 0, s>>>(p, row_of, k, T, offsets, E, R, K, c, f, status);
+    return cudaGetLastError();
+  };
+  const auto* xb = static_cast<const __nv_bfloat16*>(x);
+  if (src == 1) return go(quantize_rows_kernel<__nv_bfloat16, 1>, xb);
+  if (src == 2) return go(quantize_rows_kernel<__nv_bfloat16, 2>, xb);
+  if (dtype == MOE_DTYPE_F32)
+    return go(quantize_rows_kernel<float, 0>, static_cast<const float*>(x));
+  if (dtype == MOE_DTYPE_BF16) return go(quantize_rows_kernel<__nv_bfloat16, 0>, xb);
+  return go(quantize_rows_kernel<__half, 0>, static_cast<const __half*>(x));
+}
+
+cudaError_t launch_mx4_pack(const void* codes, const void* scales, int E, int K, int N,
+                            void* packed, cudaStream_t s) {
+  pack_kernel<<<dim3(mx4_kblocks(K), N / kMx4WTile, E), kQThreads, 0, s>>>(
+      static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), K, N,
+      static_cast<uint8_t*>(packed));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_mx4_prepack(const void* w, int E, int K, int N, int col0, int N_total,
+                               void* packed, cudaStream_t s) {
+  prepack_kernel<<<dim3(mx4_kblocks(K), N / kMx4WTile, E), 128, 0, s>>>(
+      static_cast<const __nv_bfloat16*>(w), K, N, col0 / kMx4WTile, N_total / kMx4WTile,
+      static_cast<uint8_t*>(packed));
+  return cudaGetLastError();
+}
+
+}  // namespace moe

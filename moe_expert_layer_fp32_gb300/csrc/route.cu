@@ -116,6 +116,7 @@ __device__ __forceinline__ float round_bf16(float f) {
 //     experts"): scores s = sigmoid(l); the correction bias joins only the
 //     selection key s + b (ties to the lower expert); weights = selected s over
 //     their left-to-right sum.
+//   KIND 2 (route_logits.cu): the row's logits go to topk_w [T, E] and nothing is routed.
 // wbf16 rounds every final weight to bf16.
 template <int EP, int KIND>
 __device__ __forceinline__ void route_one_token(const float* lrow, const float* corr_bias, int E,
@@ -123,6 +124,10 @@ __device__ __forceinline__ void route_one_token(const float* lrow, const float* 
                                                 int32_t* __restrict__ topk_idx,
                                                 float* __restrict__ topk_w) {
   constexpr int NV = EP / 32;
+  if constexpr (KIND == 2) {
+    for (int e = lane; e < E; e += 32) topk_w[(size_t)t * E + e] = lrow[e];
+    return;
+  }
   float v[NV];   // selection key
   float sc[NV];  // KIND 1: pre-bias scores
   unsigned taken = 0;
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(NTHR, 4) route_kernel(const uint16_t* __restri
 
   // ---- epilogue: logits (+ bias for the softmax router) to shared memory ---
   constexpr int LLD = EP + 1;
-  const bool add_bias = KIND == 0 && bias != nullptr;
+  const bool add_bias = KIND != 1 && bias != nullptr;
   float* ls = reinterpret_cast<float*>(smem_f4);  // [BT][LLD], over the drained ring
 #pragma unroll
   for (int j = 0; j < TE; ++j) {
@@ -542,7 +547,7 @@ __global__ void __launch_bounds__(NTHR, 4) route_tile_kernel(const uint16_t* __r
   __syncthreads();  // the logits below overwrite the ring
 
   constexpr int LLD = EP + 1;
-  const bool add_bias = KIND == 0 && bias != nullptr;
+  const bool add_bias = KIND != 1 && bias != nullptr;
   float* ls = reinterpret_cast<float*>(smem_f4);  // [BTT][LLD], over the drained ring
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -686,7 +691,7 @@ __global__ void __launch_bounds__(ClusterCfg<EP, TSV, CC>::NTH)
   if (tid < C::NCMP && el < ecols) {
     const int e = e0 + el;
     float l = acc;
-    if (KIND == 0 && bias != nullptr) l = __fadd_rn(l, __ldg(bias + e));
+    if (KIND != 1 && bias != nullptr) l = __fadd_rn(l, __ldg(bias + e));
     const uint32_t dst = mapa_shared(smem_u32(ls + tok * LLD + e), 0);
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(l) : "memory");
   }
@@ -884,7 +889,7 @@ __global__ void __launch_bounds__(DecodeCfg<EP, TSV>::NTH)
   } else if (warp > 0 && ct < C::NCMP && e0 + el < E) {
     const int e = e0 + el;
     float l = acc;
-    if (KIND == 0 && bias != nullptr) l = __fadd_rn(l, __ldg(bias + e));
+    if (KIND != 1 && bias != nullptr) l = __fadd_rn(l, __ldg(bias + e));
     const uint32_t dst = mapa_shared(smem_u32(ls + tok * LLD + e), 0);
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(l) : "memory");
   }
@@ -1072,6 +1077,13 @@ cudaError_t launch_kind(const void* x, const float* w_router, const float* bias,
 
 }  // namespace
 
+#ifdef MOE_ROUTER_LOGITS  // route_logits.cu compiles this file for the projection alone
+cudaError_t launch_router_logits(const void* x, const float* w_router, const float* bias, int T,
+                                 int H, int E, float* logits, cudaStream_t s) {
+  if (T == 0) return cudaSuccess;
+  return launch_kind<2>(x, w_router, bias, T, H, E, 1, 0, nullptr, logits, s);
+}
+#else
 cudaError_t launch_route(const void* x, const float* w_router, const float* bias, int T, int H,
                          int E, int k, int kind, int weights_bf16, int32_t* topk_idx,
                          float* topk_w, cudaStream_t s) {
@@ -1080,5 +1092,7 @@ cudaError_t launch_route(const void* x, const float* w_router, const float* bias
     return launch_kind<1>(x, w_router, bias, T, H, E, k, weights_bf16, topk_idx, topk_w, s);
   return launch_kind<0>(x, w_router, bias, T, H, E, k, weights_bf16, topk_idx, topk_w, s);
 }
+
+#endif
 
 }  // namespace moe

@@ -1,0 +1,503 @@
+// Selection from router logits, and its gradient.
+//
+// For a row of E logits l (one token), m_e = "masked": l_e (or, for softmax, l_e + b_e)
+// is -inf or NaN.
+//   softmax   key_e = l_e + b_e,            score_e = exp(key_e) / sum_E exp(key)
+//   sigmoid   s_e = 1 / (1 + exp(-l_e)),    key_e = s_e + b_e,   score_e = s_e
+// (the keys' arithmetic is the router kernels': one FP32 add, and for the sigmoid the
+// Cody & Waite exponential whose every step is one IEEE operation, so that a choice does
+// not depend on which kernel made it).  Groups are E / n_group consecutive experts; a
+// group's score is the sum of its group_top (1 or 2) largest keys that are not masked (-inf
+// if all are); the topk_group groups
+// with the largest scores stay, then the k experts in them with the largest keys, both
+// with ties to the lower index.  w_j = score_j, or score_j / sum of the chosen scores.
+// prob_sum[e] = sum over tokens of score_e / sum_E score (what a balance loss needs).
+//
+// Gradient, with c the chosen experts, S = sum of their scores, q = score / sum_E score,
+// g = d_prob_sum:
+//   d score_j += renorm ? (dw_j - sum_i dw_i w_i) / S : dw_j        (j chosen)
+//   softmax: d l_e = q_e (D_e - sum_i D_i q_i),  D_e = g_e + [e chosen] dw'
+//   sigmoid: d l_e = s_e (1 - s_e) (d score_e + (g_e - sum_i g_i q_i) / sum_E s)
+// For the renormalised softmax the factor 1/S cancels against q: d l_j = w_j (dw_j - sum
+// dw_i w_i) for the chosen, formed from exponentials relative to the largest chosen key,
+// so that chosen experts far below the row's largest logit keep their precision.
+//
+// One warp per token, EP/32 consecutive experts per lane.
+#include <math.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.cuh"
+#include "select_math.cuh"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBlocksPerSm = 8;
+
+struct SelectArgs {
+  const void* logits;
+  long long ld;
+  const float* bias;
+  int T, E, k;
+  int n_group, topk_group, group_top, renorm;
+};
+
+// NV logits of one lane: experts e0 .. e0 + NV - 1 of the row, -inf past E.
+template <typename Tin, int NV>
+__device__ __forceinline__ void load_row(const Tin* row, int e0, int E, bool vec, float (&l)[NV]) {
+  if (vec && e0 + NV <= E) {
+    load_floats<Tin, NV>(row + e0, l);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) l[i] = (e0 + i < E) ? to_float(row[e0 + i]) : -INFINITY;
+  }
+}
+
+// key and score of the lane's experts.  KIND 0: score is left to the caller (it needs
+// the row's maximum); masked experts and those past E have key -inf and score 0.
+template <int KIND, int NV>
+__device__ __forceinline__ void keys_of(const float (&l)[NV], const float (&b)[NV], float (&key)[NV],
+                                        float (&sc)[NV]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float v;
+    if constexpr (KIND == 0) {
+      v = __fadd_rn(l[i], b[i]);
+      sc[i] = 0.0f;
+    } else {
+      sc[i] = sigmoid_steps(l[i]);
+      v = (l[i] > -INFINITY) ? __fadd_rn(sc[i], b[i]) : -INFINITY;
+      if (!(l[i] > -INFINITY)) sc[i] = 0.0f;
+    }
+    key[i] = (v > -INFINITY) ? __fadd_rn(v, 0.0f) : -INFINITY;  // NaN: masked; -0: +0
+  }
+}
+
+// exp(key - m), 1 where key is the maximum (also +inf), 0 where masked
+__device__ __forceinline__ float exp_rel(float key, float m) {
+  if (key == -INFINITY) return 0.0f;
+  return key == m ? 1.0f : expf(key - m);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+  return key_float(__reduce_max_sync(kFull, float_key(v)));
+}
+
+// ------------------------------------------------------------------ forward ---
+template <typename Tin, int EP, int KIND, bool PROB>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a,
+                                                             int32_t* __restrict__ topk_idx,
+                                                             float* __restrict__ topk_w,
+                                                             float* __restrict__ partial) {
+  constexpr int NV = EP / 32;
+  __shared__ float s_key[kSelWarps][EP];
+  __shared__ float s_col[PROB ? kSelWarps : 1][PROB ? EP : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int e0 = lane * NV;
+  const int E = a.E, k = a.k, per = E / a.n_group;
+  const Tin* logits = static_cast<const Tin*>(a.logits);
+  const bool vec = rows_aligned<Tin, NV>(logits, a.ld);
+  float b[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) b[i] = (a.bias != nullptr && e0 + i < E) ? __ldg(a.bias + e0 + i) : 0.0f;
+  float col[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) col[i] = 0.0f;
+
+  for (long long t = (long long)blockIdx.x * kSelWarps + warp; t < a.T;
+       t += (long long)gridDim.x * kSelWarps) {
+    float l[NV], key[NV], sc[NV];
+    load_row<Tin, NV>(logits + t * a.ld, e0, E, vec, l);
+    keys_of<KIND, NV>(l, b, key, sc);
+    if constexpr (PROB) {
+      float mx = -INFINITY, z = 0.0f;
+      if constexpr (KIND == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) mx = fmaxf(mx, key[i]);
+        mx = warp_max(mx);
+      }
+      float p[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        p[i] = (KIND == 0) ? exp_rel(key[i], mx) : sc[i];
+        z += p[i];
+      }
+      z = warp_sum(z);
+      const float r = z > 0.0f ? 1.0f / z : 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) col[i] += p[i] * r;
+    }
+    // groups that stay
+    unsigned keep = kFull;
+    if (a.topk_group < a.n_group) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) s_key[warp][e0 + i] = key[i];
+      __syncwarp();
+      float g1 = -INFINITY, g2 = -INFINITY;
+      if (lane < a.n_group) {
+        for (int i = 0; i < per; ++i) {
+          const float v = s_key[warp][lane * per + i];
+          g2 = fmaxf(g2, fminf(g1, v));
+          g1 = fmaxf(g1, v);
+        }
+      }
+      __syncwarp();
+      const float gs = (a.group_top == 2 && g2 > -INFINITY) ? __fadd_rn(g1, g2) : g1;
+      int better = 0;
+      for (int h = 0; h < a.n_group; ++h) {
+        const float o = __shfl_sync(kFull, gs, h);
+        better += (o > gs || (o == gs && h < lane)) ? 1 : 0;
+      }
+      keep = __ballot_sync(kFull, lane < a.n_group && better < a.topk_group);
+    }
+    // selection keys: 0 = cannot be chosen, masked below every number
+    uint32_t u[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = e0 + i;
+      const bool in = e < E && (a.n_group == 1 || ((keep >> (e / per)) & 1u));
+      u[i] = in ? float_key(key[i]) : 0u;
+    }
+    float my_key = -INFINITY, my_sc = 0.0f;
+    int my_e = 0;
+    for (int j = 0; j < k; ++j) {
+      uint32_t bk = 0u;
+      int bi = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (u[i] > bk) {
+          bk = u[i];
+          bi = i;
+        }
+      const uint32_t m = __reduce_max_sync(kFull, bk);
+      const int owner = __ffs(__ballot_sync(kFull, bk == m)) - 1;  // lanes hold ascending experts
+      const int be = __shfl_sync(kFull, e0 + bi, owner);
+      float s = 0.0f;
+      if constexpr (KIND == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (i == bi) s = sc[i];
+        s = __shfl_sync(kFull, s, owner);
+      }
+      if (lane == j) {
+        my_key = key_float(m);
+        my_sc = s;
+        my_e = be;
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (lane == owner && i == bi) u[i] = 0u;
+    }
+    // weights: lane j holds slot j
+    float w;
+    if constexpr (KIND == 0) {
+      float m = __shfl_sync(kFull, my_key, 0);
+      float z;
+      if (a.renorm) {
+        w = (lane < k) ? exp_rel(my_key, m) : 0.0f;
+        z = warp_sum(w);
+      } else {
+        m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) m = fmaxf(m, key[i]);
+        m = warp_max(m);
+        z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) z += exp_rel(key[i], m);
+        z = warp_sum(z);
+        w = exp_rel(my_key, m);
+      }
+      w = z > 0.0f ? __fdiv_rn(w, z) : 0.0f;
+    } else {
+      w = (lane < k) ? my_sc : 0.0f;
+      if (a.renorm) {
+        const float z = warp_sum(w);
+        w = z > 0.0f ? __fdiv_rn(w, z) : 0.0f;
+      }
+    }
+    if (lane < k) {
+      topk_idx[t * k + lane] = my_e;
+      topk_w[t * k + lane] = w;
+    }
+  }
+  if constexpr (PROB) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s_col[warp][e0 + i] = col[i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kSelThreads) {
+      float v = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kSelWarps; ++q) v += s_col[q][e];
+      partial[(size_t)blockIdx.x * E + e] = v;
+    }
+  }
+}
+
+// ----------------------------------------------------------------- gradient ---
+template <typename Tin, int EP, int KIND, bool DBIAS>
+__global__ void __launch_bounds__(kSelThreads) select_bwd_kernel(
+    SelectArgs a, const int32_t* __restrict__ topk_idx, const float* __restrict__ d_w,
+    const float* __restrict__ d_prob, Tin* __restrict__ d_logits, long long ldd,
+    float* __restrict__ partial) {
+  constexpr int NV = EP / 32;
+  __shared__ float s_col[DBIAS ? kSelWarps : 1][DBIAS ? EP : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int e0 = lane * NV;
+  const int E = a.E, k = a.k;
+  const Tin* logits = static_cast<const Tin*>(a.logits);
+  const bool vec = rows_aligned<Tin, NV>(logits, a.ld);
+  const bool vecd = rows_aligned<Tin, NV>(d_logits, ldd);
+  float b[NV], g[NV], col[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    b[i] = (a.bias != nullptr && e0 + i < E) ? __ldg(a.bias + e0 + i) : 0.0f;
+    g[i] = (d_prob != nullptr && e0 + i < E) ? __ldg(d_prob + e0 + i) : 0.0f;
+    col[i] = 0.0f;
+  }
+  for (long long t = (long long)blockIdx.x * kSelWarps + warp; t < a.T;
+       t += (long long)gridDim.x * kSelWarps) {
+    float l[NV], key[NV], sc[NV];
+    load_row<Tin, NV>(logits + t * a.ld, e0, E, vec, l);
+    keys_of<KIND, NV>(l, b, key, sc);
+    const int ej = (lane < k) ? topk_idx[t * k + lane] : -1;
+    const float dj = (lane < k) ? d_w[t * k + lane] : 0.0f;
+    const bool valid = ej >= 0 && ej < E;
+    // the chosen experts' keys and scores, slot j in lane j
+    float ckey = -INFINITY, csc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int src = valid ? ej / NV : 0;
+      const float kv = __shfl_sync(kFull, key[i], src);
+      const float sv = __shfl_sync(kFull, sc[i], src);
+      if (valid && ej % NV == i) {
+        ckey = kv;
+        csc = sv;
+      }
+    }
+    float d[NV];
+    if constexpr (KIND == 0) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) m = fmaxf(m, key[i]);
+      m = warp_max(m);
+      float q[NV], z = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        q[i] = exp_rel(key[i], m);
+        z += q[i];
+      }
+      z = warp_sum(z);
+      const float rz = z > 0.0f ? 1.0f / z : 0.0f;
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        q[i] *= rz;
+        dot += g[i] * q[i];
+      }
+      float cd;  // what the chosen logit gets beside the dense part
+      if (a.renorm) {
+        const float mc = warp_max(ckey);
+        const float e = exp_rel(ckey, mc);
+        const float S = warp_sum(e);
+        const float w = S > 0.0f ? e / S : 0.0f;
+        cd = w * (dj - warp_sum(dj * w));
+      } else {
+        const float qc = exp_rel(ckey, m) * rz;
+        dot += dj * qc;
+        cd = dj * qc;
+      }
+      dot = warp_sum(dot);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) d[i] = q[i] * (g[i] - dot);
+      for (int j = 0; j < k; ++j) {
+        const int e = __shfl_sync(kFull, valid ? ej : -1, j);
+        const float v = __shfl_sync(kFull, cd, j);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (e == e0 + i) d[i] += v;
+      }
+    } else {
+      float dense = 0.0f;
+      const bool has = d_prob != nullptr;
+      float rz = 0.0f;
+      if (has) {
+        float z = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          z += sc[i];
+          dot += g[i] * sc[i];
+        }
+        z = warp_sum(z);
+        rz = z > 0.0f ? 1.0f / z : 0.0f;
+        dense = warp_sum(dot) * rz;
+      }
+      float cd = dj;
+      if (a.renorm) {
+        const float S = warp_sum(csc);
+        const float rs = S > 0.0f ? 1.0f / S : 0.0f;
+        cd = (dj - warp_sum(dj * csc) * rs) * rs;
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) d[i] = has ? (g[i] - dense) * rz : 0.0f;
+      for (int j = 0; j < k; ++j) {
+        const int e = __shfl_sync(kFull, valid ? ej : -1, j);
+        const float v = __shfl_sync(kFull, cd, j);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (e == e0 + i) d[i] += v;
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) d[i] *= sc[i] * (1.0f - sc[i]);
+    }
+    Tin* row = d_logits + t * ldd;
+    if (vecd && e0 + NV <= E) {
+      store_floats<Tin, NV>(row + e0, d);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (e0 + i < E) row[e0 + i] = from_float<Tin>(d[i]);
+    }
+    if constexpr (DBIAS) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) col[i] += d[i];
+    }
+  }
+  if constexpr (DBIAS) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s_col[warp][e0 + i] = col[i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kSelThreads) {
+      float v = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kSelWarps; ++q) v += s_col[q][e];
+      partial[(size_t)blockIdx.x * E + e] = v;
+    }
+  }
+}
+
+// out[e] = sum over b of partial[b][e], in a fixed order
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ partial, int nb,
+                                                          int E, float* __restrict__ out) {
+  __shared__ float s[32][33];
+  const int e = blockIdx.x * 32 + threadIdx.x;
+  float v = 0.0f;
+  if (e < E)
+    for (int b = threadIdx.y; b < nb; b += 32) v += partial[(size_t)b * E + e];
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y == 0 && e < E) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += s[i][threadIdx.x];
+    out[e] = t;
+  }
+}
+
+int select_blocks(int T) {
+  const long long need = ((long long)T + kSelWarps - 1) / kSelWarps;
+  const long long most = (long long)device_sm_count() * kSelBlocksPerSm;
+  return (int)(need < most ? need : most);
+}
+
+template <typename Tin, int EP, int KIND>
+cudaError_t fwd_ep(const SelectArgs& a, int32_t* idx, float* w, float* prob_sum, float* partial,
+                   cudaStream_t s) {
+  const int nb = select_blocks(a.T);
+  if (prob_sum == nullptr) {
+    select_kernel<Tin, EP, KIND, false><<<nb, kSelThreads, 0, s>>>(a, idx, w, nullptr);
+    return cudaGetLastError();
+  }
+  select_kernel<Tin, EP, KIND, true><<<nb, kSelThreads, 0, s>>>(a, idx, w, partial);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  column_sum_kernel<<<(a.E + 31) / 32, dim3(32, 32), 0, s>>>(partial, nb, a.E, prob_sum);
+  return cudaGetLastError();
+}
+
+template <typename Tin, int EP, int KIND>
+cudaError_t bwd_ep(const SelectArgs& a, const int32_t* idx, const float* d_w, const float* d_prob,
+                   void* d_logits, long long ldd, float* d_bias, float* partial, cudaStream_t s) {
+  const int nb = select_blocks(a.T);
+  Tin* d = static_cast<Tin*>(d_logits);
+  if (d_bias == nullptr) {
+    select_bwd_kernel<Tin, EP, KIND, false>
+        <<<nb, kSelThreads, 0, s>>>(a, idx, d_w, d_prob, d, ldd, nullptr);
+    return cudaGetLastError();
+  }
+  if constexpr (KIND == 0) {
+    select_bwd_kernel<Tin, EP, KIND, true>
+        <<<nb, kSelThreads, 0, s>>>(a, idx, d_w, d_prob, d, ldd, partial);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    column_sum_kernel<<<(a.E + 31) / 32, dim3(32, 32), 0, s>>>(partial, nb, a.E, d_bias);
+    return cudaGetLastError();
+  }
+  return cudaErrorInvalidValue;  // the selection-only bias has no gradient
+}
+
+// f(type tag, EP constant) for the logits' type and the experts rounded up to 32 * 2^n
+template <typename F>
+cudaError_t by_type_and_experts(int dtype, int E, F&& f) {
+  auto by_e = [&](auto tag) -> cudaError_t {
+    using Tin = decltype(tag);
+    if (E <= 32) return f(Tin{}, std::integral_constant<int, 32>{});
+    if (E <= 64) return f(Tin{}, std::integral_constant<int, 64>{});
+    if (E <= 128) return f(Tin{}, std::integral_constant<int, 128>{});
+    return f(Tin{}, std::integral_constant<int, 256>{});
+  };
+  if (dtype == MOE_DTYPE_F32) return by_e(float{});
+  if (dtype == MOE_DTYPE_BF16) return by_e(__nv_bfloat16{});
+  return by_e(__half{});
+}
+
+SelectArgs args_of(const void* logits, long long ld, const float* bias, const moe_select_opts& o,
+                   int T, int E, int k) {
+  return SelectArgs{logits, ld, bias, T, E, k, o.n_group, o.topk_group, o.group_top, o.renorm};
+}
+
+}  // namespace
+
+size_t select_partial_bytes(int T, int E) { return (size_t)select_blocks(T) * E * sizeof(float); }
+
+cudaError_t launch_select(const void* logits, int dtype, long long ld, const float* bias,
+                          const moe_select_opts& o, int T, int E, int k, int32_t* topk_idx,
+                          float* topk_w, float* prob_sum, float* partial, cudaStream_t s) {
+  const SelectArgs a = args_of(logits, ld, bias, o, T, E, k);
+  return by_type_and_experts(dtype, E, [&](auto tin, auto ep) -> cudaError_t {
+    using Tin = decltype(tin);
+    constexpr int EP = decltype(ep)::value;
+    return o.kind == MOE_ROUTER_SOFTMAX
+               ? fwd_ep<Tin, EP, 0>(a, topk_idx, topk_w, prob_sum, partial, s)
+               : fwd_ep<Tin, EP, 1>(a, topk_idx, topk_w, prob_sum, partial, s);
+  });
+}
+
+cudaError_t launch_select_bwd(const void* logits, int dtype, long long ld, const float* bias,
+                              const moe_select_opts& o, int T, int E, int k,
+                              const int32_t* topk_idx, const float* d_topk_w,
+                              const float* d_prob_sum, void* d_logits, long long ld_d,
+                              float* d_bias, float* partial, cudaStream_t s) {
+  const SelectArgs a = args_of(logits, ld, bias, o, T, E, k);
+  return by_type_and_experts(dtype, E, [&](auto tin, auto ep) -> cudaError_t {
+    using Tin = decltype(tin);
+    constexpr int EP = decltype(ep)::value;
+    return o.kind == MOE_ROUTER_SOFTMAX
+               ? bwd_ep<Tin, EP, 0>(a, topk_idx, d_topk_w, d_prob_sum, d_logits, ld_d, d_bias,
+                                    partial, s)
+               : bwd_ep<Tin, EP, 1>(a, topk_idx, d_topk_w, d_prob_sum, d_logits, ld_d, d_bias,
+                                    partial, s);
+  });
+}
+
+}  // namespace moe
