@@ -179,8 +179,16 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# the current stream's address and the current device without the Python stream object
+# (2.9 us against 0.1 us a call on the GB300's host)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(_get_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -566,14 +574,16 @@ def _dense(name, t, dtype, shape):
     return t
 
 
-def _on_device(*tensors):
-    """One device for all tensors, made current for the call's launches by the caller's
-    context; CPU tensors and mixed devices are refused."""
-    devs = {t.device for t in tensors if t is not None}
-    if any(d.type != "cuda" for d in devs):
+def _on_device(first, *rest):
+    """All tensors on the current CUDA device (the one the library launches on)."""
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if len(devs) > 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    if dev != _get_device():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{_get_device()}")
 
 
 def route_select(logits, k, opts=None, bias=None, want_prob_sum=False, stream=None):

@@ -156,11 +156,28 @@ __device__ __forceinline__ uint32_t mx4_encode8(const float (&v)[8]) {
   return r;
 }
 
-// A code's magnitude and sign as a float.
-__device__ __forceinline__ float mx4_value(uint32_t code) {
-  // magnitudes in quarters of 2: 0 .5 1 1.5 2 3 4 6 as four-bit halves 0 1 2 3 4 6 8 12
-  const float m = 0.5f * (float)((0xC8643210u >> ((code & 7u) * 4u)) & 15u);
-  return (code & 8u) ? -m : m;
+// The eight values of mx4_encode8's codes times the block's scale, as bf16 (exact).  A
+// magnitude's bf16 bytes come from two eight-byte tables by byte permutes; the sign joins
+// in FP32, where the scale multiplies.
+__device__ __forceinline__ uint4 mx4_decode8_bf16(uint32_t codes, float scale) {
+  const uint32_t mag = codes & 0x77777777u;
+  uint32_t o[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // four codes a step
+    const uint32_t sel = mag >> (16 * h);
+    // 0 0.5 1 1.5 | 2 3 4 6 = 0000 3F00 3F80 3FC0 | 4000 4040 4080 40C0
+    const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, sel);
+    const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, sel);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const uint32_t two = __byte_perm(lo, hi, p == 0 ? 0x5140 : 0x7362);  // two bf16
+      const int b = 16 * h + 8 * p;                                        // first code's bit
+      const float v0 = __uint_as_float((two << 16) | ((codes << (28 - b)) & 0x80000000u));
+      const float v1 = __uint_as_float((two & 0xFFFF0000u) | ((codes << (24 - b)) & 0x80000000u));
+      o[2 * h + p] = pack_bf16x2(v0 * scale, v1 * scale);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 }  // namespace moe

@@ -174,6 +174,19 @@ __global__ void __launch_bounds__(192, 1)
   if (warp == 0) {
     if (elect_one()) {
       // ------------------------------------------------------------ producer
+      // The weights are inputs: the first unit's first stages are on their way before the
+      // rows' quantisation, the kernel before this one, has finished.
+      int early = 0;
+      if (blockIdx.x < total) {
+        const MxUnit w = mx_unit(blockIdx.x, tb, E, NT, KB);
+        const uint32_t bytes = kMx4WBytes + (uint32_t)w.rows16 * 128u + (w.rows16 > 128 ? 2048u : 1024u);
+        for (; early < KB && early < C::STAGES; ++early) {
+          mbar_arrive_expect_tx(&full[early], bytes);
+          bulk_load(base + early * C::STAGE_BYTES, wimg + w.w_img + (size_t)early * kMx4WBytes,
+                    kMx4WBytes, &full[early]);
+        }
+      }
+      pdl_wait();
       int it = 0;
       bool aborted = false;
       for (long long u = blockIdx.x; u < total && !aborted; u += gridDim.x) {
@@ -188,13 +201,16 @@ __global__ void __launch_bounds__(192, 1)
             break;
           }
           uint8_t* st = base + s * C::STAGE_BYTES;
-          mbar_arrive_expect_tx(&full[s], kMx4WBytes + row_bytes + sf_bytes);
-          bulk_load(st, wimg + w.w_img + (size_t)kb * kMx4WBytes, kMx4WBytes, &full[s]);
+          if (it >= early) {
+            mbar_arrive_expect_tx(&full[s], kMx4WBytes + row_bytes + sf_bytes);
+            bulk_load(st, wimg + w.w_img + (size_t)kb * kMx4WBytes, kMx4WBytes, &full[s]);
+          }
           bulk_load(st + C::ROW_OFF, rimg + w.row_img + (size_t)kb * row_bytes, row_bytes, &full[s]);
           bulk_load(st + C::SF_OFF, simg + w.sf_img + (size_t)kb * kMx4SfSlot, sf_bytes, &full[s]);
         }
       }
       if (aborted) {
+        // (an abort comes from a wait for a free slot, so every early stage has been filled)
         // the copies issued into the last STAGES slots may still be in flight
         for (int i = (it > C::STAGES ? it - C::STAGES : 0); i < it; ++i)
           wait_drain(&full[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
@@ -310,9 +326,8 @@ cudaError_t go(const uint8_t* w, const uint8_t* r, const uint8_t* sf, const int3
   const long long units = mx4_max_tiles(R, E) * (N / kMx4WTile);
   const int sms = device_sm_count();
   const int grid = (int)(units < sms ? units : sms);
-  mx4_gemm_kernel<Tout><<<grid, 192, MxCfg::SMEM_BYTES, s>>>(w, r, sf, offsets, E, R, K, N,
-                                                            static_cast<Tout*>(y), status, limit);
-  return cudaGetLastError();
+  return launch_pdl(mx4_gemm_kernel<Tout>, dim3(grid), dim3(192), MxCfg::SMEM_BYTES, s, w, r, sf,
+                    offsets, E, R, K, N, static_cast<Tout*>(y), status, limit);
 }
 
 }  // namespace

@@ -11,6 +11,7 @@
 #include "common.cuh"
 #include "kernels.cuh"
 #include "mx4.cuh"
+#include "pdl.cuh"
 #include "select_math.cuh"
 
 namespace moe {
@@ -35,40 +36,43 @@ __device__ __forceinline__ uint32_t quantize8(const float (&v)[8], uint32_t& byt
 }
 
 // ------------------------------------------------------------ logical rows ---
-// blocks of 32 values numbered row-major; four lanes a block
-template <typename Tin>
+// The pieces of 8 values are numbered row-major; a block of 32 is four neighbouring lanes'.
+// Each thread keeps kQUnroll pieces in flight.  DENSE: ld == K.
+constexpr int kQUnroll = 4;
+
+template <typename Tin, bool DENSE>
 __global__ void __launch_bounds__(kQThreads) quantize_kernel(const Tin* __restrict__ x, long long ld,
-                                                             long long R, int K,
+                                                             long long n, int per_row,
                                                              uint32_t* __restrict__ codes,
                                                              uint8_t* __restrict__ scales,
-                                                             __nv_bfloat16* __restrict__ values) {
-  const int per_row = K / 8;  // lanes' pieces of a row
-  const long long n = R * per_row;
-  const long long stride = (long long)gridDim.x * kQThreads;
-  // whole warps stay together for the shuffles (n is a multiple of 4)
-  const long long n32 = (n + 31) / 32 * 32;
-  for (long long i = (long long)blockIdx.x * kQThreads + threadIdx.x; i < n32; i += stride) {
-    const bool in = i < n;
-    const long long row = in ? i / per_row : 0;
-    const int col = in ? (int)(i - row * per_row) * 8 : 0;
-    float v[8];
-    if (in) {
-      load_floats<Tin, 8>(x + row * ld + col, v);
+                                                             uint4* __restrict__ values) {
+  // n is a multiple of 4, so a block is whole or past the end
+  const long long base = (long long)blockIdx.x * (kQThreads * kQUnroll) + threadIdx.x;
+  float v[kQUnroll][8];
+#pragma unroll
+  for (int q = 0; q < kQUnroll; ++q) {
+    const long long i = base + q * kQThreads;
+    if (i < n) {
+      if constexpr (DENSE) {
+        load_floats<Tin, 8>(x + i * 8, v[q]);
+      } else {
+        const long long row = i / per_row;
+        load_floats<Tin, 8>(x + row * ld + (i - row * per_row) * 8, v[q]);
+      }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+      for (int j = 0; j < 8; ++j) v[q][j] = 0.0f;
     }
-    uint32_t byte;
-    const uint32_t c = quantize8(v, byte);
-    if (!in) continue;
-    if (codes != nullptr) codes[i] = c;
-    if (scales != nullptr && (i & 3) == 0) scales[i >> 2] = (uint8_t)byte;
-    if (values != nullptr) {
-      const float sc = mx4_scale(byte);
-      float o[8];
+  }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = mx4_value(c >> (4 * j)) * sc;
-      store_floats<__nv_bfloat16, 8>(values + i * 8, o);
+  for (int q = 0; q < kQUnroll; ++q) {
+    const long long i = base + q * kQThreads;
+    uint32_t byte;
+    const uint32_t c = quantize8(v[q], byte);
+    if (i < n) {
+      if (codes != nullptr) codes[i] = c;
+      if (scales != nullptr && (i & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+      if (values != nullptr) values[i] = mx4_decode8_bf16(c, mx4_scale(byte));
     }
   }
 }
@@ -76,65 +80,91 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const Tin* __restri
 // ------------------------------------------------------------ operand rows ---
 // SRC 0: rows of x.  SRC 1: row r of the operand is row row_of[r] / k of x (the gather of
 // the dispatch).  SRC 2: x holds [R, 2K] (gate | up), the operand is silu(gate) * up.
+//
+// A warp takes the rows rr, rr + 32, rr + 64, rr + 96 of a tile's 128-row half: four loads
+// in flight a lane, and the four rows' scales of a half k-block are one 16-byte store.
 template <typename Tin, int SRC>
 __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(
     const Tin* __restrict__ x, const int32_t* __restrict__ row_of, int k, int T,
     const int32_t* __restrict__ offsets, int E, int R, int K, uint8_t* __restrict__ codes,
     uint8_t* __restrict__ sf, int32_t* status) {
   __shared__ Mx4Tables tb;
+  pdl_launch_dependents();  // the product reads this kernel's images only after its own wait
   if (!mx4_build_tables(tb, offsets, E, R, status)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int KB = mx4_kblocks(K);
-  for (long long r = (long long)blockIdx.x * kQWarps + warp; r < R;
-       r += (long long)gridDim.x * kQWarps) {
-    const int e = mx4_find(tb.off, E, (int)r);
+  const long long items = (long long)tb.tile[E] * 64;  // (tile, half, rr)
+  for (long long it = (long long)blockIdx.x * kQWarps + warp; it < items;
+       it += (long long)gridDim.x * kQWarps) {
+    const int tile = (int)(it >> 6), half = (int)(it >> 5) & 1, rr = (int)it & 31;
+    const int e = mx4_find(tb.tile, E, tile);
     const int m = tb.off[e + 1] - tb.off[e];
-    const int local = (int)r - tb.off[e];
     const Mx4Cut cut = mx4_cut(m);
-    const int ti = local / cut.step, rt = local - ti * cut.step;
-    const int rows = min(cut.step, (m - ti * cut.step + 15) / 16 * 16);  // padded tile rows
-    uint8_t* cdst = codes + ((size_t)tb.pad[e] * 16 + (size_t)ti * cut.step) * KB * 128 + rt * 128;
-    uint8_t* sdst = sf + (size_t)(tb.tile[e] + ti) * KB * kMx4SfSlot + (rt >> 7) * 1024 +
-                    (rt & 31) * 16 + ((rt >> 5) & 3) * 4;
-    long long src = r;
-    if constexpr (SRC == 1) {
-      const int slot = row_of[r];
-      src = slot >= 0 ? slot / k : T;
-      if (src >= T) {
-        if (lane == 0) flag_error(status, MOE_ERR_DEVICE_CHECK);
-        src = 0;
+    const int ti = tile - tb.tile[e];
+    const int rows = min(cut.step, m - ti * cut.step);
+    const int r0 = half * 128 + rr;  // this warp's first row of the tile
+    if (r0 >= rows) continue;
+    const int rows16 = (rows + 15) / 16 * 16;
+    const int nr = min(4, (rows - r0 + 31) / 32);
+    const int row0 = tb.off[e] + ti * cut.step + r0;
+    uint8_t* cdst = codes + ((size_t)tb.pad[e] * 16 + (size_t)ti * cut.step) * KB * 128 + r0 * 128;
+    uint8_t* sdst = sf + (size_t)tile * KB * kMx4SfSlot + half * 1024 + rr * 16;
+    const Tin* src[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      long long r = row0 + (i < nr ? i * 32 : 0);
+      if constexpr (SRC == 1) {
+        const int slot = row_of[r];
+        r = slot >= 0 ? slot / k : T;
+        if (r >= T) {
+          if (lane == 0) flag_error(status, MOE_ERR_DEVICE_CHECK);
+          r = 0;
+        }
       }
+      src[i] = x + (size_t)r * (SRC == 2 ? 2 * (size_t)K : (size_t)K);
     }
-    const Tin* row = x + (size_t)src * (SRC == 2 ? 2 * (size_t)K : (size_t)K);
     for (int kb = 0; kb < KB; ++kb) {
       const int col = kb * kMx4KB + lane * 8;
       const bool in = col < K;  // K is a multiple of 128: whole half-warps
-      float v[8];
-      if (in) {
-        load_floats<Tin, 8>(row + col, v);
-        if constexpr (SRC == 2) {
-          float up[8];
-          load_floats<Tin, 8>(row + K + col, up);
+      float v[4][8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(silu_f32(v[i]), up[i]);
+      for (int i = 0; i < 4; ++i) {
+        if (in && i < nr) {
+          load_floats<Tin, 8>(src[i] + col, v[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
         }
-      } else {
+      }
+      if constexpr (SRC == 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        for (int i = 0; i < 4; ++i) {
+          if (in && i < nr) {
+            float up[8];
+            load_floats<Tin, 8>(src[i] + K + col, up);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(silu_f32(v[i][j]), up[j]);
+          }
+        }
       }
-      uint32_t byte;
-      const uint32_t c = quantize8(v, byte);
-      // the four scales of each half of the k-block meet in its first lane
-      uint32_t w = byte;
-      w |= __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
-      w |= __shfl_down_sync(0xFFFFFFFFu, byte, 8) << 16;
-      w |= __shfl_down_sync(0xFFFFFFFFu, byte, 12) << 24;
-      if (in) {
-        *reinterpret_cast<uint32_t*>(cdst + (size_t)kb * rows * 128 +
-                                     (((lane >> 2) ^ (rt & 7)) * 16) + (lane & 3) * 4) = c;
-        if ((lane & 15) == 0)
-          *reinterpret_cast<uint32_t*>(sdst + (size_t)kb * kMx4SfSlot + (lane >> 4) * 512) = w;
+      uint32_t w[4];
+      uint8_t* ck = cdst + (size_t)kb * rows16 * 128;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t byte;
+        const uint32_t c = quantize8(v[i], byte);
+        // the four scales of each half of the k-block meet in its first lane
+        w[i] = byte | (__shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8) |
+               (__shfl_down_sync(0xFFFFFFFFu, byte, 8) << 16) |
+               (__shfl_down_sync(0xFFFFFFFFu, byte, 12) << 24);
+        // (rows 32 apart have the same row & 7)
+        if (in && i < nr)
+          *reinterpret_cast<uint32_t*>(ck + i * 32 * 128 + (((lane >> 2) ^ (rr & 7)) * 16) +
+                                       (lane & 3) * 4) = c;
       }
+      if (in && (lane & 15) == 0)
+        *reinterpret_cast<uint4*>(sdst + (size_t)kb * kMx4SfSlot + (lane >> 4) * 512) =
+            make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -217,29 +247,32 @@ __global__ void __launch_bounds__(128) prepack_kernel(const __nv_bfloat16* __res
 
 cudaError_t launch_mx4_quantize(const void* x, int dtype, long long ld, long long R, int K,
                                 void* codes, void* scales, void* values, cudaStream_t s) {
-  const long long n = R * (K / 8);
+  const int per_row = K / 8;
+  const long long n = R * per_row;
   if (n == 0) return cudaSuccess;
-  const long long need = (n + kQThreads - 1) / kQThreads;
-  const long long most = (long long)device_sm_count() * 8 * 4;
-  const int grid = (int)(need < most ? need : most);
+  const long long grid = (n + kQThreads * kQUnroll - 1) / (kQThreads * kQUnroll);  // < 2^31
   uint32_t* c = static_cast<uint32_t*>(codes);
   uint8_t* sc = static_cast<uint8_t*>(scales);
-  __nv_bfloat16* v = static_cast<__nv_bfloat16*>(values);
-  if (dtype == MOE_DTYPE_F32)
-    quantize_kernel<<<grid, kQThreads, 0, s>>>(static_cast<const float*>(x), ld, R, K, c, sc, v);
-  else if (dtype == MOE_DTYPE_BF16)
-    quantize_kernel<<<grid, kQThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(x), ld, R, K, c, sc, v);
-  else
-    quantize_kernel<<<grid, kQThreads, 0, s>>>(static_cast<const __half*>(x), ld, R, K, c, sc, v);
-  return cudaGetLastError();
+  uint4* v = static_cast<uint4*>(values);
+  auto go = [&](auto* p) {
+    using Tin = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+    if (ld == K || R == 1)
+      quantize_kernel<Tin, true><<<(unsigned)grid, kQThreads, 0, s>>>(p, ld, n, per_row, c, sc, v);
+    else
+      quantize_kernel<Tin, false><<<(unsigned)grid, kQThreads, 0, s>>>(p, ld, n, per_row, c, sc, v);
+    return cudaGetLastError();
+  };
+  if (dtype == MOE_DTYPE_F32) return go(static_cast<const float*>(x));
+  if (dtype == MOE_DTYPE_BF16) return go(static_cast<const __nv_bfloat16*>(x));
+  return go(static_cast<const __half*>(x));
 }
 
 cudaError_t launch_mx4_rows(const void* x, int dtype, int src, const int32_t* row_of, int k, int T,
                             const int32_t* offsets, int E, int R, int K, void* codes, void* sf,
                             int32_t* status, cudaStream_t s) {
   if (R == 0) return cudaSuccess;
-  const long long need = ((long long)R + kQWarps - 1) / kQWarps;
-  const long long most = (long long)device_sm_count() * 8;
+  const long long need = mx4_max_tiles(R, E) * 64 / kQWarps;
+  const long long most = (long long)device_sm_count() * 6;
   const int grid = (int)(need < most ? need : most);
   uint8_t* c = static_cast<uint8_t*>(codes);
   uint8_t* f = static_cast<uint8_t*>(sf);

@@ -37,7 +37,7 @@ namespace {
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelBlocksPerSm = 8;
+constexpr int kSelBlocksPerSm = 4;  // 32 warps of at most 64 registers a thread
 
 struct SelectArgs {
   const void* logits;
@@ -45,6 +45,9 @@ struct SelectArgs {
   const float* bias;
   int T, E, k;
   int n_group, topk_group, group_top, renorm;
+  int per;         // experts of a group
+  int per_magic;   // (e * per_magic) >> 16 = e / per for e < 256
+  int lane_shift;  // log2 of the lanes that share a group in the group sums
 };
 
 // NV logits of one lane: experts e0 .. e0 + NV - 1 of the row, -inf past E.
@@ -94,18 +97,39 @@ __device__ __forceinline__ float warp_max(float v) {
   return key_float(__reduce_max_sync(kFull, float_key(v)));
 }
 
+// the lane's NV values to a shared row of EP
+template <int EP>
+__device__ __forceinline__ void store_row(float* row, int e0, const float (&v)[EP / 32]) {
+  store_floats<float, EP / 32>(row + e0, v);
+}
+
+// The block's column sums: every warp's columns through shared memory, in warp order.
+template <int EP>
+__device__ __forceinline__ void write_partial(float (*s_row)[EP], int warp, int e0,
+                                              const float (&col)[EP / 32], int E,
+                                              float* __restrict__ partial) {
+  store_row<EP>(s_row[warp], e0, col);
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kSelThreads) {
+    float v = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kSelWarps; ++q) v += s_row[q][e];
+    partial[(size_t)blockIdx.x * E + e] = v;
+  }
+}
+
 // ------------------------------------------------------------------ forward ---
 template <typename Tin, int EP, int KIND, bool PROB>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a,
+__global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(SelectArgs a,
                                                              int32_t* __restrict__ topk_idx,
                                                              float* __restrict__ topk_w,
                                                              float* __restrict__ partial) {
   constexpr int NV = EP / 32;
-  __shared__ float s_key[kSelWarps][EP];
-  __shared__ float s_col[PROB ? kSelWarps : 1][PROB ? EP : 1];
+  __shared__ __align__(16) float s_row[kSelWarps][EP];  // the keys; later the candidates' scores
+  __shared__ uint2 s_cand[kSelWarps][32];               // candidates: key, expert
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int e0 = lane * NV;
-  const int E = a.E, k = a.k, per = E / a.n_group;
+  const int E = a.E, k = a.k;
   const Tin* logits = static_cast<const Tin*>(a.logits);
   const bool vec = rows_aligned<Tin, NV>(logits, a.ld);
   float b[NV];
@@ -138,120 +162,195 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a,
 #pragma unroll
       for (int i = 0; i < NV; ++i) col[i] += p[i] * r;
     }
-    // groups that stay
+    // groups that stay: L lanes per group, each over every L-th of its keys
     unsigned keep = kFull;
     if (a.topk_group < a.n_group) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) s_key[warp][e0 + i] = key[i];
+      store_row<EP>(s_row[warp], e0, key);
       __syncwarp();
+      const int g = lane >> a.lane_shift, sub = lane & ((1 << a.lane_shift) - 1);
       float g1 = -INFINITY, g2 = -INFINITY;
-      if (lane < a.n_group) {
-        for (int i = 0; i < per; ++i) {
-          const float v = s_key[warp][lane * per + i];
+      if (g < a.n_group) {
+        for (int i = sub; i < a.per; i += 1 << a.lane_shift) {
+          const float v = s_row[warp][g * a.per + i];
           g2 = fmaxf(g2, fminf(g1, v));
           g1 = fmaxf(g1, v);
         }
       }
-      __syncwarp();
+      for (int o = 1; o < (1 << a.lane_shift); o <<= 1) {
+        const float o1 = __shfl_xor_sync(kFull, g1, o), o2 = __shfl_xor_sync(kFull, g2, o);
+        g2 = fmaxf(fmaxf(g2, o2), fminf(g1, o1));
+        g1 = fmaxf(g1, o1);
+      }
       const float gs = (a.group_top == 2 && g2 > -INFINITY) ? __fadd_rn(g1, g2) : g1;
       int better = 0;
       for (int h = 0; h < a.n_group; ++h) {
-        const float o = __shfl_sync(kFull, gs, h);
-        better += (o > gs || (o == gs && h < lane)) ? 1 : 0;
+        const float o = __shfl_sync(kFull, gs, h << a.lane_shift);
+        better += (o > gs || (o == gs && h < g)) ? 1 : 0;
       }
-      keep = __ballot_sync(kFull, lane < a.n_group && better < a.topk_group);
+      // bit g << lane_shift of the ballot: group g stays
+      keep = __ballot_sync(kFull, sub == 0 && g < a.n_group && better < a.topk_group);
     }
     // selection keys: 0 = cannot be chosen, masked below every number
     uint32_t u[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = e0 + i;
-      const bool in = e < E && (a.n_group == 1 || ((keep >> (e / per)) & 1u));
-      u[i] = in ? float_key(key[i]) : 0u;
+      const int g = (e * a.per_magic) >> 16;  // e / per
+      u[i] = (e < E && ((keep >> (g << a.lane_shift)) & 1u)) ? float_key(key[i]) : 0u;
     }
-    float my_key = -INFINITY, my_sc = 0.0f;
-    int my_e = 0;
-    for (int j = 0; j < k; ++j) {
-      uint32_t bk = 0u;
-      int bi = 0;
+    // A lower bound of the k-th largest key: the k-th largest of the lanes' maxima (at
+    // least k keys are not below it).  Few keys reach it, mostly one a lane.
+    uint32_t top = 0u;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (u[i] > bk) {
-          bk = u[i];
-          bi = i;
+    for (int i = 0; i < NV; ++i) top = max(top, u[i]);
+    uint32_t bound = 0u;
+    for (int j = 0; j < k; ++j) {
+      bound = __reduce_max_sync(kFull, top);
+      const int owner = __ffs(__ballot_sync(kFull, top == bound)) - 1;
+      if (lane == owner) top = 0u;
+    }
+    bound = max(bound, 1u);
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) mine += u[i] >= bound;
+    int before = mine;  // inclusive scan: candidates in expert order
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, before, o);
+      if (lane >= o) before += v;
+    }
+    const int n = __shfl_sync(kFull, before, 31);
+    before -= mine;
+
+    // slot of this lane's candidate (k or more: not chosen), its expert, key and score
+    int slot = 32, ce = 0;
+    float ck = -INFINITY, cs = 0.0f;
+    if (n <= 32) {
+      // one candidate a lane, ranked against the others
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (u[i] >= bound) {
+          s_cand[warp][before] = make_uint2(u[i], (uint32_t)(e0 + i));
+          if constexpr (KIND == 1) s_row[warp][before] = sc[i];
+          ++before;
         }
-      const uint32_t m = __reduce_max_sync(kFull, bk);
-      const int owner = __ffs(__ballot_sync(kFull, bk == m)) - 1;  // lanes hold ascending experts
-      const int be = __shfl_sync(kFull, e0 + bi, owner);
-      float s = 0.0f;
-      if constexpr (KIND == 1) {
+      }
+      __syncwarp();
+      uint32_t cu = 0u;
+      if (lane < n) {
+        const uint2 c = s_cand[warp][lane];
+        cu = c.x;
+        ce = (int)c.y;
+        if constexpr (KIND == 1) cs = s_row[warp][lane];
+        ck = key_float(cu);
+        slot = 0;
+      }
+      for (int j = 0; j < n; ++j) {
+        const uint32_t o = s_cand[warp][j].x;
+        slot += (o > cu || (o == cu && j < lane)) ? 1 : 0;
+      }
+      __syncwarp();
+    } else {
+      // many equal keys at the bound: k rounds of a warp-wide maximum
+      slot = lane;
+      for (int j = 0; j < k; ++j) {
+        uint32_t bk = 0u;
+        int bi = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (i == bi) s = sc[i];
-        s = __shfl_sync(kFull, s, owner);
-      }
-      if (lane == j) {
-        my_key = key_float(m);
-        my_sc = s;
-        my_e = be;
-      }
+          if (u[i] > bk) {
+            bk = u[i];
+            bi = i;
+          }
+        const uint32_t m = __reduce_max_sync(kFull, bk);
+        const int owner = __ffs(__ballot_sync(kFull, bk == m)) - 1;  // lanes hold ascending experts
+        const int be = __shfl_sync(kFull, e0 + bi, owner);
+        float sv = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (lane == owner && i == bi) u[i] = 0u;
+        for (int i = 0; i < NV; ++i)
+          if (i == bi) {
+            sv = sc[i];
+            if (lane == owner) u[i] = 0u;
+          }
+        sv = __shfl_sync(kFull, sv, owner);
+        if (lane == j) {
+          ck = key_float(m);
+          cs = sv;
+          ce = be;
+        }
+      }
     }
-    // weights: lane j holds slot j
+    const bool chosen = slot < k;
     float w;
     if constexpr (KIND == 0) {
-      float m = __shfl_sync(kFull, my_key, 0);
-      float z;
-      if (a.renorm) {
-        w = (lane < k) ? exp_rel(my_key, m) : 0.0f;
-        z = warp_sum(w);
-      } else {
-        m = -INFINITY;
+      // relative to the best chosen key, or to the row's for the plain probability
+      float m = a.renorm ? (chosen ? ck : -INFINITY) : -INFINITY;
+      if (!a.renorm) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) m = fmaxf(m, key[i]);
-        m = warp_max(m);
+      }
+      m = warp_max(m);
+      w = chosen ? exp_rel(ck, m) : 0.0f;
+      float z = w;
+      if (!a.renorm) {
         z = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) z += exp_rel(key[i], m);
-        z = warp_sum(z);
-        w = exp_rel(my_key, m);
       }
+      z = warp_sum(z);
       w = z > 0.0f ? __fdiv_rn(w, z) : 0.0f;
     } else {
-      w = (lane < k) ? my_sc : 0.0f;
+      w = chosen ? cs : 0.0f;
       if (a.renorm) {
         const float z = warp_sum(w);
         w = z > 0.0f ? __fdiv_rn(w, z) : 0.0f;
       }
     }
-    if (lane < k) {
-      topk_idx[t * k + lane] = my_e;
-      topk_w[t * k + lane] = w;
+    if (chosen) {
+      topk_idx[t * k + slot] = ce;
+      topk_w[t * k + slot] = w;
     }
   }
-  if constexpr (PROB) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s_col[warp][e0 + i] = col[i];
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kSelThreads) {
-      float v = 0.0f;
-#pragma unroll
-      for (int q = 0; q < kSelWarps; ++q) v += s_col[q][e];
-      partial[(size_t)blockIdx.x * E + e] = v;
-    }
-  }
+  if constexpr (PROB) write_partial<EP>(s_row, warp, e0, col, E, partial);
 }
 
 // ----------------------------------------------------------------- gradient ---
+// add[i] = the sum of v over the lanes j < k whose expert e is this lane's e0 + i (e < 0:
+// none), through a shared row; repeated experts (never from the forward pass) add up in
+// slot order.
+template <int EP>
+__device__ __forceinline__ void spread(float* row, int e0, int lane, int e, float v, int k,
+                                       float (&add)[EP / 32]) {
+  constexpr int NV = EP / 32;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) add[i] = 0.0f;
+  const unsigned same = __match_any_sync(kFull, e >= 0 ? e : -1 - lane);
+  if (__any_sync(kFull, (same & (same - 1)) != 0)) {
+    for (int j = 0; j < k; ++j) {
+      const int ej = __shfl_sync(kFull, e, j);
+      const float vj = __shfl_sync(kFull, v, j);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (ej == e0 + i) add[i] += vj;
+    }
+    return;
+  }
+  store_row<EP>(row, e0, add);
+  __syncwarp();
+  if (e >= 0) row[e] = v;
+  __syncwarp();
+  load_floats<float, NV>(row + e0, add);
+  __syncwarp();
+}
+
 template <typename Tin, int EP, int KIND, bool DBIAS>
-__global__ void __launch_bounds__(kSelThreads) select_bwd_kernel(
+__global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_bwd_kernel(
     SelectArgs a, const int32_t* __restrict__ topk_idx, const float* __restrict__ d_w,
     const float* __restrict__ d_prob, Tin* __restrict__ d_logits, long long ldd,
     float* __restrict__ partial) {
   constexpr int NV = EP / 32;
-  __shared__ float s_col[DBIAS ? kSelWarps : 1][DBIAS ? EP : 1];
+  __shared__ __align__(16) float s_row[kSelWarps][EP];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int e0 = lane * NV;
   const int E = a.E, k = a.k;
@@ -269,68 +368,63 @@ __global__ void __launch_bounds__(kSelThreads) select_bwd_kernel(
        t += (long long)gridDim.x * kSelWarps) {
     float l[NV], key[NV], sc[NV];
     load_row<Tin, NV>(logits + t * a.ld, e0, E, vec, l);
-    keys_of<KIND, NV>(l, b, key, sc);
+    // the choice is made: any exponential will do
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if constexpr (KIND == 0) {
+        const float v = __fadd_rn(l[i], b[i]);
+        key[i] = (v > -INFINITY) ? v : -INFINITY;
+      } else {
+        sc[i] = (l[i] > -INFINITY) ? __frcp_rn(__fadd_rn(1.0f, expf(-l[i]))) : 0.0f;
+      }
+    }
     const int ej = (lane < k) ? topk_idx[t * k + lane] : -1;
     const float dj = (lane < k) ? d_w[t * k + lane] : 0.0f;
     const bool valid = ej >= 0 && ej < E;
-    // the chosen experts' keys and scores, slot j in lane j
-    float ckey = -INFINITY, csc = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int src = valid ? ej / NV : 0;
-      const float kv = __shfl_sync(kFull, key[i], src);
-      const float sv = __shfl_sync(kFull, sc[i], src);
-      if (valid && ej % NV == i) {
-        ckey = kv;
-        csc = sv;
-      }
-    }
-    float d[NV];
+    // the chosen experts' keys or scores, slot j in lane j
+    __syncwarp();
+    if constexpr (KIND == 0) store_row<EP>(s_row[warp], e0, key);
+    else store_row<EP>(s_row[warp], e0, sc);
+    __syncwarp();
+    const float picked = valid ? s_row[warp][ej] : (KIND == 0 ? -INFINITY : 0.0f);
+    __syncwarp();
+    float d[NV], add[NV];
     if constexpr (KIND == 0) {
       float m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < NV; ++i) m = fmaxf(m, key[i]);
       m = warp_max(m);
-      float q[NV], z = 0.0f;
+      float z = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        q[i] = exp_rel(key[i], m);
-        z += q[i];
+        sc[i] = exp_rel(key[i], m);
+        z += sc[i];
       }
       z = warp_sum(z);
       const float rz = z > 0.0f ? 1.0f / z : 0.0f;
       float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        q[i] *= rz;
-        dot += g[i] * q[i];
+        sc[i] *= rz;
+        dot += g[i] * sc[i];
       }
       float cd;  // what the chosen logit gets beside the dense part
       if (a.renorm) {
-        const float mc = warp_max(ckey);
-        const float e = exp_rel(ckey, mc);
+        const float e = exp_rel(picked, warp_max(picked));
         const float S = warp_sum(e);
         const float w = S > 0.0f ? e / S : 0.0f;
         cd = w * (dj - warp_sum(dj * w));
       } else {
-        const float qc = exp_rel(ckey, m) * rz;
-        dot += dj * qc;
-        cd = dj * qc;
+        cd = dj * (exp_rel(picked, m) * rz);
+        dot += cd;
       }
       dot = warp_sum(dot);
+      spread<EP>(s_row[warp], e0, lane, valid ? ej : -1, cd, k, add);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) d[i] = q[i] * (g[i] - dot);
-      for (int j = 0; j < k; ++j) {
-        const int e = __shfl_sync(kFull, valid ? ej : -1, j);
-        const float v = __shfl_sync(kFull, cd, j);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (e == e0 + i) d[i] += v;
-      }
+      for (int i = 0; i < NV; ++i) d[i] = sc[i] * (g[i] - dot) + add[i];
     } else {
-      float dense = 0.0f;
+      float dense = 0.0f, rz = 0.0f;
       const bool has = d_prob != nullptr;
-      float rz = 0.0f;
       if (has) {
         float z = 0.0f, dot = 0.0f;
 #pragma unroll
@@ -344,21 +438,15 @@ __global__ void __launch_bounds__(kSelThreads) select_bwd_kernel(
       }
       float cd = dj;
       if (a.renorm) {
-        const float S = warp_sum(csc);
-        const float rs = S > 0.0f ? 1.0f / S : 0.0f;
-        cd = (dj - warp_sum(dj * csc) * rs) * rs;
+        const float S = warp_sum(picked);
+        cd = S > 0.0f ? __fdiv_rn(dj - __fdiv_rn(warp_sum(__fmul_rn(dj, picked)), S), S) : 0.0f;
       }
+      spread<EP>(s_row[warp], e0, lane, valid ? ej : -1, cd, k, add);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) d[i] = has ? (g[i] - dense) * rz : 0.0f;
-      for (int j = 0; j < k; ++j) {
-        const int e = __shfl_sync(kFull, valid ? ej : -1, j);
-        const float v = __shfl_sync(kFull, cd, j);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (e == e0 + i) d[i] += v;
+      for (int i = 0; i < NV; ++i) {
+        const float D = has ? (g[i] - dense) * rz + add[i] : add[i];
+        d[i] = __fmul_rn(__fmul_rn(D, sc[i]), __fsub_rn(1.0f, sc[i]));
       }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) d[i] *= sc[i] * (1.0f - sc[i]);
     }
     Tin* row = d_logits + t * ldd;
     if (vecd && e0 + NV <= E) {
@@ -374,15 +462,8 @@ __global__ void __launch_bounds__(kSelThreads) select_bwd_kernel(
     }
   }
   if constexpr (DBIAS) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s_col[warp][e0 + i] = col[i];
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kSelThreads) {
-      float v = 0.0f;
-#pragma unroll
-      for (int q = 0; q < kSelWarps; ++q) v += s_col[q][e];
-      partial[(size_t)blockIdx.x * E + e] = v;
-    }
+    __syncwarp();
+    write_partial<EP>(s_row, warp, e0, col, E, partial);
   }
 }
 
@@ -463,7 +544,12 @@ cudaError_t by_type_and_experts(int dtype, int E, F&& f) {
 
 SelectArgs args_of(const void* logits, long long ld, const float* bias, const moe_select_opts& o,
                    int T, int E, int k) {
-  return SelectArgs{logits, ld, bias, T, E, k, o.n_group, o.topk_group, o.group_top, o.renorm};
+  const int per = E / o.n_group;
+  int shift = 5;
+  while ((1 << (5 - shift)) < o.n_group) --shift;
+  return SelectArgs{logits,       ld,          bias,     T,   E,
+                    k,            o.n_group,   o.topk_group, o.group_top, o.renorm,
+                    per,          (65536 + per - 1) / per, shift};
 }
 
 }  // namespace
