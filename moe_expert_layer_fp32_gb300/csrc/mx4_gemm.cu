@@ -14,8 +14,8 @@
 //            K = 64.  The role runs in one elected lane for its whole loop: issued from a
 //            lane picked by its index instead, an MMA took 95 cycles of issue, the 224-row
 //            MMA itself 112.
-//   warps 2-5  epilogue: 32 lanes x 32 columns at a time from tensor memory; a warp writes
-//            32 consecutive output columns of one row per store
+//   warps 2-9  epilogue: 32 lanes x 32 columns at a time from tensor memory, two warps a
+//            lane quarter; a warp writes 32 consecutive output columns of one row per store
 // Tensor memory: two accumulators of 224 columns (a unit's epilogue runs under the next
 // one's main loop) and two sets of 24 scale columns, 496 of 512.
 //
@@ -28,11 +28,16 @@
 namespace moe {
 namespace {
 
+constexpr int kThreads = 320;  // producer, MMA issuer, eight epilogue warps
+
+// PAIR: two CTAs of a cluster run one MMA (cta_group::2) of 256 output columns.
+template <bool PAIR>
 struct MxCfg {
-  static constexpr int STAGES = 4;
+  static constexpr int STAGES = PAIR ? 6 : 4;
+  static constexpr int STAGE_ROWS = PAIR ? kMx4TileRows / 2 : kMx4TileRows;
   static constexpr int SF_OFF = kMx4WBytes;                  // row scales
   static constexpr int ROW_OFF = SF_OFF + kMx4SfSlot;        // row codes (1024-byte aligned)
-  static constexpr int STAGE_BYTES = ROW_OFF + kMx4TileRows * 128;
+  static constexpr int STAGE_BYTES = ROW_OFF + STAGE_ROWS * 128;
   static constexpr int NBAR = 2 * STAGES + 2 + 2 + 1;
   static constexpr int TMEM_COLS = 512;
   static constexpr int ACC_COLS = kMx4TileRows;
@@ -50,6 +55,36 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, P;\n\t}"
       : "=r"(p));
   return p != 0;
+}
+
+// mbar_wait_bounded with cluster-scope acquire: the even CTA's full barriers also count the
+// odd CTA's arrivals.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+template <bool PAIR>
+__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          int32_t* status, long long limit) {
+  if constexpr (!PAIR) return mbar_wait_bounded(bar, parity, abort, status, limit);
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > limit) {
+      *abort = 1;
+      flag_error(status, MOE_ERR_TIMEOUT);
+      return false;
+    }
+  }
 }
 
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes,
@@ -71,24 +106,41 @@ __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
   d |= (uint64_t)1u << 46;
   return d;
 }
+// (PAIR: each CTA's own shared memory to its own tensor memory)
+template <bool PAIR>
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-               : "memory");
+  if constexpr (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+                 : "memory");
 }
 
-// Instruction descriptor, kind::mxf4: E2M1 A and B (K-major), E8M0 scales, M = 128, N rows;
-// `id`: which two of a scale word's four bytes an MMA of K = 64 reads (0 or 2).
-__device__ __forceinline__ uint32_t idesc_mx4(int N, uint32_t id) {
+// Instruction descriptor, kind::mxf4: E2M1 A and B (K-major), E8M0 scales, M output columns
+// (128, or 256 over a pair), N rows; `id`: which two of a scale word's four bytes an MMA of
+// K = 64 reads (0 or 2).
+__device__ __forceinline__ uint32_t idesc_mx4(int M, int N, uint32_t id) {
   return (id << 4)                       // B scale bytes
          | (1u << 7) | (1u << 10)        // A, B: E2M1
          | ((uint32_t)(N >> 3) << 17)    // N / 8
          | (1u << 23)                    // scales: E8M0
-         | ((128u >> 4) << 24)           // M / 16
+         | ((uint32_t)(M >> 4) << 24)    // M / 16
          | (id << 29);                   // A scale bytes
 }
+template <bool PAIR>
 __device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                         uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
@@ -98,41 +150,52 @@ __device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_
       : "memory");
 }
 
-// One unit: a row tile of an expert times one weight tile.
+__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// One unit: a row tile of an expert times one weight tile (PAIR: two, one a CTA).
 struct MxUnit {
   int row0;              // first output row
   int rows;              // rows of the tile
   int rows16;            // padded to 16: N of its MMAs
-  int nt;                // weight tile of the expert
+  int nt;                // this CTA's weight tile of the expert (NT or more: none to store)
   size_t w_img;          // byte offsets of k-block 0's images
-  size_t row_img;
+  size_t row_img;        // (of the tile; a pair's CTAs load one half of its rows each)
   size_t sf_img;
 };
 
-__device__ __forceinline__ MxUnit mx_unit(long long u, const Mx4Tables& tb, int E, int NT, int KB) {
-  const int tile = (int)(u / NT);
+template <bool PAIR>
+__device__ __forceinline__ MxUnit mx_unit(long long u, const Mx4Tables& tb, int E, int NT, int KB,
+                                          int rank) {
+  const int nu = PAIR ? (NT + 1) / 2 : NT;  // units of a row tile
+  const int tile = (int)(u / nu);
   const int e = mx4_find(tb.tile, E, tile);
   const int m = tb.off[e + 1] - tb.off[e];
   const Mx4Cut cut = mx4_cut(m);
   const int ti = tile - tb.tile[e];
   MxUnit w;
-  w.nt = (int)(u - (long long)tile * NT);
+  w.nt = (int)(u - (long long)tile * nu);
+  if (PAIR) w.nt = 2 * w.nt + rank;
   w.row0 = tb.off[e] + ti * cut.step;
   w.rows = min(cut.step, m - ti * cut.step);
   w.rows16 = (w.rows + 15) / 16 * 16;
-  w.w_img = ((size_t)e * NT + w.nt) * KB * kMx4WBytes;
+  w.w_img = ((size_t)e * NT + min(w.nt, NT - 1)) * KB * kMx4WBytes;
   w.row_img = ((size_t)tb.pad[e] * 16 + (size_t)ti * cut.step) * KB * 128;
   w.sf_img = (size_t)tile * KB * kMx4SfSlot;
   return w;
 }
 
-template <typename Tout>
-__global__ void __launch_bounds__(192, 1)
+// Pair form: every CTA loads its own weight tile, its half of the rows' codes and all of
+// their scales, completing on its own `full` barrier; the odd CTA's idle MMA warp passes its
+// completions on to the even CTA's barrier (a bulk copy can only signal the CTA it writes),
+// whose MMA thread runs both tensor cores.  Commits free the stage in both CTAs.
+template <typename Tout, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
     mx4_gemm_kernel(const uint8_t* __restrict__ wimg, const uint8_t* __restrict__ rimg,
                     const uint8_t* __restrict__ simg, const int32_t* __restrict__ offsets, int E,
                     int R, int K, int N, Tout* __restrict__ y, int32_t* status,
                     long long spin_limit) {
-  using C = MxCfg;
+  using C = MxCfg<PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -149,39 +212,48 @@ __global__ void __launch_bounds__(192, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int NT = N / kMx4WTile;
   const int KB = mx4_kblocks(K);
+  const int rank = PAIR ? (int)cluster_ctarank() : 0;
+  const long long unit0 = PAIR ? blockIdx.x / 2 : blockIdx.x;
+  const long long unit_step = PAIR ? gridDim.x / 2 : gridDim.x;
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&full[s], (PAIR && rank == 0) ? 2 : 1);  // its producer (and the odd CTA's relay)
+      mbar_init(&empty[s], 1);                           // the MMA's commit
     }
     for (int a = 0; a < 2; ++a) {
-      mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 128);
+      mbar_init(&tfull[a], 1);                           // the MMA's commit
+      mbar_init(&tempty[a], PAIR ? 16 : 8);              // the epilogue warps (of both CTAs)
     }
     mbar_init(mma_done, 1);
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+    else tmem_alloc(tmem_slot, C::TMEM_COLS);
+  }
   const bool ok_tables = mx4_build_tables(tb, offsets, E, R, status);
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // both CTAs' barriers exist before any remote use
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const long long total = ok_tables ? (long long)tb.tile[E] * NT : 0;
+  const long long total = ok_tables ? (long long)tb.tile[E] * (PAIR ? (NT + 1) / 2 : NT) : 0;
 
   if (warp == 0) {
     if (elect_one()) {
       // ------------------------------------------------------------ producer
+      // bytes of a k-block's rows and scales that this CTA loads
+      auto row_bytes = [&](const MxUnit& w) { return (uint32_t)w.rows16 * (PAIR ? 64u : 128u); };
+      auto sf_bytes = [&](const MxUnit& w) { return w.rows16 > 128 ? 2048u : 1024u; };
       // The weights are inputs: the first unit's first stages are on their way before the
       // rows' quantisation, the kernel before this one, has finished.
       int early = 0;
-      if (blockIdx.x < total) {
-        const MxUnit w = mx_unit(blockIdx.x, tb, E, NT, KB);
-        const uint32_t bytes = kMx4WBytes + (uint32_t)w.rows16 * 128u + (w.rows16 > 128 ? 2048u : 1024u);
+      if (unit0 < total) {
+        const MxUnit w = mx_unit<PAIR>(unit0, tb, E, NT, KB, rank);
         for (; early < KB && early < C::STAGES; ++early) {
-          mbar_arrive_expect_tx(&full[early], bytes);
+          mbar_arrive_expect_tx(&full[early], kMx4WBytes + row_bytes(w) + sf_bytes(w));
           bulk_load(base + early * C::STAGE_BYTES, wimg + w.w_img + (size_t)early * kMx4WBytes,
                     kMx4WBytes, &full[early]);
         }
@@ -189,10 +261,11 @@ __global__ void __launch_bounds__(192, 1)
       pdl_wait();
       int it = 0;
       bool aborted = false;
-      for (long long u = blockIdx.x; u < total && !aborted; u += gridDim.x) {
-        const MxUnit w = mx_unit(u, tb, E, NT, KB);
-        const uint32_t row_bytes = (uint32_t)w.rows16 * 128u;
-        const uint32_t sf_bytes = w.rows16 > 128 ? 2048u : 1024u;
+      for (long long u = unit0; u < total && !aborted; u += unit_step) {
+        const MxUnit w = mx_unit<PAIR>(u, tb, E, NT, KB, rank);
+        const uint32_t rb = row_bytes(w), sb = sf_bytes(w);
+        const uint8_t* rows = rimg + w.row_img + (size_t)rank * rb;
+        const size_t row_step = (size_t)w.rows16 * 128;
         for (int kb = 0; kb < KB; ++kb, ++it) {
           const int s = it % C::STAGES;
           const uint32_t ph = (it / C::STAGES) & 1;
@@ -202,11 +275,11 @@ __global__ void __launch_bounds__(192, 1)
           }
           uint8_t* st = base + s * C::STAGE_BYTES;
           if (it >= early) {
-            mbar_arrive_expect_tx(&full[s], kMx4WBytes + row_bytes + sf_bytes);
+            mbar_arrive_expect_tx(&full[s], kMx4WBytes + rb + sb);
             bulk_load(st, wimg + w.w_img + (size_t)kb * kMx4WBytes, kMx4WBytes, &full[s]);
           }
-          bulk_load(st + C::ROW_OFF, rimg + w.row_img + (size_t)kb * row_bytes, row_bytes, &full[s]);
-          bulk_load(st + C::SF_OFF, simg + w.sf_img + (size_t)kb * kMx4SfSlot, sf_bytes, &full[s]);
+          bulk_load(st + C::ROW_OFF, rows + kb * row_step, rb, &full[s]);
+          bulk_load(st + C::SF_OFF, simg + w.sf_img + (size_t)kb * kMx4SfSlot, sb, &full[s]);
         }
       }
       if (aborted) {
@@ -218,23 +291,42 @@ __global__ void __launch_bounds__(192, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (elect_one()) {
+    if (PAIR && rank == 1) {
+      if (elect_one()) {
+        // ------------------------------------------- relay of the odd CTA's full stages
+        int it = 0;
+        bool aborted = false;
+        for (long long u = unit0; u < total && !aborted; u += unit_step) {
+          for (int kb = 0; kb < KB; ++kb, ++it) {
+            const int s = it % C::STAGES;
+            if (!mbar_wait_bounded(&full[s], (it / C::STAGES) & 1, abort_flag, status, spin_limit)) {
+              aborted = true;
+              break;
+            }
+            // CTA-scope release: the bytes are in this SM's shared memory, which only its own
+            // tensor core reads; a cluster-scope release took about 1500 cycles a stage
+            mbar_arrive_remote(mapa_shared(smem_u32(&full[s]), 0));
+          }
+        }
+      }
+    } else if (elect_one()) {
       // ---------------------------------------------------------- MMA issuer
       int it = 0, tcount = 0;
-      for (long long u = blockIdx.x; u < total; u += gridDim.x, ++tcount) {
-        const MxUnit w = mx_unit(u, tb, E, NT, KB);
+      for (long long u = unit0; u < total; u += unit_step, ++tcount) {
+        const MxUnit w = mx_unit<PAIR>(u, tb, E, NT, KB, rank);
         const int acc = tcount & 1;
         const uint32_t aph = (tcount >> 1) & 1;
         if (!mbar_wait_bounded(&tempty[acc], aph ^ 1, abort_flag, status, spin_limit)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * C::ACC_COLS;
-        const uint32_t id0 = idesc_mx4(w.rows16, 0), id1 = idesc_mx4(w.rows16, 2);
+        constexpr int M = PAIR ? 256 : 128;
+        const uint32_t id0 = idesc_mx4(M, w.rows16, 0), id1 = idesc_mx4(M, w.rows16, 2);
         const bool two = w.rows16 > 128;
         bool aborted = false;
         for (int kb = 0; kb < KB; ++kb, ++it) {
           const int s = it % C::STAGES;
           const uint32_t ph = (it / C::STAGES) & 1;
-          if (!mbar_wait_bounded(&full[s], ph, abort_flag, status, spin_limit)) {
+          if (!wait_full<PAIR>(&full[s], ph, abort_flag, status, spin_limit)) {
             aborted = true;
             break;
           }
@@ -245,36 +337,40 @@ __global__ void __launch_bounds__(192, 1)
           // scale columns: weights 4 per half k-block, rows 8 (two 128-row halves)
           const uint32_t sfa = tmem_base + C::SF_COL + (it & 1) * 24, sfb = sfa + 8;
           const bool whole = (kb + 1) * kMx4KB <= K;  // else the first half only
-          copy_scales(sfa, fa);
-          copy_scales(sfb, fb);
-          if (two) copy_scales(sfb + 4, fb + 64);
+          copy_scales<PAIR>(sfa, fa);
+          copy_scales<PAIR>(sfb, fb);
+          if (two) copy_scales<PAIR>(sfb + 4, fb + 64);
           if (whole) {
-            copy_scales(sfa + 4, fa + 32);
-            copy_scales(sfb + 8, fb + 32);
-            if (two) copy_scales(sfb + 12, fb + 96);
+            copy_scales<PAIR>(sfa + 4, fa + 32);
+            copy_scales<PAIR>(sfb + 8, fb + 32);
+            if (two) copy_scales<PAIR>(sfb + 12, fb + 96);
           }
-          mma_mx4(d, da, db, id0, sfa, sfb, kb > 0 ? 1u : 0u);
-          mma_mx4(d, da + 2, db + 2, id1, sfa, sfb, 1u);
+          mma_mx4<PAIR>(d, da, db, id0, sfa, sfb, kb > 0 ? 1u : 0u);
+          mma_mx4<PAIR>(d, da + 2, db + 2, id1, sfa, sfb, 1u);
           if (whole) {
-            mma_mx4(d, da + 4, db + 4, id0, sfa + 4, sfb + 8, 1u);
-            mma_mx4(d, da + 6, db + 6, id1, sfa + 4, sfb + 8, 1u);
+            mma_mx4<PAIR>(d, da + 4, db + 4, id0, sfa + 4, sfb + 8, 1u);
+            mma_mx4<PAIR>(d, da + 6, db + 6, id1, sfa + 4, sfb + 8, 1u);
           }
-          mma_commit(&empty[s]);
+          if constexpr (PAIR) mma_commit_pair(&empty[s], 0x3);
+          else mma_commit(&empty[s]);
         }
         if (aborted) break;
-        mma_commit(&tfull[acc]);
+        if constexpr (PAIR) mma_commit_pair(&tfull[acc], 0x3);
+        else mma_commit(&tfull[acc]);
       }
       // every MMA this thread issued completes before tensor memory is released
-      mma_commit(mma_done);
+      if constexpr (PAIR) mma_commit_pair(mma_done, 0x1);
+      else mma_commit(mma_done);
       wait_drain(mma_done, 0, kSpinLimitCycles);
     }
     __syncwarp();
   } else {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3;  // lane quarter of tensor memory this warp may access
+    const int half = (warp - 2) >> 2;  // of the quarter's two warps: every other 32 columns
     int tcount = 0;
-    for (long long u = blockIdx.x; u < total; u += gridDim.x, ++tcount) {
-      const MxUnit w = mx_unit(u, tb, E, NT, KB);
+    for (long long u = unit0; u < total; u += unit_step, ++tcount) {
+      const MxUnit w = mx_unit<PAIR>(u, tb, E, NT, KB, rank);
       const int acc = tcount & 1;
       const uint32_t aph = (tcount >> 1) & 1;
       int ok = 1;
@@ -284,53 +380,95 @@ __global__ void __launch_bounds__(192, 1)
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * C::ACC_COLS);
       Tout* dst = y + (size_t)w.row0 * N + w.nt * kMx4WTile + q * 32 + lane;
-      for (int c0 = 0; c0 < w.rows; c0 += 32) {
+      const int rows = (!PAIR || w.nt < NT) ? w.rows : 0;
+      for (int c0 = half * 32; c0 < rows; c0 += 64) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(taddr + c0, v);
         tmem_ld_wait();
-        const int n = min(32, w.rows - c0);
+        Tout* p = dst + (size_t)c0 * N;
+        if (rows - c0 >= 32) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (i < n) {
-            const float f = __uint_as_float(v[i]);
-            if constexpr (sizeof(Tout) == 4) dst[(size_t)(c0 + i) * N] = f;
-            else dst[(size_t)(c0 + i) * N] = __float2bfloat16_rn(f);
-          }
+          for (int i = 0; i < 32; ++i, p += N) store_one(p, __uint_as_float(v[i]));
+        } else {
+          const int n = rows - c0;
+#pragma unroll
+          for (int i = 0; i < 32; ++i, p += N)
+            if (i < n) store_one(p, __uint_as_float(v[i]));
         }
       }
       tc_fence_before();
-      mbar_arrive(&tempty[acc]);
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
+        else mbar_arrive(&tempty[acc]);
+      }
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // no CTA leaves while the pair may still use it
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, C::TMEM_COLS);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
 }
 
-template <typename Tout>
+// One CTA per SM (pairs: as many clusters of two as fit), at most one per unit.
+template <typename Tout, bool PAIR>
 cudaError_t go(const uint8_t* w, const uint8_t* r, const uint8_t* sf, const int32_t* offsets, int E,
                int R, int K, int N, void* y, int32_t* status, long long limit, cudaStream_t s) {
-  static bool attr[64] = {};
+  using C = MxCfg<PAIR>;
+  auto kern = mx4_gemm_kernel<Tout, PAIR>;
+  static int cache[64] = {};  // per device: CTAs that fit
   int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev >= 64 || !attr[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(
-        mx4_gemm_kernel<Tout>, cudaFuncAttributeMaxDynamicSharedMemorySize, MxCfg::SMEM_BYTES);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) attr[dev] = true;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  pdl_attr(attr[0]);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  int fit = dev < 64 ? cache[dev] : 0;
+  if (fit == 0) {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (err != cudaSuccess) return err;
+    fit = device_sm_count();
+    if (PAIR) {
+      int clusters = 0;
+      cfg.gridDim = dim3(2 * fit);
+      cfg.attrs = attr + 1;
+      cfg.numAttrs = 1;
+      err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+      if (err != cudaSuccess) return err;
+      if (clusters < 1) return cudaErrorInvalidConfiguration;
+      fit = 2 * clusters;
+    }
+    if (dev < 64) cache[dev] = fit;
   }
-  const long long units = mx4_max_tiles(R, E) * (N / kMx4WTile);
-  const int sms = device_sm_count();
-  const int grid = (int)(units < sms ? units : sms);
-  return launch_pdl(mx4_gemm_kernel<Tout>, dim3(grid), dim3(192), MxCfg::SMEM_BYTES, s, w, r, sf,
-                    offsets, E, R, K, N, static_cast<Tout*>(y), status, limit);
+  const int NT = N / kMx4WTile;
+  const long long units = mx4_max_tiles(R, E) * (PAIR ? (NT + 1) / 2 * 2 : NT);
+  cfg.gridDim = dim3((unsigned)(units < fit ? units : fit));
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, w, r, sf, offsets, E, R, K, N, static_cast<Tout*>(y), status,
+                            limit);
 }
 
 }  // namespace
+
+// Pairs halve the rows' bytes that each SM takes in, which bound the single form (64 bytes a
+// clock); a batch of few rows is bound by its weights.  Every output element is the same
+// sequence of MMAs in both forms, so its bits do not depend on the choice.
+static bool use_pair(int E, int R, int N) {
+  return N >= 2 * kMx4WTile && (long long)R >= 64LL * (R < E ? R : E);
+}
 
 cudaError_t launch_mx4_gemm(const void* packed, const void* codes, const void* sf,
                             const int32_t* offsets, int E, int R, int K, int N, void* y,
@@ -339,9 +477,12 @@ cudaError_t launch_mx4_gemm(const void* packed, const void* codes, const void* s
   const uint8_t* w = static_cast<const uint8_t*>(packed);
   const uint8_t* r = static_cast<const uint8_t*>(codes);
   const uint8_t* f = static_cast<const uint8_t*>(sf);
-  if (y_dtype == MOE_DTYPE_F32)
-    return go<float>(w, r, f, offsets, E, R, K, N, y, status, spin_limit, s);
-  return go<__nv_bfloat16>(w, r, f, offsets, E, R, K, N, y, status, spin_limit, s);
+  auto run = [&](auto kind) {
+    using T = decltype(kind);
+    return use_pair(E, R, N) ? go<T, true>(w, r, f, offsets, E, R, K, N, y, status, spin_limit, s)
+                             : go<T, false>(w, r, f, offsets, E, R, K, N, y, status, spin_limit, s);
+  };
+  return y_dtype == MOE_DTYPE_F32 ? run(float{}) : run(__nv_bfloat16{});
 }
 
 }  // namespace moe

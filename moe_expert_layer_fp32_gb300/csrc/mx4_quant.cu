@@ -8,6 +8,8 @@
 //
 // Memory-bound: 8 values a lane (one or two 16-byte loads), four lanes a block whose
 // maximum meets in two shuffles; a warp covers one row's 256-value k-block.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.cuh"
 #include "mx4.cuh"
@@ -20,19 +22,63 @@ namespace {
 constexpr int kQThreads = 256;
 constexpr int kQWarps = kQThreads / 32;
 
-// The lane's eight values to codes; `byte`: the block's scale (the same in its four lanes).
-__device__ __forceinline__ uint32_t quantize8(const float (&v)[8], uint32_t& byte) {
-  uint32_t a = 0;
+// Eight consecutive values as they were loaded, and the FP32 bits (sign cleared) of a
+// magnitude that has the largest one's exponent, over the four lanes of a block.
+template <typename Tin>
+struct Piece {
+  float v[8];
+  __device__ __forceinline__ void load(const Tin* p) { load_floats<Tin, 8>(p, v); }
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
-  a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
-  byte = mx4_scale_byte(a);
-  const float inv = mx4_inverse_scale(byte);
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  }
+  __device__ __forceinline__ uint32_t block_max() const {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
+    return max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+  }
+  __device__ __forceinline__ void scaled(float inv, float (&q)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
+  }
+};
+
+// bf16: magnitudes order as 16-bit integers, two to an instruction (the widened form costs
+// twice the integer instructions, which bound the row images' kernel)
+template <>
+struct Piece<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    r = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ uint32_t block_max() const {
+    constexpr uint32_t M = 0x7FFF7FFFu;
+    uint32_t a = __vmaxu2(__vmaxu2(r.x & M, r.y & M), __vmaxu2(r.z & M, r.w & M));
+    a = __vmaxu2(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
+    a = __vmaxu2(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+    return max(a << 16, a & 0xFFFF0000u);
+  }
+  __device__ __forceinline__ void scaled(float inv, float (&q)[8]) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      q[2 * i] = bf16_lo(w[i]) * inv;
+      q[2 * i + 1] = bf16_hi(w[i]) * inv;
+    }
+  }
+};
+
+// The lane's piece to codes; `byte`: the block's scale (the same in its four lanes).
+template <typename Tin>
+__device__ __forceinline__ uint32_t quantize8(const Piece<Tin>& p, uint32_t& byte) {
+  byte = mx4_scale_byte(p.block_max());
   float q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = (byte == 255u) ? 0.0f : v[i] * inv;
-  return mx4_encode8(q);
+  p.scaled(mx4_inverse_scale(byte), q);
+  const uint32_t c = mx4_encode8(q);
+  return byte == 255u ? 0u : c;
 }
 
 // ------------------------------------------------------------ logical rows ---
@@ -48,20 +94,19 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const Tin* __restri
                                                              uint4* __restrict__ values) {
   // n is a multiple of 4, so a block is whole or past the end
   const long long base = (long long)blockIdx.x * (kQThreads * kQUnroll) + threadIdx.x;
-  float v[kQUnroll][8];
+  Piece<Tin> v[kQUnroll];
 #pragma unroll
   for (int q = 0; q < kQUnroll; ++q) {
     const long long i = base + q * kQThreads;
     if (i < n) {
       if constexpr (DENSE) {
-        load_floats<Tin, 8>(x + i * 8, v[q]);
+        v[q].load(x + i * 8);
       } else {
         const long long row = i / per_row;
-        load_floats<Tin, 8>(x + row * ld + (i - row * per_row) * 8, v[q]);
+        v[q].load(x + row * ld + (i - row * per_row) * 8);
       }
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[q][j] = 0.0f;
+      v[q].zero();
     }
   }
 #pragma unroll
@@ -83,20 +128,24 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const Tin* __restri
 //
 // A warp takes the rows rr, rr + 32, rr + 64, rr + 96 of a tile's 128-row half: four loads
 // in flight a lane, and the four rows' scales of a half k-block are one 16-byte store.
+// `span`: k-blocks a warp takes (all of them, or one where the rows alone are few).
 template <typename Tin, int SRC>
 __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(
     const Tin* __restrict__ x, const int32_t* __restrict__ row_of, int k, int T,
-    const int32_t* __restrict__ offsets, int E, int R, int K, uint8_t* __restrict__ codes,
+    const int32_t* __restrict__ offsets, int E, int R, int K, int span, uint8_t* __restrict__ codes,
     uint8_t* __restrict__ sf, int32_t* status) {
   __shared__ Mx4Tables tb;
   pdl_launch_dependents();  // the product reads this kernel's images only after its own wait
   if (!mx4_build_tables(tb, offsets, E, R, status)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int KB = mx4_kblocks(K);
+  const int spans = (KB + span - 1) / span;
   const long long items = (long long)tb.tile[E] * 64;  // (tile, half, rr)
-  for (long long it = (long long)blockIdx.x * kQWarps + warp; it < items;
+  for (long long it = (long long)blockIdx.x * kQWarps + warp; it < items * spans;
        it += (long long)gridDim.x * kQWarps) {
-    const int tile = (int)(it >> 6), half = (int)(it >> 5) & 1, rr = (int)it & 31;
+    const long long row_item = spans == 1 ? it : it / spans;
+    const int kb0 = (int)(it - row_item * spans) * span, kb1 = min(KB, kb0 + span);
+    const int tile = (int)(row_item >> 6), half = (int)(row_item >> 5) & 1, rr = (int)row_item & 31;
     const int e = mx4_find(tb.tile, E, tile);
     const int m = tb.off[e + 1] - tb.off[e];
     const Mx4Cut cut = mx4_cut(m);
@@ -107,8 +156,10 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(
     const int rows16 = (rows + 15) / 16 * 16;
     const int nr = min(4, (rows - r0 + 31) / 32);
     const int row0 = tb.off[e] + ti * cut.step + r0;
-    uint8_t* cdst = codes + ((size_t)tb.pad[e] * 16 + (size_t)ti * cut.step) * KB * 128 + r0 * 128;
-    uint8_t* sdst = sf + (size_t)tile * KB * kMx4SfSlot + half * 1024 + rr * 16;
+    // (rows 32 apart have the same row & 7)
+    uint8_t* cdst = codes + ((size_t)tb.pad[e] * 16 + (size_t)ti * cut.step) * KB * 128 + r0 * 128 +
+                    (((lane >> 2) ^ (rr & 7)) * 16) + (lane & 3) * 4;
+    uint8_t* sdst = sf + (size_t)tile * KB * kMx4SfSlot + half * 1024 + rr * 16 + (lane >> 4) * 512;
     const Tin* src[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -121,19 +172,20 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(
           r = 0;
         }
       }
-      src[i] = x + (size_t)r * (SRC == 2 ? 2 * (size_t)K : (size_t)K);
+      src[i] = x + (size_t)r * (SRC == 2 ? 2 * (size_t)K : (size_t)K) + lane * 8;
     }
-    for (int kb = 0; kb < KB; ++kb) {
-      const int col = kb * kMx4KB + lane * 8;
-      const bool in = col < K;  // K is a multiple of 128: whole half-warps
-      float v[4][8];
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int col = kb * kMx4KB;
+      const bool in = col + lane * 8 < K;  // K is a multiple of 128: whole half-warps
+      using P = Piece<std::conditional_t<SRC == 2, float, Tin>>;
+      P v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (in && i < nr) {
-          load_floats<Tin, 8>(src[i] + col, v[i]);
+          if constexpr (SRC == 2) load_floats<Tin, 8>(src[i] + col, v[i].v);
+          else v[i].load(src[i] + col);
         } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+          v[i].zero();
         }
       }
       if constexpr (SRC == 2) {
@@ -143,28 +195,30 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(
             float up[8];
             load_floats<Tin, 8>(src[i] + K + col, up);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(silu_f32(v[i][j]), up[j]);
+            for (int j = 0; j < 8; ++j) v[i].v[j] = __fmul_rn(silu_f32(v[i].v[j]), up[j]);
           }
         }
       }
-      uint32_t w[4];
+      uint32_t byte[4];
       uint8_t* ck = cdst + (size_t)kb * rows16 * 128;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t byte;
-        const uint32_t c = quantize8(v[i], byte);
-        // the four scales of each half of the k-block meet in its first lane
-        w[i] = byte | (__shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8) |
-               (__shfl_down_sync(0xFFFFFFFFu, byte, 8) << 16) |
-               (__shfl_down_sync(0xFFFFFFFFu, byte, 12) << 24);
-        // (rows 32 apart have the same row & 7)
-        if (in && i < nr)
-          *reinterpret_cast<uint32_t*>(ck + i * 32 * 128 + (((lane >> 2) ^ (rr & 7)) * 16) +
-                                       (lane & 3) * 4) = c;
+        const uint32_t c = quantize8(v[i], byte[i]);
+        if (in && i < nr) *reinterpret_cast<uint32_t*>(ck + i * 32 * 128) = c;
       }
-      if (in && (lane & 15) == 0)
-        *reinterpret_cast<uint4*>(sdst + (size_t)kb * kMx4SfSlot + (lane >> 4) * 512) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+      // A lane's four bytes are four rows' scales of one block; the first lane of each half
+      // k-block collects the words of the other three blocks and turns the 4 x 4 bytes.
+      const uint32_t b0 = byte[0] | (byte[1] << 8) | (byte[2] << 16) | (byte[3] << 24);
+      const uint32_t b1 = __shfl_down_sync(0xFFFFFFFFu, b0, 4);
+      const uint32_t b2 = __shfl_down_sync(0xFFFFFFFFu, b0, 8);
+      const uint32_t b3 = __shfl_down_sync(0xFFFFFFFFu, b0, 12);
+      if (in && (lane & 15) == 0) {
+        const uint32_t lo01 = __byte_perm(b0, b1, 0x5140), hi01 = __byte_perm(b0, b1, 0x7362);
+        const uint32_t lo23 = __byte_perm(b2, b3, 0x5140), hi23 = __byte_perm(b2, b3, 0x7362);
+        *reinterpret_cast<uint4*>(sdst + (size_t)kb * kMx4SfSlot) =
+            make_uint4(__byte_perm(lo01, lo23, 0x5410), __byte_perm(lo01, lo23, 0x7632),
+                       __byte_perm(hi01, hi23, 0x5410), __byte_perm(hi01, hi23, 0x7632));
+      }
     }
   }
 }
@@ -271,13 +325,16 @@ cudaError_t launch_mx4_rows(const void* x, int dtype, int src, const int32_t* ro
                             const int32_t* offsets, int E, int R, int K, void* codes, void* sf,
                             int32_t* status, cudaStream_t s) {
   if (R == 0) return cudaSuccess;
-  const long long need = mx4_max_tiles(R, E) * 64 / kQWarps;
   const long long most = (long long)device_sm_count() * 6;
+  const int KB = mx4_kblocks(K);
+  // a warp per k-block while whole rows would not give every SM 16 warps
+  const int span = (long long)R < 16LL * 4 * device_sm_count() ? 1 : KB;
+  const long long need = mx4_max_tiles(R, E) * 64 / kQWarps * ((KB + span - 1) / span);
   const int grid = (int)(need < most ? need : most);
   uint8_t* c = static_cast<uint8_t*>(codes);
   uint8_t* f = static_cast<uint8_t*>(sf);
   auto go = [&](auto kern, auto* p) {
-    kern<<<grid, kQThreads, 0, s>>>(p, row_of, k, T, offsets, E, R, K, c, f, status);
+    kern<<<grid, kQThreads, 0, s>>>(p, row_of, k, T, offsets, E, R, K, span, c, f, status);
     return cudaGetLastError();
   };
   const auto* xb = static_cast<const __nv_bfloat16*>(x);

@@ -62,22 +62,41 @@ __device__ __forceinline__ void load_row(const Tin* row, int e0, int E, bool vec
 }
 
 // key and score of the lane's experts.  KIND 0: score is left to the caller (it needs
-// the row's maximum); masked experts and those past E have key -inf and score 0.
+// the row's maximum); masked experts and those past E have key -inf and score 0.  b is the
+// bias as lane_bias made it, so a sum with it is never -0 (which would order below +0).
 template <int KIND, int NV>
 __device__ __forceinline__ void keys_of(const float (&l)[NV], const float (&b)[NV], float (&key)[NV],
                                         float (&sc)[NV]) {
+  if constexpr (KIND == 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float v = __fadd_rn(l[i], b[i]);
+      key[i] = (v > -INFINITY) ? v : -INFINITY;
+      sc[i] = 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; i += 2) {
+      const float2 s = sigmoid_steps2(l[i], l[NV > 1 ? i + 1 : i]);
+      sc[i] = s.x;
+      if (NV > 1) sc[NV > 1 ? i + 1 : i] = s.y;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = l[i] > -INFINITY;
+      key[i] = in ? __fadd_rn(sc[i], b[i]) : -INFINITY;
+      sc[i] = in ? sc[i] : 0.0f;
+    }
+  }
+}
+
+// The lane's biases: NaN masks its expert as -inf does, -0 becomes +0.
+template <int NV>
+__device__ __forceinline__ void lane_bias(const float* bias, int e0, int E, float (&b)[NV]) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float v;
-    if constexpr (KIND == 0) {
-      v = __fadd_rn(l[i], b[i]);
-      sc[i] = 0.0f;
-    } else {
-      sc[i] = sigmoid_steps(l[i]);
-      v = (l[i] > -INFINITY) ? __fadd_rn(sc[i], b[i]) : -INFINITY;
-      if (!(l[i] > -INFINITY)) sc[i] = 0.0f;
-    }
-    key[i] = (v > -INFINITY) ? __fadd_rn(v, 0.0f) : -INFINITY;  // NaN: masked; -0: +0
+    const float v = (bias != nullptr && e0 + i < E) ? __ldg(bias + e0 + i) : 0.0f;
+    b[i] = (v == v) ? __fadd_rn(v, 0.0f) : -INFINITY;
   }
 }
 
@@ -85,6 +104,11 @@ __device__ __forceinline__ void keys_of(const float (&l)[NV], const float (&b)[N
 __device__ __forceinline__ float exp_rel(float key, float m) {
   if (key == -INFINITY) return 0.0f;
   return key == m ? 1.0f : expf(key - m);
+}
+
+// 1 / (1 + exp(-l)), 0 where masked: the gradient's sigmoid, with the library's exponential
+__device__ __forceinline__ float sigmoid(float l) {
+  return (l > -INFINITY) ? __frcp_rn(__fadd_rn(1.0f, expf(-l))) : 0.0f;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -126,15 +150,20 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
                                                              float* __restrict__ partial) {
   constexpr int NV = EP / 32;
   __shared__ __align__(16) float s_row[kSelWarps][EP];  // the keys; later the candidates' scores
-  __shared__ uint2 s_cand[kSelWarps][32];               // candidates: key, expert
+  __shared__ __align__(16) uint32_t s_key[kSelWarps][32];  // candidates in expert order
+  __shared__ int s_expert[kSelWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int e0 = lane * NV;
   const int E = a.E, k = a.k;
   const Tin* logits = static_cast<const Tin*>(a.logits);
   const bool vec = rows_aligned<Tin, NV>(logits, a.ld);
   float b[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) b[i] = (a.bias != nullptr && e0 + i < E) ? __ldg(a.bias + e0 + i) : 0.0f;
+  lane_bias<NV>(a.bias, e0, E, b);
+  // all experts of a lane are in one group (their count past e0 is then 0 or NV), or not
+  const bool whole = a.n_group == 1 || a.per % NV == 0;
+  const int inside = min(max(E - e0, 0), NV);
+  // a group is the experts of 2^lane_shift lanes
+  const bool by_lane = a.per == NV << a.lane_shift;
   float col[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) col[i] = 0.0f;
@@ -165,15 +194,23 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
     // groups that stay: L lanes per group, each over every L-th of its keys
     unsigned keep = kFull;
     if (a.topk_group < a.n_group) {
-      store_row<EP>(s_row[warp], e0, key);
-      __syncwarp();
       const int g = lane >> a.lane_shift, sub = lane & ((1 << a.lane_shift) - 1);
       float g1 = -INFINITY, g2 = -INFINITY;
-      if (g < a.n_group) {
-        for (int i = sub; i < a.per; i += 1 << a.lane_shift) {
-          const float v = s_row[warp][g * a.per + i];
-          g2 = fmaxf(g2, fminf(g1, v));
-          g1 = fmaxf(g1, v);
+      if (by_lane) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          g2 = fmaxf(g2, fminf(g1, key[i]));
+          g1 = fmaxf(g1, key[i]);
+        }
+      } else {
+        store_row<EP>(s_row[warp], e0, key);
+        __syncwarp();
+        if (g < a.n_group) {
+          for (int i = sub; i < a.per; i += 1 << a.lane_shift) {
+            const float v = s_row[warp][g * a.per + i];
+            g2 = fmaxf(g2, fminf(g1, v));
+            g1 = fmaxf(g1, v);
+          }
         }
       }
       for (int o = 1; o < (1 << a.lane_shift); o <<= 1) {
@@ -192,11 +229,17 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
     }
     // selection keys: 0 = cannot be chosen, masked below every number
     uint32_t u[NV];
+    if (whole) {
+      const int g = (e0 * a.per_magic) >> 16;  // e0 / per
+      const int n = (inside > 0 && ((keep >> (g << a.lane_shift)) & 1u)) ? inside : 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = e0 + i;
-      const int g = (e * a.per_magic) >> 16;  // e / per
-      u[i] = (e < E && ((keep >> (g << a.lane_shift)) & 1u)) ? float_key(key[i]) : 0u;
+      for (int i = 0; i < NV; ++i) u[i] = i < n ? float_key(key[i]) : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int g = ((e0 + i) * a.per_magic) >> 16;
+        u[i] = (i < inside && ((keep >> (g << a.lane_shift)) & 1u)) ? float_key(key[i]) : 0u;
+      }
     }
     // A lower bound of the k-th largest key: the k-th largest of the lanes' maxima (at
     // least k keys are not below it).  Few keys reach it, mostly one a lane.
@@ -227,28 +270,31 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
     float ck = -INFINITY, cs = 0.0f;
     if (n <= 32) {
       // one candidate a lane, ranked against the others
+      s_key[warp][lane] = 0u;
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (u[i] >= bound) {
-          s_cand[warp][before] = make_uint2(u[i], (uint32_t)(e0 + i));
+          s_key[warp][before] = u[i];
+          s_expert[warp][before] = e0 + i;
           if constexpr (KIND == 1) s_row[warp][before] = sc[i];
           ++before;
         }
       }
       __syncwarp();
-      uint32_t cu = 0u;
+      const uint32_t cu = s_key[warp][lane];
       if (lane < n) {
-        const uint2 c = s_cand[warp][lane];
-        cu = c.x;
-        ce = (int)c.y;
+        ce = s_expert[warp][lane];
         if constexpr (KIND == 1) cs = s_row[warp][lane];
         ck = key_float(cu);
         slot = 0;
       }
-      for (int j = 0; j < n; ++j) {
-        const uint32_t o = s_cand[warp][j].x;
-        slot += (o > cu || (o == cu && j < lane)) ? 1 : 0;
+      for (int j = 0; j < n; j += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(&s_key[warp][j]);
+        slot += (o.x > cu || (o.x == cu && j + 0 < lane)) ? 1 : 0;
+        slot += (o.y > cu || (o.y == cu && j + 1 < lane)) ? 1 : 0;
+        slot += (o.z > cu || (o.z == cu && j + 2 < lane)) ? 1 : 0;
+        slot += (o.w > cu || (o.w == cu && j + 3 < lane)) ? 1 : 0;
       }
       __syncwarp();
     } else {
@@ -325,8 +371,11 @@ __device__ __forceinline__ void spread(float* row, int e0, int lane, int e, floa
   constexpr int NV = EP / 32;
 #pragma unroll
   for (int i = 0; i < NV; ++i) add[i] = 0.0f;
-  const unsigned same = __match_any_sync(kFull, e >= 0 ? e : -1 - lane);
-  if (__any_sync(kFull, (same & (same - 1)) != 0)) {
+  __syncwarp();
+  if (e >= 0) row[e] = __int_as_float(lane);  // who has this expert
+  __syncwarp();
+  const bool again = e >= 0 && __float_as_int(row[e]) != lane;
+  if (__any_sync(kFull, again)) {
     for (int j = 0; j < k; ++j) {
       const int ej = __shfl_sync(kFull, e, j);
       const float vj = __shfl_sync(kFull, v, j);
@@ -341,11 +390,12 @@ __device__ __forceinline__ void spread(float* row, int e0, int lane, int e, floa
   if (e >= 0) row[e] = v;
   __syncwarp();
   load_floats<float, NV>(row + e0, add);
-  __syncwarp();
 }
 
-template <typename Tin, int EP, int KIND, bool DBIAS>
-__global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_bwd_kernel(
+// DENSE: every expert of a row has a gradient (d_prob, or the plain softmax probability);
+// otherwise only the chosen ones, and only their logits are read.
+template <typename Tin, int EP, int KIND, bool DENSE, bool DBIAS>
+__global__ void __launch_bounds__(kSelThreads, DENSE ? kSelBlocksPerSm : 6) select_bwd_kernel(
     SelectArgs a, const int32_t* __restrict__ topk_idx, const float* __restrict__ d_w,
     const float* __restrict__ d_prob, Tin* __restrict__ d_logits, long long ldd,
     float* __restrict__ partial) {
@@ -357,59 +407,73 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_bwd_kerne
   const Tin* logits = static_cast<const Tin*>(a.logits);
   const bool vec = rows_aligned<Tin, NV>(logits, a.ld);
   const bool vecd = rows_aligned<Tin, NV>(d_logits, ldd);
-  float b[NV], g[NV], col[NV];
+  float b[DENSE ? NV : 1], g[DENSE ? NV : 1], col[DBIAS ? NV : 1];
+  if constexpr (DENSE) {
+    lane_bias<NV>(a.bias, e0, E, b);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    b[i] = (a.bias != nullptr && e0 + i < E) ? __ldg(a.bias + e0 + i) : 0.0f;
-    g[i] = (d_prob != nullptr && e0 + i < E) ? __ldg(d_prob + e0 + i) : 0.0f;
-    col[i] = 0.0f;
+    for (int i = 0; i < NV; ++i)
+      g[i] = (d_prob != nullptr && e0 + i < E) ? __ldg(d_prob + e0 + i) : 0.0f;
+  }
+  if constexpr (DBIAS) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) col[i] = 0.0f;
   }
   for (long long t = (long long)blockIdx.x * kSelWarps + warp; t < a.T;
        t += (long long)gridDim.x * kSelWarps) {
-    float l[NV], key[NV], sc[NV];
-    load_row<Tin, NV>(logits + t * a.ld, e0, E, vec, l);
-    // the choice is made: any exponential will do
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if constexpr (KIND == 0) {
-        const float v = __fadd_rn(l[i], b[i]);
-        key[i] = (v > -INFINITY) ? v : -INFINITY;
-      } else {
-        sc[i] = (l[i] > -INFINITY) ? __frcp_rn(__fadd_rn(1.0f, expf(-l[i]))) : 0.0f;
-      }
-    }
     const int ej = (lane < k) ? topk_idx[t * k + lane] : -1;
     const float dj = (lane < k) ? d_w[t * k + lane] : 0.0f;
     const bool valid = ej >= 0 && ej < E;
-    // the chosen experts' keys or scores, slot j in lane j
-    __syncwarp();
-    if constexpr (KIND == 0) store_row<EP>(s_row[warp], e0, key);
-    else store_row<EP>(s_row[warp], e0, sc);
-    __syncwarp();
-    const float picked = valid ? s_row[warp][ej] : (KIND == 0 ? -INFINITY : 0.0f);
-    __syncwarp();
-    float d[NV], add[NV];
-    if constexpr (KIND == 0) {
-      float m = -INFINITY;
+    float d[NV];
+    float picked = KIND == 0 ? -INFINITY : 0.0f;  // slot j's key or score, in lane j
+    float sc[DENSE ? NV : 1], m = -INFINITY;
+    if constexpr (DENSE) {
+      float l[NV];
+      load_row<Tin, NV>(logits + t * a.ld, e0, E, vec, l);
+      // the choice is made: any exponential will do
+      __syncwarp();
+      if constexpr (KIND == 0) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) m = fmaxf(m, key[i]);
-      m = warp_max(m);
-      float z = 0.0f;
+        for (int i = 0; i < NV; ++i) {
+          const float v = __fadd_rn(l[i], b[i]);
+          sc[i] = (v > -INFINITY) ? v : -INFINITY;
+          m = fmaxf(m, sc[i]);
+        }
+      } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        sc[i] = exp_rel(key[i], m);
-        z += sc[i];
+        for (int i = 0; i < NV; ++i) sc[i] = sigmoid(l[i]);
       }
-      z = warp_sum(z);
-      const float rz = z > 0.0f ? 1.0f / z : 0.0f;
-      float dot = 0.0f;
+      store_row<EP>(s_row[warp], e0, sc);
+      __syncwarp();
+      if (valid) picked = s_row[warp][ej];
+    } else if (valid) {
+      const float l = to_float(logits[t * a.ld + ej]);
+      if constexpr (KIND == 0) {
+        const float v = l + (a.bias != nullptr ? __ldg(a.bias + ej) : 0.0f);
+        picked = (v > -INFINITY) ? v : -INFINITY;
+      } else {
+        picked = sigmoid(l);
+      }
+    }
+    if constexpr (KIND == 0) {
+      float dot = 0.0f, rz = 0.0f;
+      if constexpr (DENSE) {
+        m = warp_max(m);
+        float z = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        sc[i] *= rz;
-        dot += g[i] * sc[i];
+        for (int i = 0; i < NV; ++i) {
+          sc[i] = exp_rel(sc[i], m);
+          z += sc[i];
+        }
+        z = warp_sum(z);
+        rz = z > 0.0f ? 1.0f / z : 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          sc[i] *= rz;
+          dot += g[i] * sc[i];
+        }
       }
       float cd;  // what the chosen logit gets beside the dense part
-      if (a.renorm) {
+      if (!DENSE || a.renorm) {
         const float e = exp_rel(picked, warp_max(picked));
         const float S = warp_sum(e);
         const float w = S > 0.0f ? e / S : 0.0f;
@@ -418,14 +482,19 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_bwd_kerne
         cd = dj * (exp_rel(picked, m) * rz);
         dot += cd;
       }
-      dot = warp_sum(dot);
-      spread<EP>(s_row[warp], e0, lane, valid ? ej : -1, cd, k, add);
+      spread<EP>(s_row[warp], e0, lane, valid ? ej : -1, cd, k, d);
+      if constexpr (DENSE) {
+        dot = warp_sum(dot);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) d[i] = sc[i] * (g[i] - dot) + add[i];
+        for (int i = 0; i < NV; ++i) d[i] += sc[i] * (g[i] - dot);
+      }
     } else {
-      float dense = 0.0f, rz = 0.0f;
-      const bool has = d_prob != nullptr;
-      if (has) {
+      float cd = dj;
+      if (a.renorm) {
+        const float S = warp_sum(picked);
+        cd = S > 0.0f ? __fdiv_rn(dj - __fdiv_rn(warp_sum(__fmul_rn(dj, picked)), S), S) : 0.0f;
+      }
+      if constexpr (DENSE) {
         float z = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -433,19 +502,15 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_bwd_kerne
           dot += g[i] * sc[i];
         }
         z = warp_sum(z);
-        rz = z > 0.0f ? 1.0f / z : 0.0f;
-        dense = warp_sum(dot) * rz;
-      }
-      float cd = dj;
-      if (a.renorm) {
-        const float S = warp_sum(picked);
-        cd = S > 0.0f ? __fdiv_rn(dj - __fdiv_rn(warp_sum(__fmul_rn(dj, picked)), S), S) : 0.0f;
-      }
-      spread<EP>(s_row[warp], e0, lane, valid ? ej : -1, cd, k, add);
+        const float rz = z > 0.0f ? 1.0f / z : 0.0f;
+        const float mean = warp_sum(dot) * rz;
+        spread<EP>(s_row[warp], e0, lane, valid ? ej : -1, cd, k, d);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const float D = has ? (g[i] - dense) * rz + add[i] : add[i];
-        d[i] = __fmul_rn(__fmul_rn(D, sc[i]), __fsub_rn(1.0f, sc[i]));
+        for (int i = 0; i < NV; ++i)
+          d[i] = ((g[i] - mean) * rz + d[i]) * sc[i] * (1.0f - sc[i]);
+      } else {
+        cd = __fmul_rn(__fmul_rn(cd, picked), __fsub_rn(1.0f, picked));
+        spread<EP>(s_row[warp], e0, lane, valid ? ej : -1, cd, k, d);
       }
     }
     Tin* row = d_logits + t * ldd;
@@ -510,16 +575,17 @@ template <typename Tin, int EP, int KIND>
 cudaError_t bwd_ep(const SelectArgs& a, const int32_t* idx, const float* d_w, const float* d_prob,
                    void* d_logits, long long ldd, float* d_bias, float* partial, cudaStream_t s) {
   const int nb = select_blocks(a.T);
-  Tin* d = static_cast<Tin*>(d_logits);
-  if (d_bias == nullptr) {
-    select_bwd_kernel<Tin, EP, KIND, false>
-        <<<nb, kSelThreads, 0, s>>>(a, idx, d_w, d_prob, d, ldd, nullptr);
+  const bool dense = d_prob != nullptr || (KIND == 0 && !a.renorm);
+  auto go = [&](auto kern) {
+    kern<<<nb, kSelThreads, 0, s>>>(a, idx, d_w, d_prob, static_cast<Tin*>(d_logits), ldd, partial);
     return cudaGetLastError();
-  }
+  };
+  if (d_bias == nullptr)
+    return dense ? go(select_bwd_kernel<Tin, EP, KIND, true, false>)
+                 : go(select_bwd_kernel<Tin, EP, KIND, false, false>);
   if constexpr (KIND == 0) {
-    select_bwd_kernel<Tin, EP, KIND, true>
-        <<<nb, kSelThreads, 0, s>>>(a, idx, d_w, d_prob, d, ldd, partial);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = dense ? go(select_bwd_kernel<Tin, EP, KIND, true, true>)
+                                : go(select_bwd_kernel<Tin, EP, KIND, false, true>);
     if (e != cudaSuccess) return e;
     column_sum_kernel<<<(a.E + 31) / 32, dim3(32, 32), 0, s>>>(partial, nb, a.E, d_bias);
     return cudaGetLastError();

@@ -21,27 +21,34 @@ __device__ __forceinline__ float key_float(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
 }
 
-// 1 / (1 + exp(-l)) with the exponential in Cody & Waite's reduction and a Taylor
+// 1 / (1 + exp(-l)) of two logits, the exponential in Cody & Waite's reduction and a Taylor
 // polynomial of degree 7, every step one IEEE FP32 operation: the bits of the router
-// kernels' sigmoid.  They scale by 2^n with ldexp; here 2^n is applied as two exact
-// powers of two (n in [-150, 129]), which differs only where exp(-l) is below 2^-126
-// and so vanishes in 1 + exp(-l).
-__device__ __forceinline__ float sigmoid_steps(float l) {
-  float x = fminf(fmaxf(-l, -104.0f), 89.0f);
-  const float n = rintf(__fmul_rn(x, 1.44269502162933349609375f));
-  float r = fmaf(-n, 0.693145751953125f, x);
-  r = fmaf(-n, 1.428606765330187e-06f, r);
-  float p = 1.0f / 5040.0f;
-  p = fmaf(p, r, 1.0f / 720.0f);
-  p = fmaf(p, r, 1.0f / 120.0f);
-  p = fmaf(p, r, 1.0f / 24.0f);
-  p = fmaf(p, r, 1.0f / 6.0f);
-  p = fmaf(p, r, 0.5f);
-  p = fmaf(p, r, 1.0f);
-  p = fmaf(p, r, 1.0f);
-  const int i = (int)n, h = i >> 1;
-  const float e = p * __int_as_float((h + 127) << 23) * __int_as_float((i - h + 127) << 23);
-  return __frcp_rn(__fadd_rn(1.0f, e));
+// kernels' sigmoid, two lanes to an instruction.  Their rint is here the sum with 1.5 * 2^23
+// (whose low bits are then the integer), their ldexp an addition to the exponent: with -l
+// held to [-80, 89] (below, exp(-l) vanishes in 1 + exp(-l)) the integer is in [-115, 128],
+// so half the result is a normal number, and the factor 2 joins the final sum exactly.
+__device__ __forceinline__ float2 sigmoid_steps2(float l0, float l1) {
+  const float2 x = make_float2(fminf(fmaxf(-l0, -80.0f), 89.0f), fminf(fmaxf(-l1, -80.0f), 89.0f));
+  auto both = [](float c) { return make_float2(c, c); };
+  const float2 t = __fmul2_rn(x, both(1.44269502162933349609375f));
+  const float2 m = __fadd2_rn(t, both(12582912.0f));
+  const float2 n = __fadd2_rn(m, both(-12582912.0f));
+  float2 r = __ffma2_rn(n, both(-0.693145751953125f), x);
+  r = __ffma2_rn(n, both(-1.428606765330187e-06f), r);
+  float2 p = both(1.0f / 5040.0f);
+  p = __ffma2_rn(p, r, both(1.0f / 720.0f));
+  p = __ffma2_rn(p, r, both(1.0f / 120.0f));
+  p = __ffma2_rn(p, r, both(1.0f / 24.0f));
+  p = __ffma2_rn(p, r, both(1.0f / 6.0f));
+  p = __ffma2_rn(p, r, both(0.5f));
+  p = __ffma2_rn(p, r, both(1.0f));
+  p = __ffma2_rn(p, r, both(1.0f));
+  auto half_exp = [](float p, float m) {  // p 2^(n - 1)
+    return __int_as_float(__float_as_int(p) + (int)((uint32_t)__float_as_int(m) << 23) - (1 << 23));
+  };
+  const float2 e = make_float2(half_exp(p.x, m.x), half_exp(p.y, m.y));
+  const float2 d = __ffma2_rn(e, both(2.0f), both(1.0f));
+  return make_float2(__frcp_rn(d.x), __frcp_rn(d.y));
 }
 
 __device__ __forceinline__ float to_float(float v) { return v; }
