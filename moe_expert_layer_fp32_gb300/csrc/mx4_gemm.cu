@@ -96,6 +96,10 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint3
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // 32 rows of 16 bytes in shared memory to four columns of tensor memory, in each of its
 // four lane quarters
 __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
@@ -266,6 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t rb = row_bytes(w), sb = sf_bytes(w);
         const uint8_t* rows = rimg + w.row_img + (size_t)rank * rb;
         const size_t row_step = (size_t)w.rows16 * 128;
+        // single form: the next unit's weights move into L2 while this one's are multiplied
+        const bool more = !PAIR && u + unit_step < total;
+        const MxUnit nx = more ? mx_unit<PAIR>(u + unit_step, tb, E, NT, KB, rank) : w;
         for (int kb = 0; kb < KB; ++kb, ++it) {
           const int s = it % C::STAGES;
           const uint32_t ph = (it / C::STAGES) & 1;
@@ -280,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           bulk_load(st + C::ROW_OFF, rows + kb * row_step, rb, &full[s]);
           bulk_load(st + C::SF_OFF, simg + w.sf_img + (size_t)kb * kMx4SfSlot, sb, &full[s]);
+          if (more) prefetch_l2(wimg + nx.w_img + (size_t)kb * kMx4WBytes, kMx4WBytes);
         }
       }
       if (aborted) {

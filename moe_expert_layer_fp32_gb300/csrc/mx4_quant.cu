@@ -126,26 +126,56 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const Tin* __restri
 // SRC 0: rows of x.  SRC 1: row r of the operand is row row_of[r] / k of x (the gather of
 // the dispatch).  SRC 2: x holds [R, 2K] (gate | up), the operand is silu(gate) * up.
 //
-// A warp takes the rows rr, rr + 32, rr + 64, rr + 96 of a tile's 128-row half: four loads
-// in flight a lane, and the four rows' scales of a half k-block are one 16-byte store.
-// `span`: k-blocks a warp takes (all of them, or one where the rows alone are few).
+// The piece of `col` (of K) of a source row, SwiGLU applied; zeros past K or where !in.
+template <typename Tin, int SRC, typename P>
+__device__ __forceinline__ void load_piece(P& p, const Tin* row, int col, int K, bool in) {
+  if (!in) {
+    p.zero();
+  } else if constexpr (SRC == 2) {
+    float up[8];
+    load_floats<Tin, 8>(row + col, p.v);
+    load_floats<Tin, 8>(row + K + col, up);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p.v[j] = __fmul_rn(silu_f32(p.v[j]), up[j]);
+  } else {
+    p.load(row + col);
+  }
+}
+
+// First element of the source row of operand row r.
 template <typename Tin, int SRC>
-__global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(
+__device__ __forceinline__ const Tin* source_row(const Tin* x, const int32_t* row_of, int k, int T,
+                                                 int K, int r, int32_t* status) {
+  long long src = r;
+  if constexpr (SRC == 1) {
+    const int slot = row_of[r];
+    src = slot >= 0 ? slot / k : T;
+    if (src >= T) {
+      flag_error(status, MOE_ERR_DEVICE_CHECK);
+      src = 0;
+    }
+  }
+  return x + (size_t)src * (SRC == 2 ? 2 * (size_t)K : (size_t)K);
+}
+
+// MANY rows: a warp takes the rows rr, rr + 32, rr + 64, rr + 96 of a tile's 128-row half
+// over all of K: four loads in flight a lane, and the four rows' scales of a half k-block
+// are one 16-byte store.
+constexpr int kRowsBlocksPerSm = 4;
+template <typename Tin, int SRC>
+__global__ void __launch_bounds__(kQThreads, kRowsBlocksPerSm) quantize_rows_kernel(
     const Tin* __restrict__ x, const int32_t* __restrict__ row_of, int k, int T,
-    const int32_t* __restrict__ offsets, int E, int R, int K, int span, uint8_t* __restrict__ codes,
+    const int32_t* __restrict__ offsets, int E, int R, int K, uint8_t* __restrict__ codes,
     uint8_t* __restrict__ sf, int32_t* status) {
   __shared__ Mx4Tables tb;
   pdl_launch_dependents();  // the product reads this kernel's images only after its own wait
   if (!mx4_build_tables(tb, offsets, E, R, status)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int KB = mx4_kblocks(K);
-  const int spans = (KB + span - 1) / span;
   const long long items = (long long)tb.tile[E] * 64;  // (tile, half, rr)
-  for (long long it = (long long)blockIdx.x * kQWarps + warp; it < items * spans;
+  for (long long it = (long long)blockIdx.x * kQWarps + warp; it < items;
        it += (long long)gridDim.x * kQWarps) {
-    const long long row_item = spans == 1 ? it : it / spans;
-    const int kb0 = (int)(it - row_item * spans) * span, kb1 = min(KB, kb0 + span);
-    const int tile = (int)(row_item >> 6), half = (int)(row_item >> 5) & 1, rr = (int)row_item & 31;
+    const int tile = (int)(it >> 6), half = (int)(it >> 5) & 1, rr = (int)it & 31;
     const int e = mx4_find(tb.tile, E, tile);
     const int m = tb.off[e + 1] - tb.off[e];
     const Mx4Cut cut = mx4_cut(m);
@@ -162,43 +192,20 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(
     uint8_t* sdst = sf + (size_t)tile * KB * kMx4SfSlot + half * 1024 + rr * 16 + (lane >> 4) * 512;
     const Tin* src[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      long long r = row0 + (i < nr ? i * 32 : 0);
-      if constexpr (SRC == 1) {
-        const int slot = row_of[r];
-        r = slot >= 0 ? slot / k : T;
-        if (r >= T) {
-          if (lane == 0) flag_error(status, MOE_ERR_DEVICE_CHECK);
-          r = 0;
-        }
-      }
-      src[i] = x + (size_t)r * (SRC == 2 ? 2 * (size_t)K : (size_t)K) + lane * 8;
-    }
-    for (int kb = kb0; kb < kb1; ++kb) {
-      const int col = kb * kMx4KB;
-      const bool in = col + lane * 8 < K;  // K is a multiple of 128: whole half-warps
-      using P = Piece<std::conditional_t<SRC == 2, float, Tin>>;
+    for (int i = 0; i < 4; ++i)
+      src[i] = source_row<Tin, SRC>(x, row_of, k, T, K, row0 + (i < nr ? i * 32 : 0), status);
+    using P = Piece<std::conditional_t<SRC == 2, float, Tin>>;
+    // (K is a multiple of 128: whole half-warps lie inside)
+    auto load = [&](P (&v)[4], int kb) {
+      const int col = kb * kMx4KB + lane * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        load_piece<Tin, SRC>(v[i], src[i], col, K, col < K && i < nr);
+    };
+    for (int kb = 0; kb < KB; ++kb) {
+      const bool in = kb * kMx4KB + lane * 8 < K;
       P v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (in && i < nr) {
-          if constexpr (SRC == 2) load_floats<Tin, 8>(src[i] + col, v[i].v);
-          else v[i].load(src[i] + col);
-        } else {
-          v[i].zero();
-        }
-      }
-      if constexpr (SRC == 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (in && i < nr) {
-            float up[8];
-            load_floats<Tin, 8>(src[i] + K + col, up);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i].v[j] = __fmul_rn(silu_f32(v[i].v[j]), up[j]);
-          }
-        }
-      }
+      load(v, kb);
       uint32_t byte[4];
       uint8_t* ck = cdst + (size_t)kb * rows16 * 128;
 #pragma unroll
@@ -221,6 +228,45 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(
       }
     }
   }
+}
+
+// FEW rows: a warp per (row, k-block).
+template <typename Tin, int SRC>
+__global__ void __launch_bounds__(kQThreads) quantize_few_rows_kernel(
+    const Tin* __restrict__ x, const int32_t* __restrict__ row_of, int k, int T,
+    const int32_t* __restrict__ offsets, int E, int R, int K, uint8_t* __restrict__ codes,
+    uint8_t* __restrict__ sf, int32_t* status) {
+  __shared__ Mx4Tables tb;
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int KB = mx4_kblocks(K);
+  const int it = blockIdx.x * kQWarps + warp;  // < 2^31: R is small
+  const int r = it / KB, kb = it - r * KB;
+  const int col = kb * kMx4KB + lane * 8;
+  const bool in = r < R && col < K;
+  using P = Piece<std::conditional_t<SRC == 2, float, Tin>>;
+  P v;
+  const Tin* row = r < R ? source_row<Tin, SRC>(x, row_of, k, T, K, r, status) : x;
+  load_piece<Tin, SRC>(v, row, col, K, in);
+  if (!mx4_build_tables(tb, offsets, E, R, status) || r >= R) return;
+  const int e = mx4_find(tb.off, E, r);
+  const int m = tb.off[e + 1] - tb.off[e], local = r - tb.off[e];
+  const Mx4Cut cut = mx4_cut(m);
+  const int ti = local / cut.step, rt = local - ti * cut.step;
+  const int rows16 = min(cut.step, (m - ti * cut.step + 15) / 16 * 16);
+  uint32_t byte;
+  const uint32_t c = quantize8(v, byte);
+  const uint32_t w = byte | (__shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8) |
+                     (__shfl_down_sync(0xFFFFFFFFu, byte, 8) << 16) |
+                     (__shfl_down_sync(0xFFFFFFFFu, byte, 12) << 24);
+  if (!in) return;
+  uint8_t* cdst = codes + ((size_t)tb.pad[e] * 16 + (size_t)ti * cut.step) * KB * 128 +
+                  (size_t)kb * rows16 * 128 + rt * 128;
+  *reinterpret_cast<uint32_t*>(cdst + (((lane >> 2) ^ (rt & 7)) * 16) + (lane & 3) * 4) = c;
+  if ((lane & 15) == 0)
+    *reinterpret_cast<uint32_t*>(sf + ((size_t)(tb.tile[e] + ti) * KB + kb) * kMx4SfSlot +
+                                 (rt >> 7) * 1024 + (lane >> 4) * 512 + (rt & 31) * 16 +
+                                 ((rt >> 5) & 3) * 4) = w;
 }
 
 // ---------------------------------------------------------- weight images ---
@@ -325,25 +371,29 @@ cudaError_t launch_mx4_rows(const void* x, int dtype, int src, const int32_t* ro
                             const int32_t* offsets, int E, int R, int K, void* codes, void* sf,
                             int32_t* status, cudaStream_t s) {
   if (R == 0) return cudaSuccess;
-  const long long most = (long long)device_sm_count() * 6;
-  const int KB = mx4_kblocks(K);
   // a warp per k-block while whole rows would not give every SM 16 warps
-  const int span = (long long)R < 16LL * 4 * device_sm_count() ? 1 : KB;
-  const long long need = mx4_max_tiles(R, E) * 64 / kQWarps * ((KB + span - 1) / span);
+  const bool few = (long long)R < 16LL * 4 * device_sm_count();
+  const long long warps = few ? (long long)R * mx4_kblocks(K) : mx4_max_tiles(R, E) * 64;
+  const long long need = (warps + kQWarps - 1) / kQWarps;
+  const long long most = few ? need : (long long)device_sm_count() * kRowsBlocksPerSm;
   const int grid = (int)(need < most ? need : most);
   uint8_t* c = static_cast<uint8_t*>(codes);
   uint8_t* f = static_cast<uint8_t*>(sf);
-  auto go = [&](auto kern, auto* p) {
-    kern<<<grid, kQThreads, 0, s>>>(p, row_of, k, T, offsets, E, R, K, span, c, f, status);
+  auto go = [&](auto many, auto few_rows, auto* p) {
+    if (few)
+      few_rows<<<grid, kQThreads, 0, s>>>(p, row_of, k, T, offsets, E, R, K, c, f, status);
+    else
+      many<<<grid, kQThreads, 0, s>>>(p, row_of, k, T, offsets, E, R, K, c, f, status);
     return cudaGetLastError();
   };
-  const auto* xb = static_cast<const __nv_bfloat16*>(x);
-  if (src == 1) return go(quantize_rows_kernel<__nv_bfloat16, 1>, xb);
-  if (src == 2) return go(quantize_rows_kernel<__nv_bfloat16, 2>, xb);
-  if (dtype == MOE_DTYPE_F32)
-    return go(quantize_rows_kernel<float, 0>, static_cast<const float*>(x));
-  if (dtype == MOE_DTYPE_BF16) return go(quantize_rows_kernel<__nv_bfloat16, 0>, xb);
-  return go(quantize_rows_kernel<__half, 0>, static_cast<const __half*>(x));
+#define MOE_MX4_ROWS(Tin, SRC) \
+  go(quantize_rows_kernel<Tin, SRC>, quantize_few_rows_kernel<Tin, SRC>, static_cast<const Tin*>(x))
+  if (src == 1) return MOE_MX4_ROWS(__nv_bfloat16, 1);
+  if (src == 2) return MOE_MX4_ROWS(__nv_bfloat16, 2);
+  if (dtype == MOE_DTYPE_F32) return MOE_MX4_ROWS(float, 0);
+  if (dtype == MOE_DTYPE_BF16) return MOE_MX4_ROWS(__nv_bfloat16, 0);
+  return MOE_MX4_ROWS(__half, 0);
+#undef MOE_MX4_ROWS
 }
 
 cudaError_t launch_mx4_pack(const void* codes, const void* scales, int E, int K, int N,

@@ -219,13 +219,15 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
         g1 = fmaxf(g1, o1);
       }
       const float gs = (a.group_top == 2 && g2 > -INFINITY) ? __fadd_rn(g1, g2) : g1;
-      int better = 0;
-      for (int h = 0; h < a.n_group; ++h) {
-        const float o = __shfl_sync(kFull, gs, h << a.lane_shift);
-        better += (o > gs || (o == gs && h < g)) ? 1 : 0;
+      // the largest score's first lane (so its lowest group) topk_group times
+      uint32_t gk = (g < a.n_group) ? float_key(gs) : 0u;
+      keep = 0u;
+      for (int j = 0; j < a.topk_group; ++j) {
+        const uint32_t m = __reduce_max_sync(kFull, gk);
+        const uint32_t who = __ballot_sync(kFull, gk == m);
+        keep |= who & (0u - who);  // bit g << lane_shift: group g stays
+        if ((keep >> (lane & ~((1 << a.lane_shift) - 1))) & 1u) gk = 0u;
       }
-      // bit g << lane_shift of the ballot: group g stays
-      keep = __ballot_sync(kFull, sub == 0 && g < a.n_group && better < a.topk_group);
     }
     // selection keys: 0 = cannot be chosen, masked below every number
     uint32_t u[NV];
@@ -246,11 +248,13 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
     uint32_t top = 0u;
 #pragma unroll
     for (int i = 0; i < NV; ++i) top = max(top, u[i]);
-    uint32_t bound = 0u;
-    for (int j = 0; j < k; ++j) {
+    uint32_t bound;
+    for (int left = k;;) {
       bound = __reduce_max_sync(kFull, top);
-      const int owner = __ffs(__ballot_sync(kFull, top == bound)) - 1;
-      if (lane == owner) top = 0u;
+      const bool hit = top == bound;
+      left -= __popc(__ballot_sync(kFull, hit));
+      if (left <= 0 || bound == 0u) break;
+      top = hit ? 0u : top;
     }
     bound = max(bound, 1u);
     int mine = 0;
@@ -271,13 +275,13 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
     if (n <= 32) {
       // one candidate a lane, ranked against the others
       s_key[warp][lane] = 0u;
+      if constexpr (KIND == 1) store_row<EP>(s_row[warp], e0, sc);
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (u[i] >= bound) {
           s_key[warp][before] = u[i];
           s_expert[warp][before] = e0 + i;
-          if constexpr (KIND == 1) s_row[warp][before] = sc[i];
           ++before;
         }
       }
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
       const uint32_t cu = s_key[warp][lane];
       if (lane < n) {
         ce = s_expert[warp][lane];
-        if constexpr (KIND == 1) cs = s_row[warp][lane];
+        if constexpr (KIND == 1) cs = s_row[warp][ce];
         ck = key_float(cu);
         slot = 0;
       }
