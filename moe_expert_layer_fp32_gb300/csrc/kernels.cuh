@@ -170,6 +170,7 @@ cudaError_t launch_mx4_quantize(const void* x, int dtype, long long ld, long lon
                                 void* codes, void* scales, void* values, cudaStream_t s);
 // An expert operand's row images.  src 0: x [R, K]; 1: row r is row row_of[r] / k of x [T, K]
 // bf16; 2: silu(gate) * up of x [R, 2K] bf16.
+constexpr int kMx4FewRows = 152 * 16 * 4;  // 16 warps of four rows on every SM
 cudaError_t launch_mx4_rows(const void* x, int dtype, int src, const int32_t* row_of, int k, int T,
                             const int32_t* offsets, int E, int R, int K, void* codes, void* sf,
                             int32_t* status, cudaStream_t s);
@@ -181,6 +182,14 @@ cudaError_t launch_mx4_prepack(const void* w, int E, int K, int N, int col0, int
 cudaError_t launch_mx4_gemm(const void* packed, const void* codes, const void* sf,
                             const int32_t* offsets, int E, int R, int K, int N, void* y,
                             int y_dtype, int32_t* status, long long spin_limit, cudaStream_t s);
+
+// Both steps in one kernel, K <= kMx4FusedMaxK (mx4_fused.cu).  src as launch_mx4_rows; src 1
+// writes bf16 and src 2 FP32 rows.
+constexpr int kMx4FusedMaxK = 2048;
+cudaError_t launch_mx4_fused(const void* x, int dtype, int src, const int32_t* row_of, int k, int T,
+                             const void* packed, const int32_t* offsets, int E, int R, int K, int N,
+                             void* y, int y_dtype, int32_t* status, long long spin_limit,
+                             cudaStream_t s);
 
 // The limit of the GEMM kernels' bounded waits now in force (moe_set_wait_limit).
 long long wait_limit();

@@ -13,10 +13,10 @@
 // them).
 //   weights  per (expert, 128 output columns, k-block): 16384 bytes of codes, then 1024 of
 //            scales (two halves of the k-block)
-//   rows     the rows of an expert in tiles of at most kMx4TileRows, evenly cut; an expert's
-//            rows are padded to 16, a tile's k-blocks follow one another (tile rows x 128
-//            bytes each); the scales of tile i and k-block b at slot (i * KB + b) of 2048
-//            bytes, [128-row half][half of the k-block][512]
+//   rows     the rows of an expert in tiles of at most kMx4TileRows, evenly cut to a multiple
+//            of 16; a tile has a slot of kMx4TileRows rows: its k-blocks follow one another
+//            (the tile's own padded rows x 128 bytes each).  The scales of a tile's k-block b
+//            are at slot (tile * KB + b) of 2048 bytes, [128-row half][half k-block][512]
 // Padding rows are never written; they only reach accumulator columns that are not stored.
 #pragma once
 
@@ -39,40 +39,42 @@ __host__ __device__ inline int mx4_kblocks(int K) { return (K + kMx4KB - 1) / kM
 struct Mx4Cut {
   int n, step;
 };
-__host__ __device__ inline Mx4Cut mx4_cut(int m) {
+__host__ __device__ inline Mx4Cut mx4_cut(int m, int tile_rows = kMx4TileRows) {
   Mx4Cut c;
-  c.n = (m + kMx4TileRows - 1) / kMx4TileRows;
+  c.n = (m + tile_rows - 1) / tile_rows;
   c.step = c.n > 0 ? ((m + c.n - 1) / c.n + 15) / 16 * 16 : 16;
   return c;
 }
 
-// Bounds over every split of R rows among E experts.
-inline long long mx4_max_padded_rows(long long R, int E) {
+// Tiles of R rows among E experts, at most.
+inline long long mx4_max_tiles(long long R, int E, int tile_rows = kMx4TileRows) {
   const long long with = R < E ? R : E;  // experts that can have rows
-  return R + 15 * with;
+  return R / tile_rows + with;
 }
-inline long long mx4_max_tiles(long long R, int E) {
-  const long long with = R < E ? R : E;
-  return R / kMx4TileRows + with;
+
+// Bytes of a tile's slot of codes, and of its scales.
+__host__ __device__ inline size_t mx4_slot(int K) {
+  return (size_t)mx4_kblocks(K) * kMx4TileRows * 128;
 }
+__host__ __device__ inline size_t mx4_sf_slots(int K) { return (size_t)mx4_kblocks(K) * kMx4SfSlot; }
 
 // Prefix tables of a grouped operand in shared memory, from offsets [E+1]; every thread of
 // the block calls it (blockDim a multiple of 32, at least 32).  Returns false (and flags) if
 // the offsets are not 0 = o_0 <= ... <= o_E = R.
 struct Mx4Tables {
   int off[kMaxE + 1];    // first row of each expert
-  int pad[kMaxE + 1];    // its first padded row, in units of 16
   int tile[kMaxE + 1];   // its first row tile
   int ok;
 };
 
 __device__ __forceinline__ bool mx4_build_tables(Mx4Tables& s, const int32_t* __restrict__ offsets,
-                                                 int E, int R, int32_t* status) {
+                                                 int E, int R, int32_t* status,
+                                                 int tile_rows = kMx4TileRows) {
   for (int e = threadIdx.x; e <= E; e += blockDim.x) s.off[e] = offsets[e];
   __syncthreads();
   if (threadIdx.x < 32) {  // one warp scans, 32 experts a step
     const int lane = threadIdx.x;
-    int pad = 0, tile = 0;
+    int tile = 0;
     bool ok = s.off[0] == 0 && s.off[E] == R;
     for (int b = 0; b < E; b += 32) {
       const int e = b + lane;
@@ -82,26 +84,18 @@ __device__ __forceinline__ bool mx4_build_tables(Mx4Tables& s, const int32_t* __
         if (lo < 0 || hi < lo || hi > R) ok = false;
         else m = hi - lo;
       }
-      int p = (m + 15) / 16, n = mx4_cut(m).n;
-      const int p0 = p, n0 = n;
+      int n = mx4_cut(m, tile_rows).n;
+      const int n0 = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int pu = __shfl_up_sync(0xFFFFFFFFu, p, o), nu = __shfl_up_sync(0xFFFFFFFFu, n, o);
-        if (lane >= o) {
-          p += pu;
-          n += nu;
-        }
+        const int nu = __shfl_up_sync(0xFFFFFFFFu, n, o);
+        if (lane >= o) n += nu;
       }
-      if (e < E) {
-        s.pad[e] = pad + p - p0;
-        s.tile[e] = tile + n - n0;
-      }
-      pad += __shfl_sync(0xFFFFFFFFu, p, 31);
+      if (e < E) s.tile[e] = tile + n - n0;
       tile += __shfl_sync(0xFFFFFFFFu, n, 31);
     }
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (lane == 0) {
-      s.pad[E] = pad;
       s.tile[E] = tile;
       s.ok = ok;
       if (!ok) flag_error(status, MOE_ERR_DEVICE_CHECK);

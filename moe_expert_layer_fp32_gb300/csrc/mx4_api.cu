@@ -73,35 +73,48 @@ moe_status check_mx4(int E, int K, int N) {
   return MOE_OK;
 }
 
-// Row images of an operand of R rows over K among E experts.
-size_t rows_bytes(long long R, int K, int E) {
-  return up((size_t)mx4_max_padded_rows(R, E) * mx4_kblocks(K) * 128);
-}
-size_t scales_bytes(long long R, int K, int E) {
-  return up((size_t)mx4_max_tiles(R, E) * mx4_kblocks(K) * kMx4SfSlot);
-}
+// Row images of an operand of R rows over K among E experts: codes, then scales.
+size_t rows_bytes(long long R, int K, int E) { return up(mx4_max_tiles(R, E) * mx4_slot(K)); }
+size_t scales_bytes(long long R, int K, int E) { return up(mx4_max_tiles(R, E) * mx4_sf_slots(K)); }
+
+// Whether the product of R rows quantises them in its own kernel (no images).
+bool fused(int R, int K) { return K <= kMx4FusedMaxK && R < kMx4FewRows; }
 
 struct ProductLayout {
-  size_t status, rows, sf, total;
+  size_t status, images, total;
 };
-ProductLayout product_layout(long long R, int K, int E) {
+ProductLayout product_layout(int R, int K, int E) {
   ProductLayout L;
   size_t o = 0;
   L.status = o;  o += up(kAlign);
-  L.rows = o;    o += rows_bytes(R, K, E);
-  L.sf = o;      o += scales_bytes(R, K, E);
+  L.images = o;  o += fused(R, K) ? 0 : rows_bytes(R, K, E) + scales_bytes(R, K, E);
   L.total = o;
   return L;
 }
 
+// The grouped product of quantised rows (sources as launch_mx4_rows), in one kernel or two.
+moe_status do_product(const void* x, int x_dtype, int src, const int32_t* row_of, int k, int T,
+                      const int32_t* offsets, const void* packed, int E, int R, int K, int N,
+                      void* y, int y_dtype, void* images, int32_t* status, cudaStream_t s) {
+  const long long lim = wait_limit();
+  if (fused(R, K)) {
+    MOE_CUDA(launch_mx4_fused(x, x_dtype, src, row_of, k, T, packed, offsets, E, R, K, N, y, y_dtype,
+                              status, lim, s));
+    return MOE_OK;
+  }
+  void* sf = at<void>(images, rows_bytes(R, K, E));
+  MOE_CUDA(launch_mx4_rows(x, x_dtype, src, row_of, k, T, offsets, E, R, K, images, sf, status, s));
+  MOE_CUDA(launch_mx4_gemm(packed, images, sf, offsets, E, R, K, N, y, y_dtype, status, lim, s));
+  return MOE_OK;
+}
+
 struct LayerLayout {
   size_t status, logits, idx, w, counts, offsets, blk_counts, blk_base, row_of_slot, slot_of_row,
-      rows, sf, gate_up, y, total;
+      images, gate_up, y, total;
 };
 LayerLayout layer_layout(const moe_dims& d) {
   const size_t T = (size_t)d.T, R = T * d.k, E = (size_t)d.E;
   const size_t nb = (T + kPermBlock - 1) / kPermBlock;
-  const int Kmax = d.H > d.I ? d.H : d.I;
   LayerLayout L;
   size_t o = 0;
   L.status = o;       o += up(kAlign);
@@ -114,8 +127,9 @@ LayerLayout layer_layout(const moe_dims& d) {
   L.blk_base = o;     o += up(nb * E * 4);
   L.row_of_slot = o;  o += up(R * 4);
   L.slot_of_row = o;  o += up(R * 4);
-  L.rows = o;         o += rows_bytes((long long)R, Kmax, d.E);
-  L.sf = o;           o += scales_bytes((long long)R, Kmax, d.E);
+  const size_t up_img = product_layout((int)R, d.H, d.E).total;
+  const size_t down_img = product_layout((int)R, d.I, d.E).total;
+  L.images = o;       o += up_img > down_img ? up_img : down_img;
   L.gate_up = o;      o += up(R * 2 * (size_t)d.I * 2);
   L.y = o;            o += up(R * (size_t)d.H * 4);
   L.total = o;
@@ -270,14 +284,9 @@ moe_status moe_mx4_expert_product(const void* x, int32_t x_dtype, const int32_t*
   MOE_TRY(validate_ptr(packed));
   MOE_TRY(validate_ptr(y));
   MOE_TRY(validate_device());
-  cudaStream_t s = as_stream(stream);
-  int32_t* status = at<int32_t>(workspace, L.status);
-  void* rows = at<void>(workspace, L.rows);
-  void* sf = at<void>(workspace, L.sf);
-  MOE_CUDA(launch_mx4_rows(x, x_dtype, 0, nullptr, 1, R, offsets, E, R, K, rows, sf, status, s));
-  MOE_CUDA(launch_mx4_gemm(packed, rows, sf, offsets, E, R, K, N, y, y_dtype, status, wait_limit(),
-                           s));
-  return MOE_OK;
+  return do_product(x, x_dtype, 0, nullptr, 1, R, offsets, packed, E, R, K, N, y, y_dtype,
+                    at<void>(workspace, L.images), at<int32_t>(workspace, L.status),
+                    as_stream(stream));
 }
 
 size_t moe_mx4_layer_workspace_bytes(moe_dims d) {
@@ -319,8 +328,7 @@ moe_status moe_mx4_layer_fwd(const void* x, const float* w_router, const float* 
   int32_t* blk_base = at<int32_t>(workspace, L.blk_base);
   int32_t* ros = at<int32_t>(workspace, L.row_of_slot);
   int32_t* sor = at<int32_t>(workspace, L.slot_of_row);
-  void* rows = at<void>(workspace, L.rows);
-  void* sf = at<void>(workspace, L.sf);
+  void* images = at<void>(workspace, L.images);
   void* gu = at<void>(workspace, L.gate_up);
   float* y = at<float>(workspace, L.y);
   if (T > 0) {
@@ -332,14 +340,10 @@ moe_status moe_mx4_layer_fwd(const void* x, const float* w_router, const float* 
   MOE_CUDA(launch_scan(blk_counts, nb, d.E, R, counts, offsets, false, blk_base, status, s));
   if (T == 0) return MOE_OK;
   MOE_CUDA(launch_rank(idx, T, d.k, d.E, blk_base, ros, sor, status, s));
-  MOE_CUDA(launch_mx4_rows(x, MOE_DTYPE_BF16, 1, sor, d.k, T, offsets, d.E, R, d.H, rows, sf,
-                           status, s));
-  MOE_CUDA(launch_mx4_gemm(packed_gate_up, rows, sf, offsets, d.E, R, d.H, 2 * d.I, gu,
-                           MOE_DTYPE_BF16, status, wait_limit(), s));
-  MOE_CUDA(launch_mx4_rows(gu, MOE_DTYPE_BF16, 2, nullptr, 1, R, offsets, d.E, R, d.I, rows, sf,
-                           status, s));
-  MOE_CUDA(launch_mx4_gemm(packed_down, rows, sf, offsets, d.E, R, d.I, d.H, y, MOE_DTYPE_F32,
-                           status, wait_limit(), s));
+  MOE_TRY(do_product(x, MOE_DTYPE_BF16, 1, sor, d.k, T, offsets, packed_gate_up, d.E, R, d.H,
+                     2 * d.I, gu, MOE_DTYPE_BF16, images, status, s));
+  MOE_TRY(do_product(gu, MOE_DTYPE_BF16, 2, nullptr, 1, R, offsets, packed_down, d.E, R, d.I, d.H,
+                     y, MOE_DTYPE_F32, images, status, s));
   MOE_CUDA(launch_combine(y, w, ros, T, d.H, d.k, route_scale, out, s));
   return MOE_OK;
 }

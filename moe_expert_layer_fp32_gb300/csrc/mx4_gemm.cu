@@ -23,6 +23,7 @@
 #include "common.cuh"
 #include "kernels.cuh"
 #include "mx4.cuh"
+#include "mx4_mma.cuh"
 #include "pdl.cuh"
 
 namespace moe {
@@ -49,114 +50,6 @@ struct MxCfg {
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
 };
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, P;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
-// mbar_wait_bounded with cluster-scope acquire: the even CTA's full barriers also count the
-// odd CTA's arrivals.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-template <bool PAIR>
-__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          int32_t* status, long long limit) {
-  if constexpr (!PAIR) return mbar_wait_bounded(bar, parity, abort, status, limit);
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if (*abort) return false;
-    if (clock64() - t0 > limit) {
-      *abort = 1;
-      flag_error(status, MOE_ERR_TIMEOUT);
-      return false;
-    }
-  }
-}
-
-__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(smem_u32(smem_dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-
-// 32 rows of 16 bytes in shared memory to four columns of tensor memory, in each of its
-// four lane quarters
-__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)1u << 16;
-  d |= (uint64_t)(128u >> 4) << 32;  // next 8 rows
-  d |= (uint64_t)1u << 46;
-  return d;
-}
-// (PAIR: each CTA's own shared memory to its own tensor memory)
-template <bool PAIR>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
-  if constexpr (PAIR)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-                 : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-                 : "memory");
-}
-
-// Instruction descriptor, kind::mxf4: E2M1 A and B (K-major), E8M0 scales, M output columns
-// (128, or 256 over a pair), N rows; `id`: which two of a scale word's four bytes an MMA of
-// K = 64 reads (0 or 2).
-__device__ __forceinline__ uint32_t idesc_mx4(int M, int N, uint32_t id) {
-  return (id << 4)                       // B scale bytes
-         | (1u << 7) | (1u << 10)        // A, B: E2M1
-         | ((uint32_t)(N >> 3) << 17)    // N / 8
-         | (1u << 23)                    // scales: E8M0
-         | ((uint32_t)(M >> 4) << 24)    // M / 16
-         | (id << 29);                   // A scale bytes
-}
-template <bool PAIR>
-__device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                        uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                        uint32_t accumulate) {
-  if constexpr (PAIR)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
-  else
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
-      "p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
 // One unit: a row tile of an expert times one weight tile (PAIR: two, one a CTA).
 struct MxUnit {
   int row0;              // first output row
@@ -172,19 +65,20 @@ template <bool PAIR>
 __device__ __forceinline__ MxUnit mx_unit(long long u, const Mx4Tables& tb, int E, int NT, int KB,
                                           int rank) {
   const int nu = PAIR ? (NT + 1) / 2 : NT;  // units of a row tile
-  const int tile = (int)(u / nu);
+  const int done = (int)(u / nu);
+  const int tile = tb.tile[E] - 1 - done;  // the last ones are still in L2
   const int e = mx4_find(tb.tile, E, tile);
   const int m = tb.off[e + 1] - tb.off[e];
   const Mx4Cut cut = mx4_cut(m);
   const int ti = tile - tb.tile[e];
   MxUnit w;
-  w.nt = (int)(u - (long long)tile * nu);
+  w.nt = (int)(u - (long long)done * nu);
   if (PAIR) w.nt = 2 * w.nt + rank;
   w.row0 = tb.off[e] + ti * cut.step;
   w.rows = min(cut.step, m - ti * cut.step);
   w.rows16 = (w.rows + 15) / 16 * 16;
   w.w_img = ((size_t)e * NT + min(w.nt, NT - 1)) * KB * kMx4WBytes;
-  w.row_img = ((size_t)tb.pad[e] * 16 + (size_t)ti * cut.step) * KB * 128;
+  w.row_img = (size_t)tile * KB * kMx4TileRows * 128;
   w.sf_img = (size_t)tile * KB * kMx4SfSlot;
   return w;
 }
@@ -487,8 +381,9 @@ cudaError_t launch_mx4_gemm(const void* packed, const void* codes, const void* s
   const uint8_t* f = static_cast<const uint8_t*>(sf);
   auto run = [&](auto kind) {
     using T = decltype(kind);
-    return use_pair(E, R, N) ? go<T, true>(w, r, f, offsets, E, R, K, N, y, status, spin_limit, s)
-                             : go<T, false>(w, r, f, offsets, E, R, K, N, y, status, spin_limit, s);
+    return use_pair(E, R, N)
+               ? go<T, true>(w, r, f, offsets, E, R, K, N, y, status, spin_limit, s)
+               : go<T, false>(w, r, f, offsets, E, R, K, N, y, status, spin_limit, s);
   };
   return y_dtype == MOE_DTYPE_F32 ? run(float{}) : run(__nv_bfloat16{});
 }

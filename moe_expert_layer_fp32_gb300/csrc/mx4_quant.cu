@@ -13,6 +13,7 @@
 #include "common.cuh"
 #include "kernels.cuh"
 #include "mx4.cuh"
+#include "mx4_rows.cuh"
 #include "pdl.cuh"
 #include "select_math.cuh"
 
@@ -21,65 +22,6 @@ namespace {
 
 constexpr int kQThreads = 256;
 constexpr int kQWarps = kQThreads / 32;
-
-// Eight consecutive values as they were loaded, and the FP32 bits (sign cleared) of a
-// magnitude that has the largest one's exponent, over the four lanes of a block.
-template <typename Tin>
-struct Piece {
-  float v[8];
-  __device__ __forceinline__ void load(const Tin* p) { load_floats<Tin, 8>(p, v); }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  }
-  __device__ __forceinline__ uint32_t block_max() const {
-    uint32_t a = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
-    return max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
-  }
-  __device__ __forceinline__ void scaled(float inv, float (&q)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
-  }
-};
-
-// bf16: magnitudes order as 16-bit integers, two to an instruction (the widened form costs
-// twice the integer instructions, which bound the row images' kernel)
-template <>
-struct Piece<__nv_bfloat16> {
-  uint4 r;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    r = *reinterpret_cast<const uint4*>(p);
-  }
-  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ uint32_t block_max() const {
-    constexpr uint32_t M = 0x7FFF7FFFu;
-    uint32_t a = __vmaxu2(__vmaxu2(r.x & M, r.y & M), __vmaxu2(r.z & M, r.w & M));
-    a = __vmaxu2(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
-    a = __vmaxu2(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
-    return max(a << 16, a & 0xFFFF0000u);
-  }
-  __device__ __forceinline__ void scaled(float inv, float (&q)[8]) const {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      q[2 * i] = bf16_lo(w[i]) * inv;
-      q[2 * i + 1] = bf16_hi(w[i]) * inv;
-    }
-  }
-};
-
-// The lane's piece to codes; `byte`: the block's scale (the same in its four lanes).
-template <typename Tin>
-__device__ __forceinline__ uint32_t quantize8(const Piece<Tin>& p, uint32_t& byte) {
-  byte = mx4_scale_byte(p.block_max());
-  float q[8];
-  p.scaled(mx4_inverse_scale(byte), q);
-  const uint32_t c = mx4_encode8(q);
-  return byte == 255u ? 0u : c;
-}
 
 // ------------------------------------------------------------ logical rows ---
 // The pieces of 8 values are numbered row-major; a block of 32 is four neighbouring lanes'.
@@ -126,38 +68,6 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const Tin* __restri
 // SRC 0: rows of x.  SRC 1: row r of the operand is row row_of[r] / k of x (the gather of
 // the dispatch).  SRC 2: x holds [R, 2K] (gate | up), the operand is silu(gate) * up.
 //
-// The piece of `col` (of K) of a source row, SwiGLU applied; zeros past K or where !in.
-template <typename Tin, int SRC, typename P>
-__device__ __forceinline__ void load_piece(P& p, const Tin* row, int col, int K, bool in) {
-  if (!in) {
-    p.zero();
-  } else if constexpr (SRC == 2) {
-    float up[8];
-    load_floats<Tin, 8>(row + col, p.v);
-    load_floats<Tin, 8>(row + K + col, up);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) p.v[j] = __fmul_rn(silu_f32(p.v[j]), up[j]);
-  } else {
-    p.load(row + col);
-  }
-}
-
-// First element of the source row of operand row r.
-template <typename Tin, int SRC>
-__device__ __forceinline__ const Tin* source_row(const Tin* x, const int32_t* row_of, int k, int T,
-                                                 int K, int r, int32_t* status) {
-  long long src = r;
-  if constexpr (SRC == 1) {
-    const int slot = row_of[r];
-    src = slot >= 0 ? slot / k : T;
-    if (src >= T) {
-      flag_error(status, MOE_ERR_DEVICE_CHECK);
-      src = 0;
-    }
-  }
-  return x + (size_t)src * (SRC == 2 ? 2 * (size_t)K : (size_t)K);
-}
-
 // MANY rows: a warp takes the rows rr, rr + 32, rr + 64, rr + 96 of a tile's 128-row half
 // over all of K: four loads in flight a lane, and the four rows' scales of a half k-block
 // are one 16-byte store.
@@ -187,45 +97,32 @@ __global__ void __launch_bounds__(kQThreads, kRowsBlocksPerSm) quantize_rows_ker
     const int nr = min(4, (rows - r0 + 31) / 32);
     const int row0 = tb.off[e] + ti * cut.step + r0;
     // (rows 32 apart have the same row & 7)
-    uint8_t* cdst = codes + ((size_t)tb.pad[e] * 16 + (size_t)ti * cut.step) * KB * 128 + r0 * 128 +
-                    (((lane >> 2) ^ (rr & 7)) * 16) + (lane & 3) * 4;
-    uint8_t* sdst = sf + (size_t)tile * KB * kMx4SfSlot + half * 1024 + rr * 16 + (lane >> 4) * 512;
+    uint8_t* cdst = codes + tile * mx4_slot(K) + r0 * 128 + (((lane >> 2) ^ (rr & 7)) * 16) +
+                    (lane & 3) * 4;
+    uint8_t* sdst = sf + tile * mx4_sf_slots(K) + half * 1024 + rr * 16 + (lane >> 4) * 512;
     const Tin* src[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       src[i] = source_row<Tin, SRC>(x, row_of, k, T, K, row0 + (i < nr ? i * 32 : 0), status);
     using P = Piece<std::conditional_t<SRC == 2, float, Tin>>;
-    // (K is a multiple of 128: whole half-warps lie inside)
-    auto load = [&](P (&v)[4], int kb) {
-      const int col = kb * kMx4KB + lane * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        load_piece<Tin, SRC>(v[i], src[i], col, K, col < K && i < nr);
-    };
     for (int kb = 0; kb < KB; ++kb) {
-      const bool in = kb * kMx4KB + lane * 8 < K;
+      // (K is a multiple of 128: whole half-warps lie inside)
+      const int col = kb * kMx4KB + lane * 8;
+      const bool in = col < K;
       P v[4];
-      load(v, kb);
-      uint32_t byte[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load_piece<Tin, SRC>(v[i], src[i], col, K, in && i < nr);
+      uint32_t c[4];
+      const uint32_t b0 = quantize4x8(v, c);
       uint8_t* ck = cdst + (size_t)kb * rows16 * 128;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t c = quantize8(v[i], byte[i]);
-        if (in && i < nr) *reinterpret_cast<uint32_t*>(ck + i * 32 * 128) = c;
-      }
+      for (int i = 0; i < 4; ++i)
+        if (in && i < nr) *reinterpret_cast<uint32_t*>(ck + i * 32 * 128) = c[i];
       // A lane's four bytes are four rows' scales of one block; the first lane of each half
       // k-block collects the words of the other three blocks and turns the 4 x 4 bytes.
-      const uint32_t b0 = byte[0] | (byte[1] << 8) | (byte[2] << 16) | (byte[3] << 24);
-      const uint32_t b1 = __shfl_down_sync(0xFFFFFFFFu, b0, 4);
-      const uint32_t b2 = __shfl_down_sync(0xFFFFFFFFu, b0, 8);
-      const uint32_t b3 = __shfl_down_sync(0xFFFFFFFFu, b0, 12);
-      if (in && (lane & 15) == 0) {
-        const uint32_t lo01 = __byte_perm(b0, b1, 0x5140), hi01 = __byte_perm(b0, b1, 0x7362);
-        const uint32_t lo23 = __byte_perm(b2, b3, 0x5140), hi23 = __byte_perm(b2, b3, 0x7362);
-        *reinterpret_cast<uint4*>(sdst + (size_t)kb * kMx4SfSlot) =
-            make_uint4(__byte_perm(lo01, lo23, 0x5410), __byte_perm(lo01, lo23, 0x7632),
-                       __byte_perm(hi01, hi23, 0x5410), __byte_perm(hi01, hi23, 0x7632));
-      }
+      uint4 w;
+      turn_scales(b0, w);
+      if (in && (lane & 15) == 0) *reinterpret_cast<uint4*>(sdst + (size_t)kb * kMx4SfSlot) = w;
     }
   }
 }
@@ -260,8 +157,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_few_rows_kernel(
                      (__shfl_down_sync(0xFFFFFFFFu, byte, 8) << 16) |
                      (__shfl_down_sync(0xFFFFFFFFu, byte, 12) << 24);
   if (!in) return;
-  uint8_t* cdst = codes + ((size_t)tb.pad[e] * 16 + (size_t)ti * cut.step) * KB * 128 +
-                  (size_t)kb * rows16 * 128 + rt * 128;
+  uint8_t* cdst = codes + (tb.tile[e] + ti) * mx4_slot(K) + (size_t)kb * rows16 * 128 + rt * 128;
   *reinterpret_cast<uint32_t*>(cdst + (((lane >> 2) ^ (rt & 7)) * 16) + (lane & 3) * 4) = c;
   if ((lane & 15) == 0)
     *reinterpret_cast<uint32_t*>(sf + ((size_t)(tb.tile[e] + ti) * KB + kb) * kMx4SfSlot +
@@ -371,14 +267,13 @@ cudaError_t launch_mx4_rows(const void* x, int dtype, int src, const int32_t* ro
                             const int32_t* offsets, int E, int R, int K, void* codes, void* sf,
                             int32_t* status, cudaStream_t s) {
   if (R == 0) return cudaSuccess;
-  // a warp per k-block while whole rows would not give every SM 16 warps
-  const bool few = (long long)R < 16LL * 4 * device_sm_count();
+  uint8_t* c = static_cast<uint8_t*>(codes);
+  uint8_t* f = static_cast<uint8_t*>(sf);
+  const bool few = R < kMx4FewRows;
   const long long warps = few ? (long long)R * mx4_kblocks(K) : mx4_max_tiles(R, E) * 64;
   const long long need = (warps + kQWarps - 1) / kQWarps;
   const long long most = few ? need : (long long)device_sm_count() * kRowsBlocksPerSm;
   const int grid = (int)(need < most ? need : most);
-  uint8_t* c = static_cast<uint8_t*>(codes);
-  uint8_t* f = static_cast<uint8_t*>(sf);
   auto go = [&](auto many, auto few_rows, auto* p) {
     if (few)
       few_rows<<<grid, kQThreads, 0, s>>>(p, row_of, k, T, offsets, E, R, K, c, f, status);

@@ -129,6 +129,51 @@ def test_product(moe, counts, K, N, x_dtype, y_dtype):
     check_product(moe, counts, K, N, x_dtype, y_dtype, seed=len(counts) + K)
 
 
+@pytest.mark.parametrize("x_dtype,y_dtype", [("bf16", "f32"), ("f16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("counts,K,N", [
+    ([1], 2176, 128), ([0, 3, 0], 2304, 256), ([16, 17, 15, 1, 0, 33], 2432, 128), ([300, 0, 225], 2176, 384),
+    ([1] * 37, 4096, 256)])
+def test_product_long_rows(moe, counts, K, N, x_dtype, y_dtype):
+    """K past 2048: the rows' codes go through memory; single CTAs and pairs."""
+    check_product(moe, counts, K, N, x_dtype, y_dtype, seed=len(counts) + K)
+
+
+@pytest.mark.parametrize("x_dtype,y_dtype", [("bf16", "bf16"), ("f16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("counts,K,N", [
+    ([9728], 128, 128), ([5000, 0, 1, 4900, 223, 7000], 256, 384), ([100] * 130, 128, 256),
+    ([15000, 2, 0, 300], 384, 128)])
+def test_product_many_rows(moe, counts, K, N, x_dtype, y_dtype):
+    """From 9728 rows on the tiles are quantised and multiplied chunk by chunk."""
+    check_product(moe, counts, K, N, x_dtype, y_dtype, seed=len(counts) + K)
+
+
+def test_product_many_rows_again(moe):
+    """Calls that follow one another at once, on one workspace, of many chunks each."""
+    E, K, N, R = 64, 512, 256, 40000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    codes = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda").to(torch.uint8)
+    scales = torch.randint(118, 124, (E, N, K // 32), generator=g, device="cuda").to(torch.uint8)
+    packed = moe.mx4_pack(codes, scales)
+    ws = moe.mx4_new_workspace(R, K, N, E)
+    xs = [torch.randn((R, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3)]
+    cut = [torch.sort(torch.randint(0, R + 1, (E - 1,), generator=g, device="cuda")).values for _ in xs]
+    offs = [torch.cat([c.new_zeros(1), c, c.new_full((1,), R)]).int() for c in cut]
+    want = []
+    for x, o in zip(xs, offs):
+        want.append(moe.mx4_expert_product(x, o, packed, N, ws, torch.float32))
+        torch.cuda.synchronize()
+    for _ in range(3):
+        got = [moe.mx4_expert_product(x, o, packed, N, ws, torch.float32) for x, o in zip(xs, offs)]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # a few rows of it by themselves (another form of the product) are the same bits
+    o = offs[0].cpu()
+    e = int(torch.argmax(o[1:] - o[:-1]))
+    r = slice(int(o[e]), int(o[e]) + 150)
+    o1 = torch.tensor([0] * (e + 1) + [150] * (E - e), dtype=torch.int32, device="cuda")
+    y = moe.mx4_expert_product(xs[0][r].contiguous(), o1, packed, N, ws, torch.float32)
+    assert torch.equal(y, want[0][r])
+
+
 def test_product_many_experts_and_tiles(moe):
     g = np.random.default_rng(4)
     check_product(moe, g.integers(0, 40, 256).tolist(), 256, 128, "bf16", "f32")
@@ -216,7 +261,8 @@ def test_stream_and_graph(moe):
 
 
 @pytest.mark.parametrize("T,H,E,k,I,kind,groups,keep,top", [
-    (1, 256, 8, 2, 128, 0, 1, 1, 1), (37, 384, 16, 4, 256, 1, 4, 2, 2), (300, 512, 32, 8, 384, 1, 8, 4, 2)])
+    (1, 256, 8, 2, 128, 0, 1, 1, 1), (37, 384, 16, 4, 256, 1, 4, 2, 2), (300, 512, 32, 8, 384, 1, 8, 4, 2),
+    (1300, 512, 32, 8, 256, 1, 8, 4, 2), (40, 2304, 8, 2, 128, 0, 1, 1, 1)])
 def test_layer(moe, T, H, E, k, I, kind, groups, keep, top):
     """The layer is its parts: the logits' selection, the products of the gathered rows, the
     SwiGLU rows quantised, the weighted sum.  Its SiLU uses the special-function unit, a few
