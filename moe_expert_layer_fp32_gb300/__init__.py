@@ -586,24 +586,47 @@ def _on_device(first, *rest):
         raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{_get_device()}")
 
 
+# The tensor calls below go to the library directly: on small batches the host's part of a
+# call is longer than the kernel's.
+def _logits_args(logits, bias):
+    """(type code, row stride, T, E) of logits [T, E]; refuses what a kernel would misread."""
+    dt = _DTYPES.get(logits.dtype)
+    if dt is None:
+        _dtype("logits", logits)
+    if logits.dim() == 2 and logits.is_contiguous():
+        T, ld = logits.shape
+    else:
+        ld, T = _rows("logits", logits), logits.shape[0]
+    E = logits.shape[1]
+    if bias is not None:
+        _dense("bias", bias, torch.float32, (E,))
+    return dt, ld, T, E
+
+
+_default_opts = select_opts()
+
+
 def route_select(logits, k, opts=None, bias=None, want_prob_sum=False, stream=None):
     """(topk_idx [T, k] int32, topk_w [T, k] fp32[, prob_sum [E] fp32]) from logits [T, E]
     (fp32, bf16 or fp16).  opts: a select_opts (default: softmax over all experts)."""
-    ld = _rows("logits", logits)
-    T, E = logits.shape
-    dt = _dtype("logits", logits)
-    if bias is not None:
-        _dense("bias", bias, torch.float32, (E,))
+    dt, ld, T, E = _logits_args(logits, bias)
     _on_device(logits, bias)
     dev = logits.device
     idx = torch.empty((T, k), dtype=torch.int32, device=dev)
     w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    prob = ws = None
+    prob = pp = wp = None
+    n = 0
     if want_prob_sum:
         prob = torch.empty(E, dtype=torch.float32, device=dev)
-        ws = torch.empty(moe_select_workspace_bytes(T, E), dtype=torch.uint8, device=dev)
-    moe_route_select(logits, dt, ld, bias, select_opts() if opts is None else opts, T, E, k, idx, w,
-                     prob, ws, stream)
+        n = moe_select_workspace_bytes(T, E)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        pp, wp = prob.data_ptr(), ws.data_ptr()
+    r = _lib.moe_route_select(
+        logits.data_ptr(), dt, ld, None if bias is None else bias.data_ptr(),
+        ctypes.byref(_default_opts if opts is None else opts), T, E, k, idx.data_ptr(),
+        w.data_ptr(), pp, wp, n, _stream(stream))
+    if r:
+        _check("moe_route_select", r)
     return (idx, w, prob) if want_prob_sum else (idx, w)
 
 
@@ -611,40 +634,61 @@ def route_select_backward(logits, topk_idx, d_topk_w, opts=None, bias=None, d_pr
                           want_d_bias=False, stream=None):
     """d_logits [T, E] in the logits' type (and d_bias [E] fp32 if want_d_bias, softmax only)
     for d_topk_w [T, k] and, if given, d_prob_sum [E], both fp32; the choice stays fixed."""
-    ld = _rows("logits", logits)
-    T, E = logits.shape
-    dt = _dtype("logits", logits)
+    dt, ld, T, E = _logits_args(logits, bias)
     if topk_idx.dim() != 2:
         raise ValueError(f"topk_idx: [T, k], not {tuple(topk_idx.shape)}")
     k = topk_idx.shape[1]
     _dense("topk_idx", topk_idx, torch.int32, (T, k))
     _dense("d_topk_w", d_topk_w, torch.float32, (T, k))
-    for name, t in (("bias", bias), ("d_prob_sum", d_prob_sum)):
-        if t is not None:
-            _dense(name, t, torch.float32, (E,))
+    if d_prob_sum is not None:
+        _dense("d_prob_sum", d_prob_sum, torch.float32, (E,))
     _on_device(logits, topk_idx, d_topk_w, bias, d_prob_sum)
-    d_logits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    d_bias = ws = None
+    dev = logits.device
+    d_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    d_bias = bp = wp = None
+    n = 0
     if want_d_bias:
-        d_bias = torch.empty(E, dtype=torch.float32, device=logits.device)
-        ws = torch.empty(moe_select_workspace_bytes(T, E), dtype=torch.uint8, device=logits.device)
-    moe_route_select_bwd(logits, dt, ld, bias, select_opts() if opts is None else opts, T, E, k,
-                         topk_idx, d_topk_w, d_prob_sum, d_logits, E, d_bias, ws, stream)
+        d_bias = torch.empty(E, dtype=torch.float32, device=dev)
+        n = moe_select_workspace_bytes(T, E)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        bp, wp = d_bias.data_ptr(), ws.data_ptr()
+    r = _lib.moe_route_select_bwd(
+        logits.data_ptr(), dt, ld, None if bias is None else bias.data_ptr(),
+        ctypes.byref(_default_opts if opts is None else opts), T, E, k, topk_idx.data_ptr(),
+        d_topk_w.data_ptr(), None if d_prob_sum is None else d_prob_sum.data_ptr(),
+        d_logits.data_ptr(), E, bp, wp, n, _stream(stream))
+    if r:
+        _check("moe_route_select_bwd", r)
     return (d_logits, d_bias) if want_d_bias else d_logits
 
 
 def mx4_quantize(x, want_values=False, stream=None):
     """(codes [R, K/2] uint8, scales [R, K/32] uint8[, values [R, K] bf16]) of rows x [R, K]
     (fp32, bf16 or fp16), K a multiple of 32."""
-    ld = _rows("x", x)
-    dt = _dtype("x", x)
-    _on_device(x)
-    R, K = x.shape
-    codes = torch.empty((R, K // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((R, K // 32), dtype=torch.uint8, device=x.device)
-    values = torch.empty((R, K), dtype=torch.bfloat16, device=x.device) if want_values else None
-    moe_mx4_quantize(x, dt, ld, R, K, codes, scales, values, stream)
+    dt, ld, R, K = _x_args(x)
+    dev = x.device
+    codes = torch.empty((R, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((R, K // 32), dtype=torch.uint8, device=dev)
+    values = torch.empty((R, K), dtype=torch.bfloat16, device=dev) if want_values else None
+    r = _lib.moe_mx4_quantize(x.data_ptr(), dt, ld, R, K, codes.data_ptr(), scales.data_ptr(),
+                              values.data_ptr() if want_values else None, _stream(stream))
+    if r:
+        _check("moe_mx4_quantize", r)
     return (codes, scales, values) if want_values else (codes, scales)
+
+
+def _x_args(x):
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
+        _dtype("x", x)
+    if x.dim() == 2 and x.is_contiguous():
+        R, K = x.shape
+        ld = K
+    else:
+        ld = _rows("x", x)
+        R, K = x.shape
+    _on_device(x)
+    return dt, ld, R, K
 
 
 def mx4_pack(codes, scales, stream=None) -> torch.Tensor:
@@ -715,7 +759,12 @@ def mx4_expert_product(x, offsets, packed, N, workspace, dtype=torch.bfloat16, s
         raise TypeError(f"y: float32 or bfloat16, not {dtype}")
     _on_device(x, offsets, packed, workspace)
     y = torch.empty((R, N), dtype=dtype, device=x.device)
-    moe_mx4_expert_product(x, dt, offsets, packed, R, K, N, E, y, _DTYPES[dtype], workspace, stream)
+    r = _lib.moe_mx4_expert_product(
+        x.data_ptr(), dt, offsets.data_ptr(), packed.data_ptr(), R, K, N, E, y.data_ptr(),
+        _DTYPES[dtype], workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(stream))
+    if r:
+        _check("moe_mx4_expert_product", r)
     return y
 
 

@@ -64,6 +64,7 @@ __host__ __device__ inline size_t mx4_sf_slots(int K) { return (size_t)mx4_kbloc
 struct Mx4Tables {
   int off[kMaxE + 1];    // first row of each expert
   int tile[kMaxE + 1];   // its first row tile
+  int step[kMaxE];       // rows of its tiles (the last may have fewer)
   int ok;
 };
 
@@ -84,14 +85,17 @@ __device__ __forceinline__ bool mx4_build_tables(Mx4Tables& s, const int32_t* __
         if (lo < 0 || hi < lo || hi > R) ok = false;
         else m = hi - lo;
       }
-      int n = mx4_cut(m, tile_rows).n;
-      const int n0 = n;
+      const Mx4Cut cut = mx4_cut(m, tile_rows);
+      int n = cut.n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int nu = __shfl_up_sync(0xFFFFFFFFu, n, o);
         if (lane >= o) n += nu;
       }
-      if (e < E) s.tile[e] = tile + n - n0;
+      if (e < E) {
+        s.tile[e] = tile + n - cut.n;
+        s.step[e] = cut.step;
+      }
       tile += __shfl_sync(0xFFFFFFFFu, n, 31);
     }
     ok = __all_sync(0xFFFFFFFFu, ok);
@@ -114,6 +118,32 @@ __device__ __forceinline__ int mx4_find(const int* table, int E, int v) {
     else hi = mid - 1;
   }
   return lo;
+}
+
+// A row tile: its expert, first row and rows.  Walks keep the expert of the tile before (any
+// but the first costs a step or two; a search and the cut's divisions for every tile, on the
+// one thread that issues the MMAs, cost 1900 cycles a unit).
+struct Mx4Tile {
+  int e, row0, rows, rows16;
+};
+__device__ __forceinline__ Mx4Tile mx4_tile_in(int e, int tile, const Mx4Tables& tb) {
+  Mx4Tile t;
+  t.e = e;
+  const int step = tb.step[e], first = (tile - tb.tile[e]) * step;
+  t.row0 = tb.off[e] + first;
+  t.rows = min(step, tb.off[e + 1] - t.row0);
+  t.rows16 = (t.rows + 15) & ~15;
+  return t;
+}
+// e: the expert of an earlier tile of the walk (up: of a tile not after this one), or any
+// expert not after (up) or not before (down) the tile's
+__device__ __forceinline__ Mx4Tile mx4_walk_up(int& e, int tile, const Mx4Tables& tb) {
+  while (tb.tile[e + 1] <= tile) ++e;
+  return mx4_tile_in(e, tile, tb);
+}
+__device__ __forceinline__ Mx4Tile mx4_walk_down(int& e, int tile, const Mx4Tables& tb) {
+  while (tb.tile[e] > tile) --e;
+  return mx4_tile_in(e, tile, tb);
 }
 
 // Scale byte of a block whose largest magnitude has the FP32 bits `amax` (sign cleared):

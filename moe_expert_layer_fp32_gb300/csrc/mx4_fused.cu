@@ -83,24 +83,6 @@ struct Runs {
   }
 };
 
-struct Tile {
-  int e;       // expert
-  int row0;    // first row
-  int rows;    // rows of the tile
-  int rows16;  // padded to 16
-};
-__device__ __forceinline__ Tile tile_of(int tile, const Mx4Tables& tb, int E) {
-  Tile t;
-  t.e = mx4_find(tb.tile, E, tile);
-  const int m = tb.off[t.e + 1] - tb.off[t.e];
-  const Mx4Cut cut = mx4_cut(m, kFTile);
-  const int ti = tile - tb.tile[t.e];
-  t.row0 = tb.off[t.e] + ti * cut.step;
-  t.rows = min(cut.step, m - ti * cut.step);
-  t.rows16 = (t.rows + 15) / 16 * 16;
-  return t;
-}
-
 __device__ __forceinline__ void store_peer(uint32_t addr_cluster, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr_cluster), "r"(v) : "memory");
 }
@@ -163,6 +145,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   Runs runs(ok_tables ? tb.tile[E] : 0, P, gridDim.x / 2, blockIdx.x / 2);
   Run run;
+  int e = 0;  // the walk's expert (runs go up)
 
   if (warp == 0) {
     if (elect_one()) {
@@ -170,7 +153,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       int it = 0;
       bool aborted = false;
       while (!aborted && runs.next(run)) {
-        const Tile t = tile_of(run.tile, tb, E);
+        const Mx4Tile t = mx4_walk_up(e, run.tile, tb);
         for (int p = run.p0; p < run.p1 && !aborted; ++p) {
           // (an odd last tile has no partner: the odd CTA multiplies it again and stores nothing)
           const int nt = min(2 * p + rank, NT - 1);
@@ -218,7 +201,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       int it = 0, tcount = 0, q = 0;
       bool aborted = false;
       while (!aborted && runs.next(run)) {
-        const Tile t = tile_of(run.tile, tb, E);
+        const Mx4Tile t = mx4_walk_up(e, run.tile, tb);
         const int b = q & 1;
         if (!wait_full<true>(&qfull[b], (q >> 1) & 1, abort_flag, status, spin_limit)) break;
         ++q;
@@ -237,7 +220,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
           const uint32_t d = tmem_base + acc * kFTile;
           for (int kb = 0; kb < KB; ++kb, ++it) {
             const int s = it % C::STAGES;
-            if (!wait_full<true>(&full[s], (it / C::STAGES) & 1, abort_flag, status, spin_limit)) {
+            if (!mbar_wait_bounded(&full[s], (it / C::STAGES) & 1, abort_flag, status, spin_limit)) {
               aborted = true;
               break;
             }
@@ -280,7 +263,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     int tcount = 0;
     bool aborted = false;
     while (!aborted && runs.next(run)) {
-      const Tile t = tile_of(run.tile, tb, E);
+      const Mx4Tile t = mx4_walk_up(e, run.tile, tb);
       for (int p = run.p0; p < run.p1; ++p, ++tcount) {
         const int acc = tcount % kFAcc;
         int ok = 1;
@@ -322,7 +305,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     const int qw = warp - 10;
     int qc = 0;
     while (runs.next(run)) {
-      const Tile t = tile_of(run.tile, tb, E);
+      const Mx4Tile t = mx4_walk_up(e, run.tile, tb);
       const int b = qc & 1;
       int ok = 1;
       if (lane == 0)

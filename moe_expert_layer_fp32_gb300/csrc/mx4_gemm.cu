@@ -61,27 +61,44 @@ struct MxUnit {
   size_t sf_img;
 };
 
+// The units of one CTA (or pair): every `step`-th from the first, tiles from the last one down
+// (the row images written last are still in L2), a tile's weight tiles in order.
 template <bool PAIR>
-__device__ __forceinline__ MxUnit mx_unit(long long u, const Mx4Tables& tb, int E, int NT, int KB,
-                                          int rank) {
-  const int nu = PAIR ? (NT + 1) / 2 : NT;  // units of a row tile
-  const int done = (int)(u / nu);
-  const int tile = tb.tile[E] - 1 - done;  // the last ones are still in L2
-  const int e = mx4_find(tb.tile, E, tile);
-  const int m = tb.off[e + 1] - tb.off[e];
-  const Mx4Cut cut = mx4_cut(m);
-  const int ti = tile - tb.tile[e];
-  MxUnit w;
-  w.nt = (int)(u - (long long)done * nu);
-  if (PAIR) w.nt = 2 * w.nt + rank;
-  w.row0 = tb.off[e] + ti * cut.step;
-  w.rows = min(cut.step, m - ti * cut.step);
-  w.rows16 = (w.rows + 15) / 16 * 16;
-  w.w_img = ((size_t)e * NT + min(w.nt, NT - 1)) * KB * kMx4WBytes;
-  w.row_img = (size_t)tile * KB * kMx4TileRows * 128;
-  w.sf_img = (size_t)tile * KB * kMx4SfSlot;
-  return w;
-}
+struct MxUnits {
+  int e, tile, j, nu, q, r, NT, KB, rank;
+  __device__ __forceinline__ MxUnits(int first, int step, const Mx4Tables& tb, int E, int NT_, int KB_,
+                                     int rank_, bool ok)
+      : NT(NT_), KB(KB_), rank(rank_) {
+    nu = PAIR ? (NT + 1) / 2 : NT;  // units of a row tile
+    const int t = first / nu;
+    j = first - t * nu;
+    tile = (ok ? tb.tile[E] : 0) - 1 - t;
+    q = step / nu;
+    r = step - q * nu;
+    e = E - 1;
+  }
+  __device__ __forceinline__ bool more() const { return tile >= 0; }
+  __device__ __forceinline__ void advance() {
+    tile -= q;
+    j += r;
+    if (j >= nu) {
+      j -= nu;
+      --tile;
+    }
+  }
+  __device__ __forceinline__ MxUnit unit(const Mx4Tables& tb) {
+    const Mx4Tile t = mx4_walk_down(e, tile, tb);
+    MxUnit w;
+    w.nt = PAIR ? 2 * j + rank : j;
+    w.row0 = t.row0;
+    w.rows = t.rows;
+    w.rows16 = t.rows16;
+    w.w_img = (size_t)(e * NT + min(w.nt, NT - 1)) * KB * kMx4WBytes;
+    w.row_img = (size_t)tile * KB * (kMx4TileRows * 128);
+    w.sf_img = (size_t)tile * KB * kMx4SfSlot;
+    return w;
+  }
+};
 
 // Pair form: every CTA loads its own weight tile, its half of the rows' codes and all of
 // their scales, completing on its own `full` barrier; the odd CTA's idle MMA warp passes its
@@ -111,8 +128,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int NT = N / kMx4WTile;
   const int KB = mx4_kblocks(K);
   const int rank = PAIR ? (int)cluster_ctarank() : 0;
-  const long long unit0 = PAIR ? blockIdx.x / 2 : blockIdx.x;
-  const long long unit_step = PAIR ? gridDim.x / 2 : gridDim.x;
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -137,7 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (PAIR) cluster_sync();  // both CTAs' barriers exist before any remote use
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const long long total = ok_tables ? (long long)tb.tile[E] * (PAIR ? (NT + 1) / 2 : NT) : 0;
+  MxUnits<PAIR> units(PAIR ? blockIdx.x / 2 : blockIdx.x, PAIR ? gridDim.x / 2 : gridDim.x, tb, E,
+                      NT, KB, rank, ok_tables);
 
   if (warp == 0) {
     if (elect_one()) {
@@ -148,8 +164,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The weights are inputs: the first unit's first stages are on their way before the
       // rows' quantisation, the kernel before this one, has finished.
       int early = 0;
-      if (unit0 < total) {
-        const MxUnit w = mx_unit<PAIR>(unit0, tb, E, NT, KB, rank);
+      if (units.more()) {
+        const MxUnit w = units.unit(tb);
         for (; early < KB && early < C::STAGES; ++early) {
           mbar_arrive_expect_tx(&full[early], kMx4WBytes + row_bytes(w) + sf_bytes(w));
           bulk_load(base + early * C::STAGE_BYTES, wimg + w.w_img + (size_t)early * kMx4WBytes,
@@ -159,14 +175,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       pdl_wait();
       int it = 0;
       bool aborted = false;
-      for (long long u = unit0; u < total && !aborted; u += unit_step) {
-        const MxUnit w = mx_unit<PAIR>(u, tb, E, NT, KB, rank);
+      for (; units.more() && !aborted; units.advance()) {
+        const MxUnit w = units.unit(tb);
         const uint32_t rb = row_bytes(w), sb = sf_bytes(w);
         const uint8_t* rows = rimg + w.row_img + (size_t)rank * rb;
         const size_t row_step = (size_t)w.rows16 * 128;
         // single form: the next unit's weights move into L2 while this one's are multiplied
-        const bool more = !PAIR && u + unit_step < total;
-        const MxUnit nx = more ? mx_unit<PAIR>(u + unit_step, tb, E, NT, KB, rank) : w;
+        MxUnits<PAIR> ahead = units;
+        ahead.advance();
+        const bool more = !PAIR && ahead.more();
+        const size_t next_w = more ? ahead.unit(tb).w_img : 0;
         for (int kb = 0; kb < KB; ++kb, ++it) {
           const int s = it % C::STAGES;
           const uint32_t ph = (it / C::STAGES) & 1;
@@ -181,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           bulk_load(st + C::ROW_OFF, rows + kb * row_step, rb, &full[s]);
           bulk_load(st + C::SF_OFF, simg + w.sf_img + (size_t)kb * kMx4SfSlot, sb, &full[s]);
-          if (more) prefetch_l2(wimg + nx.w_img + (size_t)kb * kMx4WBytes, kMx4WBytes);
+          if (more) prefetch_l2(wimg + next_w + (size_t)kb * kMx4WBytes, kMx4WBytes);
         }
       }
       if (aborted) {
@@ -198,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------- relay of the odd CTA's full stages
         int it = 0;
         bool aborted = false;
-        for (long long u = unit0; u < total && !aborted; u += unit_step) {
+        for (; units.more() && !aborted; units.advance()) {
           for (int kb = 0; kb < KB; ++kb, ++it) {
             const int s = it % C::STAGES;
             if (!mbar_wait_bounded(&full[s], (it / C::STAGES) & 1, abort_flag, status, spin_limit)) {
@@ -214,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (elect_one()) {
       // ---------------------------------------------------------- MMA issuer
       int it = 0, tcount = 0;
-      for (long long u = unit0; u < total; u += unit_step, ++tcount) {
-        const MxUnit w = mx_unit<PAIR>(u, tb, E, NT, KB, rank);
+      for (; units.more(); units.advance(), ++tcount) {
+        const MxUnit w = units.unit(tb);
         const int acc = tcount & 1;
         const uint32_t aph = (tcount >> 1) & 1;
         if (!mbar_wait_bounded(&tempty[acc], aph ^ 1, abort_flag, status, spin_limit)) break;
@@ -228,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kb = 0; kb < KB; ++kb, ++it) {
           const int s = it % C::STAGES;
           const uint32_t ph = (it / C::STAGES) & 1;
-          if (!wait_full<PAIR>(&full[s], ph, abort_flag, status, spin_limit)) {
+          if (!mbar_wait_bounded(&full[s], ph, abort_flag, status, spin_limit)) {
             aborted = true;
             break;
           }
@@ -271,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;  // lane quarter of tensor memory this warp may access
     const int half = (warp - 2) >> 2;  // of the quarter's two warps: every other 32 columns
     int tcount = 0;
-    for (long long u = unit0; u < total; u += unit_step, ++tcount) {
-      const MxUnit w = mx_unit<PAIR>(u, tb, E, NT, KB, rank);
+    for (; units.more(); units.advance(), ++tcount) {
+      const MxUnit w = units.unit(tb);
       const int acc = tcount & 1;
       const uint32_t aph = (tcount >> 1) & 1;
       int ok = 1;

@@ -83,19 +83,16 @@ __global__ void __launch_bounds__(kQThreads, kRowsBlocksPerSm) quantize_rows_ker
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int KB = mx4_kblocks(K);
   const long long items = (long long)tb.tile[E] * 64;  // (tile, half, rr)
+  int e = 0;
   for (long long it = (long long)blockIdx.x * kQWarps + warp; it < items;
        it += (long long)gridDim.x * kQWarps) {
     const int tile = (int)(it >> 6), half = (int)(it >> 5) & 1, rr = (int)it & 31;
-    const int e = mx4_find(tb.tile, E, tile);
-    const int m = tb.off[e + 1] - tb.off[e];
-    const Mx4Cut cut = mx4_cut(m);
-    const int ti = tile - tb.tile[e];
-    const int rows = min(cut.step, m - ti * cut.step);
+    const Mx4Tile t = mx4_walk_up(e, tile, tb);
     const int r0 = half * 128 + rr;  // this warp's first row of the tile
-    if (r0 >= rows) continue;
-    const int rows16 = (rows + 15) / 16 * 16;
-    const int nr = min(4, (rows - r0 + 31) / 32);
-    const int row0 = tb.off[e] + ti * cut.step + r0;
+    if (r0 >= t.rows) continue;
+    const int rows16 = t.rows16;
+    const int nr = min(4, (t.rows - r0 + 31) / 32);
+    const int row0 = t.row0 + r0;
     // (rows 32 apart have the same row & 7)
     uint8_t* cdst = codes + tile * mx4_slot(K) + r0 * 128 + (((lane >> 2) ^ (rr & 7)) * 16) +
                     (lane & 3) * 4;
@@ -147,10 +144,9 @@ __global__ void __launch_bounds__(kQThreads) quantize_few_rows_kernel(
   load_piece<Tin, SRC>(v, row, col, K, in);
   if (!mx4_build_tables(tb, offsets, E, R, status) || r >= R) return;
   const int e = mx4_find(tb.off, E, r);
-  const int m = tb.off[e + 1] - tb.off[e], local = r - tb.off[e];
-  const Mx4Cut cut = mx4_cut(m);
-  const int ti = local / cut.step, rt = local - ti * cut.step;
-  const int rows16 = min(cut.step, (m - ti * cut.step + 15) / 16 * 16);
+  const int local = r - tb.off[e], step = tb.step[e];
+  const int ti = local / step, rt = local - ti * step;
+  const int rows16 = min(step, (tb.off[e + 1] - tb.off[e] - ti * step + 15) & ~15);
   uint32_t byte;
   const uint32_t c = quantize8(v, byte);
   const uint32_t w = byte | (__shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8) |
