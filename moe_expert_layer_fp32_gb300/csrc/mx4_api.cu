@@ -78,7 +78,7 @@ size_t rows_bytes(long long R, int K, int E) { return up(mx4_max_tiles(R, E) * m
 size_t scales_bytes(long long R, int K, int E) { return up(mx4_max_tiles(R, E) * mx4_sf_slots(K)); }
 
 // Whether the product of R rows quantises them in its own kernel (no images).
-bool fused(int R, int K) { return K <= kMx4FusedMaxK && R < kMx4FewRows; }
+bool fused(int R, int K) { return K <= kMx4FusedMaxK && R <= kMx4FusedRows; }
 
 struct ProductLayout {
   size_t status, images, total;

@@ -180,11 +180,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t rb = row_bytes(w), sb = sf_bytes(w);
         const uint8_t* rows = rimg + w.row_img + (size_t)rank * rb;
         const size_t row_step = (size_t)w.rows16 * 128;
-        // single form: the next unit's weights move into L2 while this one's are multiplied
+        // What this CTA's next unit is the first to touch moves into L2 while this one is
+        // multiplied: an expert's weights with its first tile, a tile's rows with its first
+        // weight tile.  (Six stages cover a load from L2, not one from memory.)
         MxUnits<PAIR> ahead = units;
         ahead.advance();
-        const bool more = !PAIR && ahead.more();
-        const size_t next_w = more ? ahead.unit(tb).w_img : 0;
+        const bool more = ahead.more();
+        const MxUnit nx = more ? ahead.unit(tb) : w;
+        const bool fetch_w = more && ahead.tile == tb.tile[ahead.e + 1] - 1;
+        const bool fetch_rows = more && ahead.j == 0 && rank == 0;
         for (int kb = 0; kb < KB; ++kb, ++it) {
           const int s = it % C::STAGES;
           const uint32_t ph = (it / C::STAGES) & 1;
@@ -199,7 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           bulk_load(st + C::ROW_OFF, rows + kb * row_step, rb, &full[s]);
           bulk_load(st + C::SF_OFF, simg + w.sf_img + (size_t)kb * kMx4SfSlot, sb, &full[s]);
-          if (more) prefetch_l2(wimg + next_w + (size_t)kb * kMx4WBytes, kMx4WBytes);
+          if (fetch_w) prefetch_l2(wimg + nx.w_img + (size_t)kb * kMx4WBytes, kMx4WBytes);
+          if (fetch_rows)
+            prefetch_l2(rimg + nx.row_img + (size_t)kb * nx.rows16 * 128, nx.rows16 * 128);
         }
       }
       if (aborted) {
@@ -232,18 +238,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (elect_one()) {
       // ---------------------------------------------------------- MMA issuer
       int it = 0, tcount = 0;
-      for (; units.more(); units.advance(), ++tcount) {
-        const MxUnit w = units.unit(tb);
+      int rows16 = units.more() ? units.unit(tb).rows16 : 0;
+      for (; rows16 != 0; ++tcount) {
         const int acc = tcount & 1;
         const uint32_t aph = (tcount >> 1) & 1;
+        int next16 = 0;
         if (!mbar_wait_bounded(&tempty[acc], aph ^ 1, abort_flag, status, spin_limit)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * C::ACC_COLS;
         constexpr int M = PAIR ? 256 : 128;
-        const uint32_t id0 = idesc_mx4(M, w.rows16, 0), id1 = idesc_mx4(M, w.rows16, 2);
-        const bool two = w.rows16 > 128;
+        const uint32_t id0 = idesc_mx4(M, rows16, 0), id1 = idesc_mx4(M, rows16, 2);
+        const bool two = rows16 > 128;
         bool aborted = false;
         for (int kb = 0; kb < KB; ++kb, ++it) {
+          if (kb == KB - 1) {  // the next unit, while MMAs are queued
+            units.advance();
+            if (units.more()) next16 = units.unit(tb).rows16;
+          }
           const int s = it % C::STAGES;
           const uint32_t ph = (it / C::STAGES) & 1;
           if (!mbar_wait_bounded(&full[s], ph, abort_flag, status, spin_limit)) {
@@ -277,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (aborted) break;
         if constexpr (PAIR) mma_commit_pair(&tfull[acc], 0x3);
         else mma_commit(&tfull[acc]);
+        rows16 = next16;
       }
       // every MMA this thread issued completes before tensor memory is released
       if constexpr (PAIR) mma_commit_pair(mma_done, 0x1);

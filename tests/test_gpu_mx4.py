@@ -124,7 +124,8 @@ def check_product(moe, counts, K, N, x_dtype, y_dtype, seed=0):
 @pytest.mark.parametrize("counts,K,N", [
     ([1], 128, 128), ([0, 3, 0], 256, 256), ([16, 17, 15, 1, 0, 33], 384, 128),
     ([224], 512, 256), ([225, 223], 256, 128), ([128, 129, 127], 640, 128), ([449, 1, 448], 256, 384),
-    ([1] * 37, 1024, 256), ([0] * 30 + [700] + [0] * 5, 128, 256), ([5, 90, 2, 61], 2048, 512)])
+    ([1] * 37, 1024, 256), ([0] * 30 + [700] + [0] * 5, 128, 256), ([5, 90, 2, 61], 2048, 512),
+    ([128], 2048, 384), ([97, 0, 31], 640, 128), ([48, 49, 0, 7], 256, 1152), ([129], 2048, 256)])
 def test_product(moe, counts, K, N, x_dtype, y_dtype):
     check_product(moe, counts, K, N, x_dtype, y_dtype, seed=len(counts) + K)
 
