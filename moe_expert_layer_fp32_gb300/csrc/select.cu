@@ -29,6 +29,7 @@
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "pdl.cuh"
 #include "select_math.cuh"
 
 namespace moe {
@@ -149,6 +150,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
                                                              float* __restrict__ topk_w,
                                                              float* __restrict__ partial) {
   constexpr int NV = EP / 32;
+  if constexpr (PROB) pdl_launch_dependents();  // the column sums, which wait for this kernel
   __shared__ __align__(16) float s_row[kSelWarps][EP];  // the keys; later the candidates' scores
   __shared__ __align__(16) uint32_t s_key[kSelWarps][32];  // candidates in expert order
   __shared__ int s_expert[kSelWarps][32];
@@ -167,14 +169,20 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
   float col[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) col[i] = 0.0f;
+  float bound = INFINITY;  // of the token before
+  const long long t0 = (long long)blockIdx.x * kSelWarps + warp;
+  const long long stride = (long long)gridDim.x * kSelWarps;
+  // the next token's logits are in flight while this one's experts are chosen
+  float l[NV];
+  if (t0 < a.T) load_row<Tin, NV>(logits + t0 * a.ld, e0, E, vec, l);
 
-  for (long long t = (long long)blockIdx.x * kSelWarps + warp; t < a.T;
-       t += (long long)gridDim.x * kSelWarps) {
-    float l[NV], key[NV], sc[NV];
-    load_row<Tin, NV>(logits + t * a.ld, e0, E, vec, l);
+  for (long long t = t0; t < a.T; t += stride) {
+    float key[NV], sc[NV];
     keys_of<KIND, NV>(l, b, key, sc);
-    if constexpr (PROB) {
-      float mx = -INFINITY, z = 0.0f;
+    if (t + stride < a.T) load_row<Tin, NV>(logits + (t + stride) * a.ld, e0, E, vec, l);
+    // the row's softmax: its maximum and the sum relative to it (sigmoid: the sum of scores)
+    float mx = -INFINITY, z = 0.0f;
+    if (PROB || (KIND == 0 && !a.renorm)) {
       if constexpr (KIND == 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) mx = fmaxf(mx, key[i]);
@@ -187,9 +195,11 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
         z += p[i];
       }
       z = warp_sum(z);
-      const float r = z > 0.0f ? 1.0f / z : 0.0f;
+      if constexpr (PROB) {
+        const float r = z > 0.0f ? __frcp_rn(z) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) col[i] += p[i] * r;
+        for (int i = 0; i < NV; ++i) col[i] += p[i] * r;
+      }
     }
     // groups that stay: L lanes per group, each over every L-th of its keys
     unsigned keep = kFull;
@@ -229,68 +239,81 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
         if ((keep >> (lane & ~((1 << a.lane_shift) - 1))) & 1u) gk = 0u;
       }
     }
-    // selection keys: 0 = cannot be chosen, masked below every number
-    uint32_t u[NV];
+    // experts of this lane that may be chosen: all of a lane in one group, or one by one
+    // (others get -inf here; the rare case where masked experts must be chosen sorts them out)
+    bool lane_in = true;
     if (whole) {
       const int g = (e0 * a.per_magic) >> 16;  // e0 / per
-      const int n = (inside > 0 && ((keep >> (g << a.lane_shift)) & 1u)) ? inside : 0;
+      lane_in = inside > 0 && ((keep >> (g << a.lane_shift)) & 1u);
+    }
+    auto may = [&](int i) {
+      if (whole) return lane_in && i < inside;
+      const int g = ((e0 + i) * a.per_magic) >> 16;
+      return i < inside && ((keep >> (g << a.lane_shift)) & 1u) != 0;
+    };
+    if (!whole) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) u[i] = i < n ? float_key(key[i]) : 0u;
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int g = ((e0 + i) * a.per_magic) >> 16;
-        u[i] = (i < inside && ((keep >> (g << a.lane_shift)) & 1u)) ? float_key(key[i]) : 0u;
-      }
+      for (int i = 0; i < NV; ++i)
+        if (!may(i)) key[i] = -INFINITY;
     }
     // A lower bound of the k-th largest key: the k-th largest of the lanes' maxima (at
-    // least k keys are not below it).  Few keys reach it, mostly one a lane.
-    uint32_t top = 0u;
+    // least k keys are not below it).  Few keys reach it, mostly one a lane.  The bound of
+    // the token before is tried first: any bound that k to 32 keys reach will do.
+    float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) top = max(top, u[i]);
-    uint32_t bound;
-    for (int left = k;;) {
-      bound = __reduce_max_sync(kFull, top);
-      const bool hit = top == bound;
-      left -= __popc(__ballot_sync(kFull, hit));
-      if (left <= 0 || bound == 0u) break;
-      top = hit ? 0u : top;
+    for (int i = 0; i < NV; ++i) top = fmaxf(top, key[i]);
+    if (!lane_in) top = -INFINITY;
+    int mine, before, n;
+    auto count = [&]() {
+      mine = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) mine += key[i] >= bound;
+      if (top < bound) mine = 0;  // (a lane outside the groups that stay)
+      before = mine;  // inclusive scan: candidates in expert order
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFull, before, o);
+        if (lane >= o) before += v;
+      }
+      n = __shfl_sync(kFull, before, 31);
+      before -= mine;
+    };
+    count();
+    if (n < k || n > 32) {
+      uint32_t tu = float_key(top), bu;
+      for (int left = k;;) {
+        bu = __reduce_max_sync(kFull, tu);
+        const bool hit = tu == bu;
+        left -= __popc(__ballot_sync(kFull, hit));
+        if (left <= 0 || bu <= float_key(-INFINITY)) break;
+        tu = hit ? 0u : tu;
+      }
+      bound = fmaxf(key_float(max(bu, 1u)), -3.402823466e38f);  // (not the masked keys)
+      count();
     }
-    bound = max(bound, 1u);
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) mine += u[i] >= bound;
-    int before = mine;  // inclusive scan: candidates in expert order
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(kFull, before, o);
-      if (lane >= o) before += v;
-    }
-    const int n = __shfl_sync(kFull, before, 31);
-    before -= mine;
 
-    // slot of this lane's candidate (k or more: not chosen), its expert, key and score
-    int slot = 32, ce = 0;
+    // lane j < k: slot j's expert, key and score
+    int ce = 0;
     float ck = -INFINITY, cs = 0.0f;
-    if (n <= 32) {
+    if (n >= k && n <= 32) {
       // one candidate a lane, ranked against the others
       s_key[warp][lane] = 0u;
       if constexpr (KIND == 1) store_row<EP>(s_row[warp], e0, sc);
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        if (u[i] >= bound) {
-          s_key[warp][before] = u[i];
+        if (mine > 0 && key[i] >= bound) {
+          s_key[warp][before] = float_key(key[i]);
           s_expert[warp][before] = e0 + i;
           ++before;
         }
       }
       __syncwarp();
       const uint32_t cu = s_key[warp][lane];
+      int slot = 32;  // this lane's candidate's (k or more: not chosen)
       if (lane < n) {
         ce = s_expert[warp][lane];
         if constexpr (KIND == 1) cs = s_row[warp][ce];
-        ck = key_float(cu);
         slot = 0;
       }
       for (int j = 0; j < n; j += 4) {
@@ -300,10 +323,26 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
         slot += (o.z > cu || (o.z == cu && j + 2 < lane)) ? 1 : 0;
         slot += (o.w > cu || (o.w == cu && j + 3 < lane)) ? 1 : 0;
       }
+      // slot j to lane j, so that sums over the chosen are in slot order
+      __syncwarp();
+      if (slot < k) {
+        s_key[warp][slot] = cu;
+        s_expert[warp][slot] = ce;
+        if constexpr (KIND == 1) s_row[warp][slot] = cs;
+      }
+      __syncwarp();
+      if (lane < k) {
+        ck = key_float(s_key[warp][lane]);
+        ce = s_expert[warp][lane];
+        if constexpr (KIND == 1) cs = s_row[warp][lane];
+      }
       __syncwarp();
     } else {
-      // many equal keys at the bound: k rounds of a warp-wide maximum
-      slot = lane;
+      // many equal keys at the bound, or fewer than k that are not masked: k rounds of a
+      // warp-wide maximum; 0 = cannot be chosen, masked below every number
+      uint32_t u[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) u[i] = may(i) ? float_key(key[i]) : 0u;
       for (int j = 0; j < k; ++j) {
         uint32_t bk = 0u;
         int bi = 0;
@@ -331,35 +370,28 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
         }
       }
     }
-    const bool chosen = slot < k;
+    const bool chosen = lane < k;
     float w;
     if constexpr (KIND == 0) {
-      // relative to the best chosen key, or to the row's for the plain probability
-      float m = a.renorm ? (chosen ? ck : -INFINITY) : -INFINITY;
-      if (!a.renorm) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) m = fmaxf(m, key[i]);
+      // relative to the best chosen key, or the row's plain probability
+      if (a.renorm) {
+        const float best = warp_max(chosen ? ck : -INFINITY);
+        w = chosen ? exp_rel(ck, best) : 0.0f;
+        z = warp_sum(w);
+      } else {
+        w = chosen ? exp_rel(ck, mx) : 0.0f;
       }
-      m = warp_max(m);
-      w = chosen ? exp_rel(ck, m) : 0.0f;
-      float z = w;
-      if (!a.renorm) {
-        z = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) z += exp_rel(key[i], m);
-      }
-      z = warp_sum(z);
       w = z > 0.0f ? __fdiv_rn(w, z) : 0.0f;
     } else {
       w = chosen ? cs : 0.0f;
       if (a.renorm) {
-        const float z = warp_sum(w);
-        w = z > 0.0f ? __fdiv_rn(w, z) : 0.0f;
+        const float S = warp_sum(w);
+        w = S > 0.0f ? __fdiv_rn(w, S) : 0.0f;
       }
     }
     if (chosen) {
-      topk_idx[t * k + slot] = ce;
-      topk_w[t * k + slot] = w;
+      topk_idx[t * k + lane] = ce;
+      topk_w[t * k + lane] = w;
     }
   }
   if constexpr (PROB) write_partial<EP>(s_row, warp, e0, col, E, partial);
@@ -396,6 +428,17 @@ __device__ __forceinline__ void spread(float* row, int e0, int lane, int e, floa
   load_floats<float, NV>(row + e0, add);
 }
 
+// The dense gradient's exponentials on the special-function unit: 2 FP32 steps plus |x| / 2
+// (the product with log2 e is rounded), which a gradient of many summed terms absorbs.  With
+// the library's exponential and rounded reciprocal they were a quarter of the kernel's
+// instructions, which bound it (T = 32768, E = 256: MEASURE_BWD us).
+__device__ __forceinline__ float sigmoid_fast(float l) {
+  return (l > -INFINITY) ? __fdividef(1.0f, 1.0f + __expf(-l)) : 0.0f;
+}
+__device__ __forceinline__ float exp_rel_fast(float key, float m) {
+  return key == m ? (m > -INFINITY ? 1.0f : 0.0f) : __expf(key - m);
+}
+
 // DENSE: every expert of a row has a gradient (d_prob, or the plain softmax probability);
 // otherwise only the chosen ones, and only their logits are read.
 template <typename Tin, int EP, int KIND, bool DENSE, bool DBIAS>
@@ -404,6 +447,7 @@ __global__ void __launch_bounds__(kSelThreads, DENSE ? kSelBlocksPerSm : 6) sele
     const float* __restrict__ d_prob, Tin* __restrict__ d_logits, long long ldd,
     float* __restrict__ partial) {
   constexpr int NV = EP / 32;
+  if constexpr (DBIAS) pdl_launch_dependents();
   __shared__ __align__(16) float s_row[kSelWarps][EP];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int e0 = lane * NV;
@@ -422,17 +466,33 @@ __global__ void __launch_bounds__(kSelThreads, DENSE ? kSelBlocksPerSm : 6) sele
 #pragma unroll
     for (int i = 0; i < NV; ++i) col[i] = 0.0f;
   }
-  for (long long t = (long long)blockIdx.x * kSelWarps + warp; t < a.T;
-       t += (long long)gridDim.x * kSelWarps) {
-    const int ej = (lane < k) ? topk_idx[t * k + lane] : -1;
-    const float dj = (lane < k) ? d_w[t * k + lane] : 0.0f;
+  const long long t0 = (long long)blockIdx.x * kSelWarps + warp;
+  const long long stride = (long long)gridDim.x * kSelWarps;
+  // the next token's loads are in flight while this one is computed
+  float next[DENSE ? NV : 1];
+  int next_e = -1;
+  float next_d = 0.0f;
+  auto fetch = [&](long long t) {
+    if (t >= a.T) return;
+    if (lane < k) {
+      next_e = topk_idx[t * k + lane];
+      next_d = d_w[t * k + lane];
+    }
+    if constexpr (DENSE) load_row<Tin, NV>(logits + t * a.ld, e0, E, vec, next);
+  };
+  fetch(t0);
+  for (long long t = t0; t < a.T; t += stride) {
+    const int ej = next_e;
+    const float dj = next_d;
     const bool valid = ej >= 0 && ej < E;
     float d[NV];
     float picked = KIND == 0 ? -INFINITY : 0.0f;  // slot j's key or score, in lane j
     float sc[DENSE ? NV : 1], m = -INFINITY;
     if constexpr (DENSE) {
       float l[NV];
-      load_row<Tin, NV>(logits + t * a.ld, e0, E, vec, l);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) l[i] = next[i];
+      fetch(t + stride);
       // the choice is made: any exponential will do
       __syncwarp();
       if constexpr (KIND == 0) {
@@ -444,12 +504,15 @@ __global__ void __launch_bounds__(kSelThreads, DENSE ? kSelBlocksPerSm : 6) sele
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) sc[i] = sigmoid(l[i]);
+        for (int i = 0; i < NV; ++i) sc[i] = sigmoid_fast(l[i]);
       }
       store_row<EP>(s_row[warp], e0, sc);
       __syncwarp();
       if (valid) picked = s_row[warp][ej];
-    } else if (valid) {
+    } else {
+      fetch(t + stride);
+    }
+    if (!DENSE && valid) {
       const float l = to_float(logits[t * a.ld + ej]);
       if constexpr (KIND == 0) {
         const float v = l + (a.bias != nullptr ? __ldg(a.bias + ej) : 0.0f);
@@ -465,7 +528,7 @@ __global__ void __launch_bounds__(kSelThreads, DENSE ? kSelBlocksPerSm : 6) sele
         float z = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          sc[i] = exp_rel(sc[i], m);
+          sc[i] = exp_rel_fast(sc[i], m);
           z += sc[i];
         }
         z = warp_sum(z);
@@ -542,6 +605,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
   __shared__ float s[32][33];
   const int e = blockIdx.x * 32 + threadIdx.x;
   float v = 0.0f;
+  pdl_wait();  // the partial sums are complete
   if (e < E)
     for (int b = threadIdx.y; b < nb; b += 32) v += partial[(size_t)b * E + e];
   s[threadIdx.y][threadIdx.x] = v;
@@ -571,8 +635,8 @@ cudaError_t fwd_ep(const SelectArgs& a, int32_t* idx, float* w, float* prob_sum,
   select_kernel<Tin, EP, KIND, true><<<nb, kSelThreads, 0, s>>>(a, idx, w, partial);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  column_sum_kernel<<<(a.E + 31) / 32, dim3(32, 32), 0, s>>>(partial, nb, a.E, prob_sum);
-  return cudaGetLastError();
+  return launch_pdl(column_sum_kernel, dim3((a.E + 31) / 32), dim3(32, 32), 0, s,
+                    static_cast<const float*>(partial), nb, a.E, prob_sum);
 }
 
 template <typename Tin, int EP, int KIND>
@@ -591,8 +655,8 @@ cudaError_t bwd_ep(const SelectArgs& a, const int32_t* idx, const float* d_w, co
     const cudaError_t e = dense ? go(select_bwd_kernel<Tin, EP, KIND, true, true>)
                                 : go(select_bwd_kernel<Tin, EP, KIND, false, true>);
     if (e != cudaSuccess) return e;
-    column_sum_kernel<<<(a.E + 31) / 32, dim3(32, 32), 0, s>>>(partial, nb, a.E, d_bias);
-    return cudaGetLastError();
+    return launch_pdl(column_sum_kernel, dim3((a.E + 31) / 32), dim3(32, 32), 0, s,
+                      static_cast<const float*>(partial), nb, a.E, d_bias);
   }
   return cudaErrorInvalidValue;  // the selection-only bias has no gradient
 }
