@@ -172,8 +172,10 @@ cudaError_t launch_mx4_quantize(const void* x, int dtype, long long ld, long lon
 // bf16; 2: silu(gate) * up of x [R, 2K] bf16.
 constexpr int kMx4FewRows = 152 * 16 * 4;  // 16 warps of four rows on every SM
 cudaError_t launch_mx4_rows(const void* x, int dtype, int src, const int32_t* row_of, int k, int T,
-                            const int32_t* offsets, int E, int R, int K, void* codes, void* sf,
-                            int32_t* status, cudaStream_t s);
+                            const int32_t* offsets, int E, int R, int K, int tile_rows, void* codes,
+                            void* sf, int32_t* status, cudaStream_t s);
+// Rows of the largest tile of a product of these sizes.
+int mx4_tile_rows(int E, int R, int N);
 cudaError_t launch_mx4_pack(const void* codes, const void* scales, int E, int K, int N,
                             void* packed, cudaStream_t s);
 cudaError_t launch_mx4_prepack(const void* w, int E, int K, int N, int col0, int N_total,

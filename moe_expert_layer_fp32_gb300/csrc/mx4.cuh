@@ -13,8 +13,9 @@
 // them).
 //   weights  per (expert, 128 output columns, k-block): 16384 bytes of codes, then 1024 of
 //            scales (two halves of the k-block)
-//   rows     the rows of an expert in tiles of at most kMx4TileRows, evenly cut to a multiple
-//            of 16; a tile has a slot of kMx4TileRows rows: its k-blocks follow one another
+//   rows     the rows of an expert in tiles of at most tile_rows (by the form of the product),
+//            evenly cut to a multiple of 16; a tile has a slot of tile_rows rows: its k-blocks
+//            follow one another
 //            (the tile's own padded rows x 128 bytes each).  The scales of a tile's k-block b
 //            are at slot (tile * KB + b) of 2048 bytes, [128-row half][half k-block][512]
 // Padding rows are never written; they only reach accumulator columns that are not stored.
@@ -28,7 +29,9 @@
 namespace moe {
 
 constexpr int kMx4KB = 256;           // values of a k-block: one 128-byte row of codes
-constexpr int kMx4TileRows = 224;     // rows of the largest tile (accumulator columns)
+constexpr int kMx4PairRows = 224;     // rows of the largest tile (accumulator columns) of a
+                                      // pair of CTAs, which batches of many rows run on,
+constexpr int kMx4SingleRows = 64;    // and of a single CTA
 constexpr int kMx4WTile = 128;        // output columns of a weight tile (accumulator lanes)
 constexpr int kMx4WBytes = kMx4WTile * 128 + 1024;  // image of a weight tile's k-block
 constexpr int kMx4SfSlot = 2048;      // scales of a row tile's k-block
@@ -39,7 +42,7 @@ __host__ __device__ inline int mx4_kblocks(int K) { return (K + kMx4KB - 1) / kM
 struct Mx4Cut {
   int n, step;
 };
-__host__ __device__ inline Mx4Cut mx4_cut(int m, int tile_rows = kMx4TileRows) {
+__host__ __device__ inline Mx4Cut mx4_cut(int m, int tile_rows) {
   Mx4Cut c;
   c.n = (m + tile_rows - 1) / tile_rows;
   c.step = c.n > 0 ? ((m + c.n - 1) / c.n + 15) / 16 * 16 : 16;
@@ -47,14 +50,14 @@ __host__ __device__ inline Mx4Cut mx4_cut(int m, int tile_rows = kMx4TileRows) {
 }
 
 // Tiles of R rows among E experts, at most.
-inline long long mx4_max_tiles(long long R, int E, int tile_rows = kMx4TileRows) {
+inline long long mx4_max_tiles(long long R, int E, int tile_rows) {
   const long long with = R < E ? R : E;  // experts that can have rows
   return R / tile_rows + with;
 }
 
 // Bytes of a tile's slot of codes, and of its scales.
-__host__ __device__ inline size_t mx4_slot(int K) {
-  return (size_t)mx4_kblocks(K) * kMx4TileRows * 128;
+__host__ __device__ inline size_t mx4_slot(int K, int tile_rows) {
+  return (size_t)mx4_kblocks(K) * tile_rows * 128;
 }
 __host__ __device__ inline size_t mx4_sf_slots(int K) { return (size_t)mx4_kblocks(K) * kMx4SfSlot; }
 
@@ -70,7 +73,7 @@ struct Mx4Tables {
 
 __device__ __forceinline__ bool mx4_build_tables(Mx4Tables& s, const int32_t* __restrict__ offsets,
                                                  int E, int R, int32_t* status,
-                                                 int tile_rows = kMx4TileRows) {
+                                                 int tile_rows) {
   for (int e = threadIdx.x; e <= E; e += blockDim.x) s.off[e] = offsets[e];
   __syncthreads();
   if (threadIdx.x < 32) {  // one warp scans, 32 experts a step

@@ -74,8 +74,12 @@ moe_status check_mx4(int E, int K, int N) {
 }
 
 // Row images of an operand of R rows over K among E experts: codes, then scales.
-size_t rows_bytes(long long R, int K, int E) { return up(mx4_max_tiles(R, E) * mx4_slot(K)); }
-size_t scales_bytes(long long R, int K, int E) { return up(mx4_max_tiles(R, E) * mx4_sf_slots(K)); }
+size_t rows_bytes(long long R, int K, int E, int tile_rows) {
+  return up(mx4_max_tiles(R, E, tile_rows) * mx4_slot(K, tile_rows));
+}
+size_t images_bytes(long long R, int K, int E, int tile_rows) {
+  return rows_bytes(R, K, E, tile_rows) + up(mx4_max_tiles(R, E, tile_rows) * mx4_sf_slots(K));
+}
 
 // Whether the product of R rows quantises them in its own kernel (no images).
 bool fused(int R, int K) { return K <= kMx4FusedMaxK && R <= kMx4FusedRows; }
@@ -87,7 +91,9 @@ ProductLayout product_layout(int R, int K, int E) {
   ProductLayout L;
   size_t o = 0;
   L.status = o;  o += up(kAlign);
-  L.images = o;  o += fused(R, K) ? 0 : rows_bytes(R, K, E) + scales_bytes(R, K, E);
+  const size_t pair = images_bytes(R, K, E, kMx4PairRows);  // (the form goes by N too)
+  const size_t single = images_bytes(R, K, E, kMx4SingleRows);
+  L.images = o;  o += fused(R, K) ? 0 : (pair > single ? pair : single);
   L.total = o;
   return L;
 }
@@ -102,8 +108,10 @@ moe_status do_product(const void* x, int x_dtype, int src, const int32_t* row_of
                               status, lim, s));
     return MOE_OK;
   }
-  void* sf = at<void>(images, rows_bytes(R, K, E));
-  MOE_CUDA(launch_mx4_rows(x, x_dtype, src, row_of, k, T, offsets, E, R, K, images, sf, status, s));
+  const int tile_rows = mx4_tile_rows(E, R, N);
+  void* sf = at<void>(images, rows_bytes(R, K, E, tile_rows));
+  MOE_CUDA(launch_mx4_rows(x, x_dtype, src, row_of, k, T, offsets, E, R, K, tile_rows, images, sf,
+                           status, s));
   MOE_CUDA(launch_mx4_gemm(packed, images, sf, offsets, E, R, K, N, y, y_dtype, status, lim, s));
   return MOE_OK;
 }

@@ -16,8 +16,8 @@
 //            MMA itself 112.
 //   warps 2-9  epilogue: 32 lanes x 32 columns at a time from tensor memory, two warps a
 //            lane quarter; a warp writes 32 consecutive output columns of one row per store
-// Tensor memory: two accumulators of 224 columns (a unit's epilogue runs under the next
-// one's main loop) and two sets of 24 scale columns, 496 of 512.
+// Tensor memory: two accumulators of up to 224 columns (a unit's epilogue runs under the next
+// one's main loop) and two sets of 24 scale columns, at most 496 of 512.
 //
 // Every wait is bounded and drains as in expert_gemm.cu.
 #include "common.cuh"
@@ -34,14 +34,15 @@ constexpr int kThreads = 320;  // producer, MMA issuer, eight epilogue warps
 // PAIR: two CTAs of a cluster run one MMA (cta_group::2) of 256 output columns.
 template <bool PAIR>
 struct MxCfg {
-  static constexpr int STAGES = PAIR ? 6 : 4;
-  static constexpr int STAGE_ROWS = PAIR ? kMx4TileRows / 2 : kMx4TileRows;
+  static constexpr int TILE_ROWS = PAIR ? kMx4PairRows : kMx4SingleRows;
+  static constexpr int STAGES = PAIR ? 6 : 7;
+  static constexpr int STAGE_ROWS = PAIR ? TILE_ROWS / 2 : TILE_ROWS;
   static constexpr int SF_OFF = kMx4WBytes;                  // row scales
   static constexpr int ROW_OFF = SF_OFF + kMx4SfSlot;        // row codes (1024-byte aligned)
   static constexpr int STAGE_BYTES = ROW_OFF + STAGE_ROWS * 128;
   static constexpr int NBAR = 2 * STAGES + 2 + 2 + 1;
   static constexpr int TMEM_COLS = 512;
-  static constexpr int ACC_COLS = kMx4TileRows;
+  static constexpr int ACC_COLS = TILE_ROWS;
   static constexpr int SF_COL = 2 * ACC_COLS;                // first scale column
   static constexpr int SMEM_BYTES =
       1024 + STAGES * STAGE_BYTES + NBAR * 8 + 16 + (int)sizeof(Mx4Tables) + 16;
@@ -94,7 +95,7 @@ struct MxUnits {
     w.rows = t.rows;
     w.rows16 = t.rows16;
     w.w_img = (size_t)(e * NT + min(w.nt, NT - 1)) * KB * kMx4WBytes;
-    w.row_img = (size_t)tile * KB * (kMx4TileRows * 128);
+    w.row_img = (size_t)tile * KB * (MxCfg<PAIR>::TILE_ROWS * 128);
     w.sf_img = (size_t)tile * KB * kMx4SfSlot;
     return w;
   }
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (PAIR) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
     else tmem_alloc(tmem_slot, C::TMEM_COLS);
   }
-  const bool ok_tables = mx4_build_tables(tb, offsets, E, R, status);
+  const bool ok_tables = mx4_build_tables(tb, offsets, E, R, status, C::TILE_ROWS);
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();  // both CTAs' barriers exist before any remote use
@@ -384,7 +385,7 @@ cudaError_t go(const uint8_t* w, const uint8_t* r, const uint8_t* sf, const int3
     if (dev < 64) cache[dev] = fit;
   }
   const int NT = N / kMx4WTile;
-  const long long units = mx4_max_tiles(R, E) * (PAIR ? (NT + 1) / 2 * 2 : NT);
+  const long long units = mx4_max_tiles(R, E, C::TILE_ROWS) * (PAIR ? (NT + 1) / 2 * 2 : NT);
   cfg.gridDim = dim3((unsigned)(units < fit ? units : fit));
   cfg.stream = s;
   cfg.attrs = attr;
@@ -395,12 +396,14 @@ cudaError_t go(const uint8_t* w, const uint8_t* r, const uint8_t* sf, const int3
 
 }  // namespace
 
-// Pairs halve the rows' bytes that each SM takes in, which bound the single form (64 bytes a
-// clock); a batch of few rows is bound by its weights.  Every output element is the same
-// sequence of MMAs in both forms, so its bits do not depend on the choice.
+// Pairs share the rows' bytes that a single CTA takes in alone (64 bytes a clock bound the main
+// loop of large tiles); a batch of few rows is bound by its weights, and single CTAs with a
+// deeper ring stream them faster.  Every output element is the same sequence of MMAs in both
+// forms, so its bits do not depend on the choice.
 static bool use_pair(int E, int R, int N) {
   return N >= 2 * kMx4WTile && (long long)R >= 64LL * (R < E ? R : E);
 }
+int mx4_tile_rows(int E, int R, int N) { return use_pair(E, R, N) ? kMx4PairRows : kMx4SingleRows; }
 
 cudaError_t launch_mx4_gemm(const void* packed, const void* codes, const void* sf,
                             const int32_t* offsets, int E, int R, int K, int N, void* y,

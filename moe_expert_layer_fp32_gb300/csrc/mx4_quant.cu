@@ -75,11 +75,11 @@ constexpr int kRowsBlocksPerSm = 4;
 template <typename Tin, int SRC>
 __global__ void __launch_bounds__(kQThreads, kRowsBlocksPerSm) quantize_rows_kernel(
     const Tin* __restrict__ x, const int32_t* __restrict__ row_of, int k, int T,
-    const int32_t* __restrict__ offsets, int E, int R, int K, uint8_t* __restrict__ codes,
-    uint8_t* __restrict__ sf, int32_t* status) {
+    const int32_t* __restrict__ offsets, int E, int R, int K, int tile_rows,
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, int32_t* status) {
   __shared__ Mx4Tables tb;
   pdl_launch_dependents();  // the product reads this kernel's images only after its own wait
-  if (!mx4_build_tables(tb, offsets, E, R, status)) return;
+  if (!mx4_build_tables(tb, offsets, E, R, status, tile_rows)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int KB = mx4_kblocks(K);
   const long long items = (long long)tb.tile[E] * 64;  // (tile, half, rr)
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kQThreads, kRowsBlocksPerSm) quantize_rows_ker
     const int nr = min(4, (t.rows - r0 + 31) / 32);
     const int row0 = t.row0 + r0;
     // (rows 32 apart have the same row & 7)
-    uint8_t* cdst = codes + tile * mx4_slot(K) + r0 * 128 + (((lane >> 2) ^ (rr & 7)) * 16) +
+    uint8_t* cdst = codes + tile * mx4_slot(K, tile_rows) + r0 * 128 + (((lane >> 2) ^ (rr & 7)) * 16) +
                     (lane & 3) * 4;
     uint8_t* sdst = sf + tile * mx4_sf_slots(K) + half * 1024 + rr * 16 + (lane >> 4) * 512;
     const Tin* src[4];
@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(kQThreads, kRowsBlocksPerSm) quantize_rows_ker
 template <typename Tin, int SRC>
 __global__ void __launch_bounds__(kQThreads) quantize_few_rows_kernel(
     const Tin* __restrict__ x, const int32_t* __restrict__ row_of, int k, int T,
-    const int32_t* __restrict__ offsets, int E, int R, int K, uint8_t* __restrict__ codes,
-    uint8_t* __restrict__ sf, int32_t* status) {
+    const int32_t* __restrict__ offsets, int E, int R, int K, int tile_rows,
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, int32_t* status) {
   __shared__ Mx4Tables tb;
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_few_rows_kernel(
   P v;
   const Tin* row = r < R ? source_row<Tin, SRC>(x, row_of, k, T, K, r, status) : x;
   load_piece<Tin, SRC>(v, row, col, K, in);
-  if (!mx4_build_tables(tb, offsets, E, R, status) || r >= R) return;
+  if (!mx4_build_tables(tb, offsets, E, R, status, tile_rows) || r >= R) return;
   const int e = mx4_find(tb.off, E, r);
   const int local = r - tb.off[e], step = tb.step[e];
   const int ti = local / step, rt = local - ti * step;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_few_rows_kernel(
                      (__shfl_down_sync(0xFFFFFFFFu, byte, 8) << 16) |
                      (__shfl_down_sync(0xFFFFFFFFu, byte, 12) << 24);
   if (!in) return;
-  uint8_t* cdst = codes + (tb.tile[e] + ti) * mx4_slot(K) + (size_t)kb * rows16 * 128 + rt * 128;
+  uint8_t* cdst = codes + (tb.tile[e] + ti) * mx4_slot(K, tile_rows) + (size_t)kb * rows16 * 128 + rt * 128;
   *reinterpret_cast<uint32_t*>(cdst + (((lane >> 2) ^ (rt & 7)) * 16) + (lane & 3) * 4) = c;
   if ((lane & 15) == 0)
     *reinterpret_cast<uint32_t*>(sf + ((size_t)(tb.tile[e] + ti) * KB + kb) * kMx4SfSlot +
@@ -260,21 +260,21 @@ cudaError_t launch_mx4_quantize(const void* x, int dtype, long long ld, long lon
 }
 
 cudaError_t launch_mx4_rows(const void* x, int dtype, int src, const int32_t* row_of, int k, int T,
-                            const int32_t* offsets, int E, int R, int K, void* codes, void* sf,
-                            int32_t* status, cudaStream_t s) {
+                            const int32_t* offsets, int E, int R, int K, int tile_rows, void* codes,
+                            void* sf, int32_t* status, cudaStream_t s) {
   if (R == 0) return cudaSuccess;
   uint8_t* c = static_cast<uint8_t*>(codes);
   uint8_t* f = static_cast<uint8_t*>(sf);
   const bool few = R < kMx4FewRows;
-  const long long warps = few ? (long long)R * mx4_kblocks(K) : mx4_max_tiles(R, E) * 64;
+  const long long warps = few ? (long long)R * mx4_kblocks(K) : mx4_max_tiles(R, E, tile_rows) * 64;
   const long long need = (warps + kQWarps - 1) / kQWarps;
   const long long most = few ? need : (long long)device_sm_count() * kRowsBlocksPerSm;
   const int grid = (int)(need < most ? need : most);
   auto go = [&](auto many, auto few_rows, auto* p) {
     if (few)
-      few_rows<<<grid, kQThreads, 0, s>>>(p, row_of, k, T, offsets, E, R, K, c, f, status);
+      few_rows<<<grid, kQThreads, 0, s>>>(p, row_of, k, T, offsets, E, R, K, tile_rows, c, f, status);
     else
-      many<<<grid, kQThreads, 0, s>>>(p, row_of, k, T, offsets, E, R, K, c, f, status);
+      many<<<grid, kQThreads, 0, s>>>(p, row_of, k, T, offsets, E, R, K, tile_rows, c, f, status);
     return cudaGetLastError();
   };
 #define MOE_MX4_ROWS(Tin, SRC) \

@@ -107,6 +107,12 @@ __device__ __forceinline__ float exp_rel(float key, float m) {
   return key == m ? 1.0f : expf(key - m);
 }
 
+// exp_rel on the special-function unit: within 2 FP32 steps plus |key - m| / 2 (the product
+// with log2 e is rounded), for sums of many terms
+__device__ __forceinline__ float exp_rel_fast(float key, float m) {
+  return key == m ? (m > -INFINITY ? 1.0f : 0.0f) : __expf(key - m);
+}
+
 // 1 / (1 + exp(-l)), 0 where masked: the gradient's sigmoid, with the library's exponential
 __device__ __forceinline__ float sigmoid(float l) {
   return (l > -INFINITY) ? __frcp_rn(__fadd_rn(1.0f, expf(-l))) : 0.0f;
@@ -191,7 +197,9 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
       float p[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        p[i] = (KIND == 0) ? exp_rel(key[i], mx) : sc[i];
+        // (with renorm they only make prob_sum)
+        if constexpr (KIND == 0) p[i] = a.renorm ? exp_rel_fast(key[i], mx) : exp_rel(key[i], mx);
+        else p[i] = sc[i];
         z += p[i];
       }
       z = warp_sum(z);
@@ -434,9 +442,6 @@ __device__ __forceinline__ void spread(float* row, int e0, int lane, int e, floa
 // instructions, which bound it (T = 32768, E = 256: MEASURE_BWD us).
 __device__ __forceinline__ float sigmoid_fast(float l) {
   return (l > -INFINITY) ? __fdividef(1.0f, 1.0f + __expf(-l)) : 0.0f;
-}
-__device__ __forceinline__ float exp_rel_fast(float key, float m) {
-  return key == m ? (m > -INFINITY ? 1.0f : 0.0f) : __expf(key - m);
 }
 
 // DENSE: every expert of a row has a gradient (d_prob, or the plain softmax probability);
