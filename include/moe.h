@@ -420,8 +420,8 @@ moe_status moe_router_logits(const void* x, const float* w_router, const float* 
  * A logit (or key) of -inf or NaN masks its expert: key -inf, score 0, left out of
  * group sums (a group of masked experts scores -inf); masked experts are chosen only
  * when nothing else is left.  A row whose chosen scores are all 0 gets weights 0.
- * +inf keys share the probability 1 among them for the first of the chosen.
- * Sigmoid scores below FP32's range (logits below about -88) are 0. */
+ * Softmax keys of +inf share the probability equally.  Sigmoid scores below FP32's
+ * range (logits below about -88) are 0. */
 typedef struct {
   int32_t kind;        /* moe_router_kind */
   int32_t n_group;     /* 1..32, divides E */
