@@ -23,6 +23,10 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
+from . import _tensor_calls as _calls  # noqa: E402  (built with the library; needs torch loaded)
+
+_calls.bind(LIB_PATH)
+
 MOE_OK = 0
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_MISALIGNED",
           4: "MOE_ERR_WORKSPACE", 5: "MOE_ERR_CUDA", 6: "MOE_ERR_TIMEOUT",
@@ -586,8 +590,10 @@ def _on_device(first, *rest):
         raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{_get_device()}")
 
 
-# The tensor calls below go to the library directly: on small batches the host's part of a
-# call is longer than the kernel's.
+# The tensor calls below first try _tensor_calls, which makes the whole call for arguments of
+# the plain kind (dense tensors on the current device and stream); it returns None for others,
+# which are then handled or refused here.  On small batches the host's part of a call is longer
+# than the kernel's.
 def _logits_args(logits, bias):
     """(type code, row stride, T, E) of logits [T, E]; refuses what a kernel would misread."""
     dt = _DTYPES.get(logits.dtype)
@@ -598,9 +604,18 @@ def _logits_args(logits, bias):
     else:
         ld, T = _rows("logits", logits), logits.shape[0]
     E = logits.shape[1]
+    if T >= 1 << 31:
+        raise ValueError(f"logits: at most 2^31 - 1 tokens, not {T}")
     if bias is not None:
         _dense("bias", bias, torch.float32, (E,))
     return dt, ld, T, E
+
+
+def _made(name, r):
+    """What a _tensor_calls function returned: its result, or the status of a refusal."""
+    if type(r) is int:
+        _check(name, r)
+    return r
 
 
 _default_opts = select_opts()
@@ -609,6 +624,11 @@ _default_opts = select_opts()
 def route_select(logits, k, opts=None, bias=None, want_prob_sum=False, stream=None):
     """(topk_idx [T, k] int32, topk_w [T, k] fp32[, prob_sum [E] fp32]) from logits [T, E]
     (fp32, bf16 or fp16).  opts: a select_opts (default: softmax over all experts)."""
+    if opts is None:
+        opts = _default_opts
+    r = _calls.route_select(logits, k, opts, bias, bool(want_prob_sum), stream)
+    if r is not None:
+        return _made("moe_route_select", r)
     dt, ld, T, E = _logits_args(logits, bias)
     _on_device(logits, bias)
     dev = logits.device
@@ -623,7 +643,7 @@ def route_select(logits, k, opts=None, bias=None, want_prob_sum=False, stream=No
         pp, wp = prob.data_ptr(), ws.data_ptr()
     r = _lib.moe_route_select(
         logits.data_ptr(), dt, ld, None if bias is None else bias.data_ptr(),
-        ctypes.byref(_default_opts if opts is None else opts), T, E, k, idx.data_ptr(),
+        ctypes.byref(opts), T, E, k, idx.data_ptr(),
         w.data_ptr(), pp, wp, n, _stream(stream))
     if r:
         _check("moe_route_select", r)
@@ -634,6 +654,12 @@ def route_select_backward(logits, topk_idx, d_topk_w, opts=None, bias=None, d_pr
                           want_d_bias=False, stream=None):
     """d_logits [T, E] in the logits' type (and d_bias [E] fp32 if want_d_bias, softmax only)
     for d_topk_w [T, k] and, if given, d_prob_sum [E], both fp32; the choice stays fixed."""
+    if opts is None:
+        opts = _default_opts
+    r = _calls.route_select_backward(logits, topk_idx, d_topk_w, opts, bias, d_prob_sum,
+                                     bool(want_d_bias), stream)
+    if r is not None:
+        return _made("moe_route_select_bwd", r)
     dt, ld, T, E = _logits_args(logits, bias)
     if topk_idx.dim() != 2:
         raise ValueError(f"topk_idx: [T, k], not {tuple(topk_idx.shape)}")
@@ -654,7 +680,7 @@ def route_select_backward(logits, topk_idx, d_topk_w, opts=None, bias=None, d_pr
         bp, wp = d_bias.data_ptr(), ws.data_ptr()
     r = _lib.moe_route_select_bwd(
         logits.data_ptr(), dt, ld, None if bias is None else bias.data_ptr(),
-        ctypes.byref(_default_opts if opts is None else opts), T, E, k, topk_idx.data_ptr(),
+        ctypes.byref(opts), T, E, k, topk_idx.data_ptr(),
         d_topk_w.data_ptr(), None if d_prob_sum is None else d_prob_sum.data_ptr(),
         d_logits.data_ptr(), E, bp, wp, n, _stream(stream))
     if r:
@@ -665,6 +691,9 @@ def route_select_backward(logits, topk_idx, d_topk_w, opts=None, bias=None, d_pr
 def mx4_quantize(x, want_values=False, stream=None):
     """(codes [R, K/2] uint8, scales [R, K/32] uint8[, values [R, K] bf16]) of rows x [R, K]
     (fp32, bf16 or fp16), K a multiple of 32."""
+    r = _calls.mx4_quantize(x, bool(want_values), stream)
+    if r is not None:
+        return _made("moe_mx4_quantize", r)
     dt, ld, R, K = _x_args(x)
     dev = x.device
     codes = torch.empty((R, K // 2), dtype=torch.uint8, device=dev)
@@ -745,12 +774,19 @@ def mx4_new_workspace(R, K, N, E, device="cuda") -> torch.Tensor:
 def mx4_expert_product(x, offsets, packed, N, workspace, dtype=torch.bfloat16, stream=None):
     """y [R, N] (bf16 or fp32): rows x [R, K] of each expert (offsets [E+1] int32) quantised to
     microscaled 4 bits, times the expert's packed weights."""
+    if dtype is torch.bfloat16 or dtype is torch.float32:
+        r = _calls.mx4_expert_product(x, offsets, packed, N, workspace, dtype is torch.bfloat16,
+                                      stream)
+        if r is not None:
+            return _made("moe_mx4_expert_product", r)
     if x.dim() != 2 or not x.is_contiguous():
         raise ValueError(f"x: a dense [R, K] tensor, not {tuple(x.shape)} strides {x.stride()}")
     dt = _dtype("x", x)
     if offsets.dim() != 1:
         raise ValueError(f"offsets: [E + 1], not {tuple(offsets.shape)}")
     E, (R, K) = offsets.numel() - 1, x.shape
+    if R >= 1 << 31:
+        raise ValueError(f"x: at most 2^31 - 1 rows, not {R}")
     _dense("offsets", offsets, torch.int32, (E + 1,))
     if packed.numel() * packed.element_size() != moe_mx4_packed_bytes(E, K, N):
         raise ValueError(f"packed: {packed.numel() * packed.element_size()} bytes, not those of "

@@ -1,6 +1,7 @@
 """Builds libmoe_gb300.so (the C ABI of include/moe.h) from csrc/ with nvcc for
 sm_103a, in-tree.  One nvcc process per translation unit, run in parallel, then
-one link.  Usage: ``python moe_expert_layer_fp32_gb300/build.py [--force] [-v]``
+one link; beside them g++ builds _tensor_calls.so (csrc/tensor_calls.cpp, the
+tensor calls' fast path) against torch's headers.  Usage: ``python moe_expert_layer_fp32_gb300/build.py [--force] [-v]``
 (run it by path: importing the package itself needs the built library)."""
 from __future__ import annotations
 
@@ -16,6 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build", "moe_gb300")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
+CALLS_SRC = os.path.join(CSRC, "tensor_calls.cpp")
+CALLS = os.path.join(PKG, "_tensor_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -52,10 +55,27 @@ def built_for_this_machine(path: str) -> bool:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not built_for_this_machine(LIB):
+    if not built_for_this_machine(LIB) or not built_for_this_machine(CALLS):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in sources() + headers() + [__file__])
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
+    return all(os.path.getmtime(p) <= t for p in sources() + headers() + [CALLS_SRC, __file__])
+
+
+def build_calls() -> str:
+    import sysconfig
+    from torch.utils import cpp_extension
+    inc = cpp_extension.include_paths() + [
+        sysconfig.get_paths()["include"], os.path.join(os.path.dirname(nvcc()), "..", "include"),
+        os.path.join(ROOT, "include")]
+    tmp = CALLS + f".tmp{os.getpid()}"
+    r = subprocess.run(
+        [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", CALLS_SRC, "-o", tmp,
+         *["-I" + i for i in inc], *["-L" + d for d in cpp_extension.library_paths()], "-lc10",
+         "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ldl"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -76,8 +96,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        results = list(ex.map(compile_one, sources()))
+    # (the longest first: the routers, then the rest)
+    order = sorted(sources(), key=os.path.getsize, reverse=True)
+    with cf.ThreadPoolExecutor(max_workers=min(12, os.cpu_count() or 1)) as ex:
+        calls = ex.submit(build_calls)
+        results = list(ex.map(compile_one, sorted(order, key=lambda p: "route" not in p)))
+        calls.result()
     if verbose:
         for obj, log in results:
             sys.stderr.write(log)

@@ -14,10 +14,10 @@
 //   weights  per (expert, 128 output columns, k-block): 16384 bytes of codes, then 1024 of
 //            scales (two halves of the k-block)
 //   rows     the rows of an expert in tiles of at most tile_rows (by the form of the product),
-//            evenly cut to a multiple of 16; a tile has a slot of tile_rows rows: its k-blocks
-//            follow one another
-//            (the tile's own padded rows x 128 bytes each).  The scales of a tile's k-block b
-//            are at slot (tile * KB + b) of 2048 bytes, [128-row half][half k-block][512]
+//            evenly cut to a multiple of 16; a tile has a slot of tile_rows rows, in which its
+//            k-blocks follow one another (the tile's own padded rows x 128 bytes each).  The
+//            scales of a tile's k-block b are at slot (tile * KB + b) of 2048 bytes,
+//            [128-row half][half k-block][512]
 // Padding rows are never written; they only reach accumulator columns that are not stored.
 #pragma once
 
@@ -44,8 +44,8 @@ struct Mx4Cut {
 };
 __host__ __device__ inline Mx4Cut mx4_cut(int m, int tile_rows) {
   Mx4Cut c;
-  c.n = (m + tile_rows - 1) / tile_rows;
-  c.step = c.n > 0 ? ((m + c.n - 1) / c.n + 15) / 16 * 16 : 16;
+  c.n = m / tile_rows + (m % tile_rows != 0);
+  c.step = c.n > 0 ? (m / c.n + (m % c.n != 0) + 15) / 16 * 16 : 16;
   return c;
 }
 

@@ -40,7 +40,7 @@ struct MxCfg {
   static constexpr int SF_OFF = kMx4WBytes;                  // row scales
   static constexpr int ROW_OFF = SF_OFF + kMx4SfSlot;        // row codes (1024-byte aligned)
   static constexpr int STAGE_BYTES = ROW_OFF + STAGE_ROWS * 128;
-  static constexpr int NBAR = 2 * STAGES + 2 + 2 + 1;
+  static constexpr int NBAR = 3 * STAGES + 2 + 2 + 1;
   static constexpr int TMEM_COLS = 512;
   static constexpr int ACC_COLS = TILE_ROWS;
   static constexpr int SF_COL = 2 * ACC_COLS;                // first scale column
@@ -103,8 +103,8 @@ struct MxUnits {
 
 // Pair form: every CTA loads its own weight tile, its half of the rows' codes and all of
 // their scales, completing on its own `full` barrier; the odd CTA's idle MMA warp passes its
-// completions on to the even CTA's barrier (a bulk copy can only signal the CTA it writes),
-// whose MMA thread runs both tensor cores.  Commits free the stage in both CTAs.
+// completions on to `odd_full` of the even CTA (a bulk copy can only signal the CTA it
+// writes), whose MMA thread runs both tensor cores.  Commits free the stage in both CTAs.
 template <typename Tout, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     mx4_gemm_kernel(const uint8_t* __restrict__ wimg, const uint8_t* __restrict__ rimg,
@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::STAGES * C::STAGE_BYTES);
   uint64_t* full = bars;
   uint64_t* empty = bars + C::STAGES;
-  uint64_t* tfull = bars + 2 * C::STAGES;
+  uint64_t* odd_full = bars + 2 * C::STAGES;  // even CTA of a pair: the odd CTA's stages
+  uint64_t* tfull = bars + 3 * C::STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
@@ -133,8 +134,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], (PAIR && rank == 0) ? 2 : 1);  // its producer (and the odd CTA's relay)
+      mbar_init(&full[s], 1);                            // its producer
       mbar_init(&empty[s], 1);                           // the MMA's commit
+      mbar_init(&odd_full[s], 1);                        // the odd CTA's relay
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);                           // the MMA's commit
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // CTA-scope release: the bytes are in this SM's shared memory, which only its own
             // tensor core reads; a cluster-scope release took about 1500 cycles a stage
-            mbar_arrive_remote(mapa_shared(smem_u32(&full[s]), 0));
+            mbar_arrive_remote(mapa_shared(smem_u32(&odd_full[s]), 0));
           }
         }
       }
@@ -258,7 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int s = it % C::STAGES;
           const uint32_t ph = (it / C::STAGES) & 1;
-          if (!mbar_wait_bounded(&full[s], ph, abort_flag, status, spin_limit)) {
+          if (!mbar_wait_bounded(&full[s], ph, abort_flag, status, spin_limit) ||
+              (PAIR && !mbar_wait_bounded(&odd_full[s], ph, abort_flag, status, spin_limit))) {
             aborted = true;
             break;
           }

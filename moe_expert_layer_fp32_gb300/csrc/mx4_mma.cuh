@@ -1,5 +1,4 @@
-// Device steps that the grouped 4-bit products share: bulk copies, bounded waits with cluster
-// scope, and the block-scaled MMA (tcgen05 kind::mxf4) of one CTA or of a pair.
+// Device steps that the grouped 4-bit products share: bulk copies and the block-scaled MMA (tcgen05 kind::mxf4) of one CTA or of a pair.
 #pragma once
 
 #include "common.cuh"
@@ -13,36 +12,6 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, P;\n\t}"
       : "=r"(p));
   return p != 0;
-}
-
-// mbar_wait_bounded with cluster-scope acquire: the even CTA's full barriers also count the
-// odd CTA's arrivals.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-template <bool PAIR>
-__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          int32_t* status, long long limit) {
-  if constexpr (!PAIR) return mbar_wait_bounded(bar, parity, abort, status, limit);
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if (*abort) return false;
-    if (clock64() - t0 > limit) {
-      *abort = 1;
-      flag_error(status, MOE_ERR_TIMEOUT);
-      return false;
-    }
-  }
 }
 
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes,

@@ -78,6 +78,20 @@ def test_quantize_strides_outputs_and_empty(moe):
     assert c.shape == (0, 32) and s.shape == (0, 2)
 
 
+def test_quantize_past_32_bits(moe):
+    """More than 2^31 elements: the last rows are quantised as they are alone."""
+    R, K = 1_100_000, 2048
+    x = torch.empty((R, K), dtype=torch.bfloat16, device="cuda")
+    tile = torch.randn((1000, K), device="cuda").to(torch.bfloat16)
+    for r in range(0, R, 1000):
+        x[r:r + 1000].copy_(tile)
+    x[-7:] = torch.randn((7, K), device="cuda").to(torch.bfloat16) * 3
+    codes, scales, values = moe.mx4_quantize(x, want_values=True)
+    c, s, v = moe.mx4_quantize(x[-1000:], want_values=True)
+    assert torch.equal(codes[-1000:], c) and torch.equal(scales[-1000:], s)
+    assert torch.equal(values[-1000:], v)
+
+
 def weights(E, K, N, seed):
     """(codes [E, N, K/2], scales [E, N, K/32], values [E, N, K]) with scales over 2^-10 .. 2^4."""
     g = np.random.default_rng(seed)
@@ -193,6 +207,21 @@ def test_product_row_alone(moe):
         assert torch.equal(y1[0], y[r])
 
 
+def test_product_past_32_bits(moe):
+    """An output of more than 2^31 elements: the last expert's rows are those they are alone."""
+    R, K, N, E = 540_000, 128, 4096, 5
+    codes, scales, _ = weights(E, K, N, 6)
+    packed = moe.mx4_pack(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda())
+    x = torch.randn((R, K), device="cuda").to(torch.bfloat16)
+    off = torch.tensor([0, 130_000, 400_001, 400_001, R - 500, R], dtype=torch.int32, device="cuda")
+    ws = moe.mx4_new_workspace(R, K, N, E)
+    y = moe.mx4_expert_product(x, off, packed, N, ws)
+    assert moe.moe_read_device_status(ws) == 0
+    for e, a, b in ((4, R - 500, R), (3, R - 700, R - 500), (0, 0, 100)):
+        o = torch.tensor([0] * (e + 1) + [b - a] * (E - e), dtype=torch.int32, device="cuda")
+        assert torch.equal(moe.mx4_expert_product(x[a:b], o, packed, N, ws), y[a:b])
+
+
 def test_product_nan_stays_in_its_row(moe):
     K, N, E = 256, 128, 2
     codes, scales, wv = weights(E, K, N, 9)
@@ -224,6 +253,31 @@ def test_bad_offsets_are_flagged(moe):
     assert moe.moe_read_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("R,K", [(512, 256), (64, 512)])  # images and a product; one kernel
+def test_wait_timeout_is_reported_and_context_survives(moe, R, K):
+    """The products' bounded waits run out under a limit far below a copy's round trip: the call
+    reports it, and the next one is right.  (N = 128: single CTAs.)"""
+    E, N = 4, 128
+    codes, scales, _ = weights(E, K, N, 5)
+    packed = moe.mx4_pack(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda())
+    x = rows(R, K, 1, "bf16").cuda()
+    off = torch.tensor([0, 7, 7, R - 9, R], dtype=torch.int32, device="cuda")
+    ws = moe.mx4_new_workspace(R, K, N, E)
+    want = moe.mx4_expert_product(x, off, packed, N, ws)
+    assert moe.moe_read_device_status(ws) == 0
+    statuses = []
+    try:
+        moe.moe_set_wait_limit(16)
+        for _ in range(3):
+            moe.mx4_expert_product(x, off, packed, N, ws)
+            statuses.append(moe.moe_read_device_status(ws))
+    finally:
+        moe.moe_set_wait_limit(0)
+    assert 6 in statuses and set(statuses) <= {0, 6}, statuses
+    assert torch.equal(moe.mx4_expert_product(x, off, packed, N, ws), want)
+    assert moe.moe_read_device_status(ws) == 0
+
+
 def test_prepack_is_quantize_and_pack(moe):
     E, K, N = 3, 384, 256
     g = torch.Generator().manual_seed(8)
@@ -235,6 +289,34 @@ def test_prepack_is_quantize_and_pack(moe):
     want = moe.mx4_pack(codes.view(E, N + 128, K // 2), scales.view(E, N + 128, K // 32))
     assert torch.equal(moe.mx4_prepack(w, w2), want)
     assert torch.equal(moe.mx4_prepack(both), want)
+
+
+def test_both_ways_of_calling(moe):
+    """The native fast path (current stream) and the Python path (a stream given) are one call."""
+    K, N, E, R = 256, 128, 3, 70
+    codes, scales, _ = weights(E, K, N, 2)
+    packed = moe.mx4_pack(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda())
+    off = torch.tensor([0, 30, 30, R], dtype=torch.int32, device="cuda")
+    ws = moe.mx4_new_workspace(R, K, N, E)
+    s = torch.cuda.current_stream()
+    for dt in ("bf16", "f16", "f32"):
+        x = rows(R, K, 3, dt, spread=1.0).cuda()
+        for out in (torch.bfloat16, torch.float32):
+            a = moe.mx4_expert_product(x, off, packed, N, ws, out)
+            b = moe.mx4_expert_product(x, off, packed, N, ws, out, stream=s)
+            assert a.dtype == b.dtype == out and torch.equal(a, b)
+        for want in (False, True):
+            q = [moe.mx4_quantize(x, want, stream=t) for t in (None, s)]
+            assert len(q[0]) == len(q[1]) == 2 + want and all(torch.equal(a, b) for a, b in zip(*q))
+    for t in (None, s):
+        with pytest.raises(moe.MoEError):      # K not a multiple of 32
+            moe.mx4_quantize(x[:, :40].contiguous(), stream=t)
+        with pytest.raises(moe.MoEError):      # a workspace of another size
+            moe.mx4_expert_product(x, off, packed, N, ws[:64], stream=t)
+    with pytest.raises(ValueError, match="packed"):
+        moe.mx4_expert_product(x, off, packed[256:], N, ws)
+    with pytest.raises(TypeError, match="y:"):
+        moe.mx4_expert_product(x, off, packed, N, ws, torch.float16)
 
 
 def test_stream_and_graph(moe):

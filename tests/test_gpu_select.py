@@ -258,6 +258,33 @@ def test_empty_batch_stream_and_graph(moe):
     assert torch.equal(dgot, moe.route_select_backward(l, want[0], dw))
 
 
+def test_both_ways_of_calling(moe):
+    """The native fast path (current stream) and the Python path (a stream given) are one call."""
+    l = torch.randn((33, 64), device="cuda")
+    b = torch.randn(64, device="cuda")
+    s = torch.cuda.current_stream()
+    for kind in (0, 1):
+        o = moe.select_opts(kind, 8, 3, 2)
+        a = moe.route_select(l, 4, o, bias=b, want_prob_sum=True)
+        c = moe.route_select(l, 4, o, bias=b, want_prob_sum=True, stream=s)
+        assert all(torch.equal(p, q) and p.dtype == q.dtype for p, q in zip(a, c)) and len(a) == len(c) == 3
+        assert len(moe.route_select(l, 4)) == len(moe.route_select(l, 4, stream=s)) == 2
+        dw, g = torch.randn((33, 4), device="cuda"), torch.randn(64, device="cuda")
+        for want in (False, True) if kind == 0 else (False,):
+            r = [moe.route_select_backward(l, a[0], dw, o, bias=b, d_prob_sum=g, want_d_bias=want, stream=x)
+                 for x in (None, s)]
+            r = [x if want else (x,) for x in r]
+            assert all(torch.equal(p, q) for p, q in zip(*r))
+    for bad in (dict(k=65), dict(k=4, opts=moe.select_opts(7))):
+        for x in (None, s):
+            with pytest.raises(moe.MoEError):
+                moe.route_select(l, stream=x, **bad)
+    with pytest.raises(ValueError, match="bias"):
+        moe.route_select(l, 4, bias=b[:32])
+    with pytest.raises(ValueError, match="overlap"):
+        moe.route_select(l[:1].expand(3, 64), 4)
+
+
 def test_large_batch_is_its_rows(moe):
     """Every token's choice, weights and gradient are those it has alone in another batch."""
     T, E, k = 20011, 256, 8
@@ -273,3 +300,19 @@ def test_large_batch_is_its_rows(moe):
         assert torch.equal(i2, idx[r]) and torch.equal(w2, w[r])
         assert torch.equal(moe.route_select_backward(l[r].contiguous(), i2, dw[r].contiguous(), o,
                                                      bias=b), d[r])
+
+
+def test_past_32_bits(moe):
+    """Logits of more than 2^31 elements: the last tokens are those they are alone."""
+    T, E, k = 8_400_000, 256, 4
+    l = torch.empty((T, E), dtype=torch.bfloat16, device="cuda")
+    tile = torch.randn((10_000, E), device="cuda").to(torch.bfloat16)
+    for t in range(0, T, 10_000):
+        l[t:t + 10_000].copy_(tile)
+    l[-9:] = torch.randn((9, E), device="cuda").to(torch.bfloat16)
+    idx, w = moe.route_select(l, k)
+    i2, w2 = moe.route_select(l[-500:], k)
+    assert torch.equal(idx[-500:], i2) and torch.equal(w[-500:], w2)
+    dw = torch.randn((T, k), device="cuda")
+    d = moe.route_select_backward(l, idx, dw)
+    assert torch.equal(d[-500:], moe.route_select_backward(l[-500:], i2, dw[-500:].contiguous()))
