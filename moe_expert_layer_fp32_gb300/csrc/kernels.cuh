@@ -185,18 +185,6 @@ cudaError_t launch_mx4_gemm(const void* packed, const void* codes, const void* s
                             const int32_t* offsets, int E, int R, int K, int N, void* y,
                             int y_dtype, int32_t* status, long long spin_limit, cudaStream_t s);
 
-// Both steps in one kernel, K <= kMx4FusedMaxK (mx4_fused.cu), used up to kMx4FusedRows rows.
-// src as launch_mx4_rows; src 1 writes bf16 and src 2 FP32 rows.  Measured on GB300, K = N =
-// 2048, one kernel against two: 8 rows of 8 experts 12.8 against 18.0 us called from Python
-// (the second launch costs the host more than the kernel takes), 7.4 against 6.6 us in a CUDA
-// graph; 64 rows of 64 experts 29.7 against 29.7 us; 512 rows of 8 experts 13.6 against 9.1 us.
-constexpr int kMx4FusedMaxK = 2048;
-constexpr int kMx4FusedRows = 128;
-cudaError_t launch_mx4_fused(const void* x, int dtype, int src, const int32_t* row_of, int k, int T,
-                             const void* packed, const int32_t* offsets, int E, int R, int K, int N,
-                             void* y, int y_dtype, int32_t* status, long long spin_limit,
-                             cudaStream_t s);
-
 // The limit of the GEMM kernels' bounded waits now in force (moe_set_wait_limit).
 long long wait_limit();
 

@@ -81,9 +81,6 @@ size_t images_bytes(long long R, int K, int E, int tile_rows) {
   return rows_bytes(R, K, E, tile_rows) + up(mx4_max_tiles(R, E, tile_rows) * mx4_sf_slots(K));
 }
 
-// Whether the product of R rows quantises them in its own kernel (no images).
-bool fused(int R, int K) { return K <= kMx4FusedMaxK && R <= kMx4FusedRows; }
-
 struct ProductLayout {
   size_t status, images, total;
 };
@@ -93,21 +90,16 @@ ProductLayout product_layout(int R, int K, int E) {
   L.status = o;  o += up(kAlign);
   const size_t pair = images_bytes(R, K, E, kMx4PairRows);  // (the form goes by N too)
   const size_t single = images_bytes(R, K, E, kMx4SingleRows);
-  L.images = o;  o += fused(R, K) ? 0 : (pair > single ? pair : single);
+  L.images = o;  o += pair > single ? pair : single;
   L.total = o;
   return L;
 }
 
-// The grouped product of quantised rows (sources as launch_mx4_rows), in one kernel or two.
+// The grouped product of quantised rows (sources as launch_mx4_rows).
 moe_status do_product(const void* x, int x_dtype, int src, const int32_t* row_of, int k, int T,
                       const int32_t* offsets, const void* packed, int E, int R, int K, int N,
                       void* y, int y_dtype, void* images, int32_t* status, cudaStream_t s) {
   const long long lim = wait_limit();
-  if (fused(R, K)) {
-    MOE_CUDA(launch_mx4_fused(x, x_dtype, src, row_of, k, T, packed, offsets, E, R, K, N, y, y_dtype,
-                              status, lim, s));
-    return MOE_OK;
-  }
   const int tile_rows = mx4_tile_rows(E, R, N);
   void* sf = at<void>(images, rows_bytes(R, K, E, tile_rows));
   MOE_CUDA(launch_mx4_rows(x, x_dtype, src, row_of, k, T, offsets, E, R, K, tile_rows, images, sf,

@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       pdl_wait();
+      pdl_launch_dependents();  // (whatever comes next waits for this kernel itself)
       int it = 0;
       bool aborted = false;
       for (; units.more() && !aborted; units.advance()) {

@@ -1,4 +1,4 @@
-// Device steps that the grouped 4-bit products share: bulk copies and the block-scaled MMA (tcgen05 kind::mxf4) of one CTA or of a pair.
+// Device steps of the grouped 4-bit product: bulk copies and the block-scaled MMA (tcgen05 kind::mxf4) of one CTA or of a pair.
 #pragma once
 
 #include "common.cuh"

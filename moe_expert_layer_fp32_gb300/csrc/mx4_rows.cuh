@@ -1,5 +1,5 @@
-// Device steps of the 4-bit row quantisation that the row-image kernels and the fused product
-// share: pieces of eight values, their block maxima and codes, and where a row comes from.
+// Device steps of the 4-bit row quantisation: pieces of eight values, their block maxima and
+// codes, and where a row comes from.
 #pragma once
 
 #include <type_traits>

@@ -253,7 +253,7 @@ def test_bad_offsets_are_flagged(moe):
     assert moe.moe_read_device_status(ws) == 0
 
 
-@pytest.mark.parametrize("R,K", [(512, 256), (64, 512)])  # images and a product; one kernel
+@pytest.mark.parametrize("R,K", [(512, 256), (64, 512)])
 def test_wait_timeout_is_reported_and_context_survives(moe, R, K):
     """The products' bounded waits run out under a limit far below a copy's round trip: the call
     reports it, and the next one is right.  (N = 128: single CTAs.)"""
