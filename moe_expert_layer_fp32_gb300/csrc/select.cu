@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
                                                              float* __restrict__ partial) {
   constexpr int NV = EP / 32;
   if constexpr (PROB) pdl_launch_dependents();  // the column sums, which wait for this kernel
-  __shared__ __align__(16) float s_row[kSelWarps][EP];  // the keys; later the candidates' scores
+  __shared__ __align__(16) float s_row[kSelWarps][EP];  // keys
+  __shared__ __align__(16) float s_score[KIND == 1 ? kSelWarps : 1][KIND == 1 ? EP : 4];
   __shared__ __align__(16) uint32_t s_key[kSelWarps][32];  // candidates in expert order
   __shared__ int s_expert[kSelWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -281,11 +282,13 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
     for (int i = 0; i < NV; ++i) top = fmaxf(top, key[i]);
     if (!lane_in) top = -INFINITY;
     int mine, before, n;
+    unsigned mask;  // this lane's candidates
     auto count = [&]() {
-      mine = 0;
+      mask = 0u;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) mine += key[i] >= bound;
-      if (top < bound) mine = 0;  // (a lane outside the groups that stay)
+      for (int i = 0; i < NV; ++i) mask |= (key[i] >= bound ? 1u : 0u) << i;
+      if (top < bound) mask = 0u;  // (a lane outside the groups that stay)
+      mine = __popc(mask);
       before = mine;  // inclusive scan: candidates in expert order
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -314,25 +317,15 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
     float ck = -INFINITY, cs = 0.0f;
     if (n >= k && n <= 32) {
       // one candidate a lane, ranked against the others
-      s_key[warp][lane] = 0u;
-      if constexpr (KIND == 1) store_row<EP>(s_row[warp], e0, sc);
+      store_row<EP>(s_row[warp], e0, key);
+      if constexpr (KIND == 1) store_row<EP>(s_score[warp], e0, sc);
+      for (; mask != 0u; mask &= mask - 1u) s_expert[warp][before++] = e0 + __ffs(mask) - 1;
       __syncwarp();
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (mine > 0 && key[i] >= bound) {
-          s_key[warp][before] = float_key(key[i]);
-          s_expert[warp][before] = e0 + i;
-          ++before;
-        }
-      }
+      const int mine_e = lane < n ? s_expert[warp][lane] : 0;
+      const uint32_t cu = lane < n ? float_key(s_row[warp][mine_e]) : 0u;
+      s_key[warp][lane] = cu;
       __syncwarp();
-      const uint32_t cu = s_key[warp][lane];
-      int slot = 32;  // this lane's candidate's (k or more: not chosen)
-      if (lane < n) {
-        ce = s_expert[warp][lane];
-        if constexpr (KIND == 1) cs = s_row[warp][ce];
-        slot = 0;
-      }
+      int slot = lane < n ? 0 : 32;  // this lane's candidate's (k or more: not chosen)
       for (int j = 0; j < n; j += 4) {
         const uint4 o = *reinterpret_cast<const uint4*>(&s_key[warp][j]);
         slot += (o.x > cu || (o.x == cu && j + 0 < lane)) ? 1 : 0;
@@ -341,17 +334,12 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
         slot += (o.w > cu || (o.w == cu && j + 3 < lane)) ? 1 : 0;
       }
       // slot j to lane j, so that sums over the chosen are in slot order
-      __syncwarp();
-      if (slot < k) {
-        s_key[warp][slot] = cu;
-        s_expert[warp][slot] = ce;
-        if constexpr (KIND == 1) s_row[warp][slot] = cs;
-      }
+      if (slot < k) s_expert[warp][slot] = mine_e;
       __syncwarp();
       if (lane < k) {
-        ck = key_float(s_key[warp][lane]);
         ce = s_expert[warp][lane];
-        if constexpr (KIND == 1) cs = s_row[warp][lane];
+        ck = s_row[warp][ce];
+        if constexpr (KIND == 1) cs = s_score[warp][ce];
       }
       __syncwarp();
     } else {
