@@ -72,22 +72,51 @@ __device__ __forceinline__ void load_row(const Tin* row, int e0, int E, bool vec
 }
 
 // key and score of the lane's experts.  KIND 0: score is left to the caller (it needs
-// the row's maximum); masked experts and those past E have key -inf and score 0.  b is the
-// bias as lane_bias made it, so a sum with it is never -0 (which would order below +0).
+// the row's maximum); masked experts and those past E (of the lane's NV, `inside` are within)
+// have key -inf and score 0.  b is the bias as lane_bias made it, so a sum with it is never -0 (which would order below +0).
 template <int KIND, int NV>
-__device__ __forceinline__ void keys_of(const float (&l)[NV], const float (&b)[NV], float (&key)[NV],
-                                        float (&sc)[NV]) {
+__device__ __forceinline__ void keys_of(const float (&l)[NV], const float (&b)[NV], int inside,
+                                        float (&key)[NV], float (&sc)[NV]) {
   if constexpr (KIND == 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const float v = __fadd_rn(l[i], b[i]);
-      key[i] = (v > -INFINITY) ? v : -INFINITY;
+      key[i] = fmaxf(__fadd_rn(l[i], b[i]), -INFINITY);  // (a maximum drops NaN)
       sc[i] = 0.0f;
     }
   } else {
+    // A row whose logits are all numbers within +-80 (nearly every one) needs no limits and
+    // no masks: comparisons and selections issue at half the rate of the arithmetic.  (0 l is
+    // not 0 for an infinity or a NaN.)
+    float zero = 0.0f, big = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      zero = fmaf(l[i], 0.0f, zero);
+      big = fmaxf(big, fabsf(l[i]));
+    }
+    const bool plain = inside == 0 || (inside == NV && zero == 0.0f && big <= 80.0f);
+    if (__all_sync(kFull, plain)) {
+#pragma unroll
+      for (int i = 0; i < NV; i += 2) {
+        const float2 s = sigmoid_steps2<false>(l[i], l[NV > 1 ? i + 1 : i]);
+        sc[i] = s.x;
+        key[i] = __fadd_rn(s.x, b[i]);
+        if (NV > 1) {
+          sc[NV > 1 ? i + 1 : i] = s.y;
+          key[NV > 1 ? i + 1 : i] = __fadd_rn(s.y, b[NV > 1 ? i + 1 : i]);
+        }
+      }
+      if (inside == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          key[i] = -INFINITY;
+          sc[i] = 0.0f;
+        }
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < NV; i += 2) {
-      const float2 s = sigmoid_steps2(l[i], l[NV > 1 ? i + 1 : i]);
+      const float2 s = sigmoid_steps2<true>(l[i], l[NV > 1 ? i + 1 : i]);
       sc[i] = s.x;
       if (NV > 1) sc[NV > 1 ? i + 1 : i] = s.y;
     }
@@ -194,7 +223,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
 
   for (long long t = t0; t < a.T; t += stride) {
     float key[NV], sc[NV];
-    keys_of<KIND, NV>(l, b, key, sc);
+    keys_of<KIND, NV>(l, b, inside, key, sc);
     if (t + stride < a.T) load_row<Tin, NV>(logits + (t + stride) * a.ld, e0, E, vec, l);
     // the row's softmax: its maximum and the sum relative to it (sigmoid: the sum of scores)
     float mx = -INFINITY, z = 0.0f;
@@ -204,11 +233,12 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
         for (int i = 0; i < NV; ++i) mx = fmaxf(mx, key[i]);
         mx = warp_max(mx);
       }
+      // (with renorm they only make prob_sum, a sum of many terms: the special-function unit)
+      const bool fast = a.renorm && fabsf(mx) < INFINITY;
       float p[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        // (with renorm they only make prob_sum)
-        if constexpr (KIND == 0) p[i] = a.renorm ? exp_rel_fast(key[i], mx) : exp_rel(key[i], mx);
+        if constexpr (KIND == 0) p[i] = fast ? __expf(key[i] - mx) : exp_rel(key[i], mx);
         else p[i] = sc[i];
         z += p[i];
       }

@@ -27,8 +27,12 @@ __device__ __forceinline__ float key_float(uint32_t u) {
 // (whose low bits are then the integer), their ldexp an addition to the exponent: with -l
 // held to [-80, 89] (below, exp(-l) vanishes in 1 + exp(-l)) the integer is in [-115, 128],
 // so half the result is a normal number, and the factor 2 joins the final sum exactly.
+// CLAMP: false where the caller has seen |l| <= 80.
+template <bool CLAMP>
 __device__ __forceinline__ float2 sigmoid_steps2(float l0, float l1) {
-  const float2 x = make_float2(fminf(fmaxf(-l0, -80.0f), 89.0f), fminf(fmaxf(-l1, -80.0f), 89.0f));
+  float2 x = make_float2(-l0, -l1);
+  if constexpr (CLAMP)
+    x = make_float2(fminf(fmaxf(x.x, -80.0f), 89.0f), fminf(fmaxf(x.y, -80.0f), 89.0f));
   auto both = [](float c) { return make_float2(c, c); };
   const float2 t = __fmul2_rn(x, both(1.44269502162933349609375f));
   const float2 m = __fadd2_rn(t, both(12582912.0f));
