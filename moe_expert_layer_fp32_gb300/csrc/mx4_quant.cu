@@ -7,7 +7,11 @@
 // divides exactly, so the only rounding is the one to the code.
 //
 // Memory-bound: 8 values a lane (one or two 16-byte loads), four lanes a block whose
-// maximum meets in two shuffles; a warp covers one row's 256-value k-block.
+// maximum meets in two shuffles; a warp covers one row's 256-value k-block.  Measured on GB300:
+// 32768 x 4096 bf16 rows with their values 90 us for 608 MB, the copy rate (four pieces in
+// flight a thread and values by byte permutes: 127 us without); the row images of 131072 x
+// 2048 117 us (ncu) for 537 MB read and 285 written, of which half is still in L2 when the
+// product starts; integer instructions are next (ALU pipe two thirds busy).
 #include <type_traits>
 
 #include "common.cuh"

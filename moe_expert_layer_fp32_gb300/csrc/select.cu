@@ -23,15 +23,17 @@
 // so that chosen experts far below the row's largest logit keep their precision.
 //
 // One warp per token, EP/32 consecutive experts per lane; 32 warps an SM at 64 registers.
-// What each has to move is one pass over the logits (T = 32768, E = 256 in FP32: 34 MB, 5 us);
-// what bounds the selection is its instructions, about 900 a token and warp, issued in three
-// of four cycles.  Measured on GB300 at that size, sigmoid scores, 8 of 256 experts from 4 of 8
-// groups, with prob_sum: 38.5 us in a CUDA graph, of which the sigmoids take 6, the groups 4,
-// the choice of eight instead of one 5, prob_sum 5.5, the rest (loads, keys, ranking, weights,
-// launches) 18.  The steps that brought it there from 81 us: candidates above a bound of the
-// k-th key ranked side by side instead of k argmax rounds over all keys (45), two sigmoids an
-// instruction and group maxima in registers (40), the next token's loads in flight (38.5).
-// The gradient with every expert's share: 18.4 us for 67 MB (10 us), latency and issue.
+// What each has to move is one pass over the logits (T = 32768, E = 256 in FP32: 34 MB, 5 us).
+// What bounds the selection is its instructions, some 900 a token and warp, issued in three of
+// four cycles; comparisons, selections and integers issue at half the rate of the arithmetic.
+// Measured on GB300 at that size, sigmoid scores, 8 of 256 experts from 4 of 8 groups, in a
+// CUDA graph: 30.4 us, with prob_sum 35.6; of it the sigmoids take 5, the groups 4, the choice
+// of eight instead of one 3.5.  The steps that brought it there from 81 us: candidates above a
+// bound of the k-th key ranked side by side instead of k argmax rounds over all keys (45), two
+// sigmoids an instruction and group maxima in registers (40), the next token's loads in flight
+// (38.5), candidates by a lane mask (37.4), no limits and masks for plain rows (35.6).  Three
+// heads a lane and k rounds of warp maxima instead of bound and ranks took 45.9.
+// The gradient with every expert's share: 18.3 us for 67 MB (10 us), latency and issue.
 #include <math.h>
 
 #include <type_traits>
