@@ -439,7 +439,8 @@ size_t moe_select_workspace_bytes(int32_t T, int32_t E);
  *          rows that are not are read element by element)
  *   bias [E] fp32 or NULL; topk_idx [T, k] int32 and topk_w [T, k] fp32 out
  *   prob_sum [E] fp32 out or NULL: the sum over tokens of score[e] / (sum of all E
- *          scores), what a load-balance loss is made of; needs the workspace
+ *          scores), what a load-balance loss is made of, added in FP32 in an order that
+ *          T fixes; needs the workspace
  * 1 <= E <= 256, 1 <= k <= min(E, 16).  The routing scale belongs to the combine. */
 moe_status moe_route_select(const void* logits, int32_t dtype, int64_t ld, const float* bias,
                             const moe_select_opts* opts, int32_t T, int32_t E, int32_t k,
@@ -454,7 +455,8 @@ moe_status moe_route_select(const void* logits, int32_t dtype, int64_t ld, const
  *   topk_idx [T, k] as moe_route_select wrote it (ids outside [0, E) contribute
  *   nothing); d_topk_w [T, k] fp32; d_prob_sum [E] fp32 or NULL
  *   d_bias [E] fp32 out or NULL, softmax kind only (its bias joins the logits): the
- *   column sums of the gradient in FP32, in a fixed order; needs the workspace. */
+ *   column sums of the gradient in FP32, in an order that T fixes; needs the
+ *   workspace. */
 moe_status moe_route_select_bwd(const void* logits, int32_t dtype, int64_t ld, const float* bias,
                                 const moe_select_opts* opts, int32_t T, int32_t E, int32_t k,
                                 const int32_t* topk_idx, const float* d_topk_w,
