@@ -590,6 +590,15 @@ def _on_device(first, *rest):
         raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{_get_device()}")
 
 
+def _on_stream(stream):
+    """Context in which `stream` (a torch stream or an address) is current: what a call
+    allocates then belongs to the stream that its kernels run on."""
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream) if stream
+                  else torch.cuda.default_stream())
+    return torch.cuda.stream(stream)
+
+
 # The tensor calls below first try _tensor_calls, which makes the whole call for arguments of
 # the plain kind (dense tensors on the current device and stream); it returns None for others,
 # which are then handled or refused here.  On small batches the host's part of a call is longer
@@ -624,9 +633,12 @@ _default_opts = select_opts()
 def route_select(logits, k, opts=None, bias=None, want_prob_sum=False, stream=None):
     """(topk_idx [T, k] int32, topk_w [T, k] fp32[, prob_sum [E] fp32]) from logits [T, E]
     (fp32, bf16 or fp16).  opts: a select_opts (default: softmax over all experts)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return route_select(logits, k, opts, bias, want_prob_sum)
     if opts is None:
         opts = _default_opts
-    r = _calls.route_select(logits, k, opts, bias, bool(want_prob_sum), stream)
+    r = _calls.route_select(logits, k, opts, bias, bool(want_prob_sum))
     if r is not None:
         return _made("moe_route_select", r)
     dt, ld, T, E = _logits_args(logits, bias)
@@ -654,10 +666,14 @@ def route_select_backward(logits, topk_idx, d_topk_w, opts=None, bias=None, d_pr
                           want_d_bias=False, stream=None):
     """d_logits [T, E] in the logits' type (and d_bias [E] fp32 if want_d_bias, softmax only)
     for d_topk_w [T, k] and, if given, d_prob_sum [E], both fp32; the choice stays fixed."""
+    if stream is not None:
+        with _on_stream(stream):
+            return route_select_backward(logits, topk_idx, d_topk_w, opts, bias, d_prob_sum,
+                                         want_d_bias)
     if opts is None:
         opts = _default_opts
     r = _calls.route_select_backward(logits, topk_idx, d_topk_w, opts, bias, d_prob_sum,
-                                     bool(want_d_bias), stream)
+                                     bool(want_d_bias))
     if r is not None:
         return _made("moe_route_select_bwd", r)
     dt, ld, T, E = _logits_args(logits, bias)
@@ -691,7 +707,10 @@ def route_select_backward(logits, topk_idx, d_topk_w, opts=None, bias=None, d_pr
 def mx4_quantize(x, want_values=False, stream=None):
     """(codes [R, K/2] uint8, scales [R, K/32] uint8[, values [R, K] bf16]) of rows x [R, K]
     (fp32, bf16 or fp16), K a multiple of 32."""
-    r = _calls.mx4_quantize(x, bool(want_values), stream)
+    if stream is not None:
+        with _on_stream(stream):
+            return mx4_quantize(x, want_values)
+    r = _calls.mx4_quantize(x, bool(want_values))
     if r is not None:
         return _made("moe_mx4_quantize", r)
     dt, ld, R, K = _x_args(x)
@@ -722,6 +741,9 @@ def _x_args(x):
 
 def mx4_pack(codes, scales, stream=None) -> torch.Tensor:
     """Packed operand from checkpoint tensors codes [E, N, K/2] and scales [E, N, K/32]."""
+    if stream is not None:
+        with _on_stream(stream):
+            return mx4_pack(codes, scales)
     if codes.dim() != 3:
         raise ValueError(f"codes: [E, N, K/2], not {tuple(codes.shape)}")
     E, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
@@ -739,6 +761,9 @@ def mx4_pack(codes, scales, stream=None) -> torch.Tensor:
 def mx4_prepack(*weights, stream=None) -> torch.Tensor:
     """Packed operand from bf16 weights [E, K, N_i] in the logical layout, quantised along K;
     several (gate, up) lie side by side in one operand of sum(N_i) columns."""
+    if stream is not None:
+        with _on_stream(stream):
+            return mx4_prepack(*weights)
     if not weights or any(w.dim() != 3 for w in weights):
         raise ValueError("weights: one or more [E, K, N] tensors")
     E, K = weights[0].shape[:2]
@@ -774,9 +799,11 @@ def mx4_new_workspace(R, K, N, E, device="cuda") -> torch.Tensor:
 def mx4_expert_product(x, offsets, packed, N, workspace, dtype=torch.bfloat16, stream=None):
     """y [R, N] (bf16 or fp32): rows x [R, K] of each expert (offsets [E+1] int32) quantised to
     microscaled 4 bits, times the expert's packed weights."""
+    if stream is not None:
+        with _on_stream(stream):
+            return mx4_expert_product(x, offsets, packed, N, workspace, dtype)
     if dtype is torch.bfloat16 or dtype is torch.float32:
-        r = _calls.mx4_expert_product(x, offsets, packed, N, workspace, dtype is torch.bfloat16,
-                                      stream)
+        r = _calls.mx4_expert_product(x, offsets, packed, N, workspace, dtype is torch.bfloat16)
         if r is not None:
             return _made("moe_mx4_expert_product", r)
     if x.dim() != 2 or not x.is_contiguous():
@@ -812,6 +839,10 @@ def mx4_layer_forward(x, w_router, bias, packed_gate_up, packed_down, d, workspa
                       route_scale=1.0, want_routing=False, stream=None):
     """out [T, H] bf16 (and topk_idx, topk_w, counts if want_routing) of the layer with
     microscaled 4-bit experts."""
+    if stream is not None:
+        with _on_stream(stream):
+            return mx4_layer_forward(x, w_router, bias, packed_gate_up, packed_down, d, workspace,
+                                     opts, route_scale, want_routing)
     dev = x.device
     out = torch.empty((d.T, d.H), dtype=torch.bfloat16, device=dev)
     idx = w = counts = None

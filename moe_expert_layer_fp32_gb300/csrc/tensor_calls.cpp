@@ -71,11 +71,8 @@ bool maybe(PyObject* o, at::Tensor& t) {
   return true;
 }
 
-// The current stream's, for None
-bool stream_of(PyObject* o, int device, void*& s) {
-  if (o != Py_None) return false;
-  s = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
-  return true;
+void* current_stream(int device) {
+  return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
 }
 
 // A moe_select_opts structure (through the buffer protocol)
@@ -112,16 +109,15 @@ PyObject* pack(std::initializer_list<at::Tensor> ts) {
   return r;
 }
 
-// (logits, k, opts, bias, want_prob_sum, stream)
+// (logits, k, opts, bias, want_prob_sum)
 PyObject* route_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   at::Tensor l, bias;
   int dt, dev;
   int64_t k;
   moe_select_opts o;
-  void* s;
-  if (n != 6 || !matrix(a[0], l, dt, dev) || !int_of(a[1], k) || !opts_of(a[2], o) ||
-      !maybe(a[3], bias) || !stream_of(a[5], dev, s))
+  if (n != 5 || !matrix(a[0], l, dt, dev) || !int_of(a[1], k) || !opts_of(a[2], o) ||
+      !maybe(a[3], bias))
     Py_RETURN_NONE;
   const int64_t T = l.size(0), E = l.size(1);
   if (bias.defined() && !plain(bias, at::kFloat, dev, {E})) Py_RETURN_NONE;
@@ -134,22 +130,22 @@ PyObject* route_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const int r = lib.route_select(l.data_ptr(), dt, E, (const float*)ptr(bias), &o, (int32_t)T,
                                  (int32_t)E, (int32_t)k, (int32_t*)idx.data_ptr(),
-                                 (float*)w.data_ptr(), (float*)ptr(prob), ptr(ws), bytes, s);
+                                 (float*)w.data_ptr(), (float*)ptr(prob), ptr(ws), bytes,
+                                 current_stream(dev));
   if (r != MOE_OK) return PyLong_FromLong(r);
   return prob.defined() ? pack({idx, w, prob}) : pack({idx, w});
   END_HANDLE_TH_ERRORS
 }
 
-// (logits, topk_idx, d_topk_w, opts, bias, d_prob_sum, want_d_bias, stream)
+// (logits, topk_idx, d_topk_w, opts, bias, d_prob_sum, want_d_bias)
 PyObject* route_select_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   at::Tensor l, idx, dw, bias, dp;
   int dt, dev;
   moe_select_opts o;
-  void* s;
-  if (n != 8 || !matrix(a[0], l, dt, dev) || a[1] == Py_None || !maybe(a[1], idx) ||
+  if (n != 7 || !matrix(a[0], l, dt, dev) || a[1] == Py_None || !maybe(a[1], idx) ||
       a[2] == Py_None || !maybe(a[2], dw) || !opts_of(a[3], o) || !maybe(a[4], bias) ||
-      !maybe(a[5], dp) || !stream_of(a[7], dev, s))
+      !maybe(a[5], dp))
     Py_RETURN_NONE;
   const int64_t T = l.size(0), E = l.size(1);
   if (!plain(idx, at::kInt, dev, {T, -1})) Py_RETURN_NONE;
@@ -167,39 +163,37 @@ PyObject* route_select_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int r = lib.route_select_bwd(
       l.data_ptr(), dt, E, (const float*)ptr(bias), &o, (int32_t)T, (int32_t)E, (int32_t)k,
       (const int32_t*)idx.data_ptr(), (const float*)dw.data_ptr(), (const float*)ptr(dp),
-      d.data_ptr(), E, (float*)ptr(db), ptr(ws), bytes, s);
+      d.data_ptr(), E, (float*)ptr(db), ptr(ws), bytes, current_stream(dev));
   if (r != MOE_OK) return PyLong_FromLong(r);
   return db.defined() ? pack({d, db}) : THPVariable_Wrap(d);
   END_HANDLE_TH_ERRORS
 }
 
-// (x, want_values, stream)
+// (x, want_values)
 PyObject* mx4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   at::Tensor x;
   int dt, dev;
-  void* s;
-  if (n != 3 || !matrix(a[0], x, dt, dev) || !stream_of(a[2], dev, s)) Py_RETURN_NONE;
+  if (n != 2 || !matrix(a[0], x, dt, dev)) Py_RETURN_NONE;
   const int64_t R = x.size(0), K = x.size(1);
   at::Tensor codes = make({R, K / 2}, at::kByte, dev), scales = make({R, K / 32}, at::kByte, dev), values;
   if (a[1] == Py_True) values = make({R, K}, at::kBFloat16, dev);
   const int r = lib.mx4_quantize(x.data_ptr(), dt, K, R, (int32_t)K, codes.data_ptr(),
-                                 scales.data_ptr(), ptr(values), s);
+                                 scales.data_ptr(), ptr(values), current_stream(dev));
   if (r != MOE_OK) return PyLong_FromLong(r);
   return values.defined() ? pack({codes, scales, values}) : pack({codes, scales});
   END_HANDLE_TH_ERRORS
 }
 
-// (x, offsets, packed, N, workspace, bf16, stream)
+// (x, offsets, packed, N, workspace, bf16)
 PyObject* mx4_expert_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   at::Tensor x, off, packed, ws;
   int dt, dev;
   int64_t N;
-  void* s;
-  if (n != 7 || !matrix(a[0], x, dt, dev) || a[1] == Py_None || !maybe(a[1], off) ||
+  if (n != 6 || !matrix(a[0], x, dt, dev) || a[1] == Py_None || !maybe(a[1], off) ||
       a[2] == Py_None || !maybe(a[2], packed) || !int_of(a[3], N) || a[4] == Py_None ||
-      !maybe(a[4], ws) || !stream_of(a[6], dev, s))
+      !maybe(a[4], ws))
     Py_RETURN_NONE;
   if (!plain(off, at::kInt, dev, {-1}) || off.size(0) < 2 || !plain(packed, at::kByte, dev, {-1}) ||
       !plain(ws, at::kByte, dev, {-1}))
@@ -212,7 +206,7 @@ PyObject* mx4_expert_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int r = lib.mx4_expert_product(x.data_ptr(), dt, (const int32_t*)off.data_ptr(),
                                        packed.data_ptr(), (int32_t)R, (int32_t)K, (int32_t)N,
                                        (int32_t)E, y.data_ptr(), bf16 ? MOE_DTYPE_BF16 : MOE_DTYPE_F32,
-                                       ws.data_ptr(), (size_t)ws.size(0), s);
+                                       ws.data_ptr(), (size_t)ws.size(0), current_stream(dev));
   if (r != MOE_OK) return PyLong_FromLong(r);
   return THPVariable_Wrap(y);
   END_HANDLE_TH_ERRORS

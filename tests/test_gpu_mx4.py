@@ -292,27 +292,35 @@ def test_prepack_is_quantize_and_pack(moe):
 
 
 def test_both_ways_of_calling(moe):
-    """The native fast path (current stream) and the Python path (a stream given) are one call."""
+    """The native fast path and the Python path (a workspace of another type, rows of a wider
+    tensor) are one call, on the current stream and on one that is given."""
     K, N, E, R = 256, 128, 3, 70
     codes, scales, _ = weights(E, K, N, 2)
     packed = moe.mx4_pack(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda())
     off = torch.tensor([0, 30, 30, R], dtype=torch.int32, device="cuda")
     ws = moe.mx4_new_workspace(R, K, N, E)
-    s = torch.cuda.current_stream()
+    side = torch.cuda.Stream()
     for dt in ("bf16", "f16", "f32"):
-        x = rows(R, K, 3, dt, spread=1.0).cuda()
+        wide = rows(R, K + 64, 3, dt, spread=1.0).cuda()
+        v = wide[:, :K]
+        x = v.contiguous()
+        side.wait_stream(torch.cuda.current_stream())
         for out in (torch.bfloat16, torch.float32):
             a = moe.mx4_expert_product(x, off, packed, N, ws, out)
-            b = moe.mx4_expert_product(x, off, packed, N, ws, out, stream=s)
-            assert a.dtype == b.dtype == out and torch.equal(a, b)
+            for w, s in ((ws.view(torch.int32), None), (ws, side), (ws.view(torch.int32), side.cuda_stream)):
+                torch.cuda.synchronize()  # one workspace
+                b = moe.mx4_expert_product(x, off, packed, N, w, out, stream=s)
+                torch.cuda.synchronize()
+                assert a.dtype == b.dtype == out and torch.equal(a, b)
         for want in (False, True):
-            q = [moe.mx4_quantize(x, want, stream=t) for t in (None, s)]
-            assert len(q[0]) == len(q[1]) == 2 + want and all(torch.equal(a, b) for a, b in zip(*q))
-    for t in (None, s):
+            q = [moe.mx4_quantize(t, want, stream=s) for t, s in ((x, None), (v, None), (x, side), (v, side))]
+            torch.cuda.synchronize()
+            assert all(len(c) == 2 + want and all(torch.equal(a, b) for a, b in zip(q[0], c)) for c in q)
+    for s in (None, side):
         with pytest.raises(moe.MoEError):      # K not a multiple of 32
-            moe.mx4_quantize(x[:, :40].contiguous(), stream=t)
-        with pytest.raises(moe.MoEError):      # a workspace of another size
-            moe.mx4_expert_product(x, off, packed, N, ws[:64], stream=t)
+            moe.mx4_quantize(x[:, :40].contiguous(), stream=s)
+        with pytest.raises(moe.MoEError):      # a workspace too small
+            moe.mx4_expert_product(x, off, packed, N, ws[:256], stream=s)
     with pytest.raises(ValueError, match="packed"):
         moe.mx4_expert_product(x, off, packed[256:], N, ws)
     with pytest.raises(TypeError, match="y:"):

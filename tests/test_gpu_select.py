@@ -259,26 +259,34 @@ def test_empty_batch_stream_and_graph(moe):
 
 
 def test_both_ways_of_calling(moe):
-    """The native fast path (current stream) and the Python path (a stream given) are one call."""
-    l = torch.randn((33, 64), device="cuda")
+    """The native fast path (dense rows) and the Python path (rows of a wider tensor) are one call,
+    on the current stream and on one that is given."""
+    wide = torch.randn((33, 72), device="cuda")
+    v = wide[:, :64]
+    l = v.contiguous()
     b = torch.randn(64, device="cuda")
-    s = torch.cuda.current_stream()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ways = [(l, None), (v, None), (l, side), (v, side), (l, side.cuda_stream)]
     for kind in (0, 1):
         o = moe.select_opts(kind, 8, 3, 2)
-        a = moe.route_select(l, 4, o, bias=b, want_prob_sum=True)
-        c = moe.route_select(l, 4, o, bias=b, want_prob_sum=True, stream=s)
-        assert all(torch.equal(p, q) and p.dtype == q.dtype for p, q in zip(a, c)) and len(a) == len(c) == 3
-        assert len(moe.route_select(l, 4)) == len(moe.route_select(l, 4, stream=s)) == 2
-        dw, g = torch.randn((33, 4), device="cuda"), torch.randn(64, device="cuda")
+        r = [moe.route_select(x, 4, o, bias=b, want_prob_sum=True, stream=s) for x, s in ways]
+        torch.cuda.synchronize()
+        for c in r[1:]:
+            assert len(c) == 3 and all(torch.equal(p, q) and p.dtype == q.dtype for p, q in zip(r[0], c))
+        assert all(len(moe.route_select(x, 4, stream=s)) == 2 for x, s in ways)
+        idx, dw, g = r[0][0], torch.randn((33, 4), device="cuda"), torch.randn(64, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
         for want in (False, True) if kind == 0 else (False,):
-            r = [moe.route_select_backward(l, a[0], dw, o, bias=b, d_prob_sum=g, want_d_bias=want, stream=x)
-                 for x in (None, s)]
+            r = [moe.route_select_backward(x, idx, dw, o, bias=b, d_prob_sum=g, want_d_bias=want, stream=s)
+                 for x, s in ways]
+            torch.cuda.synchronize()
             r = [x if want else (x,) for x in r]
-            assert all(torch.equal(p, q) for p, q in zip(*r))
+            assert all(torch.equal(p, q) for c in r[1:] for p, q in zip(r[0], c))
     for bad in (dict(k=65), dict(k=4, opts=moe.select_opts(7))):
-        for x in (None, s):
+        for x, s in ways:
             with pytest.raises(moe.MoEError):
-                moe.route_select(l, stream=x, **bad)
+                moe.route_select(x, stream=s, **bad)
     with pytest.raises(ValueError, match="bias"):
         moe.route_select(l, 4, bias=b[:32])
     with pytest.raises(ValueError, match="overlap"):
