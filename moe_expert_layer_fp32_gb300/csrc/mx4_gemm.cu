@@ -28,12 +28,15 @@
 // for rows and weights.  What the steps brought, packed case with its row images: single CTAs
 // of 224 rows 346 us; pairs 323; units walked without searches and divisions on the issuing
 // thread (1900 cycles a unit before, hidden now) 294 -> 280; what a unit touches first moved
-// into L2 ahead 277.  Not kept: the rows' images made and multiplied chunk by chunk side by
+// into L2 ahead 277; the odd CTA's bytes counted by the even one, three tensor loads a k-block in
+// place of its own bulk copies and a relay without cluster scope, 288.  Not kept: the rows' images made and multiplied chunk by chunk side by
 // side (no gain: every product's start and drain cost what the overlap saved), every CTA
 // prefetching its next unit (six CTAs ask for the same rows: 198 -> 240), quantising inside
 // this kernel (457 us: too few warps for the loads beside the tensor core's share of memory).
 //
 // Every wait is bounded and drains as in expert_gemm.cu.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.cuh"
 #include "mx4.cuh"
@@ -54,7 +57,7 @@ struct MxCfg {
   static constexpr int SF_OFF = kMx4WBytes;                  // row scales
   static constexpr int ROW_OFF = SF_OFF + kMx4SfSlot;        // row codes (1024-byte aligned)
   static constexpr int STAGE_BYTES = ROW_OFF + STAGE_ROWS * 128;
-  static constexpr int NBAR = 3 * STAGES + 2 + 2 + 1;
+  static constexpr int NBAR = 2 * STAGES + 2 + 2 + 1;
   static constexpr int TMEM_COLS = 512;
   static constexpr int ACC_COLS = TILE_ROWS;
   static constexpr int SF_COL = 2 * ACC_COLS;                // first scale column
@@ -115,13 +118,32 @@ struct MxUnits {
   }
 };
 
+// The images as matrices of 1024-byte lines (every image, tile and half tile is whole lines), for
+// the odd CTA of a pair: boxes of a weight image, of one and of two lines of scales, and of each
+// height that a half tile can have (16 n rows: n lines).  A map per height, so that a k-block
+// is three loads: with heights of 8, 4, 2 and 1 lines (up to six loads) the packed case took 321 us
+// against 288; the lines' width (128 to 1024 bytes) made no difference.
+constexpr int kMxHeights = kMx4PairRows / 16;
+struct MxPairMaps {
+  CUtensorMap w, sf[2], rows[kMxHeights];
+};
+struct MxNoMaps {};
+static_assert(kMx4WBytes % 1024 == 0 && kMx4SfSlot == 2048 && kMx4PairRows % 16 == 0 &&
+                  sizeof(MxPairMaps) <= 3840,
+              "whole lines; kernel parameters");
+
 // Pair form: every CTA loads its own weight tile, its half of the rows' codes and all of
-// their scales, completing on its own `full` barrier; the odd CTA's idle MMA warp passes its
-// completions on to `odd_full` of the even CTA (a bulk copy can only signal the CTA it
-// writes), whose MMA thread runs both tensor cores.  Commits free the stage in both CTAs.
+// their scales; the bytes of both count on the even CTA's `full` barrier (the only full
+// barriers in use), whose MMA thread runs both tensor cores.  So the odd CTA's loads are
+// cta_group::2 tensor loads, which may signal the pair's other CTA while they write their own
+// (a plain bulk copy signals the CTA that it writes).  Commits free the stage in both CTAs.
+// Not kept: the odd CTA's completions on a barrier of its own, handed on by a thread of it.
+// Handing operand bytes on takes a cluster-scope release, about 1500 cycles a stage (packed
+// case 372 us); a CTA-scope one is no ordering between two CTAs.
 template <typename Tout, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-    mx4_gemm_kernel(const uint8_t* __restrict__ wimg, const uint8_t* __restrict__ rimg,
+    mx4_gemm_kernel(const __grid_constant__ std::conditional_t<PAIR, MxPairMaps, MxNoMaps> maps,
+                    const uint8_t* __restrict__ wimg, const uint8_t* __restrict__ rimg,
                     const uint8_t* __restrict__ simg, const int32_t* __restrict__ offsets, int E,
                     int R, int K, int N, Tout* __restrict__ y, int32_t* status,
                     long long spin_limit) {
@@ -132,8 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::STAGES * C::STAGE_BYTES);
   uint64_t* full = bars;
   uint64_t* empty = bars + C::STAGES;
-  uint64_t* odd_full = bars + 2 * C::STAGES;  // even CTA of a pair: the odd CTA's stages
-  uint64_t* tfull = bars + 3 * C::STAGES;
+  uint64_t* tfull = bars + 2 * C::STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
@@ -148,9 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1);                            // its producer
+      mbar_init(&full[s], 1);                            // the (even) producer; all bytes
       mbar_init(&empty[s], 1);                           // the MMA's commit
-      mbar_init(&odd_full[s], 1);                        // the odd CTA's relay
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);                           // the MMA's commit
@@ -158,6 +178,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(mma_done, 1);
     fence_mbar_init();
+  }
+  if constexpr (PAIR) {
+    if (threadIdx.x == 0 && rank == 1) {
+      prefetch_tensormap(&maps.w);
+      prefetch_tensormap(&maps.sf[0]);
+      prefetch_tensormap(&maps.sf[1]);
+    }
   }
   if (warp == 1) {
     if constexpr (PAIR) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
@@ -178,15 +205,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       // bytes of a k-block's rows and scales that this CTA loads
       auto row_bytes = [&](const MxUnit& w) { return (uint32_t)w.rows16 * (PAIR ? 64u : 128u); };
       auto sf_bytes = [&](const MxUnit& w) { return w.rows16 > 128 ? 2048u : 1024u; };
+      // the bytes that stage s will get (of a pair: from both CTAs, counted by the even one)
+      auto arm = [&](int s, const MxUnit& w) {
+        if (!PAIR || rank == 0)
+          mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * (kMx4WBytes + row_bytes(w) + sf_bytes(w)));
+      };
+      auto load_weights = [&](int s, const MxUnit& w, int kb) {
+        uint8_t* st = base + s * C::STAGE_BYTES;
+        if constexpr (PAIR) {
+          if (rank == 1) {
+            tma_load_2d_pair(&maps.w, st, mapa_shared(smem_u32(&full[s]), 0), 0,
+                             (int)(w.w_img / 1024) + kb * (kMx4WBytes / 1024));
+            return;
+          }
+        }
+        bulk_load(st, wimg + w.w_img + (size_t)kb * kMx4WBytes, kMx4WBytes, &full[s]);
+      };
+      auto load_rows = [&](int s, const MxUnit& w, int kb) {
+        uint8_t* st = base + s * C::STAGE_BYTES;
+        const uint32_t rb = row_bytes(w), sb = sf_bytes(w);
+        const size_t rows = w.row_img + (size_t)rank * rb + (size_t)kb * w.rows16 * 128;
+        const size_t scales = w.sf_img + (size_t)kb * kMx4SfSlot;
+        if constexpr (PAIR) {
+          if (rank == 1) {
+            const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+            tma_load_2d_pair(&maps.rows[w.rows16 / 16 - 1], st + C::ROW_OFF, bar, 0, (int)(rows / 1024));
+            tma_load_2d_pair(&maps.sf[sb / 1024 - 1], st + C::SF_OFF, bar, 0, (int)(scales / 1024));
+            return;
+          }
+        }
+        bulk_load(st + C::ROW_OFF, rimg + rows, rb, &full[s]);
+        bulk_load(st + C::SF_OFF, simg + scales, sb, &full[s]);
+      };
       // The weights are inputs: the first unit's first stages are on their way before the
       // rows' quantisation, the kernel before this one, has finished.
       int early = 0;
       if (units.more()) {
         const MxUnit w = units.unit(tb);
         for (; early < KB && early < C::STAGES; ++early) {
-          mbar_arrive_expect_tx(&full[early], kMx4WBytes + row_bytes(w) + sf_bytes(w));
-          bulk_load(base + early * C::STAGE_BYTES, wimg + w.w_img + (size_t)early * kMx4WBytes,
-                    kMx4WBytes, &full[early]);
+          arm(early, w);
+          load_weights(early, w, early);
         }
       }
       pdl_wait();
@@ -195,9 +253,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool aborted = false;
       for (; units.more() && !aborted; units.advance()) {
         const MxUnit w = units.unit(tb);
-        const uint32_t rb = row_bytes(w), sb = sf_bytes(w);
-        const uint8_t* rows = rimg + w.row_img + (size_t)rank * rb;
-        const size_t row_step = (size_t)w.rows16 * 128;
         // What this CTA's next unit is the first to touch moves into L2 while this one is
         // multiplied: an expert's weights with its first tile, a tile's rows with its first
         // weight tile.  (Six stages cover a load from L2, not one from memory.)
@@ -214,19 +269,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             aborted = true;
             break;
           }
-          uint8_t* st = base + s * C::STAGE_BYTES;
           if (it >= early) {
-            mbar_arrive_expect_tx(&full[s], kMx4WBytes + rb + sb);
-            bulk_load(st, wimg + w.w_img + (size_t)kb * kMx4WBytes, kMx4WBytes, &full[s]);
+            arm(s, w);
+            load_weights(s, w, kb);
           }
-          bulk_load(st + C::ROW_OFF, rows + kb * row_step, rb, &full[s]);
-          bulk_load(st + C::SF_OFF, simg + w.sf_img + (size_t)kb * kMx4SfSlot, sb, &full[s]);
+          load_rows(s, w, kb);
           if (fetch_w) prefetch_l2(wimg + nx.w_img + (size_t)kb * kMx4WBytes, kMx4WBytes);
           if (fetch_rows)
             prefetch_l2(rimg + nx.row_img + (size_t)kb * nx.rows16 * 128, nx.rows16 * 128);
         }
       }
-      if (aborted) {
+      if (aborted && rank == 0) {
         // (an abort comes from a wait for a free slot, so every early stage has been filled)
         // the copies issued into the last STAGES slots may still be in flight
         for (int i = (it > C::STAGES ? it - C::STAGES : 0); i < it; ++i)
@@ -235,25 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (PAIR && rank == 1) {
-      if (elect_one()) {
-        // ------------------------------------------- relay of the odd CTA's full stages
-        int it = 0;
-        bool aborted = false;
-        for (; units.more() && !aborted; units.advance()) {
-          for (int kb = 0; kb < KB; ++kb, ++it) {
-            const int s = it % C::STAGES;
-            if (!mbar_wait_bounded(&full[s], (it / C::STAGES) & 1, abort_flag, status, spin_limit)) {
-              aborted = true;
-              break;
-            }
-            // CTA-scope release: the bytes are in this SM's shared memory, which only its own
-            // tensor core reads; a cluster-scope release took about 1500 cycles a stage
-            mbar_arrive_remote(mapa_shared(smem_u32(&odd_full[s]), 0));
-          }
-        }
-      }
-    } else if (elect_one()) {
+    if (rank == 0 && elect_one()) {
       // ---------------------------------------------------------- MMA issuer
       int it = 0, tcount = 0;
       int rows16 = units.more() ? units.unit(tb).rows16 : 0;
@@ -275,8 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int s = it % C::STAGES;
           const uint32_t ph = (it / C::STAGES) & 1;
-          if (!mbar_wait_bounded(&full[s], ph, abort_flag, status, spin_limit) ||
-              (PAIR && !mbar_wait_bounded(&odd_full[s], ph, abort_flag, status, spin_limit))) {
+          if (!mbar_wait_bounded(&full[s], ph, abort_flag, status, spin_limit)) {
             aborted = true;
             break;
           }
@@ -408,7 +442,21 @@ cudaError_t go(const uint8_t* w, const uint8_t* r, const uint8_t* sf, const int3
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, w, r, sf, offsets, E, R, K, N, static_cast<Tout*>(y), status,
+  std::conditional_t<PAIR, MxPairMaps, MxNoMaps> maps;
+  if constexpr (PAIR) {
+    const uint64_t tiles = (uint64_t)mx4_max_tiles(R, E, C::TILE_ROWS);
+    auto lines = [](CUtensorMap* m, const void* p, uint64_t n, uint32_t box) {
+      return encode_rowmajor_2d(m, p, 256, n, true, 256, box);
+    };
+    bool ok = lines(&maps.w, w, (uint64_t)E * NT * mx4_kblocks(K) * (kMx4WBytes / 1024),
+                    kMx4WBytes / 1024);
+    for (uint32_t j = 0; j < 2; ++j)
+      ok = ok && lines(&maps.sf[j], sf, tiles * (mx4_sf_slots(K) / 1024), j + 1);
+    for (uint32_t j = 0; j < kMxHeights; ++j)
+      ok = ok && lines(&maps.rows[j], r, tiles * (mx4_slot(K, C::TILE_ROWS) / 1024), j + 1);
+    if (!ok) return cudaErrorInvalidValue;
+  }
+  return cudaLaunchKernelEx(&cfg, kern, maps, w, r, sf, offsets, E, R, K, N, static_cast<Tout*>(y), status,
                             limit);
 }
 
