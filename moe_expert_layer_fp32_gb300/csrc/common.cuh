@@ -237,6 +237,11 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t saddr, uint32_t rank) {
   return r;
 }
 
+// A word of another CTA's shared memory, by its shared::cluster address.
+__device__ __forceinline__ void st_shared_remote(uint32_t addr_cluster, int v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr_cluster), "r"(v) : "memory");
+}
+
 // TMA tile load into this CTA's shared memory whose completion (bytes) is counted
 // on the mbarrier at shared::cluster address `bar_cluster`, which may belong to the
 // peer CTA of the pair.

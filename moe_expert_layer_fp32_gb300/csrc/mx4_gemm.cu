@@ -29,12 +29,15 @@
 // of 224 rows 346 us; pairs 323; units walked without searches and divisions on the issuing
 // thread (1900 cycles a unit before, hidden now) 294 -> 280; what a unit touches first moved
 // into L2 ahead 277; the odd CTA's bytes counted by the even one, three tensor loads a k-block in
-// place of its own bulk copies and a relay without cluster scope, 288.  Not kept: the rows' images made and multiplied chunk by chunk side by
-// side (no gain: every product's start and drain cost what the overlap saved), every CTA
-// prefetching its next unit (six CTAs ask for the same rows: 198 -> 240), quantising inside
-// this kernel (457 us: too few warps for the loads beside the tensor core's share of memory).
+// place of its own bulk copies and a relay without cluster scope, 288.  Not kept: the rows' images
+// made and multiplied chunk by chunk side by side (no gain: every product's start and drain cost
+// what the overlap saved), every CTA prefetching its next unit (six CTAs ask for the same rows:
+// 198 -> 240), quantising inside this kernel (457 us: too few warps for the loads beside the
+// tensor core's share of memory).
 //
-// Every wait is bounded and drains as in expert_gemm.cu.
+// Every wait is bounded.  A wait that runs out, in whichever role, raises the CTA's abort flag;
+// once all roles of the CTA (or pair) are done, a raised flag makes the producers wait for the
+// copies that no role waited for, so that none is in flight when shared memory is given up.
 #include <type_traits>
 
 #include "common.cuh"
@@ -159,6 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* peer_abort = abort_flag + 1;   // pair: the other CTA's flag and the k-blocks
+  volatile int* peer_issued = abort_flag + 2;  // that it has issued, written by it at its end
   Mx4Tables& tb = *reinterpret_cast<Mx4Tables*>(tmem_slot + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -168,6 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
+    *peer_abort = 0;
+    *peer_issued = 0;
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);                            // the (even) producer; all bytes
       mbar_init(&empty[s], 1);                           // the MMA's commit
@@ -190,53 +197,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (PAIR) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
     else tmem_alloc(tmem_slot, C::TMEM_COLS);
   }
-  const bool ok_tables = mx4_build_tables(tb, offsets, E, R, status, C::TILE_ROWS);
+  mx4_build_tables(tb, offsets, E, R, status, C::TILE_ROWS);
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();  // both CTAs' barriers exist before any remote use
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  MxUnits<PAIR> units(PAIR ? blockIdx.x / 2 : blockIdx.x, PAIR ? gridDim.x / 2 : gridDim.x, tb, E,
-                      NT, KB, rank, ok_tables);
+  auto first_unit = [&]() {
+    return MxUnits<PAIR>(PAIR ? blockIdx.x / 2 : blockIdx.x, PAIR ? gridDim.x / 2 : gridDim.x, tb, E,
+                         NT, KB, rank, tb.ok != 0);
+  };
+  MxUnits<PAIR> units = first_unit();
+  int issued = -1;  // the producer's thread: k-blocks issued
+
+  // ---- the producer's steps
+  // bytes of a k-block's rows and scales that this CTA loads
+  auto row_bytes = [&](const MxUnit& w) { return (uint32_t)w.rows16 * (PAIR ? 64u : 128u); };
+  auto sf_bytes = [&](const MxUnit& w) { return w.rows16 > 128 ? 2048u : 1024u; };
+  // the bytes that stage s will get (of a pair: from both CTAs, counted by the even one)
+  auto arm = [&](int s, const MxUnit& w) {
+    if (!PAIR || rank == 0)
+      mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * (kMx4WBytes + row_bytes(w) + sf_bytes(w)));
+  };
+  auto load_weights = [&](int s, const MxUnit& w, int kb) {
+    uint8_t* st = base + s * C::STAGE_BYTES;
+    if constexpr (PAIR) {
+      if (rank == 1) {
+        tma_load_2d_pair(&maps.w, st, mapa_shared(smem_u32(&full[s]), 0), 0,
+                         (int)(w.w_img / 1024) + kb * (kMx4WBytes / 1024));
+        return;
+      }
+    }
+    bulk_load(st, wimg + w.w_img + (size_t)kb * kMx4WBytes, kMx4WBytes, &full[s]);
+  };
+  auto load_rows = [&](int s, const MxUnit& w, int kb) {
+    uint8_t* st = base + s * C::STAGE_BYTES;
+    const uint32_t rb = row_bytes(w), sb = sf_bytes(w);
+    const size_t rows = w.row_img + (size_t)rank * rb + (size_t)kb * w.rows16 * 128;
+    const size_t scales = w.sf_img + (size_t)kb * kMx4SfSlot;
+    if constexpr (PAIR) {
+      if (rank == 1) {
+        const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+        tma_load_2d_pair(&maps.rows[w.rows16 / 16 - 1], st + C::ROW_OFF, bar, 0, (int)(rows / 1024));
+        tma_load_2d_pair(&maps.sf[sb / 1024 - 1], st + C::SF_OFF, bar, 0, (int)(scales / 1024));
+        return;
+      }
+    }
+    bulk_load(st + C::ROW_OFF, rimg + rows, rb, &full[s]);
+    bulk_load(st + C::SF_OFF, simg + scales, sb, &full[s]);
+  };
 
   if (warp == 0) {
     if (elect_one()) {
       // ------------------------------------------------------------ producer
-      // bytes of a k-block's rows and scales that this CTA loads
-      auto row_bytes = [&](const MxUnit& w) { return (uint32_t)w.rows16 * (PAIR ? 64u : 128u); };
-      auto sf_bytes = [&](const MxUnit& w) { return w.rows16 > 128 ? 2048u : 1024u; };
-      // the bytes that stage s will get (of a pair: from both CTAs, counted by the even one)
-      auto arm = [&](int s, const MxUnit& w) {
-        if (!PAIR || rank == 0)
-          mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * (kMx4WBytes + row_bytes(w) + sf_bytes(w)));
-      };
-      auto load_weights = [&](int s, const MxUnit& w, int kb) {
-        uint8_t* st = base + s * C::STAGE_BYTES;
-        if constexpr (PAIR) {
-          if (rank == 1) {
-            tma_load_2d_pair(&maps.w, st, mapa_shared(smem_u32(&full[s]), 0), 0,
-                             (int)(w.w_img / 1024) + kb * (kMx4WBytes / 1024));
-            return;
-          }
-        }
-        bulk_load(st, wimg + w.w_img + (size_t)kb * kMx4WBytes, kMx4WBytes, &full[s]);
-      };
-      auto load_rows = [&](int s, const MxUnit& w, int kb) {
-        uint8_t* st = base + s * C::STAGE_BYTES;
-        const uint32_t rb = row_bytes(w), sb = sf_bytes(w);
-        const size_t rows = w.row_img + (size_t)rank * rb + (size_t)kb * w.rows16 * 128;
-        const size_t scales = w.sf_img + (size_t)kb * kMx4SfSlot;
-        if constexpr (PAIR) {
-          if (rank == 1) {
-            const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
-            tma_load_2d_pair(&maps.rows[w.rows16 / 16 - 1], st + C::ROW_OFF, bar, 0, (int)(rows / 1024));
-            tma_load_2d_pair(&maps.sf[sb / 1024 - 1], st + C::SF_OFF, bar, 0, (int)(scales / 1024));
-            return;
-          }
-        }
-        bulk_load(st + C::ROW_OFF, rimg + rows, rb, &full[s]);
-        bulk_load(st + C::SF_OFF, simg + scales, sb, &full[s]);
-      };
       // The weights are inputs: the first unit's first stages are on their way before the
       // rows' quantisation, the kernel before this one, has finished.
       int early = 0;
@@ -279,12 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_l2(rimg + nx.row_img + (size_t)kb * nx.rows16 * 128, nx.rows16 * 128);
         }
       }
-      if (aborted && rank == 0) {
-        // (an abort comes from a wait for a free slot, so every early stage has been filled)
-        // the copies issued into the last STAGES slots may still be in flight
-        for (int i = (it > C::STAGES ? it - C::STAGES : 0); i < it; ++i)
-          wait_drain(&full[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
-      }
+      issued = it;
+      if constexpr (PAIR) st_shared_remote(mapa_shared(smem_u32((const void*)peer_issued), rank ^ 1), it);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -392,7 +401,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();  // no CTA leaves while the pair may still use it
+  bool aborted = *abort_flag != 0;
+  if constexpr (PAIR) {
+    if (threadIdx.x == 0 && aborted)
+      st_shared_remote(mapa_shared(smem_u32((const void*)peer_abort), rank ^ 1), 1);
+    cluster_sync();  // no CTA leaves while the pair may still use it
+    aborted = aborted || *peer_abort != 0;  // (the same in both CTAs)
+  }
+  if (aborted) {
+    // All MMAs are complete and no role waits any more.  Copies into the last STAGES slots may
+    // still be in flight (of a unit that no MMA took: whoever gave up, the producer need not
+    // have noticed).  A stage that only one CTA of a pair has issued gets the other's bytes now
+    // (its slot's last MMAs are complete, or the one could not have issued it), so that its barrier
+    // completes; the even CTA waits for the bytes of both.
+    if (issued >= 0) {
+      int n = issued;
+      if constexpr (PAIR) {
+        MxUnits<PAIR> u = first_unit();
+        for (int i = n / KB; i > 0; --i) u.advance();
+        for (; n < *peer_issued; ++n) {
+          const MxUnit w = u.unit(tb);
+          arm(n % C::STAGES, w);
+          load_weights(n % C::STAGES, w, n % KB);
+          load_rows(n % C::STAGES, w, n % KB);
+          if (n % KB == KB - 1) u.advance();
+        }
+      }
+      if (rank == 0)
+        for (int i = n > C::STAGES ? n - C::STAGES : 0; i < n; ++i)
+          wait_drain(&full[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
+    }
+    if constexpr (PAIR) cluster_sync();  // the odd CTA's copies count on the even CTA's barriers
+  }
   if (warp == 1) {
     tc_fence_after();
     if constexpr (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);

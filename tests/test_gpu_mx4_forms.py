@@ -40,3 +40,34 @@ def test_pairs_are_single_ctas(moe, K, N):
             y1 = moe.mx4_expert_product(x[r].contiguous(), o1, packed, N, ws1, torch.float32)
             assert torch.equal(y1, y[r]), (seed, e)
         assert moe.moe_read_device_status(ws1) == 0
+
+
+@pytest.mark.parametrize("counts,K,N", [
+    ([7, 0, 400, 9], 256, 128),        # single CTAs: one k-block a unit, the ring holds every unit
+    ([7, 0, 20, 9], 1536, 128),        # six k-blocks: no wait for a free slot
+    ([7, 0, 400, 9], 4096, 128),       # sixteen k-blocks: waits for free slots
+    ([300, 0, 225, 129], 256, 256),    # pairs: the ring holds every unit
+    ([300, 16, 225, 129], 1536, 384),  # pairs, an odd number of weight tiles
+    ([300, 0, 225, 129], 4096, 512),   # pairs, waits for free slots
+    ([90000], 256, 256),               # pairs with several units each
+])
+def test_timeout_in_every_form(moe, counts, K, N):
+    """Under a limit far below a copy's round trip some wait runs out, in whichever role and CTA:
+    the call reports it, its copies have landed when it ends, and the next call is right."""
+    E, R = len(counts), sum(counts)
+    packed, x = operands(moe, E, K, N, R, K + N)
+    off = torch.tensor([0] + counts).cumsum(0).int().cuda()
+    ws = moe.mx4_new_workspace(R, K, N, E)
+    want = moe.mx4_expert_product(x, off, packed, N, ws)
+    assert moe.moe_read_device_status(ws) == 0
+    seen = []
+    for limit in (16, 16, 16, 200, 1000, 3000):
+        try:
+            moe.moe_set_wait_limit(limit)
+            moe.mx4_expert_product(x, off, packed, N, ws)
+            seen.append(moe.moe_read_device_status(ws))
+        finally:
+            moe.moe_set_wait_limit(0)
+        assert torch.equal(moe.mx4_expert_product(x, off, packed, N, ws), want)
+        assert moe.moe_read_device_status(ws) == 0
+    assert 6 in seen[:3] and set(seen) <= {0, 6}, seen
