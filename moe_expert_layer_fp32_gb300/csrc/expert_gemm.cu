@@ -36,10 +36,12 @@
 // split depend only on H and I, never on T: batch-invariant by construction.
 //
 // Every wait is bounded (clock64 limit, spin_limit); a wait that runs out raises a
-// CTA-wide abort flag and records MOE_ERR_TIMEOUT; the roles then drain their own
-// in-flight TMA copies and MMAs (bounded by the fixed default limit, whatever
-// spin_limit is) before TMEM is released, and
-// the two CTAs of a pair meet at a cluster barrier before either exits.
+// CTA-wide abort flag and records MOE_ERR_TIMEOUT.  The MMA issuer then waits for its
+// MMAs; once every role of the CTA (or pair) is done, a raised flag makes the producer
+// wait for its copies in flight, whichever role gave up (a producer whose k-blocks all
+// fit the ring never waits and need not have noticed).  Both waits are bounded by the
+// fixed default limit, whatever spin_limit is, and come before TMEM is released; the
+// two CTAs of a pair meet at a cluster barrier before either exits.
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -243,11 +245,11 @@ __global__ void __launch_bounds__(192, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int total = s_prefix[E];
+  int it = 0;  // k-blocks issued (the producer's thread)
 
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ producer
-      int it = 0;  // k-blocks issued
       bool aborted = false;
       for (int u = blockIdx.x; u < total && !aborted; u += gridDim.x) {
         const Work w = decode<BN>(u, s_prefix, s_off, E, NT, KB, a_local);
@@ -262,11 +264,6 @@ __global__ void __launch_bounds__(192, 1)
           tma_load_2d(&maps.a128, sA + s * C::A_BYTES, &full[s], kb * GK, w.a_load_row);
           tma_load_2d(&maps.b_tile, sB + s * C::B_BYTES, &full[s], 0, w.b_load_row + kb * BN);
         }
-      }
-      if (aborted) {
-        // the copies issued into the last STAGES slots may still be in flight
-        for (int i = (it > C::STAGES ? it - C::STAGES : 0); i < it; ++i)
-          wait_drain(&full[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
       }
     }
   } else if (warp == 1) {
@@ -331,6 +328,11 @@ __global__ void __launch_bounds__(192, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) {
+    // the copies issued into the last STAGES slots may still be in flight
+    for (int i = (it > C::STAGES ? it - C::STAGES : 0); i < it; ++i)
+      wait_drain(&full[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);
@@ -415,6 +417,8 @@ __global__ void __launch_bounds__(192, 1)
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* peer_abort = abort_flag + 1;   // the other CTA's flag, and the k-blocks that it
+  volatile int* peer_issued = abort_flag + 2;  // has issued: written by it at its end
   int* s_prefix = reinterpret_cast<int*>(tmem_slot + 4);
   int* s_off = s_prefix + (kMaxE + 1);
 
@@ -443,6 +447,8 @@ __global__ void __launch_bounds__(192, 1)
     }
     s_prefix[E] = p;
     *abort_flag = 0;
+    *peer_abort = 0;
+    *peer_issued = 0;
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);   // the even CTA's producer; bytes from both CTAs
       mbar_init(&empty[s], 1);  // the pair MMA's commit, multicast
@@ -465,11 +471,17 @@ __global__ void __launch_bounds__(192, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int total = s_prefix[E];
+  int it = 0;  // k-blocks issued (the producer's thread)
+  auto load = [&](int s, const PairWork& w, int kb) {
+    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
+    const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+    tma_load_2d_pair(&maps.a128, sA + s * C::A_BYTES, bar, kb * GK, w.a_load_row);
+    tma_load_2d_pair(&maps.b_tile, sB + s * C::B_BYTES, bar, 0, w.b_load_row + kb * BN);
+  };
 
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ producer
-      int it = 0;
       bool aborted = false;
       for (int u = unit0; u < total && !aborted; u += unit_step) {
         const PairWork w = decode_pair<BN>(u, rank, s_prefix, s_off, E, NT, KB, a_local);
@@ -480,17 +492,10 @@ __global__ void __launch_bounds__(192, 1)
             aborted = true;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
-          const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
-          tma_load_2d_pair(&maps.a128, sA + s * C::A_BYTES, bar, kb * GK, w.a_load_row);
-          tma_load_2d_pair(&maps.b_tile, sB + s * C::B_BYTES, bar, 0, w.b_load_row + kb * BN);
+          load(s, w, kb);
         }
       }
-      if (aborted && rank == 0) {
-        // copies into the last STAGES slots (both CTAs' bytes count here) may be in flight
-        for (int i = (it > C::STAGES ? it - C::STAGES : 0); i < it; ++i)
-          wait_drain(&full[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
-      }
+      st_shared_remote(mapa_shared(smem_u32((const void*)peer_issued), rank ^ 1), it);
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
@@ -554,7 +559,28 @@ __global__ void __launch_bounds__(192, 1)
 
   tc_fence_before();
   __syncthreads();
+  bool aborted = *abort_flag != 0;
+  if (threadIdx.x == 0 && aborted)
+    st_shared_remote(mapa_shared(smem_u32((const void*)peer_abort), rank ^ 1), 1);
   cluster_sync();  // no CTA leaves or frees tensor memory while the pair may still use it
+  aborted = aborted || *peer_abort != 0;  // (the same in both CTAs)
+  if (aborted) {
+    // All MMAs are complete and no role waits any more.  Copies into the last STAGES slots
+    // may still be in flight.  A stage that only one CTA has issued gets the other's bytes
+    // now (its slot's last MMAs are complete, or the one could not have issued it), so
+    // that its barrier completes; the even CTA waits for the bytes of both.
+    if (threadIdx.x == 0) {
+      for (; it < *peer_issued; ++it) {
+        const int kb = it % KB;
+        load(it % C::STAGES,
+             decode_pair<BN>(unit0 + it / KB * unit_step, rank, s_prefix, s_off, E, NT, KB, a_local), kb);
+      }
+      if (rank == 0)
+        for (int i = (it > C::STAGES ? it - C::STAGES : 0); i < it; ++i)
+          wait_drain(&full[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
+    }
+    cluster_sync();  // the odd CTA's copies count on the even CTA's barriers
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, C::TMEM_COLS);

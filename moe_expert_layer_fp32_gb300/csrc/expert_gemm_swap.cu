@@ -42,8 +42,8 @@
 //
 // Roles and bounded waits are those of the tile kernels: warp 0 lane 0 TMA
 // producer, warp 1 lane 0 MMA issuer, warps 2..5 epilogue (TMEM lane quarter =
-// warp % 4); every wait has a clock limit and an abort path that drains this
-// CTA's own copies and MMAs before tensor memory is freed.
+// warp % 4); every wait has a clock limit, and after one that ran out this CTA's own
+// copies and MMAs are drained, whichever role gave up, before tensor memory is freed.
 //
 // Both GEMMs are programmatic dependent launches (pdl.cuh).  The gate/up GEMM
 // waits for its predecessor (the dispatch) before reading the offsets; the down
@@ -279,11 +279,11 @@ __global__ void __launch_bounds__(192, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int total = s_prefix[E];
+  int it = 0;  // k-blocks issued (the producer's thread)
 
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ producer
-      int it = 0;
       bool aborted = false;
       bool first = true;
       for (int u = blockIdx.x; u < total && !aborted; u += gridDim.x, first = false) {
@@ -323,10 +323,6 @@ __global__ void __launch_bounds__(192, 1)
           if (kb >= ndefer) tma_load_2d(xm, sX + s * X_BYTES, &full[s], kb * SK, w.x_load_row);
         }
         if (ndefer > 0 && ndefer == KB && !aborted) load_deferred(ndefer);
-      }
-      if (aborted) {
-        for (int i = (it > STAGES ? it - STAGES : 0); i < it; ++i)
-          wait_drain(&full[i % STAGES], (i / STAGES) & 1, kSpinLimitCycles);
       }
     }
   } else if (warp == 1) {
@@ -459,6 +455,11 @@ __global__ void __launch_bounds__(192, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) {
+    // the copies issued into the last STAGES slots may still be in flight
+    for (int i = (it > STAGES ? it - STAGES : 0); i < it; ++i)
+      wait_drain(&full[i % STAGES], (i / STAGES) & 1, kSpinLimitCycles);
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);
