@@ -538,7 +538,8 @@ moe_status moe_mx4_layer_fwd(const void* x, const float* w_router, const float* 
 moe_status moe_read_device_status(void* workspace, int32_t* status_out, void* stream);
 
 /* Diagnostics: the limit, in SM clock cycles, of every bounded wait inside the
- * grouped GEMM kernels of calls launched afterwards (process-wide; cycles <= 0
+ * grouped GEMM kernels and the router of at most eight tokens (whose rows then get
+ * index -1 and weight 0) of calls launched afterwards (process-wide; cycles <= 0
  * restores the default of 4e9, about 2 s).  A wait that runs out records
  * MOE_ERR_TIMEOUT in the workspace status word; the kernel then waits for its own
  * copies and MMAs in flight (always with the default limit), releases its tensor

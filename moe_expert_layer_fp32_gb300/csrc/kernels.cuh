@@ -185,7 +185,7 @@ cudaError_t launch_mx4_gemm(const void* packed, const void* codes, const void* s
                             const int32_t* offsets, int E, int R, int K, int N, void* y,
                             int y_dtype, int32_t* status, long long spin_limit, cudaStream_t s);
 
-// The limit of the GEMM kernels' bounded waits now in force (moe_set_wait_limit).
+// The limit of the kernels' bounded waits now in force (moe_set_wait_limit).
 long long wait_limit();
 
 // The router's projection alone: logits [T, E] = the FP32 chains plus the optional bias.

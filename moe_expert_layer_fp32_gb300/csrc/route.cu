@@ -747,18 +747,20 @@ struct DecodeMaps {
 };
 
 // Bounded parity wait without a status word (the router has none): false once
-// *abort is raised or `limit` cycles pass (then it raises *abort).
+// *abort is raised or `limit` cycles pass (then it raises *abort).  The limit is looked at
+// before the first try_wait, which may itself suspend for longer than a copy takes: so a
+// short limit does run out.
 __device__ __forceinline__ bool route_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                            long long limit) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_test_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
     if (clock64() - t0 > limit) {
       *abort = 1;
       return false;
     }
+    if (mbar_try_wait(bar, parity)) return true;
   }
 }
 
@@ -806,16 +808,20 @@ __global__ void __launch_bounds__(DecodeCfg<EP, TSV>::NTH)
   if (tid == 0) pdl_launch_dependents();
 
   float acc = 0.0f;
+  bool failed = false;  // a wait of this warp ran out, or another's before it was done
+  int issued = 0;       // the copying thread: chunks
   const int ct = tid - 32;
   const int el = ct % EC, tok = ct / EC;
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------------------- copies
-      int c = 0;
-      for (; c < nchunks; ++c) {
+      for (int c = 0; c < nchunks; ++c) {
         const int s = c % CNST;
         const uint32_t ph = (c / CNST) & 1;
-        if (!route_wait(&empty[s], ph ^ 1, abort_flag, spin_limit)) break;
+        if (!route_wait(&empty[s], ph ^ 1, abort_flag, spin_limit)) {
+          failed = true;
+          break;
+        }
         // boxes that start inside H (none lies wholly past the tensor)
         const int nbx = min(C::NB, (H - c * HC + C::BR - 1) / C::BR);
         mbar_arrive_expect_tx(&full[s], nbx * (C::WB_BYTES + C::XB_BYTES));
@@ -825,10 +831,7 @@ __global__ void __launch_bounds__(DecodeCfg<EP, TSV>::NTH)
           tma_load_2d(&maps.x, sX + s * C::X_BYTES + b * C::XB_BYTES, &full[s], c * HC + b * C::BR,
                       t0);
         }
-      }
-      if (*abort_flag) {  // let the copies in flight land before the CTA exits
-        for (int i = (c > CNST ? c - CNST : 0); i < c; ++i)
-          wait_drain(&full[i % CNST], (i / CNST) & 1, kSpinLimitCycles);
+        issued = c + 1;
       }
     }
     __syncwarp();
@@ -839,7 +842,10 @@ __global__ void __launch_bounds__(DecodeCfg<EP, TSV>::NTH)
       const int s = c % CNST;
       const uint32_t ph = (c / CNST) & 1;
       const bool ok = __all_sync(0xFFFFFFFFu, route_wait(&full[s], ph, abort_flag, spin_limit));
-      if (!ok) break;
+      if (!ok) {
+        failed = true;
+        break;
+      }
       if (active) {
         const int rows = min(HC, H - c * HC);
         // the stage's W_r rows are contiguous over its boxes; its x holds one
@@ -881,11 +887,9 @@ __global__ void __launch_bounds__(DecodeCfg<EP, TSV>::NTH)
     }
   }
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (*abort_flag) {
-    if (tid == 0) {
-      const uint32_t dst = mapa_shared(smem_u32(s_err), 0);
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst), "r"(1) : "memory");
-    }
+  // (each warp for itself: the CTA's flag may be raised after another warp has come here)
+  if (failed) {
+    if (lane == 0) st_shared_remote(mapa_shared(smem_u32(s_err), 0), 1);
   } else if (warp > 0 && ct < C::NCMP && e0 + el < E) {
     const int e = e0 + el;
     float l = acc;
@@ -894,6 +898,12 @@ __global__ void __launch_bounds__(DecodeCfg<EP, TSV>::NTH)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(l) : "memory");
   }
   cluster_sync();
+  // every role is done: copies that no warp waited for land before the CTA exits
+  if (tid == 0 && *abort_flag) {
+    for (int i = (issued > CNST ? issued - CNST : 0); i < issued; ++i)
+      wait_drain(&full[i % CNST], (i / CNST) & 1, kSpinLimitCycles);
+  }
+  __syncwarp();
   if (rank == 0) {
     for (int tl = warp; tl < TSV; tl += C::NTH / 32) {
       const int t = t0 + tl;
@@ -998,7 +1008,7 @@ cudaError_t launch_decode(const void* x, const float* wr, const float* bias, int
     if (dv < 64) ok[dv] = 1;
   }
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, m, bias, T, H, E, k, wbf16, idx, w, kSpinLimitCycles);
+  return cudaLaunchKernelEx(&cfg, kern, m, bias, T, H, E, k, wbf16, idx, w, wait_limit());
 }
 
 template <int EP, int KIND>
