@@ -404,7 +404,8 @@ typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dt
 /* The projection of moe_route alone: logits[t, e] = the FP32 fused multiply-add
  * chain over h of float(x[t,h]) * w_router[h,e], plus bias[e] if given (the same
  * bits moe_route selects by).  x [T, H] bf16; logits [T, E] fp32 out.  d.k and d.I
- * are not used beyond the limits. */
+ * are not used beyond the limits.  There is no status word: if a bounded wait runs out
+ * (up to eight tokens), every logit of the call is NaN. */
 moe_status moe_router_logits(const void* x, const float* w_router, const float* bias, moe_dims d,
                              float* logits, void* stream);
 

@@ -188,9 +188,10 @@ cudaError_t launch_mx4_gemm(const void* packed, const void* codes, const void* s
 // The limit of the kernels' bounded waits now in force (moe_set_wait_limit).
 long long wait_limit();
 
-// The router's projection alone: logits [T, E] = the FP32 chains plus the optional bias.
+// The router's projection alone: logits [T, E] = the FP32 chains plus the optional bias.  A wait
+// that runs out (T <= 8) leaves NaN logits and MOE_ERR_TIMEOUT in *status (may be null).
 cudaError_t launch_router_logits(const void* x, const float* w_router, const float* bias, int T,
-                                 int H, int E, float* logits, cudaStream_t s);
+                                 int H, int E, float* logits, int32_t* status, cudaStream_t s);
 
 // number of SMs of the current device (cached per device)
 int device_sm_count();

@@ -152,7 +152,8 @@ moe_status moe_router_logits(const void* x, const float* w_router, const float* 
   if (bias != nullptr) MOE_TRY(validate_ptr(bias));
   MOE_TRY(validate_ptr(logits));
   MOE_TRY(validate_device());
-  MOE_CUDA(launch_router_logits(x, w_router, bias, d.T, d.H, d.E, logits, as_stream(stream)));
+  MOE_CUDA(launch_router_logits(x, w_router, bias, d.T, d.H, d.E, logits, nullptr,
+                                as_stream(stream)));
   return MOE_OK;
 }
 
@@ -332,7 +333,7 @@ moe_status moe_mx4_layer_fwd(const void* x, const float* w_router, const float* 
   void* gu = at<void>(workspace, L.gate_up);
   float* y = at<float>(workspace, L.y);
   if (T > 0) {
-    MOE_CUDA(launch_router_logits(x, w_router, nullptr, T, d.H, d.E, logits, s));
+    MOE_CUDA(launch_router_logits(x, w_router, nullptr, T, d.H, d.E, logits, status, s));
     MOE_CUDA(launch_select(logits, MOE_DTYPE_F32, d.E, bias, *opts, T, d.E, d.k, idx, w, nullptr,
                            nullptr, s));
   }

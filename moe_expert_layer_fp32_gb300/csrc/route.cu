@@ -768,7 +768,7 @@ template <int EP, int TSV, int KIND>
 __global__ void __launch_bounds__(DecodeCfg<EP, TSV>::NTH)
     route_decode_kernel(const __grid_constant__ DecodeMaps maps, const float* __restrict__ bias,
                         int T, int H, int E, int k, int wbf16, int32_t* __restrict__ topk_idx,
-                        float* __restrict__ topk_w, long long spin_limit) {
+                        float* __restrict__ topk_w, int32_t* status, long long spin_limit) {
   using C = DecodeCfg<EP, TSV>;
   constexpr int EC = C::EC, HC = C::HC, CNST = C::CNST, LLD = C::LLD;
   extern __shared__ uint8_t smem_raw[];
@@ -909,7 +909,10 @@ __global__ void __launch_bounds__(DecodeCfg<EP, TSV>::NTH)
       const int t = t0 + tl;
       if (t >= T) continue;
       if (*s_err) {  // a wait ran out: no routing (the dispatch rejects index -1)
-        if (lane < k) {
+        if constexpr (KIND == 2) {  // (topk_w is the logits; topk_idx is not there)
+          for (int e = lane; e < E; e += 32) topk_w[(size_t)t * E + e] = __int_as_float(0x7FC00000);
+          if (lane == 0) flag_error(status, MOE_ERR_TIMEOUT);
+        } else if (lane < k) {
           topk_idx[(size_t)t * k + lane] = -1;
           topk_w[(size_t)t * k + lane] = 0.0f;
         }
@@ -970,7 +973,7 @@ cudaError_t launch_cluster(const void* x, const float* wr, const float* bias, in
 
 template <int EP, int TSV, int KIND>
 cudaError_t launch_decode(const void* x, const float* wr, const float* bias, int T, int H, int E,
-                          int k, int wbf16, int32_t* idx, float* w, cudaStream_t s) {
+                          int k, int wbf16, int32_t* idx, float* w, cudaStream_t s, int32_t* status) {
   using C = DecodeCfg<EP, TSV>;
   auto kern = route_decode_kernel<EP, TSV, KIND>;
   static int ok[64] = {};  // 0: unknown, 1: launchable, -1: a 16-CTA cluster does not fit
@@ -1008,22 +1011,23 @@ cudaError_t launch_decode(const void* x, const float* wr, const float* bias, int
     if (dv < 64) ok[dv] = 1;
   }
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, m, bias, T, H, E, k, wbf16, idx, w, wait_limit());
+  return cudaLaunchKernelEx(&cfg, kern, m, bias, T, H, E, k, wbf16, idx, w, status,
+                            wait_limit());
 }
 
 template <int EP, int KIND>
 cudaError_t launch_ep(const void* x, const float* wr, const float* bias, int T, int H, int E, int k,
-                      int wbf16, int32_t* idx, float* w, cudaStream_t s) {
+                      int wbf16, int32_t* idx, float* w, cudaStream_t s, int32_t* status) {
   if (T <= kRouteSmallMaxT) {
     // one cluster holds every token (T <= 8) and there are 64 experts or more:
     // sixteen CTAs, four or more experts each.  Measured on GB300 (router stage,
     // L2 flushed): large T = 8 38 against 46 us, T = 1 33 against 34 us;
     // fine_grained T = 1 17 against 18 us; at T = 64 eight CTAs were 2 us faster.
     if constexpr (EP >= 64) {
-      if (T == 1) return launch_decode<EP, 1, KIND>(x, wr, bias, T, H, E, k, wbf16, idx, w, s);
-      if (T == 2) return launch_decode<EP, 2, KIND>(x, wr, bias, T, H, E, k, wbf16, idx, w, s);
-      if (T <= 4) return launch_decode<EP, 4, KIND>(x, wr, bias, T, H, E, k, wbf16, idx, w, s);
-      if (T <= 8) return launch_decode<EP, 8, KIND>(x, wr, bias, T, H, E, k, wbf16, idx, w, s);
+      if (T == 1) return launch_decode<EP, 1, KIND>(x, wr, bias, T, H, E, k, wbf16, idx, w, s, status);
+      if (T == 2) return launch_decode<EP, 2, KIND>(x, wr, bias, T, H, E, k, wbf16, idx, w, s, status);
+      if (T <= 4) return launch_decode<EP, 4, KIND>(x, wr, bias, T, H, E, k, wbf16, idx, w, s, status);
+      if (T <= 8) return launch_decode<EP, 8, KIND>(x, wr, bias, T, H, E, k, wbf16, idx, w, s, status);
     }
     if (T == 1) return launch_cluster<EP, 1, KIND>(x, wr, bias, T, H, E, k, wbf16, idx, w, s);
     if (T == 2) return launch_cluster<EP, 2, KIND>(x, wr, bias, T, H, E, k, wbf16, idx, w, s);
@@ -1077,21 +1081,24 @@ cudaError_t launch_ep(const void* x, const float* wr, const float* bias, int T, 
 
 template <int KIND>
 cudaError_t launch_kind(const void* x, const float* w_router, const float* bias, int T, int H,
-                        int E, int k, int wbf16, int32_t* topk_idx, float* topk_w, cudaStream_t s) {
-  if (E <= 32) return launch_ep<32, KIND>(x, w_router, bias, T, H, E, k, wbf16, topk_idx, topk_w, s);
-  if (E <= 64) return launch_ep<64, KIND>(x, w_router, bias, T, H, E, k, wbf16, topk_idx, topk_w, s);
-  if (E <= 128)
-    return launch_ep<128, KIND>(x, w_router, bias, T, H, E, k, wbf16, topk_idx, topk_w, s);
-  return launch_ep<256, KIND>(x, w_router, bias, T, H, E, k, wbf16, topk_idx, topk_w, s);
+                        int E, int k, int wbf16, int32_t* topk_idx, float* topk_w, cudaStream_t s,
+                        int32_t* status = nullptr) {
+  auto by_experts = [&](auto launch) {
+    return launch(x, w_router, bias, T, H, E, k, wbf16, topk_idx, topk_w, s, status);
+  };
+  if (E <= 32) return by_experts(launch_ep<32, KIND>);
+  if (E <= 64) return by_experts(launch_ep<64, KIND>);
+  if (E <= 128) return by_experts(launch_ep<128, KIND>);
+  return by_experts(launch_ep<256, KIND>);
 }
 
 }  // namespace
 
 #ifdef MOE_ROUTER_LOGITS  // route_logits.cu compiles this file for the projection alone
 cudaError_t launch_router_logits(const void* x, const float* w_router, const float* bias, int T,
-                                 int H, int E, float* logits, cudaStream_t s) {
+                                 int H, int E, float* logits, int32_t* status, cudaStream_t s) {
   if (T == 0) return cudaSuccess;
-  return launch_kind<2>(x, w_router, bias, T, H, E, 1, 0, nullptr, logits, s);
+  return launch_kind<2>(x, w_router, bias, T, H, E, 1, 0, nullptr, logits, s, status);
 }
 #else
 cudaError_t launch_route(const void* x, const float* w_router, const float* bias, int T, int H,

@@ -59,3 +59,55 @@ def test_route_timeout_marks_every_row(moe, T, H, E, kind):
         again = run()
         assert all(torch.equal(p, q) for p, q in zip(again, want))
     assert marked >= 3
+
+
+@pytest.mark.parametrize("T,H,E", SHAPES)
+def test_router_logits_timeout_is_nan(moe, T, H, E):
+    """The projection alone: every logit of the call NaN, or right; nothing else is written."""
+    x, wr, b = inputs(T, H, E)
+    d = moe.dims(T, H, E, 8, 128)
+
+    def run():
+        both = torch.full((T + 1, E), 77.0, device="cuda")
+        moe.moe_router_logits(x, wr, b, d, both[:T])
+        return both
+
+    want = run()
+    assert torch.isfinite(want).all()
+    marked = 0
+    for limit in (16, 16, 16, 300, 1000, 2000, 3000, 5000):
+        got = limited(moe, limit, run)
+        assert (got[T] == 77.0).all()
+        if torch.isnan(got).any():
+            marked += 1
+            assert torch.isnan(got[:T]).all()
+        else:
+            assert torch.equal(got, want)
+        assert torch.equal(run(), want)
+    assert marked >= 3
+
+
+@pytest.mark.parametrize("T,E", [(1, 64), (8, 256)])
+def test_mx4_layer_timeout_is_reported(moe, T, E):
+    H, k, I = 512, 4, 128
+    x, wr, b = inputs(T, H, E)
+    d = moe.dims(T, H, E, k, I)
+    g = torch.Generator(device="cuda").manual_seed(E)
+
+    def normal(*shape):
+        return (torch.randn(shape, generator=g, device="cuda") * 0.05).to(torch.bfloat16)
+
+    gu, dn = moe.mx4_prepack(normal(E, H, I), normal(E, H, I)), moe.mx4_prepack(normal(E, I, H))
+    ws = moe.mx4_new_layer_workspace(d)
+
+    def run():
+        return moe.mx4_layer_forward(x, wr, b, gu, dn, d, ws, want_routing=True)
+
+    want = run()
+    assert moe.moe_read_device_status(ws) == 0
+    for _ in range(3):
+        out, idx, w, counts = limited(moe, 16, run)
+        assert moe.STATUS[moe.moe_read_device_status(ws)] == "MOE_ERR_TIMEOUT"
+        assert (w == 0).all() and ((idx >= 0) & (idx < E)).all()  # NaN logits mask every expert
+        assert all(torch.equal(p, q) for p, q in zip(run(), want))
+        assert moe.moe_read_device_status(ws) == 0
