@@ -418,7 +418,7 @@ moe_status moe_router_logits(const void* x, const float* w_router, const float* 
  * largest keys are chosen, in that order (ties: lower expert).  n_group = 1: no
  * groups.
  *   w_j = score_j, divided by the sum of the k chosen scores if renorm is nonzero.
- * A logit (or key) of -inf or NaN masks its expert: key -inf, score 0, left out of
+ * A logit, bias or key of -inf or NaN masks its expert: key -inf, score 0, left out of
  * group sums (a group of masked experts scores -inf); masked experts are chosen only
  * when nothing else is left.  A row whose chosen scores are all 0 gets weights 0.
  * Softmax keys of +inf share the probability equally.  Sigmoid scores below FP32's

@@ -1,6 +1,6 @@
 // Selection from router logits, and its gradient.
 //
-// For a row of E logits l (one token), m_e = "masked": l_e (or, for softmax, l_e + b_e)
+// For a row of E logits l (one token), m_e = "masked": l_e, b_e or (for softmax) l_e + b_e
 // is -inf or NaN.
 //   softmax   key_e = l_e + b_e,            score_e = exp(key_e) / sum_E exp(key)
 //   sigmoid   s_e = 1 / (1 + exp(-l_e)),    key_e = s_e + b_e,   score_e = s_e
@@ -75,10 +75,11 @@ __device__ __forceinline__ void load_row(const Tin* row, int e0, int E, bool vec
 
 // key and score of the lane's experts.  KIND 0: score is left to the caller (it needs
 // the row's maximum); masked experts and those past E (of the lane's NV, `inside` are within)
-// have key -inf and score 0.  b is the bias as lane_bias made it, so a sum with it is never -0 (which would order below +0).
+// have key -inf and score 0.  b is the bias as lane_bias made it, so a sum with it is never -0
+// (which would order below +0); open: none of the lane's is -inf.
 template <int KIND, int NV>
-__device__ __forceinline__ void keys_of(const float (&l)[NV], const float (&b)[NV], int inside,
-                                        float (&key)[NV], float (&sc)[NV]) {
+__device__ __forceinline__ void keys_of(const float (&l)[NV], const float (&b)[NV], bool open,
+                                        int inside, float (&key)[NV], float (&sc)[NV]) {
   if constexpr (KIND == 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -95,7 +96,7 @@ __device__ __forceinline__ void keys_of(const float (&l)[NV], const float (&b)[N
       zero = fmaf(l[i], 0.0f, zero);
       big = fmaxf(big, fabsf(l[i]));
     }
-    const bool plain = inside == 0 || (inside == NV && zero == 0.0f && big <= 80.0f);
+    const bool plain = inside == 0 || (inside == NV && open && zero == 0.0f && big <= 80.0f);
     if (__all_sync(kFull, plain)) {
 #pragma unroll
       for (int i = 0; i < NV; i += 2) {
@@ -124,21 +125,30 @@ __device__ __forceinline__ void keys_of(const float (&l)[NV], const float (&b)[N
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const bool in = l[i] > -INFINITY;
+      const bool in = l[i] > -INFINITY && b[i] > -INFINITY;
       key[i] = in ? __fadd_rn(sc[i], b[i]) : -INFINITY;
       sc[i] = in ? sc[i] : 0.0f;
     }
   }
 }
 
-// The lane's biases: NaN masks its expert as -inf does, -0 becomes +0.
+// The lane's values of an FP32 vector over the experts (16-byte aligned), 0 where there is none.
+template <int NV>
+__device__ __forceinline__ void lane_vector(const float* p, int e0, int E, float (&v)[NV]) {
+  if (p != nullptr && e0 + NV <= E) {
+    load_floats<float, NV>(p + e0, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = (p != nullptr && e0 + i < E) ? __ldg(p + e0 + i) : 0.0f;
+  }
+}
+
+// Biases as the keys take them: NaN masks its expert as -inf does, -0 becomes +0.
 template <int NV>
 __device__ __forceinline__ void lane_bias(const float* bias, int e0, int E, float (&b)[NV]) {
+  lane_vector<NV>(bias, e0, E, b);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const float v = (bias != nullptr && e0 + i < E) ? __ldg(bias + e0 + i) : 0.0f;
-    b[i] = (v == v) ? __fadd_rn(v, 0.0f) : -INFINITY;
-  }
+  for (int i = 0; i < NV; ++i) b[i] = (b[i] == b[i]) ? __fadd_rn(b[i], 0.0f) : -INFINITY;
 }
 
 // exp(key - m), 1 where key is the maximum (also +inf), 0 where masked
@@ -222,10 +232,13 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
   // the next token's logits are in flight while this one's experts are chosen
   float l[NV];
   if (t0 < a.T) load_row<Tin, NV>(logits + t0 * a.ld, e0, E, vec, l);
+  bool open = true;  // the bias masks none of the lane's experts
+#pragma unroll
+  for (int i = 0; i < NV; ++i) open = open && b[i] > -INFINITY;
 
   for (long long t = t0; t < a.T; t += stride) {
     float key[NV], sc[NV];
-    keys_of<KIND, NV>(l, b, inside, key, sc);
+    keys_of<KIND, NV>(l, b, open, inside, key, sc);
     if (t + stride < a.T) load_row<Tin, NV>(logits + (t + stride) * a.ld, e0, E, vec, l);
     // the row's softmax: its maximum and the sum relative to it (sigmoid: the sum of scores)
     float mx = -INFINITY, z = 0.0f;
@@ -492,9 +505,7 @@ __global__ void __launch_bounds__(kSelThreads, DENSE ? kSelBlocksPerSm : 6) sele
   float b[DENSE ? NV : 1], g[DENSE ? NV : 1], col[DBIAS ? NV : 1];
   if constexpr (DENSE) {
     lane_bias<NV>(a.bias, e0, E, b);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      g[i] = (d_prob != nullptr && e0 + i < E) ? __ldg(d_prob + e0 + i) : 0.0f;
+    lane_vector<NV>(d_prob, e0, E, g);
   }
   if constexpr (DBIAS) {
 #pragma unroll
@@ -515,6 +526,14 @@ __global__ void __launch_bounds__(kSelThreads, DENSE ? kSelBlocksPerSm : 6) sele
     if constexpr (DENSE) load_row<Tin, NV>(logits + t * a.ld, e0, E, vec, next);
   };
   fetch(t0);
+  // sigmoid: experts that the bias masks (it joins nothing else here)
+  unsigned off = 0u;
+  if constexpr (DENSE && KIND == 1) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (b[i] == -INFINITY) off |= 1u << i;
+  }
+  const bool any_off = __any_sync(kFull, off != 0u);
   for (long long t = t0; t < a.T; t += stride) {
     const int ej = next_e;
     const float dj = next_d;
@@ -539,6 +558,11 @@ __global__ void __launch_bounds__(kSelThreads, DENSE ? kSelBlocksPerSm : 6) sele
       } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) sc[i] = sigmoid_fast(l[i]);
+        if (any_off) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if ((off >> i) & 1u) sc[i] = 0.0f;
+        }
       }
       store_row<EP>(s_row[warp], e0, sc);
       __syncwarp();
@@ -552,7 +576,8 @@ __global__ void __launch_bounds__(kSelThreads, DENSE ? kSelBlocksPerSm : 6) sele
         const float v = l + (a.bias != nullptr ? __ldg(a.bias + ej) : 0.0f);
         picked = (v > -INFINITY) ? v : -INFINITY;
       } else {
-        picked = sigmoid(l);
+        const bool open = a.bias == nullptr || __ldg(a.bias + ej) > -INFINITY;
+        picked = open ? sigmoid(l) : 0.0f;
       }
     }
     if constexpr (KIND == 0) {
