@@ -163,9 +163,14 @@ __device__ __forceinline__ float exp_rel_fast(float key, float m) {
   return key == m ? (m > -INFINITY ? 1.0f : 0.0f) : __expf(key - m);
 }
 
-// 1 / (1 + exp(-l)), 0 where masked: the gradient's sigmoid, with the library's exponential
-__device__ __forceinline__ float sigmoid(float l) {
-  return (l > -INFINITY) ? __frcp_rn(__fadd_rn(1.0f, expf(-l))) : 0.0f;
+// The gradient's sigmoid s and its slope s (1 - s), both 0 where masked.  With t = exp(-|l|) and
+// r = 1 / (1 + t), s is r or t r by the sign of l and the slope t r r for both: no difference is
+// taken (1 - s has no digits left where s is 1 to the last bit, from l = 17 on) and t does not
+// overflow.
+__device__ __forceinline__ float2 sigmoid_and_slope(float l) {
+  l = fmaxf(l, -INFINITY);  // (a maximum drops NaN)
+  const float t = expf(-fabsf(l)), r = __frcp_rn(__fadd_rn(1.0f, t)), u = __fmul_rn(t, r);
+  return make_float2(l < 0.0f ? u : r, __fmul_rn(u, r));
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -481,9 +486,13 @@ __device__ __forceinline__ void spread(float* row, int e0, int lane, int e, floa
 // The dense gradient's exponentials on the special-function unit: 2 FP32 steps plus |x| / 2
 // (the product with log2 e is rounded), which a gradient of many summed terms absorbs.  With
 // the library's exponential and rounded reciprocal they were a quarter of the kernel's
-// instructions (T = 32768, E = 256: 22.5 us against 18.4 with these and the loads ahead).
-__device__ __forceinline__ float sigmoid_fast(float l) {
-  return (l > -INFINITY) ? __fdividef(1.0f, 1.0f + __expf(-l)) : 0.0f;
+// instructions (T = 32768, E = 256: 22.5 us against 18.4 with these and the loads ahead).  Without
+// d_prob_sum the chosen experts' sigmoid is expf's: the two calls' gradients of a chosen logit
+// agree to these steps, not to the last bit.
+__device__ __forceinline__ float2 sigmoid_and_slope_fast(float l) {
+  l = fmaxf(l, -INFINITY);
+  const float t = __expf(-fabsf(l)), r = __fdividef(1.0f, 1.0f + t), u = t * r;
+  return make_float2(l < 0.0f ? u : r, u * r);
 }
 
 // DENSE: every expert of a row has a gradient (d_prob, or the plain softmax probability);
@@ -540,7 +549,10 @@ __global__ void __launch_bounds__(kSelThreads, DENSE ? kSelBlocksPerSm : 6) sele
     const bool valid = ej >= 0 && ej < E;
     float d[NV];
     float picked = KIND == 0 ? -INFINITY : 0.0f;  // slot j's key or score, in lane j
+    float slope = 0.0f;                               // slot j's s (1 - s)
+    // the lane's keys, then probabilities; sigmoid: scores, then slopes
     float sc[DENSE ? NV : 1], m = -INFINITY;
+    float z = 0.0f, dot = 0.0f;  // sigmoid: the lane's sums of scores and of g times them
     if constexpr (DENSE) {
       float l[NV];
 #pragma unroll
@@ -556,15 +568,26 @@ __global__ void __launch_bounds__(kSelThreads, DENSE ? kSelBlocksPerSm : 6) sele
           m = fmaxf(m, sc[i]);
         }
       } else {
+        float s[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) sc[i] = sigmoid_fast(l[i]);
+        for (int i = 0; i < NV; ++i) {
+          const float2 v = sigmoid_and_slope_fast(l[i]);
+          s[i] = v.x;
+          sc[i] = v.y;
+        }
         if (any_off) {
 #pragma unroll
           for (int i = 0; i < NV; ++i)
-            if ((off >> i) & 1u) sc[i] = 0.0f;
+            if ((off >> i) & 1u) s[i] = sc[i] = 0.0f;
         }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          z += s[i];
+          dot += g[i] * s[i];
+        }
+        store_row<EP>(s_row[warp], e0, s);
       }
-      store_row<EP>(s_row[warp], e0, sc);
+      if constexpr (KIND == 0) store_row<EP>(s_row[warp], e0, sc);
       __syncwarp();
       if (valid) picked = s_row[warp][ej];
     } else {
@@ -577,14 +600,15 @@ __global__ void __launch_bounds__(kSelThreads, DENSE ? kSelBlocksPerSm : 6) sele
         picked = (v > -INFINITY) ? v : -INFINITY;
       } else {
         const bool open = a.bias == nullptr || __ldg(a.bias + ej) > -INFINITY;
-        picked = open ? sigmoid(l) : 0.0f;
+        const float2 v = sigmoid_and_slope(open ? l : -INFINITY);
+        picked = v.x;
+        slope = v.y;
       }
     }
     if constexpr (KIND == 0) {
-      float dot = 0.0f, rz = 0.0f;
+      float rz = 0.0f;
       if constexpr (DENSE) {
         m = warp_max(m);
-        float z = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           sc[i] = exp_rel_fast(sc[i], m);
@@ -621,21 +645,15 @@ __global__ void __launch_bounds__(kSelThreads, DENSE ? kSelBlocksPerSm : 6) sele
         cd = S > 0.0f ? __fdiv_rn(dj - __fdiv_rn(warp_sum(__fmul_rn(dj, picked)), S), S) : 0.0f;
       }
       if constexpr (DENSE) {
-        float z = 0.0f, dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          z += sc[i];
-          dot += g[i] * sc[i];
-        }
         z = warp_sum(z);
         const float rz = z > 0.0f ? 1.0f / z : 0.0f;
         const float mean = warp_sum(dot) * rz;
         spread<EP>(s_row[warp], e0, lane, valid ? ej : -1, cd, k, d);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          d[i] = ((g[i] - mean) * rz + d[i]) * sc[i] * (1.0f - sc[i]);
+          d[i] = ((g[i] - mean) * rz + d[i]) * sc[i];
       } else {
-        cd = __fmul_rn(__fmul_rn(cd, picked), __fsub_rn(1.0f, picked));
+        cd = __fmul_rn(cd, slope);
         spread<EP>(s_row[warp], e0, lane, valid ? ej : -1, cd, k, d);
       }
     }

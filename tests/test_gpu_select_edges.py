@@ -60,3 +60,55 @@ def test_a_bias_of_minus_infinity_or_nan_masks_its_expert(moe, T, E, k, groups, 
             a = moe.route_select_backward(l, want[0], dw, o, bias=bad, d_prob_sum=d_prob)
             c = moe.route_select_backward(masked, want[0], dw, o, bias=b, d_prob_sum=d_prob)
             assert torch.equal(a, c) and (a[:, off] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,k,far", [(40, 64, 6, 20.0), (17, 256, 8, 20.0), (9, 40, 4, 12.0), (3, 8, 8, 20.0)])
+def test_sigmoid_gradient_of_a_saturated_router(moe, T, E, k, far, dtype):
+    """d l carries s (1 - s), relative to itself also where s is 1 to the last bit.
+
+    On the way to one element: sums (E/32 + 5 twice, k), 10 products and divisions, and at most five
+    exponentials (its own three times, those of the two sums), each within 2 + |l| / 2 steps of 2u on
+    the special-function unit and 6u more for the reciprocal and the sum it stands in."""
+    gen = torch.Generator().manual_seed(E)
+    l = ((torch.rand((T, E), generator=gen) * 2 - 1) * far).to(dtype)
+    l[0, :3] = torch.tensor([10.0, 12.0, 16.0]).to(dtype)
+    d_w, d_p = torch.randn((T, k), generator=gen), torch.randn(E, generator=gen)
+    n = 2 * (E / 32 + 5) + 2 * 5 + 10 + 5 * (2 * (2 + far / 2) + 6)
+    for renorm in (True, False):
+        o = moe.select_opts(1, renorm=renorm)
+        idx, _ = moe.route_select(l.cuda(), k, o)
+        for prob in (None, d_p):
+            d = moe.route_select_backward(l.cuda(), idx, d_w.cuda(), o,
+                                          d_prob_sum=None if prob is None else prob.cuda()).cpu()
+            x = l.double().requires_grad_(True)
+            i = idx.cpu().long()
+            p64 = None if prob is None else prob.double()
+            g = torch.autograd.grad(ref.loss(x, None, 1, i, renorm, d_w.double(), p64), x)[0]
+            x = x.detach()
+            s, one_minus = torch.sigmoid(x), torch.sigmoid(-x)
+            a = d_w.double().abs()
+            if renorm:
+                c = s.gather(1, i)
+                a = (a + (a * c).sum(1, keepdim=True) / c.sum(1, keepdim=True)) / c.sum(1, keepdim=True)
+            M = torch.zeros_like(x).scatter_(1, i, a)
+            if prob is not None:
+                z = s.sum(1, keepdim=True)
+                M = M + (p64.abs() + (p64.abs() * s).sum(1, keepdim=True) / z) / z
+            # (the reference's own 1 - s loses 2^-53 / (1 - s) of itself: nothing at these tolerances)
+            tol = n * U * s * one_minus * M + torch.finfo(dtype).eps / 2 * g.abs()
+            err = (d.double() - g).abs()
+            assert (err <= tol).all(), float((err / tol.clamp(min=1e-300)).max())
+
+
+def test_sigmoid_gradient_at_the_ends(moe):
+    """Logits of any size give finite gradients; 0 where the exponential is."""
+    l = torch.tensor([[-1e30, -200.0, -80.0, 0.0, 80.0, 200.0, 1e30, float("inf")]])
+    for renorm in (True, False):
+        o = moe.select_opts(1, renorm=renorm)
+        idx, w = moe.route_select(l.cuda(), 8, o)
+        for prob in (None, torch.linspace(-1, 1, 8).cuda()):
+            d = moe.route_select_backward(l.cuda(), idx, torch.linspace(1, 2, 8).cuda()[None], o, d_prob_sum=prob)
+            assert torch.isfinite(d).all() and (d[0, [0, 1, 5, 6, 7]] == 0).all()
+            # e^-80 of a term of size 1 (and not 0)
+            assert 1e-37 < abs(float(d[0, 4])) < 1e-33 and 1e-37 < abs(float(d[0, 2])) < 1e-33
