@@ -413,10 +413,10 @@ moe_status moe_router_logits(const void* x, const float* w_router, const float* 
  *   kind MOE_ROUTER_SOFTMAX              key = l + b, score = softmax(key)
  *   kind MOE_ROUTER_SIGMOID_BIAS_SELECT  score = sigmoid(l), key = score + b
  * The experts form n_group groups of E / n_group consecutive ones.  A group's score
- * is the sum of its group_top (1 or 2) largest keys; the topk_group groups with the
- * largest scores stay (ties: lower group), and the k experts in them with the
- * largest keys are chosen, in that order (ties: lower expert).  n_group = 1: no
- * groups.
+ * is the FP32 sum of its group_top (1 or 2) largest keys, not below FP32's lowest
+ * number; the topk_group groups with the largest scores stay (ties: lower group), and
+ * the k experts in them with the largest keys are chosen, in that order (ties: lower
+ * expert).  n_group = 1: no groups.
  *   w_j = score_j, divided by the sum of the k chosen scores if renorm is nonzero.
  * A logit, bias or key of -inf or NaN masks its expert: key -inf, score 0, left out of
  * group sums (a group of masked experts scores -inf); masked experts are chosen only

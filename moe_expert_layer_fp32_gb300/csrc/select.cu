@@ -49,6 +49,7 @@ namespace {
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr float kLowest = -3.402823466e38f;  // FP32's
 constexpr int kSelBlocksPerSm = 4;  // 32 warps of at most 64 registers a thread
 
 struct SelectArgs {
@@ -296,7 +297,8 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
         g2 = fmaxf(fmaxf(g2, o2), fminf(g1, o1));
         g1 = fmaxf(g1, o1);
       }
-      const float gs = (a.group_top == 2 && g2 > -INFINITY) ? __fadd_rn(g1, g2) : g1;
+      // (two keys of FP32's lowest values add up to that lowest value, not to a masked group's -inf)
+      const float gs = (a.group_top == 2 && g2 > -INFINITY) ? fmaxf(__fadd_rn(g1, g2), kLowest) : g1;
       // the largest score's first lane (so its lowest group) topk_group times
       uint32_t gk = (g < a.n_group) ? float_key(gs) : 0u;
       keep = 0u;
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelBlocksPerSm) select_kernel(Se
         if (left <= 0 || bu <= float_key(-INFINITY)) break;
         tu = hit ? 0u : tu;
       }
-      bound = fmaxf(key_float(max(bu, 1u)), -3.402823466e38f);  // (not the masked keys)
+      bound = fmaxf(key_float(max(bu, 1u)), kLowest);  // (not the masked keys)
       count();
     }
 

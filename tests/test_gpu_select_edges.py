@@ -112,3 +112,24 @@ def test_sigmoid_gradient_at_the_ends(moe):
             assert torch.isfinite(d).all() and (d[0, [0, 1, 5, 6, 7]] == 0).all()
             # e^-80 of a term of size 1 (and not 0)
             assert 1e-37 < abs(float(d[0, 4])) < 1e-33 and 1e-37 < abs(float(d[0, 2])) < 1e-33
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_groups_of_lowest_values_stand_above_masked_groups(moe, kind, dtype):
+    """Keys of the type's lowest value are numbers: their group's sum of two is one too, and a group
+    of masked experts does not tie with it."""
+    low = torch.finfo(dtype).min
+    if kind == 0:
+        l, b = torch.full((3, 16), low, dtype=dtype), None
+    else:
+        l, b = torch.zeros((3, 16), dtype=dtype), torch.full((16,), torch.finfo(torch.float32).min)
+    l[0, :4] = -np.inf
+    l[1, :8] = np.nan
+    l[2, :12] = -np.inf
+    o = moe.select_opts(kind, 4, 1, 2)
+    idx, w = moe.route_select(l.cuda(), 2, o, bias=None if b is None else b.cuda())
+    i0, w0, _, _ = ref.select(l.double().numpy(), None if b is None else b.double().numpy(), kind, 2, 4, 1, 2)
+    assert i0.tolist() == [[4, 5], [8, 9], [12, 13]]
+    np.testing.assert_array_equal(idx.cpu().numpy(), i0)
+    np.testing.assert_allclose(w.cpu().numpy(), w0, rtol=8 * U)
