@@ -95,6 +95,12 @@ def _opts(o):
     return None if o is None else ctypes.byref(o)
 
 
+def _select(o):
+    if o is not None and not isinstance(o, moe_select_opts):
+        raise TypeError(f"opts: a select_opts, not {type(o).__name__}")
+    return o
+
+
 _vp, _sz, _i32, _i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
 _sig = {
     "moe_workspace_bytes": (_sz, [moe_dims]),
@@ -444,7 +450,7 @@ def moe_route_select(logits, dtype, ld, bias, opts, T, E, k, topk_idx, topk_w, p
                      workspace=None, stream=None):
     wp, wb = _ws_or_none(workspace)
     _check("moe_route_select", _lib.moe_route_select(
-        _ptr(logits), int(dtype), int(ld), _ptr(bias), _opts(opts), int(T), int(E), int(k),
+        _ptr(logits), int(dtype), int(ld), _ptr(bias), _opts(_select(opts)), int(T), int(E), int(k),
         _ptr(topk_idx), _ptr(topk_w), _ptr(prob_sum), wp, wb, _stream(stream)))
 
 
@@ -452,7 +458,7 @@ def moe_route_select_bwd(logits, dtype, ld, bias, opts, T, E, k, topk_idx, d_top
                          d_logits, ld_d, d_bias=None, workspace=None, stream=None):
     wp, wb = _ws_or_none(workspace)
     _check("moe_route_select_bwd", _lib.moe_route_select_bwd(
-        _ptr(logits), int(dtype), int(ld), _ptr(bias), _opts(opts), int(T), int(E), int(k),
+        _ptr(logits), int(dtype), int(ld), _ptr(bias), _opts(_select(opts)), int(T), int(E), int(k),
         _ptr(topk_idx), _ptr(d_topk_w), _ptr(d_prob_sum), _ptr(d_logits), int(ld_d), _ptr(d_bias),
         wp, wb, _stream(stream)))
 
@@ -500,7 +506,7 @@ def moe_mx4_layer_fwd(x, w_router, bias, opts, route_scale, packed_gate_up, pack
                       topk_idx_out, topk_w_out, counts_out, workspace, stream=None):
     wp, wb = _ws(workspace)
     _check("moe_mx4_layer_fwd", _lib.moe_mx4_layer_fwd(
-        _ptr(x), _ptr(w_router), _ptr(bias), _opts(opts), float(route_scale),
+        _ptr(x), _ptr(w_router), _ptr(bias), _opts(_select(opts)), float(route_scale),
         _ptr(packed_gate_up), _ptr(packed_down), d, _ptr(out), _ptr(topk_idx_out),
         _ptr(topk_w_out), _ptr(counts_out), wp, wb, _stream(stream)))
 
@@ -578,6 +584,18 @@ def _dense(name, t, dtype, shape):
     return t
 
 
+def _buffer(name, t, nbytes=None, of=""):
+    """A dense tensor of any type; of exactly nbytes, if given."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: a tensor, not {type(t).__name__}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a dense tensor, not strides {t.stride()}")
+    n = t.numel() * t.element_size()
+    if nbytes is not None and n != nbytes:
+        raise ValueError(f"{name}: {n} bytes, not the {nbytes} of {of}")
+    return t
+
+
 def _on_device(first, *rest):
     """All tensors on the current CUDA device (the one the library launches on)."""
     dev = first.get_device()
@@ -636,8 +654,7 @@ def route_select(logits, k, opts=None, bias=None, want_prob_sum=False, stream=No
     if stream is not None:
         with _on_stream(stream):
             return route_select(logits, k, opts, bias, want_prob_sum)
-    if opts is None:
-        opts = _default_opts
+    opts = _default_opts if opts is None else _select(opts)
     r = _calls.route_select(logits, k, opts, bias, bool(want_prob_sum))
     if r is not None:
         return _made("moe_route_select", r)
@@ -670,8 +687,7 @@ def route_select_backward(logits, topk_idx, d_topk_w, opts=None, bias=None, d_pr
         with _on_stream(stream):
             return route_select_backward(logits, topk_idx, d_topk_w, opts, bias, d_prob_sum,
                                          want_d_bias)
-    if opts is None:
-        opts = _default_opts
+    opts = _default_opts if opts is None else _select(opts)
     r = _calls.route_select_backward(logits, topk_idx, d_topk_w, opts, bias, d_prob_sum,
                                      bool(want_d_bias))
     if r is not None:
@@ -815,9 +831,8 @@ def mx4_expert_product(x, offsets, packed, N, workspace, dtype=torch.bfloat16, s
     if R >= 1 << 31:
         raise ValueError(f"x: at most 2^31 - 1 rows, not {R}")
     _dense("offsets", offsets, torch.int32, (E + 1,))
-    if packed.numel() * packed.element_size() != moe_mx4_packed_bytes(E, K, N):
-        raise ValueError(f"packed: {packed.numel() * packed.element_size()} bytes, not those of "
-                         f"{E} experts of {K} x {N}")
+    _buffer("packed", packed, moe_mx4_packed_bytes(E, K, N), f"{E} experts of {K} x {N}")
+    _buffer("workspace", workspace)
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"y: float32 or bfloat16, not {dtype}")
     _on_device(x, offsets, packed, workspace)
@@ -843,6 +858,18 @@ def mx4_layer_forward(x, w_router, bias, packed_gate_up, packed_down, d, workspa
         with _on_stream(stream):
             return mx4_layer_forward(x, w_router, bias, packed_gate_up, packed_down, d, workspace,
                                      opts, route_scale, want_routing)
+    opts = _default_opts if opts is None else _select(opts)
+    for name, t, dt, shape in (("x", x, torch.bfloat16, (d.T, d.H)),
+                               ("w_router", w_router, torch.float32, (d.H, d.E)),
+                               ("bias", bias, torch.float32, (d.E,))):
+        if t is not None or name != "bias":
+            _dense(name, _buffer(name, t), dt, shape)
+    up, down = moe_mx4_packed_bytes(d.E, d.H, 2 * d.I), moe_mx4_packed_bytes(d.E, d.I, d.H)
+    if up and down:  # (else the dims are outside the limits, which the call below refuses)
+        _buffer("packed_gate_up", packed_gate_up, up, f"{d.E} experts of {d.H} x {2 * d.I}")
+        _buffer("packed_down", packed_down, down, f"{d.E} experts of {d.I} x {d.H}")
+        _buffer("workspace", workspace)
+        _on_device(x, w_router, bias, packed_gate_up, packed_down, workspace)
     dev = x.device
     out = torch.empty((d.T, d.H), dtype=torch.bfloat16, device=dev)
     idx = w = counts = None
@@ -850,8 +877,8 @@ def mx4_layer_forward(x, w_router, bias, packed_gate_up, packed_down, d, workspa
         idx = torch.empty((d.T, d.k), dtype=torch.int32, device=dev)
         w = torch.empty((d.T, d.k), dtype=torch.float32, device=dev)
         counts = torch.empty(d.E, dtype=torch.int32, device=dev)
-    moe_mx4_layer_fwd(x, w_router, bias, select_opts() if opts is None else opts, route_scale,
-                      packed_gate_up, packed_down, d, out, idx, w, counts, workspace, stream)
+    moe_mx4_layer_fwd(x, w_router, bias, opts, route_scale, packed_gate_up, packed_down, d, out, idx,
+                      w, counts, workspace, stream)
     return (out, idx, w, counts) if want_routing else out
 
 
