@@ -638,6 +638,14 @@ def _logits_args(logits, bias):
     return dt, ld, T, E
 
 
+def _choice_args(name, T, E, k):
+    """The library's limits on a choice of k of E experts, before anything of that size is allocated."""
+    if E <= 0 or k <= 0 or k > E:
+        raise MoEError(name, 1)
+    if E > 256 or k > 16 or T * k >= 1 << 31:
+        raise MoEError(name, 2)
+
+
 def _made(name, r):
     """What a _tensor_calls function returned: its result, or the status of a refusal."""
     if type(r) is int:
@@ -659,6 +667,7 @@ def route_select(logits, k, opts=None, bias=None, want_prob_sum=False, stream=No
     if r is not None:
         return _made("moe_route_select", r)
     dt, ld, T, E = _logits_args(logits, bias)
+    _choice_args("moe_route_select", T, E, k)
     _on_device(logits, bias)
     dev = logits.device
     idx = torch.empty((T, k), dtype=torch.int32, device=dev)

@@ -120,7 +120,9 @@ PyObject* route_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !maybe(a[3], bias))
     Py_RETURN_NONE;
   const int64_t T = l.size(0), E = l.size(1);
-  if (bias.defined() && !plain(bias, at::kFloat, dev, {E})) Py_RETURN_NONE;
+  // (a k outside the limits: the Python path refuses it before it allocates)
+  if (k < 1 || k > 16 || k > E || (bias.defined() && !plain(bias, at::kFloat, dev, {E})))
+    Py_RETURN_NONE;
   at::Tensor idx = make({T, k}, at::kInt, dev), w = make({T, k}, at::kFloat, dev), prob, ws;
   size_t bytes = 0;
   if (a[4] == Py_True) {

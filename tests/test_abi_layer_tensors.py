@@ -81,3 +81,26 @@ def test_selection_options_are_the_selections(moe):  # noqa: F811
             moe.route_select_backward(l, idx, w, bad)
         with pytest.raises(TypeError, match="opts"):
             moe.moe_route_select(4096, 0, E, None, bad, T, E, K, 4096, 4096, stream=0)
+
+
+@pytest.mark.parametrize("experts,k,code", [
+    (E, 1 << 40, "INVALID_ARG"), (E, E + 1, "INVALID_ARG"), (E, 0, "INVALID_ARG"), (E, -1, "INVALID_ARG"),
+    (64, 17, "UNSUPPORTED"), (300, 4, "UNSUPPORTED")])
+def test_a_choice_outside_the_limits_is_refused_before_it_is_allocated(moe, experts, k, code):  # noqa: F811
+    with pytest.raises(moe.MoEError) as e:
+        moe.route_select(torch.zeros((T, experts)), k)
+    assert moe.STATUS[e.value.code] == "MOE_ERR_" + code
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k", [1 << 40, 1 << 30, 17, 0, -1])
+def test_a_choice_outside_the_limits_on_both_paths(moe, cuda_ok, k):  # noqa: F811
+    wide = torch.zeros((4096, 72), device="cuda")
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    for l in (wide[:, :64], wide[:, :64].contiguous()):
+        held = torch.cuda.max_memory_allocated()
+        with pytest.raises(moe.MoEError):
+            moe.route_select(l, k)
+        assert torch.cuda.max_memory_allocated() == held
+    assert torch.cuda.memory_allocated() >= before
