@@ -96,11 +96,9 @@ def test_a_choice_outside_the_limits_is_refused_before_it_is_allocated(moe, expe
 @pytest.mark.parametrize("k", [1 << 40, 1 << 30, 17, 0, -1])
 def test_a_choice_outside_the_limits_on_both_paths(moe, cuda_ok, k):  # noqa: F811
     wide = torch.zeros((4096, 72), device="cuda")
-    before = torch.cuda.memory_allocated()
     torch.cuda.reset_peak_memory_stats()
     for l in (wide[:, :64], wide[:, :64].contiguous()):
         held = torch.cuda.max_memory_allocated()
         with pytest.raises(moe.MoEError):
             moe.route_select(l, k)
         assert torch.cuda.max_memory_allocated() == held
-    assert torch.cuda.memory_allocated() >= before
