@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -23,9 +24,24 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _tensor_calls as _calls  # noqa: E402  (built with the library; needs torch loaded)
+try:  # the tensor calls' fast path, built with the library against one torch's headers
+    from . import _tensor_calls as _calls
+    if _calls.torch_version != torch.__version__:
+        raise ImportError(f"built with torch {_calls.torch_version}, this is {torch.__version__}")
+    _calls.bind(LIB_PATH)
+    NATIVE_TENSOR_CALLS = True
+except ImportError as _e:
+    warnings.warn(f"the native tensor calls are not available ({_e}): the same calls go through "
+                  "Python, which takes longer on the host (build: python "
+                  "moe_expert_layer_fp32_gb300/build.py)")
+    NATIVE_TENSOR_CALLS = False
 
-_calls.bind(LIB_PATH)
+    class _calls:  # declines every call
+        @staticmethod
+        def _decline(*args):
+            return None
+
+        route_select = route_select_backward = mx4_quantize = mx4_expert_product = _decline
 
 MOE_OK = 0
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_MISALIGNED",

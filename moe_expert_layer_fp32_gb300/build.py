@@ -1,8 +1,10 @@
 """Builds libmoe_gb300.so (the C ABI of include/moe.h) from csrc/ with nvcc for
 sm_103a, in-tree.  One nvcc process per translation unit, run in parallel, then
 one link; beside them g++ builds _tensor_calls.so (csrc/tensor_calls.cpp, the
-tensor calls' fast path) against torch's headers.  Usage: ``python moe_expert_layer_fp32_gb300/build.py [--force] [-v]``
-(run it by path: importing the package itself needs the built library)."""
+tensor calls' fast path) against torch's headers; a host without g++ or those headers
+goes without it, and the package calls the library from Python alone.  Usage:
+``python moe_expert_layer_fp32_gb300/build.py [--force] [-v]`` (run it by path: importing the
+package itself needs the built library)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -54,28 +56,58 @@ def built_for_this_machine(path: str) -> bool:
     return want is None or int.from_bytes(head[18:20], "little") == want
 
 
+def newest_source() -> float:
+    return max(os.path.getmtime(p) for p in sources() + headers() + [CALLS_SRC, __file__])
+
+
 def up_to_date() -> bool:
-    if not built_for_this_machine(LIB) or not built_for_this_machine(CALLS):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return all(os.path.getmtime(p) <= t for p in sources() + headers() + [CALLS_SRC, __file__])
+    built = [LIB] if calls_missing() else [LIB, CALLS]
+    return (all(built_for_this_machine(p) for p in built) and
+            newest_source() <= min(os.path.getmtime(p) for p in built))
 
 
-def build_calls() -> str:
+def cxx() -> str:
+    return os.environ.get("CXX", "g++")
+
+
+def calls_includes():
     import sysconfig
     from torch.utils import cpp_extension
-    inc = cpp_extension.include_paths() + [
+    return cpp_extension.include_paths() + [
         sysconfig.get_paths()["include"], os.path.join(os.path.dirname(nvcc()), "..", "include"),
         os.path.join(ROOT, "include")]
+
+
+def calls_missing():
+    """What _tensor_calls.so cannot be built without and is not here, or None."""
+    if shutil.which(cxx()) is None:
+        return f"no compiler {cxx()}"
+    inc = calls_includes()
+    for h in ("Python.h", "torch/csrc/autograd/python_variable.h"):
+        if not any(os.path.exists(os.path.join(i, h)) for i in inc):
+            return f"no header {h}"
+    return None
+
+
+def build_calls() -> None:
+    import torch
+    from torch.utils import cpp_extension
+    missing = calls_missing()
+    if missing:
+        print(f"_tensor_calls.so: not built ({missing}); the tensor calls go through Python",
+              file=sys.stderr)
+        if os.path.exists(CALLS):  # an older one would not match the sources
+            os.remove(CALLS)
+        return
     tmp = CALLS + f".tmp{os.getpid()}"
     r = subprocess.run(
-        [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", CALLS_SRC, "-o", tmp,
-         *["-I" + i for i in inc], *["-L" + d for d in cpp_extension.library_paths()], "-lc10",
-         "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ldl"], capture_output=True, text=True)
+        [cxx(), "-O2", "-std=c++17", "-fPIC", "-shared", CALLS_SRC, "-o", tmp,
+         f'-DMOE_BUILT_WITH_TORCH="{torch.__version__}"', *["-I" + i for i in calls_includes()],
+         *["-L" + d for d in cpp_extension.library_paths()], "-lc10", "-lc10_cuda", "-ltorch_cpu",
+         "-ltorch_python", "-ldl"], capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{cxx()} failed on {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS)
-    return CALLS
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -248,4 +248,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_calls", nullptr, -1, metho
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tensor_calls() { return PyModule_Create(&module); }
+// torch_version: the torch whose headers this was built with; the package uses it with no other
+PyMODINIT_FUNC PyInit__tensor_calls() {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", MOE_BUILT_WITH_TORCH) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
