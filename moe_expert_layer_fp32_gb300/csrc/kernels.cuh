@@ -170,7 +170,6 @@ cudaError_t launch_mx4_quantize(const void* x, int dtype, long long ld, long lon
                                 void* codes, void* scales, void* values, cudaStream_t s);
 // An expert operand's row images.  src 0: x [R, K]; 1: row r is row row_of[r] / k of x [T, K]
 // bf16; 2: silu(gate) * up of x [R, 2K] bf16.
-constexpr int kMx4FewRows = 152 * 16 * 4;  // 16 warps of four rows on every SM
 cudaError_t launch_mx4_rows(const void* x, int dtype, int src, const int32_t* row_of, int k, int T,
                             const int32_t* offsets, int E, int R, int K, int tile_rows, void* codes,
                             void* sf, int32_t* status, cudaStream_t s);
