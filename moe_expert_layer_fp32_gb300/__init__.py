@@ -674,7 +674,11 @@ _default_opts = select_opts()
 
 def route_select(logits, k, opts=None, bias=None, want_prob_sum=False, stream=None):
     """(topk_idx [T, k] int32, topk_w [T, k] fp32[, prob_sum [E] fp32]) from logits [T, E]
-    (fp32, bf16 or fp16).  opts: a select_opts (default: softmax over all experts)."""
+    (fp32, bf16 or fp16).  opts: a select_opts (default: softmax over all experts).
+
+    Not part of autograd: the results carry no gradient, whatever the logits require.  A
+    training step calls route_select_backward (as in examples/mx4_layer.py), or wraps the two
+    in a torch.autograd.Function."""
     if stream is not None:
         with _on_stream(stream):
             return route_select(logits, k, opts, bias, want_prob_sum)
@@ -707,7 +711,8 @@ def route_select(logits, k, opts=None, bias=None, want_prob_sum=False, stream=No
 def route_select_backward(logits, topk_idx, d_topk_w, opts=None, bias=None, d_prob_sum=None,
                           want_d_bias=False, stream=None):
     """d_logits [T, E] in the logits' type (and d_bias [E] fp32 if want_d_bias, softmax only)
-    for d_topk_w [T, k] and, if given, d_prob_sum [E], both fp32; the choice stays fixed."""
+    for d_topk_w [T, k] and, if given, d_prob_sum [E], both fp32; the choice stays fixed.
+    The gradient itself: nothing is recorded for or taken from autograd."""
     if stream is not None:
         with _on_stream(stream):
             return route_select_backward(logits, topk_idx, d_topk_w, opts, bias, d_prob_sum,
@@ -747,7 +752,7 @@ def route_select_backward(logits, topk_idx, d_topk_w, opts=None, bias=None, d_pr
 
 def mx4_quantize(x, want_values=False, stream=None):
     """(codes [R, K/2] uint8, scales [R, K/32] uint8[, values [R, K] bf16]) of rows x [R, K]
-    (fp32, bf16 or fp16), K a multiple of 32."""
+    (fp32, bf16 or fp16), K a multiple of 32.  Not part of autograd."""
     if stream is not None:
         with _on_stream(stream):
             return mx4_quantize(x, want_values)

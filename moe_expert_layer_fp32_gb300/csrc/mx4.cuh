@@ -6,7 +6,8 @@
 // codes share a byte, the even one in the low half.  (OCP Microscaling Formats v1.0:
 // element E2M1, scale E8M0, block size 32.)
 //
-// Operand images.  The product reads shared-memory images that one bulk copy brings in:
+// Operand images.  The product reads shared-memory images that one bulk copy (or tensor load of
+// 1024-byte lines) brings in:
 // rows of 128 bytes (256 codes, a k-block) whose 16-byte chunk c sits at c ^ (row & 7)
 // (the MMA's 128-byte swizzle), and the scales of 128 rows x 128 K as 512 bytes, row r's
 // four scales at (r % 32) * 16 + (r / 32) * 4 (the order in which tensor memory takes

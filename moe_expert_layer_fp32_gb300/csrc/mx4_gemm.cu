@@ -8,8 +8,8 @@
 // The weights take the MMA's M side: 128 output columns in the accumulator's lanes, a
 // tile of up to 224 rows of the expert in its columns (N is the tile's own row count, so
 // a short tile costs what it holds).  Persistent CTAs, one per SM, warp-specialised:
-//   warp 0   producer: three bulk copies a k-block of 256 (weights with their scales,
-//            rows, row scales) into a ring of STAGES shared-memory images
+//   warp 0   producer: three copies a k-block of 256 (weights with their scales, rows, row
+//            scales) into a ring of STAGES shared-memory images
 //   warp 1   MMA issuer: the scales from shared into tensor memory, then four MMAs of
 //            K = 64.  The role runs in one elected lane for its whole loop: issued from a
 //            lane picked by its index instead, an MMA took 95 cycles of issue, the 224-row
@@ -21,8 +21,8 @@
 //
 // What it has to do: read each row's codes and each active expert's weights (0.53 bytes a
 // value) once, write y.  Measured on GB300 (ncu, alone): 131072 rows of 128 experts, K = 2048,
-// N = 1536, bf16 out: 164 us for 825 GFLOP and 0.71 GB (107 us at the copy rate), 5.0 PFLOP/s,
-// tensor pipe busy 56%; 512 rows of 64 experts, K = N = 2048: 28.8 us for 140 MB of weights
+// N = 1536, bf16 out: 171 us for 825 GFLOP and 0.71 GB (107 us at the copy rate), 4.8 PFLOP/s,
+// tensor pipe busy 53%; 512 rows of 64 experts, K = N = 2048: 29.6 us for 140 MB of weights
 // (21 us).  Per k-block the pair's MMAs take 416 cycles at 208 rows (the K = 64 rate of 16384
 // products a clock and SM) and the loads 528 (34 KB at 64 bytes a clock); the rest is waiting
 // for rows and weights.  What the steps brought, packed case with its row images: single CTAs

@@ -5,7 +5,9 @@
 //  - before pdl_wait() it reads nothing the previous kernel writes and writes
 //    nothing the previous kernel reads or writes;
 //  - it calls pdl_launch_dependents() only after its own pdl_wait(), so a kernel
-//    that starts early has every kernel but its direct predecessor complete.
+//    that starts early has every kernel but its direct predecessor complete.  A kernel
+//    that is itself launched without the attribute starts after its predecessor has
+//    finished, and may call it at once, without a wait.
 // pdl_wait() returns at once when the kernel was launched without the attribute
 // or its predecessor has finished; a kernel that never calls
 // pdl_launch_dependents() lets its dependent start when it completes.

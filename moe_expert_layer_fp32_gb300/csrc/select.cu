@@ -8,16 +8,18 @@
 // Cody & Waite exponential whose every step is one IEEE operation, so that a choice does
 // not depend on which kernel made it).  Groups are E / n_group consecutive experts; a
 // group's score is the sum of its group_top (1 or 2) largest keys that are not masked (-inf
-// if all are); the topk_group groups
-// with the largest scores stay, then the k experts in them with the largest keys, both
-// with ties to the lower index.  w_j = score_j, or score_j / sum of the chosen scores.
-// prob_sum[e] = sum over tokens of score_e / sum_E score (what a balance loss needs).
+// if all are); the topk_group groups with the largest scores stay, then the k experts in them
+// with the largest keys, both with ties to the lower index.  w_j = score_j, or score_j / sum of
+// the chosen scores.  prob_sum[e] = sum over tokens of score_e / sum_E score (what a balance loss
+// needs), like d_bias an FP32 sum over each warp's tokens, the block's warps and the blocks, with
+// T / 4864 + 60 terms in a chain (608 blocks).
 //
 // Gradient, with c the chosen experts, S = sum of their scores, q = score / sum_E score,
 // g = d_prob_sum:
 //   d score_j += renorm ? (dw_j - sum_i dw_i w_i) / S : dw_j        (j chosen)
 //   softmax: d l_e = q_e (D_e - sum_i D_i q_i),  D_e = g_e + [e chosen] dw'
-//   sigmoid: d l_e = s_e (1 - s_e) (d score_e + (g_e - sum_i g_i q_i) / sum_E s)
+//   sigmoid: d l_e = s_e (1 - s_e) (d score_e + (g_e - sum_i g_i q_i) / sum_E s), the factor
+//            from exp(-|l_e|) without a difference
 // For the renormalised softmax the factor 1/S cancels against q: d l_j = w_j (dw_j - sum
 // dw_i w_i) for the chosen, formed from exponentials relative to the largest chosen key,
 // so that chosen experts far below the row's largest logit keep their precision.
@@ -27,13 +29,15 @@
 // What bounds the selection is its instructions, some 900 a token and warp, issued in three of
 // four cycles; comparisons, selections and integers issue at half the rate of the arithmetic.
 // Measured on GB300 at that size, sigmoid scores, 8 of 256 experts from 4 of 8 groups, in a
-// CUDA graph: 30.4 us, with prob_sum 35.6; of it the sigmoids take 5, the groups 4, the choice
+// CUDA graph: 30.0 us, with prob_sum 34.5; of it the sigmoids take 5, the groups 4, the choice
 // of eight instead of one 3.5.  The steps that brought it there from 81 us: candidates above a
 // bound of the k-th key ranked side by side instead of k argmax rounds over all keys (45), two
 // sigmoids an instruction and group maxima in registers (40), the next token's loads in flight
-// (38.5), candidates by a lane mask (37.4), no limits and masks for plain rows (35.6).  Three
-// heads a lane and k rounds of warp maxima instead of bound and ranks took 45.9.
-// The gradient with every expert's share: 18.3 us for 67 MB (10 us), latency and issue.
+// (38.5), candidates by a lane mask (37.4), no limits and masks for plain rows (35.6), the bias
+// by 16-byte loads (34.5).  Three heads a lane and k rounds of warp maxima instead of bound and
+// ranks took 45.9.
+// The gradient with every expert's share: 16.2-16.7 us in a graph for 67 MB (10 us), latency and
+// issue; of the chosen alone (no d_prob_sum, renormalised) 13.5.
 #include <math.h>
 
 #include <type_traits>
