@@ -21,19 +21,20 @@
 //
 // What it has to do: read each row's codes and each active expert's weights (0.53 bytes a
 // value) once, write y.  Measured on GB300 (ncu, alone): 131072 rows of 128 experts, K = 2048,
-// N = 1536, bf16 out: 171 us for 825 GFLOP and 0.71 GB (107 us at the copy rate), 4.8 PFLOP/s,
-// tensor pipe busy 53%; 512 rows of 64 experts, K = N = 2048: 29.6 us for 140 MB of weights
+// N = 1536, bf16 out: 169 us for 825 GFLOP and 0.71 GB (107 us at the copy rate), 4.9 PFLOP/s,
+// tensor pipe busy 55%; 512 rows of 64 experts, K = N = 2048: 29.6 us for 140 MB of weights
 // (21 us).  Per k-block the pair's MMAs take 416 cycles at 208 rows (the K = 64 rate of 16384
 // products a clock and SM) and the loads 528 (34 KB at 64 bytes a clock); the rest is waiting
 // for rows and weights.  What the steps brought, packed case with its row images: single CTAs
 // of 224 rows 346 us; pairs 323; units walked without searches and divisions on the issuing
 // thread (1900 cycles a unit before, hidden now) 294 -> 280; what a unit touches first moved
 // into L2 ahead 277; the odd CTA's bytes counted by the even one, three tensor loads a k-block in
-// place of its own bulk copies and a relay without cluster scope, 288.  Not kept: the rows' images
-// made and multiplied chunk by chunk side by side (no gain: every product's start and drain cost
-// what the overlap saved), every CTA prefetching its next unit (six CTAs ask for the same rows:
-// 198 -> 240), quantising inside this kernel (457 us: too few warps for the loads beside the
-// tensor core's share of memory).
+// place of its own bulk copies and a relay without cluster scope, 288; rows before weights 282.5.
+// Not kept: the rows' images made and multiplied chunk by chunk side by side (no gain: every
+// product's start and drain cost what the overlap saved), every CTA prefetching its next unit
+// (six CTAs ask for the same rows: 198 -> 240), quantising inside this kernel (457 us: too few
+// warps for the loads beside the tensor core's share of memory), the odd CTA's loads from two
+// threads (280.4 in a graph).
 //
 // Every wait is bounded.  A wait that runs out, in whichever role, raises the CTA's abort flag;
 // once all roles of the CTA (or pair) are done, a raised flag makes the producers wait for the
@@ -282,11 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             aborted = true;
             break;
           }
-          if (it >= early) {
-            arm(s, w);
-            load_weights(s, w, kb);
-          }
+          // (rows before weights: packed case 282.8 us the other way round, 279.0 so, in a graph)
+          if (it >= early) arm(s, w);
           load_rows(s, w, kb);
+          if (it >= early) load_weights(s, w, kb);
           if (fetch_w) prefetch_l2(wimg + nx.w_img + (size_t)kb * kMx4WBytes, kMx4WBytes);
           if (fetch_rows)
             prefetch_l2(rimg + nx.row_img + (size_t)kb * nx.rows16 * 128, nx.rows16 * 128);
