@@ -533,6 +533,103 @@ moe_status moe_mx4_layer_fwd(const void* x, const float* w_router, const float* 
                              void* out, int32_t* topk_idx_out, float* topk_w_out,
                              int32_t* counts_out, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Training the experts: grouped products in the logical layouts with their
+ * gradients, the gradient of the SwiGLU, the experts' backward pass, and
+ * orthogonalised updates.
+ *
+ * dtype is MOE_DTYPE_BF16 or MOE_DTYPE_F16, the type of both operands of a product;
+ * products are exact, sums FP32, and a 16-bit output is rounded once.  Matrices have
+ * rows of adjacent elements, ld elements apart and starting on 16-byte boundaries
+ * (ld * element size a multiple of 16); stacks of E matrices es elements apart, es a
+ * multiple of ld.  K, N, H and I are multiples of 8, at most 32768 (I: 16384);
+ * 1 <= E <= 256.  offsets [E+1] int32 as moe_load_stats writes them: expert e has the
+ * rows [offsets[e], offsets[e+1]).  Offsets that are not a non-decreasing sequence
+ * from 0 to R are flagged (MOE_ERR_DEVICE_CHECK) and no output is written.
+ * Workspaces as moe_workspace_bytes describes them (status word first). */
+
+/* Workspace of the two grouped calls below (0: outside the limits). */
+size_t moe_grouped_workspace_bytes(int32_t E, int32_t K, int32_t N);
+
+/* Grouped product: y[r, n] = sum over k of x[r, k] * W_e[k, n] for the rows r of
+ * expert e, w [E, K, N] as the weights of moe_prepack_expert_weights; transposed
+ * nonzero: y[r, n] = sum over k of x[r, k] * W_e[n, k], w [E, N, K], which is also the
+ * gradient of the first for its rows (x the gradient of y, w the same tensor).
+ *   x [R, K]; y [R, N] of y_dtype (any moe_dtype)
+ * A row's result does not depend on the other rows. */
+moe_status moe_grouped_product(const void* x, int64_t x_ld, int32_t dtype, const int32_t* offsets,
+                               const void* w, int64_t w_ld, int64_t w_es, int32_t transposed,
+                               int32_t R, int32_t K, int32_t N, int32_t E, void* y, int64_t y_ld,
+                               int32_t y_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradient of the product for the weights: d_w[e, k, n] = sum over the rows r of expert
+ * e of x[r, k] * dy[r, n], in an order that the rows' number fixes; 0 for an expert
+ * without rows.
+ *   x [R, K], dy [R, N] of dtype; d_w [E, K, N] of w_dtype (any moe_dtype)
+ *   accumulate nonzero (FP32 only): d_w += instead (an expert without rows is not
+ *   touched). */
+moe_status moe_grouped_weight_grad(const void* x, int64_t x_ld, const void* dy, int64_t dy_ld,
+                                   int32_t dtype, const int32_t* offsets, int32_t R, int32_t K,
+                                   int32_t N, int32_t E, void* d_w, int64_t w_ld, int64_t w_es,
+                                   int32_t w_dtype, int32_t accumulate, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
+/* h[r, i] = row_w[r] * silu(gate_up[r, i]) * gate_up[r, I + i], one rounding (row_w NULL:
+ * 1).  gate_up [R, 2 I], h [R, I] of dtype. */
+moe_status moe_swiglu(const void* gate_up, int64_t gate_up_ld, const float* row_w, int32_t dtype,
+                      int32_t R, int32_t I, void* h, int64_t h_ld, void* stream);
+
+/* Gradient of moe_swiglu for d_h [R, I], the gradient of its result:
+ *   d_gate_up [R, 2 I] out; d_row_w [R] fp32 out or NULL: sum over i of d_h[r, i] *
+ *   silu(gate) * up; h [R, I] out or NULL: moe_swiglu's result once more (what the
+ *   gradient of a product that follows reads) */
+moe_status moe_swiglu_bwd(const void* gate_up, int64_t gate_up_ld, const void* d_h, int64_t d_ld,
+                          const float* row_w, int32_t dtype, int32_t R, int32_t I,
+                          void* d_gate_up, int64_t d_gate_up_ld, void* h, int64_t h_ld,
+                          float* d_row_w, void* stream);
+
+/* Workspace of moe_expert_ffn_bwd (0: outside the limits). */
+size_t moe_expert_ffn_bwd_workspace_bytes(int32_t R, int32_t H, int32_t I, int32_t E);
+
+/* Backward pass of the experts, for the combined output
+ *   out[t] = sum over t's rows r of row_w[r] * (silu(gate) * up)[r] W_down,
+ *   [gate | up][r] = x_perm[r] W_gate_up
+ * and d_y[r] = the gradient of out[t] for the token t of row r (moe_permute of d_out).
+ *   x_perm, d_y [R, H]; w_gate_up [E, H, 2 I] (gate columns first), w_down [E, I, H], all
+ *   dense, of dtype
+ *   gate_up [R, 2 I] of dtype as moe_grouped_product left it, or NULL: computed again
+ *   row_w [R] fp32 or NULL: 1
+ * Outputs, each may be NULL: d_x_perm [R, H] of d_x_dtype, a row's gradient before the
+ * sum over its token's rows; d_w_gate_up and d_w_down in the weights' shapes, of
+ * d_w_dtype (accumulate nonzero, FP32 only: +=); d_row_w [R] fp32.  The gradient of
+ * gate and up, that of their product and the product itself are rounded to dtype. */
+moe_status moe_expert_ffn_bwd(const void* x_perm, const int32_t* offsets, const void* w_gate_up,
+                              const void* w_down, const void* gate_up, const float* row_w,
+                              const void* d_y, int32_t dtype, int32_t R, int32_t H, int32_t I,
+                              int32_t E, void* d_x_perm, int32_t d_x_dtype, void* d_w_gate_up,
+                              void* d_w_down, int32_t d_w_dtype, int32_t accumulate,
+                              float* d_row_w, void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace of moe_orthogonalize (0: outside the limits: rows and cols at most 16384). */
+size_t moe_orthogonalize_workspace_bytes(int32_t E, int32_t rows, int32_t cols);
+
+/* Orthogonalised updates of a stack of E matrices m [E, rows, cols] of dtype (any
+ * moe_dtype; ld and es any that keep elements apart):
+ *   X = M_e / (|M_e| + eps), |.| the Frobenius norm; then `steps` (1..64) times
+ *   X = a X + (b X X^T + c (X X^T)^2) X   (X^T X on the right for rows > cols)
+ * and out[e] = scale * X of out_dtype (bf16 or fp16).  coefficients: a, b, c (host); 3.4445,
+ * -4.7750, 2.0315 with five steps bring singular values above about 0.002 of the norm
+ * to between 0.7 and 1.2.  A zero matrix gives zeros; one with an infinity or a NaN gives NaN,
+ * and the others' results do not depend on it.
+ * X and the products are held in FP16 (times 1024; |X| stays near 1) between steps and
+ * summed in FP32: see the error of each step's rounding where singular values are far
+ * below the others: a step lifts them, and the rounding noise beside them, a times.
+ * Out may be m. */
+moe_status moe_orthogonalize(const void* m, int32_t dtype, int64_t ld, int64_t es, int32_t E,
+                             int32_t rows, int32_t cols, const float* coefficients, int32_t steps,
+                             float eps, float scale, void* out, int32_t out_dtype, int64_t out_ld,
+                             int64_t out_es, void* workspace, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, returns the workspace status word in *status_out
  * (MOE_OK or the first device-side error recorded since the last read) and
  * clears it. */

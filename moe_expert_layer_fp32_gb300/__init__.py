@@ -63,7 +63,10 @@ ABI_SYMBOLS = ("moe_workspace_bytes", "moe_packed_weight_bytes", "moe_route", "m
                "moe_router_logits", "moe_select_workspace_bytes", "moe_route_select",
                "moe_route_select_bwd", "moe_mx4_quantize", "moe_mx4_packed_bytes",
                "moe_mx4_pack", "moe_mx4_prepack", "moe_mx4_product_workspace_bytes",
-               "moe_mx4_expert_product", "moe_mx4_layer_workspace_bytes", "moe_mx4_layer_fwd")
+               "moe_mx4_expert_product", "moe_mx4_layer_workspace_bytes", "moe_mx4_layer_fwd",
+               "moe_grouped_workspace_bytes", "moe_grouped_product", "moe_grouped_weight_grad",
+               "moe_swiglu", "moe_swiglu_bwd", "moe_expert_ffn_bwd_workspace_bytes",
+               "moe_expert_ffn_bwd", "moe_orthogonalize_workspace_bytes", "moe_orthogonalize")
 
 
 class moe_dims(ctypes.Structure):
@@ -177,6 +180,22 @@ _sig = {
     "moe_mx4_layer_workspace_bytes": (_sz, [moe_dims]),
     "moe_mx4_layer_fwd": (ctypes.c_int, [_vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, moe_dims,
                                          _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_grouped_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "moe_grouped_product": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _i64, _i64, _i32, _i32, _i32,
+                                           _i32, _i32, _vp, _i64, _i32, _vp, _sz, _vp]),
+    "moe_grouped_weight_grad": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i32, _vp, _i32, _i32, _i32,
+                                               _i32, _vp, _i64, _i64, _i32, _i32, _vp, _sz, _vp]),
+    "moe_swiglu": (ctypes.c_int, [_vp, _i64, _vp, _i32, _i32, _i32, _vp, _i64, _vp]),
+    "moe_swiglu_bwd": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _vp, _i64, _vp,
+                                      _i64, _vp, _vp]),
+    "moe_expert_ffn_bwd_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "moe_expert_ffn_bwd": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
+                                          _i32, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _sz,
+                                          _vp]),
+    "moe_orthogonalize_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "moe_orthogonalize": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i32, _i32, _i32, _vp, _i32,
+                                         ctypes.c_float, ctypes.c_float, _vp, _i32, _i64, _i64, _vp,
+                                         _sz, _vp]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -525,6 +544,70 @@ def moe_mx4_layer_fwd(x, w_router, bias, opts, route_scale, packed_gate_up, pack
         _ptr(x), _ptr(w_router), _ptr(bias), _opts(_select(opts)), float(route_scale),
         _ptr(packed_gate_up), _ptr(packed_down), d, _ptr(out), _ptr(topk_idx_out),
         _ptr(topk_w_out), _ptr(counts_out), wp, wb, _stream(stream)))
+
+
+def moe_grouped_workspace_bytes(E, K, N) -> int:
+    return int(_lib.moe_grouped_workspace_bytes(int(E), int(K), int(N)))
+
+
+def moe_grouped_product(x, x_ld, dtype, offsets, w, w_ld, w_es, transposed, R, K, N, E, y, y_ld,
+                        y_dtype, workspace, stream=None):
+    wp, wb = _ws(workspace)
+    _check("moe_grouped_product", _lib.moe_grouped_product(
+        _ptr(x), int(x_ld), int(dtype), _ptr(offsets), _ptr(w), int(w_ld), int(w_es),
+        int(bool(transposed)), int(R), int(K), int(N), int(E), _ptr(y), int(y_ld), int(y_dtype), wp,
+        wb, _stream(stream)))
+
+
+def moe_grouped_weight_grad(x, x_ld, dy, dy_ld, dtype, offsets, R, K, N, E, d_w, w_ld, w_es,
+                            w_dtype, accumulate, workspace, stream=None):
+    wp, wb = _ws(workspace)
+    _check("moe_grouped_weight_grad", _lib.moe_grouped_weight_grad(
+        _ptr(x), int(x_ld), _ptr(dy), int(dy_ld), int(dtype), _ptr(offsets), int(R), int(K), int(N),
+        int(E), _ptr(d_w), int(w_ld), int(w_es), int(w_dtype), int(bool(accumulate)), wp, wb,
+        _stream(stream)))
+
+
+def moe_swiglu(gate_up, gate_up_ld, row_w, dtype, R, I, h, h_ld, stream=None):
+    _check("moe_swiglu", _lib.moe_swiglu(_ptr(gate_up), int(gate_up_ld), _ptr(row_w), int(dtype),
+                                         int(R), int(I), _ptr(h), int(h_ld), _stream(stream)))
+
+
+def moe_swiglu_bwd(gate_up, gate_up_ld, d_h, d_ld, row_w, dtype, R, I, d_gate_up, d_gate_up_ld,
+                   h=None, h_ld=0, d_row_w=None, stream=None):
+    _check("moe_swiglu_bwd", _lib.moe_swiglu_bwd(
+        _ptr(gate_up), int(gate_up_ld), _ptr(d_h), int(d_ld), _ptr(row_w), int(dtype), int(R),
+        int(I), _ptr(d_gate_up), int(d_gate_up_ld), _ptr(h), int(h_ld), _ptr(d_row_w),
+        _stream(stream)))
+
+
+def moe_expert_ffn_bwd_workspace_bytes(R, H, I, E) -> int:
+    return int(_lib.moe_expert_ffn_bwd_workspace_bytes(int(R), int(H), int(I), int(E)))
+
+
+def moe_expert_ffn_bwd(x_perm, offsets, w_gate_up, w_down, gate_up, row_w, d_y, dtype, R, H, I, E,
+                       d_x_perm, d_x_dtype, d_w_gate_up, d_w_down, d_w_dtype, accumulate, d_row_w,
+                       workspace, stream=None):
+    wp, wb = _ws(workspace)
+    _check("moe_expert_ffn_bwd", _lib.moe_expert_ffn_bwd(
+        _ptr(x_perm), _ptr(offsets), _ptr(w_gate_up), _ptr(w_down), _ptr(gate_up), _ptr(row_w),
+        _ptr(d_y), int(dtype), int(R), int(H), int(I), int(E), _ptr(d_x_perm), int(d_x_dtype),
+        _ptr(d_w_gate_up), _ptr(d_w_down), int(d_w_dtype), int(bool(accumulate)), _ptr(d_row_w), wp,
+        wb, _stream(stream)))
+
+
+def moe_orthogonalize_workspace_bytes(E, rows, cols) -> int:
+    return int(_lib.moe_orthogonalize_workspace_bytes(int(E), int(rows), int(cols)))
+
+
+def moe_orthogonalize(m, dtype, ld, es, E, rows, cols, coefficients, steps, eps, scale, out,
+                      out_dtype, out_ld, out_es, workspace, stream=None):
+    wp, wb = _ws(workspace)
+    co = None if coefficients is None else (ctypes.c_float * 3)(*coefficients)
+    _check("moe_orthogonalize", _lib.moe_orthogonalize(
+        _ptr(m), int(dtype), int(ld), int(es), int(E), int(rows), int(cols), co, int(steps),
+        float(eps), float(scale), _ptr(out), int(out_dtype), int(out_ld), int(out_es), wp, wb,
+        _stream(stream)))
 
 
 def moe_set_wait_limit(cycles: int) -> None:
@@ -910,6 +993,261 @@ def mx4_layer_forward(x, w_router, bias, packed_gate_up, packed_down, d, workspa
     moe_mx4_layer_fwd(x, w_router, bias, opts, route_scale, packed_gate_up, packed_down, d, out, idx,
                       w, counts, workspace, stream)
     return (out, idx, w, counts) if want_routing else out
+
+
+# ------------------------------------------------------ training the experts ---
+# (as the calls above: not part of autograd; a training step calls the gradients itself)
+def _stack(name, t, dtype, shape):
+    """(row stride, matrix stride) of a 3D tensor of rows of adjacent elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: a tensor, not {type(t).__name__}")
+    if (dtype is not None and t.dtype != dtype) or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: a {dtype} tensor of shape {tuple(shape)}, not {t.dtype} "
+                         f"{tuple(t.shape)}")
+    E, rows, cols = shape
+    if cols > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent (stride {t.stride()})")
+    ld = t.stride(1) if rows > 1 else cols
+    es = t.stride(0) if E > 1 else rows * ld
+    if ld < cols or es < rows * ld:
+        raise ValueError(f"{name}: rows and matrices must not overlap (stride {t.stride()})")
+    return ld, es
+
+
+def _rows16(name, t, dtype, shape):
+    """Row stride of a 2D tensor of this 16-bit type and shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: a tensor, not {type(t).__name__}")
+    if t.dtype not in (torch.bfloat16, torch.float16) or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name}: {dtype or 'bfloat16 or float16'}, not {t.dtype}")
+    if t.dim() != 2 or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: {tuple(shape)}, not {tuple(t.shape)}")
+    if t.shape[0] >= 1 << 31 or t.shape[1] >= 1 << 31:
+        raise ValueError(f"{name}: at most 2^31 - 1 rows and columns, not {tuple(t.shape)}")
+    return _rows(name, t)
+
+
+def _offsets(offsets):
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets: a tensor [E + 1]")
+    _dense("offsets", offsets, torch.int32, (offsets.numel(),))
+    return offsets.numel() - 1
+
+
+def grouped_new_workspace(E, K, N, device="cuda") -> torch.Tensor:
+    """Workspace of grouped_product and grouped_weight_grad with E experts of K x N (either way
+    round), for any number of rows."""
+    return _zeroed(moe_grouped_workspace_bytes(E, K, N), "moe_grouped_workspace_bytes", device)
+
+
+def grouped_product(x, offsets, w, workspace, transposed=False, dtype=None, out=None, stream=None):
+    """y [R, N] (fp32, bf16 or fp16; default: x's type): the rows x [R, K] (bf16 or fp16) of each
+    expert (offsets [E+1] int32) times its matrix of w [E, K, N], or w [E, N, K] if transposed,
+    of x's type.  out: written instead of a new tensor.  Not part of autograd: the gradients are
+    this call with the other `transposed`, and grouped_weight_grad."""
+    if stream is not None:
+        with _on_stream(stream):
+            return grouped_product(x, offsets, w, workspace, transposed, dtype, out)
+    E = _offsets(offsets)
+    x_ld = _rows16("x", x, None, (None, None))
+    R, K = x.shape
+    if w.dim() != 3:
+        raise ValueError(f"w: [E, K, N] or [E, N, K], not {tuple(w.shape)}")
+    N = w.shape[1] if transposed else w.shape[2]
+    w_ld, w_es = _stack("w", w, x.dtype, (E, N, K) if transposed else (E, K, N))
+    _buffer("workspace", workspace)
+    if out is None:
+        _on_device(x, offsets, w, workspace)
+        dtype = x.dtype if dtype is None else dtype
+        if dtype not in _DTYPES:
+            raise TypeError(f"y: float32, bfloat16 or float16, not {dtype}")
+        if moe_grouped_workspace_bytes(E, K, N) == 0:
+            raise MoEError("moe_grouped_product", 2)
+        out, y_ld = torch.empty((R, N), dtype=dtype, device=x.device), N
+    else:
+        _on_device(x, offsets, w, workspace, out)
+        if dtype not in (None, out.dtype):
+            raise TypeError(f"out: {dtype}, not {out.dtype}")
+        _dtype("out", out)
+        y_ld = _rows("out", out, N)
+        if out.shape[0] != R:
+            raise ValueError(f"out: {R} rows, not {out.shape[0]}")
+    moe_grouped_product(x, x_ld, _DTYPES[x.dtype], offsets, w, w_ld, w_es, transposed, R, K, N, E,
+                        out, y_ld, _DTYPES[out.dtype], workspace)
+    return out
+
+
+def grouped_weight_grad(x, dy, offsets, workspace, dtype=torch.float32, out=None, accumulate=False,
+                        stream=None):
+    """d_w [E, K, N] (fp32, bf16 or fp16): the sums over each expert's rows of x [R, K]^T dy [R, N]
+    (both bf16 or both fp16); zeros for an expert without rows.  out: written instead of a new
+    tensor, or, with accumulate (fp32 only), added to."""
+    if stream is not None:
+        with _on_stream(stream):
+            return grouped_weight_grad(x, dy, offsets, workspace, dtype, out, accumulate)
+    E = _offsets(offsets)
+    x_ld = _rows16("x", x, None, (None, None))
+    R, K = x.shape
+    dy_ld = _rows16("dy", dy, x.dtype, (R, None))
+    N = dy.shape[1]
+    _buffer("workspace", workspace)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate: needs out")
+        _on_device(x, dy, offsets, workspace)
+        if dtype not in _DTYPES:
+            raise TypeError(f"d_w: float32, bfloat16 or float16, not {dtype}")
+        if moe_grouped_workspace_bytes(E, K, N) == 0:
+            raise MoEError("moe_grouped_weight_grad", 2)
+        out, w_ld, w_es = torch.empty((E, K, N), dtype=dtype, device=x.device), N, K * N
+    else:
+        _on_device(x, dy, offsets, workspace, out)
+        _dtype("out", out)
+        w_ld, w_es = _stack("out", out, None, (E, K, N))
+    moe_grouped_weight_grad(x, x_ld, dy, dy_ld, _DTYPES[x.dtype], offsets, R, K, N, E, out, w_ld,
+                            w_es, _DTYPES[out.dtype], accumulate, workspace)
+    return out
+
+
+def _gate_up_args(gate_up, row_weights):
+    ld = _rows16("gate_up", gate_up, None, (None, None))
+    R, n = gate_up.shape
+    if n % 2:
+        raise ValueError(f"gate_up: [R, 2 I], not {tuple(gate_up.shape)}")
+    if row_weights is not None:
+        _dense("row_weights", row_weights, torch.float32, (R,))
+    return ld, R, n // 2
+
+
+def swiglu(gate_up, row_weights=None, stream=None):
+    """h [R, I] = row_weights * silu(gate) * up of gate_up [R, 2 I] (bf16 or fp16, gate first), one
+    rounding."""
+    if stream is not None:
+        with _on_stream(stream):
+            return swiglu(gate_up, row_weights)
+    ld, R, I = _gate_up_args(gate_up, row_weights)
+    _on_device(gate_up, row_weights)
+    h = torch.empty((R, I), dtype=gate_up.dtype, device=gate_up.device)
+    moe_swiglu(gate_up, ld, row_weights, _DTYPES[gate_up.dtype], R, I, h, I)
+    return h
+
+
+def swiglu_backward(gate_up, d_h, row_weights=None, stream=None):
+    """(d_gate_up [R, 2 I], h [R, I][, d_row_weights [R] fp32 if row_weights]) for d_h [R, I], the
+    gradient of swiglu's result h, which is computed again."""
+    if stream is not None:
+        with _on_stream(stream):
+            return swiglu_backward(gate_up, d_h, row_weights)
+    ld, R, I = _gate_up_args(gate_up, row_weights)
+    d_ld = _rows16("d_h", d_h, gate_up.dtype, (R, I))
+    _on_device(gate_up, d_h, row_weights)
+    d_gate_up = torch.empty((R, 2 * I), dtype=gate_up.dtype, device=gate_up.device)
+    h = torch.empty((R, I), dtype=gate_up.dtype, device=gate_up.device)
+    d_w = None if row_weights is None else torch.empty(R, dtype=torch.float32, device=gate_up.device)
+    moe_swiglu_bwd(gate_up, ld, d_h, d_ld, row_weights, _DTYPES[gate_up.dtype], R, I, d_gate_up,
+                   2 * I, h, I, d_w)
+    return (d_gate_up, h) if d_w is None else (d_gate_up, h, d_w)
+
+
+def expert_ffn_backward_new_workspace(R, H, I, E, device="cuda") -> torch.Tensor:
+    """Workspace of expert_ffn_backward for up to R rows."""
+    return _zeroed(moe_expert_ffn_bwd_workspace_bytes(R, H, I, E),
+                   "moe_expert_ffn_bwd_workspace_bytes", device)
+
+
+def expert_ffn_backward(x_perm, offsets, w_gate_up, w_down, d_y, workspace, row_weights=None,
+                        gate_up=None, d_x_dtype=None, d_w_dtype=torch.float32, d_w_gate_up=None,
+                        d_w_down=None, accumulate=False, stream=None):
+    """(d_x_perm [R, H], d_w_gate_up [E, H, 2 I], d_w_down [E, I, H][, d_row_weights [R] fp32 if
+    row_weights]): the experts' backward pass for d_y [R, H], the gradient of the layer's output
+    for each row's token (moe_permute's rows of it).  x_perm [R, H], w_gate_up [E, H, 2 I] (gate
+    columns first), w_down [E, I, H], all dense and bf16 or all fp16; gate_up [R, 2 I] as
+    grouped_product gave it, or None: computed again.  d_w_gate_up and d_w_down: written instead
+    of new tensors, or, with accumulate (fp32 only), added to."""
+    if stream is not None:
+        with _on_stream(stream):
+            return expert_ffn_backward(x_perm, offsets, w_gate_up, w_down, d_y, workspace,
+                                       row_weights, gate_up, d_x_dtype, d_w_dtype, d_w_gate_up,
+                                       d_w_down, accumulate)
+    E = _offsets(offsets)
+    _rows16("x_perm", x_perm, None, (None, None))
+    dt, (R, H) = x_perm.dtype, x_perm.shape
+    if w_gate_up.dim() != 3 or w_gate_up.shape[2] % 2:
+        raise ValueError(f"w_gate_up: [E, H, 2 I], not {tuple(w_gate_up.shape)}")
+    I = w_gate_up.shape[2] // 2
+    for name, t, shape in (("x_perm", x_perm, (R, H)), ("d_y", d_y, (R, H)),
+                           ("w_gate_up", w_gate_up, (E, H, 2 * I)), ("w_down", w_down, (E, I, H)),
+                           ("gate_up", gate_up, (R, 2 * I))):
+        if t is not None or name != "gate_up":
+            _dense(name, _buffer(name, t), dt, shape)
+    if row_weights is not None:
+        _dense("row_weights", row_weights, torch.float32, (R,))
+    _buffer("workspace", workspace)
+    d_x_dtype = dt if d_x_dtype is None else d_x_dtype
+    if d_x_dtype not in _DTYPES or d_w_dtype not in _DTYPES:
+        raise TypeError("gradients: float32, bfloat16 or float16")
+    given = [t for t in (d_w_gate_up, d_w_down) if t is not None]
+    if accumulate and len(given) < 2:
+        raise ValueError("accumulate: needs d_w_gate_up and d_w_down")
+    for name, t, shape in (("d_w_gate_up", d_w_gate_up, (E, H, 2 * I)),
+                           ("d_w_down", d_w_down, (E, I, H))):
+        if t is not None:
+            _dense(name, t, d_w_dtype, shape)
+    _on_device(x_perm, offsets, w_gate_up, w_down, d_y, workspace, row_weights, gate_up, *given)
+    if moe_expert_ffn_bwd_workspace_bytes(R, H, I, E) == 0:
+        raise MoEError("moe_expert_ffn_bwd", 2)
+    dev = x_perm.device
+    d_x = torch.empty((R, H), dtype=d_x_dtype, device=dev)
+    if d_w_gate_up is None:
+        d_w_gate_up = torch.empty((E, H, 2 * I), dtype=d_w_dtype, device=dev)
+    if d_w_down is None:
+        d_w_down = torch.empty((E, I, H), dtype=d_w_dtype, device=dev)
+    d_w = None if row_weights is None else torch.empty(R, dtype=torch.float32, device=dev)
+    moe_expert_ffn_bwd(x_perm, offsets, w_gate_up, w_down, gate_up, row_weights, d_y, _DTYPES[dt], R,
+                       H, I, E, d_x, _DTYPES[d_x_dtype], d_w_gate_up, d_w_down, _DTYPES[d_w_dtype],
+                       accumulate, d_w, workspace)
+    out = (d_x, d_w_gate_up, d_w_down)
+    return out if d_w is None else out + (d_w,)
+
+
+def orthogonalize_new_workspace(E, rows, cols, device="cuda") -> torch.Tensor:
+    """Workspace of orthogonalize for a stack of E matrices (either way round)."""
+    return _zeroed(moe_orthogonalize_workspace_bytes(E, rows, cols),
+                   "moe_orthogonalize_workspace_bytes", device)
+
+
+def orthogonalize(m, workspace, coefficients=(3.4445, -4.7750, 2.0315), steps=5, eps=1e-7,
+                  scale=1.0, dtype=torch.bfloat16, out=None, stream=None):
+    """[E, rows, cols] (bf16 or fp16): scale times the matrices m [E, rows, cols] (fp32, bf16 or
+    fp16) orthogonalised by `steps` Newton-Schulz steps X <- a X + (b X X^T + c (X X^T)^2) X from
+    X = m / (|m| + eps).  out: written instead of a new tensor (m itself, too)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return orthogonalize(m, workspace, coefficients, steps, eps, scale, dtype, out)
+    if not isinstance(m, torch.Tensor) or m.dim() != 3:
+        raise ValueError("m: a tensor [E, rows, cols]")
+    code = _dtype("m", m)
+    E, rows, cols = m.shape
+    if moe_orthogonalize_workspace_bytes(E, rows, cols) == 0:
+        raise MoEError("moe_orthogonalize", 2)
+    ld, es = _stack("m", m, m.dtype, m.shape)
+    coefficients = tuple(float(v) for v in coefficients)
+    if len(coefficients) != 3:
+        raise ValueError(f"coefficients: three, not {len(coefficients)}")
+    _buffer("workspace", workspace)
+    if out is None:
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"out: bfloat16 or float16, not {dtype}")
+        _on_device(m, workspace)
+        out, o_ld, o_es = torch.empty((E, rows, cols), dtype=dtype, device=m.device), cols, rows * cols
+    else:
+        if out.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"out: bfloat16 or float16, not {out.dtype}")
+        _on_device(m, workspace, out)
+        o_ld, o_es = _stack("out", out, None, m.shape)
+    moe_orthogonalize(m, code, ld, es, E, rows, cols, coefficients, steps, eps, scale, out,
+                      _DTYPES[out.dtype], o_ld, o_es, workspace)
+    return out
 
 
 def layer_forward_host_batches(x_host_batches, w_router, bias, packed, d, out_host_batches,

@@ -1,0 +1,87 @@
+// Launchers of the operators that train the experts (train_gemm.cu, train_rows.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe.h"
+
+namespace moe {
+
+constexpr int kMapBytes = 128;  // a tensor map in global memory
+
+// A map of 16-bit elements [d2][d1][d0], rows ld and slices es elements apart, boxes of
+// 64 x box1 x 1 with 128-byte swizzle, zeros outside (moe_api.cu).
+bool encode_16bit_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2,
+                     uint64_t ld, uint64_t es, uint32_t box1);
+
+// Makes a map that another kernel wrote to global memory visible to this thread's TMA copies.
+__device__ __forceinline__ void acquire_map(const void* map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
+}
+
+// y [R, N] of y_type = the rows of x [R, K] times their expert's matrix, [K, N] or (turned) [N, K].
+struct TrainProduct {
+  const void* x;
+  const int32_t* offsets;
+  const void* w;
+  void* y;
+  int E, R, K, N, type, y_type;
+  bool turned;
+  long long x_ld, w_ld, w_es, y_ld;
+  int32_t* status;
+  long long limit;
+};
+bool product_pair_form(int E, int R);
+cudaError_t launch_product(const TrainProduct& q, cudaStream_t s);
+
+// out [E, K, N] = (or, FP32, +=) the sums over each expert's rows of x [R, K]^T dy [R, N]; R > 0.
+// maps: 2 * E * kMapBytes bytes of scratch, 128-byte aligned.
+struct TrainWgrad {
+  const void *x, *dy;
+  const int32_t* offsets;
+  void* out;
+  int E, R, K, N, type, out_type;
+  bool accumulate;
+  long long x_ld, dy_ld, ld, es;
+  uint8_t* maps;
+  int32_t* status;
+  long long limit;
+};
+cudaError_t launch_wgrad(const TrainWgrad& q, cudaStream_t s);
+
+// out_e = alpha A_e B_e + beta C_e, FP16 operands with padded rows: A [M, K]; B [K, N], or (sym)
+// A B^T with B [N, K], the result symmetric.  padded: out is such a buffer too, else it may be
+// stored transposed (turned).
+struct TrainBatch {
+  const void *a, *b, *c;
+  void* out;
+  int E, M, N, K, out_type;
+  bool sym, padded, turned;
+  long long a_ld, a_es, b_ld, b_es, c_ld, c_es, ld, es;
+  float alpha, beta;
+  const float *alpha_e, *beta_e;
+  int32_t* status;
+  long long limit;
+};
+cudaError_t launch_batch(const TrainBatch& q, cudaStream_t s);
+
+// h [R, I] = w silu(gate) up of gate_up [R, 2 I] (w: [R] FP32 or null)
+cudaError_t launch_swiglu(const void* gate_up, long long gu_ld, const float* w, int type, int R,
+                          int I, void* h, long long h_ld, cudaStream_t s);
+// its gradient for d [R, I]; h (w silu(gate) up) and d_w [R] may be null
+cudaError_t launch_swiglu_bwd(const void* gate_up, long long gu_ld, const void* d, long long d_ld,
+                              const float* w, int type, int R, int I, void* d_gate_up,
+                              long long dgu_ld, void* h, long long h_ld, float* d_w,
+                              cudaStream_t s);
+
+// First step of an orthogonalisation: x [E][m][ld] FP16 (m = min, n = max of rows, cols; ld = n
+// padded to 8) = M 2^k, f[e] = 2^-k / (|M| + eps), f[E + e] = f[e]^2.
+constexpr int kNormParts = 512;  // at most, partial sums of squares an expert
+cudaError_t launch_orth_start(const void* m, int type, long long ld_m, long long es_m, int E,
+                              int rows, int cols, float eps, float* parts, void* x, float* f,
+                              cudaStream_t s);
+
+}  // namespace moe

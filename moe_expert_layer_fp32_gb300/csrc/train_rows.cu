@@ -1,0 +1,270 @@
+// Row-wise operators that train the experts: SwiGLU and its gradient, and the first step of an
+// orthogonalisation (norm, scaling and, for tall matrices, transposition).
+#include "common.cuh"
+#include "kernels.cuh"
+#include "pdl.cuh"
+#include "train.cuh"
+
+namespace moe {
+namespace {
+
+template <int TYPE>
+__device__ __forceinline__ float2 two(uint32_t v) {
+  if constexpr (TYPE == MOE_DTYPE_BF16) return make_float2(bf16_lo(v), bf16_hi(v));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+template <int TYPE>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  if constexpr (TYPE == MOE_DTYPE_BF16) {
+    return pack_bf16x2(lo, hi);
+  } else {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// s = sigmoid(g), act = g s, h = act u:
+//   d_gate = w d u s (1 + g (1 - s)), d_up = w d act, d_w = sum d h, and w h once more for the
+//   down projection's gradient.  One rounding each; the row's sum in FP32.
+template <int TYPE>
+__device__ __forceinline__ void swiglu_bwd_pair(uint32_t g, uint32_t u, uint32_t d, float w,
+                                                uint32_t& dg, uint32_t& du, uint32_t& h,
+                                                float& dw) {
+  const float2 gf = two<TYPE>(g), uf = two<TYPE>(u), df = two<TYPE>(d);
+  float2 rg, ru, rh;
+  auto one = [&](float a, float b, float c, float& x, float& y, float& z) {
+    const float s = __fdividef(1.0f, 1.0f + __expf(-a));
+    const float act = a * s, hh = act * b, wd = w * c;
+    x = wd * b * s * fmaf(a, 1.0f - s, 1.0f);
+    y = wd * act;
+    z = w * hh;
+    dw = fmaf(c, hh, dw);
+  };
+  one(gf.x, uf.x, df.x, rg.x, ru.x, rh.x);
+  one(gf.y, uf.y, df.y, rg.y, ru.y, rh.y);
+  dg = pack<TYPE>(rg.x, rg.y);
+  du = pack<TYPE>(ru.x, ru.y);
+  h = pack<TYPE>(rh.x, rh.y);
+}
+
+// A warp a row, 16-byte pieces; PIECES of a lane's are loaded before the first is used.
+constexpr int PIECES = 3, ROW_WARPS = 8;
+
+template <int TYPE, bool BWD>
+__global__ void __launch_bounds__(32 * ROW_WARPS)
+    swiglu_kernel(const uint8_t* __restrict__ gu, long long gu_ld, const uint8_t* __restrict__ d,
+                  long long d_ld, const float* __restrict__ w, int R, int I, uint8_t* dgu,
+                  long long dgu_ld, uint8_t* h, long long h_ld, float* d_w) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  for (long long r = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5); r < R;
+       r += (long long)gridDim.x * ROW_WARPS) {
+    const uint4* pg = reinterpret_cast<const uint4*>(gu + 2 * r * gu_ld);
+    const uint4* pu = reinterpret_cast<const uint4*>(gu + 2 * (r * gu_ld + I));
+    const uint4* pd = BWD ? reinterpret_cast<const uint4*>(d + 2 * r * d_ld) : nullptr;
+    uint4* og = BWD ? reinterpret_cast<uint4*>(dgu + 2 * r * dgu_ld) : nullptr;
+    uint4* ou = BWD ? reinterpret_cast<uint4*>(dgu + 2 * (r * dgu_ld + I)) : nullptr;
+    uint4* oh = h ? reinterpret_cast<uint4*>(h + 2 * r * h_ld) : nullptr;
+    const float wr = w ? __ldg(w + r) : 1.0f;
+    float dw = 0.0f;
+    const int n = I / 8;
+    for (int c0 = lane; c0 < n; c0 += 32 * PIECES) {
+      uint4 vg[PIECES], vu[PIECES], vd[PIECES];
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int c = c0 + 32 * i;
+        if (c < n) {
+          vg[i] = __ldcs(pg + c);
+          vu[i] = __ldcs(pu + c);
+          if constexpr (BWD) vd[i] = __ldcs(pd + c);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int c = c0 + 32 * i;
+        if (c < n) {
+          const uint32_t* a = reinterpret_cast<const uint32_t*>(&vg[i]);
+          const uint32_t* b = reinterpret_cast<const uint32_t*>(&vu[i]);
+          uint4 rg, ru, rh;
+          uint32_t *xg = reinterpret_cast<uint32_t*>(&rg), *xu = reinterpret_cast<uint32_t*>(&ru),
+                   *xh = reinterpret_cast<uint32_t*>(&rh);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (BWD) {
+              const uint32_t* e = reinterpret_cast<const uint32_t*>(&vd[i]);
+              swiglu_bwd_pair<TYPE>(a[j], b[j], e[j], wr, xg[j], xu[j], xh[j], dw);
+            } else {
+              const float2 gf = two<TYPE>(a[j]), uf = two<TYPE>(b[j]);
+              xh[j] = pack<TYPE>(wr * (silu_f32(gf.x) * uf.x), wr * (silu_f32(gf.y) * uf.y));
+            }
+          }
+          if constexpr (BWD) {
+            __stcs(og + c, rg);
+            __stcs(ou + c, ru);
+          }
+          if (oh) __stcs(oh + c, rh);
+        }
+      }
+    }
+    if (BWD && d_w) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dw += __shfl_xor_sync(0xFFFFFFFFu, dw, o);
+      if (lane == 0) d_w[r] = dw;
+    }
+  }
+}
+
+template <bool BWD>
+cudaError_t launch_rows(const void* gu, long long gu_ld, const void* d, long long d_ld,
+                        const float* w, int type, int R, int I, void* dgu, long long dgu_ld,
+                        void* h, long long h_ld, float* d_w, cudaStream_t s) {
+  if (R == 0) return cudaSuccess;
+  const long long need = ((long long)R + ROW_WARPS - 1) / ROW_WARPS;
+  const long long most = 8LL * device_sm_count();
+  const dim3 grid((unsigned)(need < most ? need : most));
+  auto kern = type == MOE_DTYPE_BF16 ? swiglu_kernel<MOE_DTYPE_BF16, BWD>
+                                     : swiglu_kernel<MOE_DTYPE_F16, BWD>;
+  return launch_pdl(kern, grid, dim3(32 * ROW_WARPS), 0, s, static_cast<const uint8_t*>(gu), gu_ld,
+                    static_cast<const uint8_t*>(d), d_ld, w, R, I, static_cast<uint8_t*>(dgu),
+                    dgu_ld, static_cast<uint8_t*>(h), h_ld, d_w);
+}
+
+// ------------------------------------------------ start of an orthogonalisation ---
+__device__ __forceinline__ float element(const void* p, long long i, int type) {
+  if (type == MOE_DTYPE_F32) return __ldg(static_cast<const float*>(p) + i);
+  if (type == MOE_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+
+struct Squares {  // of v, and of v scaled by 2^-64 and 2^64 for where those leave FP32's range
+  float mid, big, small;
+  __device__ void add(float v) {
+    mid = fmaf(v, v, mid);
+    const float b = v * 0x1p-64f, t = v * 0x1p64f;
+    big = fmaf(b, b, big);
+    small = fmaf(t, t, small);
+  }
+};
+
+__device__ __forceinline__ float block_sum(float v, float* sh) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float t = 0.0f;
+  for (int i = 0; i < (int)blockDim.x / 32; ++i) t += sh[i];
+  return t;
+}
+
+// parts [E][3][nb]: the sums of squares of nb groups of rows.
+__global__ void __launch_bounds__(256)
+    squares_kernel(const void* __restrict__ m, int type, long long ld, long long es, int rows,
+                   int cols, int per, float* __restrict__ parts) {
+  __shared__ float sh[8];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int e = blockIdx.y, nb = gridDim.x;
+  const int r0 = blockIdx.x * per, r1 = min(rows, r0 + per);
+  Squares q = {0.0f, 0.0f, 0.0f};
+  for (int r = r0; r < r1; ++r)
+    for (int c = threadIdx.x; c < cols; c += blockDim.x) q.add(element(m, e * es + r * ld + c, type));
+  const float a = block_sum(q.mid, sh), b = block_sum(q.big, sh), c = block_sum(q.small, sh);
+  if (threadIdx.x == 0) {
+    float* o = parts + ((long long)e * 3) * nb + blockIdx.x;
+    o[0] = a;
+    o[nb] = b;
+    o[2 * nb] = c;
+  }
+}
+
+// A 64 x 64 tile of x [E][M][ldx] (M x N, ldx = N padded to 8, the padding zero) = M 2^k in FP16.
+// 2^k brings the norm to [512, 1024): the elements of a BF16 matrix stay exact, and neither a
+// product of rows nor (with eps) 1 / norm comes near FP32's ends.
+__global__ void __launch_bounds__(256)
+    scale_kernel(const void* __restrict__ m, int type, long long ld, long long es, int M, int N,
+                 int turned, int ldx, float eps, const float* __restrict__ parts, int nb,
+                 __half* __restrict__ x, float* __restrict__ f, int E) {
+  __shared__ float sh[8];
+  __shared__ float tile[64][65];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int e = blockIdx.z;
+  float s[3];
+  for (int j = 0; j < 3; ++j) {
+    float v = 0.0f;
+    for (int i = threadIdx.x; i < nb; i += blockDim.x) v += parts[((long long)e * 3 + j) * nb + i];
+    s[j] = block_sum(v, sh);
+  }
+  float norm;
+  if (!(s[0] <= 0x1p120f)) norm = sqrtf(s[1]) * 0x1p64f;       // (NaN too)
+  else if (s[0] < 0x1p-80f) norm = sqrtf(s[2]) * 0x1p-64f;
+  else norm = sqrtf(s[0]);
+  int k = 0;
+  const bool finite = norm <= 0x1.fffffep127f;
+  if (finite && norm > 0.0f) {
+    int ex;
+    frexpf(norm, &ex);  // norm = r 2^ex, r in [0.5, 1)
+    k = 10 - ex;
+  }
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    const float total = norm + eps;
+    float v = !finite ? __int_as_float(0x7FC00000) : total > 0.0f ? ldexpf(1.0f / total, -k) : 0.0f;
+    f[e] = v;
+    f[E + e] = v * v;
+  }
+  const float s1 = ldexpf(1.0f, k / 2), s2 = ldexpf(1.0f, k - k / 2);
+  const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;  // of x
+  // read along the source's rows
+  const int lane = threadIdx.x & 63, row = threadIdx.x >> 6;
+#pragma unroll 4
+  for (int t = row; t < 64; t += 4) {
+    const int i = turned ? i0 + lane : i0 + t, j = turned ? j0 + t : j0 + lane;
+    float v = 0.0f;
+    if (i < M && j < N) v = element(m, e * es + (turned ? j * ld + i : i * ld + j), type) * s1 * s2;
+    if (turned) tile[lane][t] = v;
+    else tile[t][lane] = v;
+  }
+  __syncthreads();
+  __half* o = x + (long long)e * M * ldx;
+#pragma unroll 4
+  for (int t = row; t < 64; t += 4) {
+    const int i = i0 + t, j = j0 + lane;
+    if (i < M && j < ldx) o[(long long)i * ldx + j] = __float2half_rn(tile[t][lane]);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu(const void* gate_up, long long gu_ld, const float* w, int type, int R,
+                          int I, void* h, long long h_ld, cudaStream_t s) {
+  return launch_rows<false>(gate_up, gu_ld, nullptr, 0, w, type, R, I, nullptr, 0, h, h_ld, nullptr,
+                            s);
+}
+
+cudaError_t launch_swiglu_bwd(const void* gate_up, long long gu_ld, const void* d, long long d_ld,
+                              const float* w, int type, int R, int I, void* d_gate_up,
+                              long long dgu_ld, void* h, long long h_ld, float* d_w,
+                              cudaStream_t s) {
+  return launch_rows<true>(gate_up, gu_ld, d, d_ld, w, type, R, I, d_gate_up, dgu_ld, h, h_ld, d_w,
+                           s);
+}
+
+cudaError_t launch_orth_start(const void* m, int type, long long ld_m, long long es_m, int E,
+                              int rows, int cols, float eps, float* parts, void* x, float* f,
+                              cudaStream_t s) {
+  int per = (16384 + cols - 1) / cols;  // rows a block
+  if ((rows + per - 1) / per > kNormParts) per = (rows + kNormParts - 1) / kNormParts;
+  const int nb = (rows + per - 1) / per;
+  cudaError_t err = launch_pdl(squares_kernel, dim3(nb, E), dim3(256), 0, s, m, type, ld_m, es_m,
+                               rows, cols, per, parts);
+  if (err != cudaSuccess) return err;
+  const bool turned = rows > cols;
+  const int M = turned ? cols : rows, N = turned ? rows : cols, ldx = (N + 7) / 8 * 8;
+  return launch_pdl(scale_kernel, dim3((ldx + 63) / 64, (M + 63) / 64, E), dim3(256), 0, s, m, type,
+                    ld_m, es_m, M, N, turned ? 1 : 0, ldx, eps, parts, nb, static_cast<__half*>(x),
+                    f, E);
+}
+
+}  // namespace moe
