@@ -180,18 +180,30 @@ bool GemmOperand::encode(CUtensorMap* m, uint32_t box_rows) const {
   return r == CUDA_SUCCESS;
 }
 
-bool encode_16bit_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2,
-                     uint64_t ld, uint64_t es, uint32_t box1) {
+static bool encode_3d(CUtensorMap* m, const void* ptr, bool fp32, uint64_t d0, uint64_t d1, uint64_t d2,
+                      uint64_t ld, uint64_t es, uint32_t box1) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
+  const uint64_t b = fp32 ? 4 : 2;
   cuuint64_t dims[3] = {d0, d1, d2};
-  cuuint64_t strides[2] = {ld * 2, (d2 > 1 ? es : d1 * ld) * 2};
-  cuuint32_t box[3] = {64, box1, 1};
+  cuuint64_t strides[2] = {ld * b, (d2 > 1 ? es : d1 * ld) * b};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / b), box1, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool encode_16bit_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2,
+                     uint64_t ld, uint64_t es, uint32_t box1) {
+  return encode_3d(m, ptr, false, d0, d1, d2, ld, es, box1);
+}
+
+bool encode_out_3d(CUtensorMap* m, const void* ptr, bool fp32, uint64_t d0, uint64_t d1, uint64_t d2,
+                   uint64_t ld, uint64_t es) {
+  return encode_3d(m, ptr, fp32, d0, d1, d2, ld, es, 32);
 }
 
 bool encode_rowmajor_2d(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, bool fp32,

@@ -10,17 +10,14 @@
 
 namespace moe {
 
-constexpr int kMapBytes = 128;  // a tensor map in global memory
-
 // A map of 16-bit elements [d2][d1][d0], rows ld and slices es elements apart, boxes of
 // 64 x box1 x 1 with 128-byte swizzle, zeros outside (moe_api.cu).
 bool encode_16bit_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2,
                      uint64_t ld, uint64_t es, uint32_t box1);
 
-// Makes a map that another kernel wrote to global memory visible to this thread's TMA copies.
-__device__ __forceinline__ void acquire_map(const void* map) {
-  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
-}
+// The same for an output of FP32 or 16-bit elements, boxes of 128 bytes x 32 rows.
+bool encode_out_3d(CUtensorMap* m, const void* ptr, bool fp32, uint64_t d0, uint64_t d1, uint64_t d2,
+                   uint64_t ld, uint64_t es);
 
 // y [R, N] of y_type = the rows of x [R, K] times their expert's matrix, [K, N] or (turned) [N, K].
 struct TrainProduct {
@@ -38,7 +35,7 @@ bool product_pair_form(int E, int R);
 cudaError_t launch_product(const TrainProduct& q, cudaStream_t s);
 
 // out [E, K, N] = (or, FP32, +=) the sums over each expert's rows of x [R, K]^T dy [R, N]; R > 0.
-// maps: 2 * E * kMapBytes bytes of scratch, 128-byte aligned.
+// tail_x, tail_dy: wgrad_tail_bytes(E, K) and (E, N) bytes of scratch.
 struct TrainWgrad {
   const void *x, *dy;
   const int32_t* offsets;
@@ -46,20 +43,28 @@ struct TrainWgrad {
   int E, R, K, N, type, out_type;
   bool accumulate;
   long long x_ld, dy_ld, ld, es;
-  uint8_t* maps;
+  void *tail_x, *tail_dy;
   int32_t* status;
   long long limit;
 };
+size_t wgrad_tail_bytes(int E, int cols);
 cudaError_t launch_wgrad(const TrainWgrad& q, cudaStream_t s);
 
-// out_e = alpha A_e B_e + beta C_e, FP16 operands with padded rows: A [M, K]; B [K, N], or (sym)
-// A B^T with B [N, K], the result symmetric.  padded: out is such a buffer too, else it may be
-// stored transposed (turned).
+// out_e = alpha A_e B_e + beta C_e (C null: without), out [M, N] over K, FP16 operands with padded
+// rows.  Symmetric matrices (marked ~) hold the tiles on and above the diagonal: 256 wide if pair, else
+// 128, the same choice in every call on them.
+//   GRAM_ROWS  ~out = A A^T         A [M, K], b = a
+//   GRAM_COLS  ~out = A^T A         A [K, M], b = a
+//   SQUARE     ~out = A A           ~A [M, M], b = a
+//   LEFT       out = A B            ~A [M, M], B [M, N]
+//   RIGHT      out = A B            A [M, N], ~B [N, N]
+// padded: out is a padded buffer too; else (LEFT, RIGHT) rows of any length.
 struct TrainBatch {
+  enum Form { GRAM_ROWS, GRAM_COLS, SQUARE, LEFT, RIGHT } form;
   const void *a, *b, *c;
   void* out;
   int E, M, N, K, out_type;
-  bool sym, padded, turned;
+  bool pair, padded;
   long long a_ld, a_es, b_ld, b_es, c_ld, c_es, ld, es;
   float alpha, beta;
   const float *alpha_e, *beta_e;
@@ -77,8 +82,7 @@ cudaError_t launch_swiglu_bwd(const void* gate_up, long long gu_ld, const void* 
                               long long dgu_ld, void* h, long long h_ld, float* d_w,
                               cudaStream_t s);
 
-// First step of an orthogonalisation: x [E][m][ld] FP16 (m = min, n = max of rows, cols; ld = n
-// padded to 8) = M 2^k, f[e] = 2^-k / (|M| + eps), f[E + e] = f[e]^2.
+// First step of an orthogonalisation: x [E][rows][ld] FP16 (ld = cols padded to 8) = M 2^k, f[e] = 2^-k / (|M| + eps), f[E + e] = f[e]^2.
 constexpr int kNormParts = 512;  // at most, partial sums of squares an expert
 cudaError_t launch_orth_start(const void* m, int type, long long ld_m, long long es_m, int E,
                               int rows, int cols, float eps, float* parts, void* x, float* f,

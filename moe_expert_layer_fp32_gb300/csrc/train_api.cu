@@ -68,15 +68,16 @@ moe_status check_stack(const void* ptr, int E, long long rows, long long cols, l
   return es >= (1LL << 38) ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-// status word, then the weight gradient's tensor maps
+// status word, then the weight gradient's tails of x and dy
 struct GroupedLayout {
-  size_t status, maps, total;
+  size_t status, tail_x, tail_dy, total;
 };
-GroupedLayout grouped_layout(int E) {
+GroupedLayout grouped_layout(int E, int K, int N) {
   GroupedLayout L;
   L.status = 0;
-  L.maps = up(kAlign);
-  L.total = L.maps + up(2 * (size_t)E * kMapBytes);
+  L.tail_x = up(kAlign);
+  L.tail_dy = L.tail_x + up(wgrad_tail_bytes(E, K));
+  L.total = L.tail_dy + up(wgrad_tail_bytes(E, N));
   return L;
 }
 
@@ -139,7 +140,9 @@ moe_status do_wgrad(const void* x, long long x_ld, const void* dy, long long dy_
   q.dy_ld = dy_ld;
   q.ld = ld;
   q.es = es;
-  q.maps = at<uint8_t>(ws, grouped_layout(E).maps);
+  const GroupedLayout L = grouped_layout(E, K, N);
+  q.tail_x = at<void>(ws, L.tail_x);
+  q.tail_dy = at<void>(ws, L.tail_dy);
   q.status = static_cast<int32_t*>(ws);
   q.limit = wait_limit();
   MOE_CUDA(launch_wgrad(q, s));
@@ -151,8 +154,8 @@ struct OrthLayout {
   size_t status, parts, f, x0, x1, a, b, total;
 };
 OrthLayout orth_layout(int E, int rows, int cols) {
-  const size_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
-  const size_t x = up(E * m * ((n + 7) / 8 * 8) * 2), a = up(E * m * ((m + 7) / 8 * 8) * 2);
+  const size_t m = rows < cols ? rows : cols;
+  const size_t x = up((size_t)E * rows * ((cols + 7) / 8 * 8) * 2), a = up(E * m * ((m + 7) / 8 * 8) * 2);
   OrthLayout L;
   size_t o = 0;
   L.status = o;  o += up(kAlign);
@@ -176,11 +179,11 @@ bool orth_sizes(int E, int rows, int cols) {
 struct BwdLayout {
   size_t grouped, gate_up, d_gate_up, d_h, h, total;
 };
-BwdLayout bwd_layout(int R, int I, int E) {
+BwdLayout bwd_layout(int R, int H, int I, int E) {
   const size_t n = up((size_t)R * I * 2);
   BwdLayout L;
   size_t o = 0;
-  L.grouped = o;    o += grouped_layout(E).total;
+  L.grouped = o;    o += grouped_layout(E, H, 2 * I).total;
   L.gate_up = o;    o += 2 * n;
   L.d_gate_up = o;  o += 2 * n;
   L.d_h = o;        o += n;
@@ -197,7 +200,7 @@ using namespace moe;
 extern "C" {
 
 size_t moe_grouped_workspace_bytes(int32_t E, int32_t K, int32_t N) {
-  return check_grouped(E, K, N) == MOE_OK ? grouped_layout(E).total : 0;
+  return check_grouped(E, K, N) == MOE_OK ? grouped_layout(E, K, N).total : 0;
 }
 
 moe_status moe_grouped_product(const void* x, int64_t x_ld, int32_t dtype, const int32_t* offsets,
@@ -212,7 +215,7 @@ moe_status moe_grouped_product(const void* x, int64_t x_ld, int32_t dtype, const
                      : check_stack(w, E, K, N, w_ld, w_es, dtype));
   MOE_TRY(check_matrix(y, R, N, y_ld, y_dtype));
   MOE_TRY(validate_ptr(offsets));
-  MOE_TRY(check_workspace(workspace, ws_bytes, grouped_layout(E).total));
+  MOE_TRY(check_workspace(workspace, ws_bytes, grouped_layout(E, K, N).total));
   MOE_TRY(validate_device());
   return do_product(x, x_ld, dtype, offsets, w, w_ld, w_es, transposed != 0, R, K, N, E, y, y_ld,
                     y_dtype, workspace, as_stream(stream));
@@ -231,7 +234,7 @@ moe_status moe_grouped_weight_grad(const void* x, int64_t x_ld, const void* dy, 
   MOE_TRY(check_matrix(dy, R, N, dy_ld, dtype));
   MOE_TRY(check_stack(d_w, E, K, N, w_ld, w_es, w_dtype));
   MOE_TRY(validate_ptr(offsets));
-  MOE_TRY(check_workspace(workspace, ws_bytes, grouped_layout(E).total));
+  MOE_TRY(check_workspace(workspace, ws_bytes, grouped_layout(E, K, N).total));
   MOE_TRY(validate_device());
   return do_wgrad(x, x_ld, dy, dy_ld, dtype, offsets, R, K, N, E, d_w, w_ld, w_es, w_dtype,
                   accumulate != 0, workspace, as_stream(stream));
@@ -269,7 +272,7 @@ moe_status moe_swiglu_bwd(const void* gate_up, int64_t gate_up_ld, const void* d
 
 size_t moe_expert_ffn_bwd_workspace_bytes(int32_t R, int32_t H, int32_t I, int32_t E) {
   if (R < 0 || I > 16384 || check_grouped(E, H, I) != MOE_OK) return 0;
-  return bwd_layout(R, I, E).total;
+  return bwd_layout(R, H, I, E).total;
 }
 
 moe_status moe_expert_ffn_bwd(const void* x_perm, const int32_t* offsets, const void* w_gate_up,
@@ -293,7 +296,7 @@ moe_status moe_expert_ffn_bwd(const void* x_perm, const int32_t* offsets, const 
                         static_cast<const void*>(d_w_gate_up), static_cast<const void*>(d_w_down),
                         static_cast<const void*>(d_row_w)})
     if (p != nullptr) MOE_TRY(validate_ptr(p));
-  const BwdLayout L = bwd_layout(R, I, E);
+  const BwdLayout L = bwd_layout(R, H, I, E);
   MOE_TRY(check_workspace(workspace, ws_bytes, L.total));
   MOE_TRY(validate_device());
   cudaStream_t s = as_stream(stream);
@@ -347,8 +350,11 @@ moe_status moe_orthogonalize(const void* m, int32_t dtype, int64_t ld, int64_t e
   MOE_TRY(check_workspace(workspace, ws_bytes, L.total));
   MOE_TRY(validate_device());
   cudaStream_t s = as_stream(stream);
-  const int M = rows < cols ? rows : cols, N = rows < cols ? cols : rows;
-  const long long lx = (N + 7) / 8 * 8, la = (M + 7) / 8 * 8;
+  // the shorter side's products: X X^T, or X^T X of a tall matrix, S x S
+  const bool tall = rows > cols;
+  const int S = tall ? cols : rows;
+  const long long lx = (cols + 7) / 8 * 8, la = (S + 7) / 8 * 8;
+  const long long xs = rows * lx, as = S * la;
   void *x = at<void>(workspace, L.x0), *x1 = at<void>(workspace, L.x1);
   void *A = at<void>(workspace, L.a), *B = at<void>(workspace, L.b);
   float* f = at<float>(workspace, L.f);
@@ -356,23 +362,23 @@ moe_status moe_orthogonalize(const void* m, int32_t dtype, int64_t ld, int64_t e
                              f, s));
   TrainBatch q = {};
   q.E = E;
-  q.M = M;
+  q.pair = S > 128;
   q.status = static_cast<int32_t*>(workspace);
   q.limit = wait_limit();
   for (int i = 0; i < steps; ++i) {
     const bool first = i == 0, last = i == steps - 1;
     const float held = first ? 1.0f : kHeld;  // x holds X times this (the first: X / f_e)
     // A = X X^T
+    q.form = tall ? TrainBatch::GRAM_COLS : TrainBatch::GRAM_ROWS;
     q.a = q.b = x;
     q.a_ld = q.b_ld = lx;
-    q.a_es = q.b_es = M * lx;
-    q.N = M;
-    q.K = N;
-    q.sym = q.padded = true;
-    q.turned = false;
+    q.a_es = q.b_es = xs;
+    q.M = q.N = S;
+    q.K = tall ? rows : cols;
+    q.padded = true;
     q.out = A;
     q.ld = la;
-    q.es = M * la;
+    q.es = as;
     q.out_type = MOE_DTYPE_F16;
     q.c = nullptr;
     q.alpha = kHeld / (held * held);
@@ -381,44 +387,36 @@ moe_status moe_orthogonalize(const void* m, int32_t dtype, int64_t ld, int64_t e
     q.beta_e = nullptr;
     MOE_CUDA(launch_batch(q, s));
     // B = b A + c A A
-    q.a = q.b = A;
-    q.a_ld = q.b_ld = la;
-    q.a_es = q.b_es = M * la;
-    q.K = M;
+    q.form = TrainBatch::SQUARE;
+    q.a = q.b = q.c = A;
+    q.a_ld = q.b_ld = q.c_ld = la;
+    q.a_es = q.b_es = q.c_es = as;
+    q.K = S;
     q.out = B;
-    q.c = A;
-    q.c_ld = la;
-    q.c_es = M * la;
     q.alpha = c / kHeld;
     q.alpha_e = nullptr;
     q.beta = b;
     MOE_CUDA(launch_batch(q, s));
-    // X = a X + B X
+    // X = a X + B X (tall: X B)
     const float next = last ? scale : kHeld;
-    q.a = B;
-    q.b = x;
-    q.b_ld = lx;
-    q.b_es = M * lx;
-    q.N = N;
-    q.sym = false;
+    q.form = tall ? TrainBatch::RIGHT : TrainBatch::LEFT;
+    (tall ? q.b : q.a) = B;
+    (tall ? q.a : q.b) = x;
+    (tall ? q.a_ld : q.b_ld) = lx;
+    (tall ? q.a_es : q.b_es) = xs;
+    q.M = rows;
+    q.N = cols;
     q.c = x;
     q.c_ld = lx;
-    q.c_es = M * lx;
+    q.c_es = xs;
     q.alpha = next / (held * kHeld);
     q.beta = a * next / held;
     q.alpha_e = q.beta_e = first ? f : nullptr;
-    if (last) {
-      q.padded = false;
-      q.turned = rows > cols;
-      q.out = out;
-      q.ld = out_ld;
-      q.es = out_es;
-      q.out_type = out_dtype;
-    } else {
-      q.out = x1;
-      q.ld = lx;
-      q.es = M * lx;
-    }
+    q.padded = !last;
+    q.out = last ? out : x1;
+    q.ld = last ? out_ld : lx;
+    q.es = last ? out_es : xs;
+    q.out_type = last ? out_dtype : MOE_DTYPE_F16;
     MOE_CUDA(launch_batch(q, s));
     void* t = x;
     x = x1;

@@ -3,25 +3,28 @@
 //   PRODUCT  y[r] = x[r] W_e (W [E, K, N]) or x[r] W_e^T (W [E, N, K]) for the rows r of expert e
 //   WGRAD    dW_e = sum over the rows r of expert e of x[r]^T dy[r]
 //   BATCH    out_e = alpha A_e B_e + beta C_e, one of each an expert (Newton-Schulz steps)
-//   SYM      the same where the result is symmetric (X X^T, its square): the tiles on and above
-//            the diagonal are computed and stored twice
+//   SYM      the same where the result is symmetric (X X^T, its square): only the tiles on and
+//            above the diagonal are computed and stored
 //
 // All read the operands in the caller's layout.  An operand whose contraction index runs along
 // its rows (x and W^T of a product) is staged K-major, the others (W, and both operands of a
 // weight gradient) MN-major: tcgen05 takes either from 128-byte-swizzled shared memory, so
-// nothing is transposed or packed beforehand.
+// nothing is transposed or packed beforehand.  A symmetric operand is read by its upper tiles: a
+// k-block left of the diagonal comes MN-major from its mirror image.
 //
-// Roles of a CTA (192 threads): warp 0 the TMA producer, warp 1 the MMA issuer, warps 2..5
-// the epilogue, over a ring of k-blocks of 64 and two accumulators in TMEM.  Forms:
+// Roles of a CTA (352 threads): warp 0 loads A (TMA), warp 10 B, warp 1 issues the MMAs, warps 2..9
+// are the epilogue (two a TMEM lane quarter, every other 128 bytes of a row), over a ring of
+// k-blocks of 64 and two accumulators in TMEM.  Forms:
 //   pair     two CTAs share one M = 256 MMA over 256 columns (cta_group::2): each SM stages
 //            32 KB a k-block for 256 x 256 x 64 products
 //   single   one CTA, 128 x 128, for few rows: of A only the 16-row boxes that hold rows of the
 //            expert are loaded, so that the ring streams weights
 //
-// A weight gradient contracts over an expert's rows, which end anywhere.  Its tensor maps are
-// made on the device (wgrad_maps_kernel), one an expert and operand, that end with the expert's
-// last row: TMA fills the rest of the last k-block with zeros, so another expert's rows (or
-// infinities and NaN among them) never enter the sum.
+// A weight gradient contracts over an expert's rows, which end anywhere.  The rows of an
+// expert's last, partial k-block are copied beforehand (tails_kernel) and filled up with zeros, so
+// another expert's rows (or infinities and NaN among them) never enter the sum.  (Tensor maps
+// that end with the expert's rows, made on the device, need a proxy fence whenever a CTA
+// changes the expert: 411 against XXX us for 64 experts of 512 rows, 2048 x 2048 FP32.)
 //
 // Bounded waits, and what happens when one runs out, as in expert_gemm.cu.
 #include "common.cuh"
@@ -33,8 +36,10 @@ namespace moe {
 namespace {
 
 enum Kind { PRODUCT, WGRAD, BATCH, SYM };
+enum Major { KM, MN, UPPER };  // UPPER: a symmetric matrix of which the upper tiles are there
 
 constexpr int GM = 128, GK = 64, UK = 16;
+constexpr int EPI_WARPS = 8, B_WARP = 2 + EPI_WARPS, THREADS = 32 * (B_WARP + 1);
 constexpr int BOX_ROWS = 16;  // A boxes of the single form of a product
 
 template <int CTAS, int BN>
@@ -46,24 +51,39 @@ struct Shape {
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int NBAR = 2 * STAGES + 2 + 2 + 1;
-  static constexpr int EPI_LD = 33;
-  static constexpr int EPI_BYTES = 4 * 32 * EPI_LD * 4;
+  static constexpr int EPI_BYTES = EPI_WARPS * 32 * 128;
   static constexpr int SMEM_BYTES =
-      1024 + STAGES * STAGE_BYTES + EPI_BYTES + NBAR * 8 + 32 + 3 * (kMaxE + 1) * 4;
+      STAGES * STAGE_BYTES + EPI_BYTES + NBAR * 8 + 48 + 2 * (kMaxE + 1) * 4;
 };
+
+// n / d for n < 2^31 by a multiplication: m = 2^32 (2^s - d) / d + 1, s = ceil(log2 d).
+struct Div {
+  uint32_t m;
+  int s, d;
+};
+Div make_div(int d) {
+  Div v = {0, 0, d};
+  while ((1LL << v.s) < d) ++v.s;
+  v.m = (uint32_t)(((1ULL << 32) * ((1ULL << v.s) - d)) / d + 1);
+  return v;
+}
+__device__ __forceinline__ int operator/(int n, const Div& v) {
+  return (int)((__umulhi((uint32_t)n, v.m) + (uint32_t)n) >> v.s);
+}
 
 struct Args {
   CUtensorMap a, b;
-  const uint8_t* maps;  // WGRAD: kMapBytes each, the experts' A maps and then their B maps
+  CUtensorMap o;       // the output, boxes of 128 bytes x 32 rows, if tma
+  CUtensorMap at, bt;  // UPPER: the same matrix in MN-major boxes; WGRAD: the experts' tails
   const int32_t* offsets;
   int E, R, M, N, K;
+  Div nt, per;  // column tiles, and tiles an expert (not PRODUCT)
   void* out;
   long long ld, es;
-  int out_type, turned, vec;  // turned: stored transposed; vec: rows in 16-byte pieces
-  int m_lim, n_lim;           // rows and columns that may be stored
-  const void* c;              // out += beta c, at the untransposed place; FP16, or FP32 as the output
+  int out_type, tma;  // (else: rows that start anywhere)
+  int n_lim;          // columns that may be stored
+  const void* c;      // BATCH, SYM: FP16 rows in 16-byte pieces; WGRAD: the FP32 output
   long long c_ld, c_es;
-  int c_type;
   float alpha, beta;
   const float *alpha_e, *beta_e;  // per expert, or null
   uint32_t formats;
@@ -74,17 +94,17 @@ struct Args {
 struct Tile {
   int e, row0, nrows, col0;  // output rows [row0, row0 + nrows) of this CTA, first column
   int a_mn, b_mn;            // this CTA's first A row and B row (or column) of the maps
-  int kb, last16;            // k-blocks, and 16-deep steps of the last
+  int k0, kb, last16;        // first k (WGRAD: row), k-blocks, and 16-deep steps of the last
+  bool tail;                 // WGRAD: the last k-block is the expert's tail
   int boxes;                 // A boxes of the single product form
-  bool mirror;
 };
 
-__device__ __forceinline__ void tma_load_3d(const void* map, void* dst, uint64_t* bar, int c0,
-                                            int c1, int c2) {
+__device__ __forceinline__ void tma_load_3d(const void* map, void* dst, uint32_t bar, int c0, int c1,
+                                            int c2) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tma_load_3d_pair(const void* map, void* dst, uint32_t bar_cluster,
@@ -107,112 +127,161 @@ __device__ __forceinline__ uint64_t sdesc_mn_major_sw128(uint32_t saddr) {
   d |= (uint64_t)2u << 61;
   return d;
 }
-template <bool MN>
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, int k16) {
-  if constexpr (MN) return sdesc_mn_major_sw128(saddr + k16 * (UK * 128));
-  else return sdesc_k_major_sw128(saddr + k16 * (UK * 2));
+template <int TYPE>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (TYPE == MOE_DTYPE_BF16) {
+    return pack_bf16x2(lo, hi);
+  } else {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
 }
 
-__device__ __forceinline__ uint16_t to16(float v, int type) {
-  return type == MOE_DTYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v))
-                                : __half_as_ushort(__float2half_rn(v));
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1,
+                                             int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
+      : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, int type) {
-  return (uint32_t)to16(lo, type) | ((uint32_t)to16(hi, type) << 16);
+// This thread's stores have read their shared memory (all: and are performed).
+__device__ __forceinline__ void tma_stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void tma_stores_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// One 32 x 32 block of an accumulator that the warp has staged in shared memory (row i at
-// i * 33: conflict-free by rows and by columns) goes to rows row0.. and columns col0.. of out,
-// as far as nrows and ncols allow; `turned`: element (i, j) to row j, column i.
-__device__ __forceinline__ void store_block(const float* st, int lane, void* out, long long ld,
-                                            int type, bool vec, bool turned, long long row0,
-                                            int col0, int nrows, int ncols) {
-  // (i, j) of the output block; staged element (si, sj)
-  const long long r0 = turned ? col0 : row0;
-  const long long c0 = turned ? row0 : col0;
-  const int nr = turned ? ncols : nrows, nc = turned ? nrows : ncols;
-  const int di = turned ? 1 : 33, dj = turned ? 33 : 1;
-  if (type == MOE_DTYPE_F32) {
-    float* o = static_cast<float*>(out) + r0 * ld + c0;
-    if (vec) {
+// A warp's 32 rows x 128 bytes in shared memory: 16-byte piece c of row r at place c ^ (r & 7), the
+// 128-byte swizzle of a TMA store; a lane writing its row and eight lanes reading one row both
+// meet every bank once.
+__device__ __forceinline__ uint4* piece(uint4* st, int r, int c) { return st + 8 * r + (c ^ (r & 7)); }
+
+// Epilogue of one warp: its 32 rows (TMEM lanes at taddr) by every other 128-byte span of the
+// tile's columns, from span `first`.  With a map the block leaves by TMA (clipped at the output's
+// ends), else (an expert's last rows, sums added to the output, rows that start anywhere) through
+// registers, four whole spans an instruction.  out and c point to the rows' first element at
+// the tile's first column.
+template <int TYPE, bool ADD16, bool ADD32>
+__device__ __forceinline__ void store_tile(uint32_t taddr, bool sums, uint4* st, int lane, int first,
+                                           const CUtensorMap* map, int col0, int row0, int e,
+                                           void* out, long long ld, bool vec, int nrows, int ncols,
+                                           const void* c, long long c_ld, float alpha, float beta) {
+  constexpr int COLS = TYPE == MOE_DTYPE_F32 ? 32 : 64, PER = COLS / 8;  // of a span, of a piece
+  constexpr int BYTES = 128 / COLS;
+#pragma unroll 1
+  for (int c0 = first * COLS; c0 < ncols; c0 += 2 * COLS) {
+    const int cp = lane & 7, r4 = lane >> 3;  // this lane's piece and row (of four) in memory order
+    const bool in = c0 + cp * PER < ncols;
+    uint4 add[8];
+    if constexpr (ADD16 || ADD32) {
+      const uint8_t* src = static_cast<const uint8_t*>(c) + (size_t)(c0 + cp * PER) * BYTES;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3), c = 4 * (lane & 7);
-        const float* s = st + r * di + c * dj;
-        if (r < nr && c < nc)
-          *reinterpret_cast<float4*>(o + r * ld + c) =
-              make_float4(s[0], s[dj], s[2 * dj], s[3 * dj]);
+        const int r = 4 * i + r4;
+        add[i] = in && r < nrows ? *reinterpret_cast<const uint4*>(src + r * c_ld * BYTES)
+                                 : make_uint4(0, 0, 0, 0);
+      }
+    }
+    uint32_t w[32];
+    if constexpr (TYPE == MOE_DTYPE_F32) {
+      if (sums) {
+        tmem_ld_32x32b_x32(taddr + c0, w);
+        tmem_ld_wait();
       }
     } else {
-#pragma unroll 8
-      for (int r = 0; r < 32; ++r)
-        if (r < nr && lane < nc) o[r * ld + lane] = st[r * di + lane * dj];
+      if constexpr (ADD16) {
+        if (lane == 0) tma_stores_read();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *piece(st, 4 * i + r4, cp) = add[i];
+        __syncwarp();
+      }
+      uint32_t v[64];
+      if (sums) {
+        tmem_ld_32x32b_x32(taddr + c0, *reinterpret_cast<uint32_t(*)[32]>(v));
+        tmem_ld_32x32b_x32(taddr + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+        tmem_ld_wait();
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        uint32_t a[4];
+        if constexpr (ADD16) {
+          const uint4 x = *piece(st, lane, q);
+          a[0] = x.x, a[1] = x.y, a[2] = x.z, a[3] = x.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float lo = __uint_as_float(v[8 * q + 2 * j]), hi = __uint_as_float(v[8 * q + 2 * j + 1]);
+          if constexpr (ADD16) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a[j]));
+            lo = fmaf(alpha, lo, beta * f.x);
+            hi = fmaf(alpha, hi, beta * f.y);
+          } else {
+            lo *= alpha;
+            hi *= alpha;
+          }
+          w[4 * q + j] = pack16<TYPE>(lo, hi);
+        }
+      }
     }
-  } else {
-    uint16_t* o = static_cast<uint16_t*>(out) + r0 * ld + c0;
+    if (!sums) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = 0;
+    }
+    if constexpr (!ADD16) {
+      if (lane == 0) tma_stores_read();
+      __syncwarp();
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      *piece(st, lane, q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    if (map != nullptr) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) tma_store_3d(map, st, col0 + c0, row0, e);
+      continue;
+    }
+    __syncwarp();
     if (vec) {
+      uint8_t* dst = static_cast<uint8_t*>(out) + (size_t)(c0 + cp * PER) * BYTES;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2), c = 8 * (lane & 3);
-        const float* s = st + r * di + c * dj;
-        uint32_t w[4];
+      for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + r4;
+        uint4 x = *piece(st, r, cp);
+        if constexpr (ADD32) {
+          float* p = reinterpret_cast<float*>(&x);
+          const float* y = reinterpret_cast<const float*>(&add[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack16(s[2 * j * dj], s[(2 * j + 1) * dj], type);
-        if (r < nr && c < nc)
-          *reinterpret_cast<uint4*>(o + r * ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int j = 0; j < 4; ++j) p[j] += y[j];
+        }
+        if (in && r < nrows) *reinterpret_cast<uint4*>(dst + r * ld * BYTES) = x;
       }
-    } else {
-#pragma unroll 8
-      for (int r = 0; r < 32; ++r)
-        if (r < nr && lane < nc) o[r * ld + lane] = to16(st[r * di + lane * dj], type);
+    } else if constexpr (TYPE != MOE_DTYPE_F32) {  // rows that start anywhere: two columns a lane
+      uint16_t* dst = static_cast<uint16_t*>(out) + c0 + 2 * lane;
+      const int n = ncols - c0 - 2 * lane;
+#pragma unroll 4
+      for (int r = 0; r < 32; ++r) {
+        const uint32_t x = reinterpret_cast<const uint32_t*>(piece(st, r, lane >> 2))[lane & 3];
+        if (r < nrows && n > 0) dst[r * ld] = (uint16_t)x;
+        if (r < nrows && n > 1) dst[r * ld + 1] = (uint16_t)(x >> 16);
+      }
     }
+    __syncwarp();
   }
 }
 
-// st = alpha st + beta c over the block (c FP16 in 16-byte pieces of a padded buffer, or FP32)
-__device__ __forceinline__ void add_block(float* st, int lane, const void* c, long long ld,
-                                          int type, bool vec, float beta, long long row0, int col0,
-                                          int nrows, int ncols) {
-  if (type == MOE_DTYPE_F16) {
-    const uint16_t* p = static_cast<const uint16_t*>(c) + row0 * ld + col0;
-    uint4 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2), cc = 8 * (lane & 3);
-      v[i] = r < nrows && cc < ncols ? *reinterpret_cast<const uint4*>(p + r * ld + cc)
-                                     : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float* s = st + (8 * i + (lane >> 2)) * 33 + 8 * (lane & 3);
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        s[2 * j] = fmaf(beta, f.x, s[2 * j]);
-        s[2 * j + 1] = fmaf(beta, f.y, s[2 * j + 1]);
-      }
-    }
-  } else {
-    const float* p = static_cast<const float*>(c) + row0 * ld + col0;
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r)
-      if (r < nrows && lane < ncols) st[r * 33 + lane] = fmaf(beta, p[r * ld + lane], st[r * 33 + lane]);
-  }
-  __syncwarp();
-}
-
-template <int CTAS, int BN, Kind KIND, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constant__ Args p) {
+template <int CTAS, int BN, Kind KIND, Major A, Major B>
+__global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_constant__ Args p) {
   using C = Shape<CTAS, BN>;
   constexpr int TM = GM * CTAS;
   constexpr bool BOXED = KIND == PRODUCT && CTAS == 1;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  uint8_t* sA = base;
-  uint8_t* sB = base + C::STAGES * C::A_BYTES;
-  float* s_epi = reinterpret_cast<float*>(sB + C::STAGES * C::B_BYTES);
+  extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's period; there is no other)
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + C::STAGES * C::A_BYTES;
+  uint4* s_epi = reinterpret_cast<uint4*>(sB + C::STAGES * C::B_BYTES);
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_epi) + C::EPI_BYTES);
   uint64_t* full = bars;
   uint64_t* empty = bars + C::STAGES;
@@ -221,37 +290,36 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* peer_abort = abort_flag + 1;   // the other CTA's flag, and the k-blocks that it
-  volatile int* peer_issued = abort_flag + 2;  // has issued: written by it at its end
-  int* s_total = reinterpret_cast<int*>(tmem_slot + 4);
+  volatile int* peer_abort = abort_flag + 1;  // the other CTA's flag, written by it at its end
+  volatile int* issued = abort_flag + 2;  // k-blocks issued of A and B here, and by the other CTA
+  int* s_total = reinterpret_cast<int*>(tmem_slot + 7);
   int* s_bad = s_total + 1;
-  int* s_off = reinterpret_cast<int*>(tmem_slot + 8);
+  int* s_off = reinterpret_cast<int*>(tmem_slot + 12);
   int* s_prefix = s_off + (kMaxE + 1);  // PRODUCT: first unit of an expert
-  int* s_exp = s_prefix + (kMaxE + 1);  // WGRAD: experts by falling number of rows
+  int* s_exp = s_prefix;                // WGRAD: experts by falling number of rows
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CTAS == 2 ? (int)cluster_ctarank() : 0;
   const int P = gridDim.x / CTAS, unit0 = blockIdx.x / CTAS;
-  const int NT = (p.N + BN - 1) / BN;
-  const int MT = (p.M + TM - 1) / TM;  // (not PRODUCT)
+  const int NT = p.nt.d, MT = (p.M + TM - 1) / TM;
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     *peer_abort = 0;
-    *peer_issued = 0;
-    *s_bad = 0;
+    for (int i = 0; i < 4; ++i) issued[i] = 0;
+    *s_bad = (smem_u32(smem) & 1023u) != 0;  // (never: asked for above)
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 4 * CTAS);  // the epilogue warps
+      mbar_init(&tempty[a], EPI_WARPS * CTAS);  // the epilogue warps
     }
     mbar_init(mma_done, 1);
     fence_mbar_init();
-    if (KIND != WGRAD) prefetch_tensormap(&p.a);
-    if (KIND != WGRAD) prefetch_tensormap(&p.b);
+    prefetch_tensormap(&p.a);
+    prefetch_tensormap(&p.b);
   }
   pdl_wait();
   if (warp == 1) {
@@ -277,7 +345,7 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
         }
         s_exp[r] = e;
       }
-      if (threadIdx.x == 0) *s_total = p.E * MT * NT;
+      if (threadIdx.x == 0) *s_total = p.E * p.per.d;
     } else if (warp == 5) {
       int carry = 0;
       for (int e0 = 0; e0 < p.E; e0 += 32) {
@@ -296,7 +364,7 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
       if (lane == 0) *s_total = carry;
     }
   } else if (threadIdx.x == 0) {
-    *s_total = p.E * (KIND == SYM ? MT * (MT + 1) / 2 : MT * NT);
+    *s_total = p.E * p.per.d;
   }
   tc_fence_before();
   __syncthreads();
@@ -315,7 +383,6 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
   auto tile_of = [&](int u) {
     Tile t;
     t.boxes = 0;
-    t.mirror = false;
     if constexpr (KIND == PRODUCT) {
       int lo = 0, hi = p.E - 1;  // largest e with s_prefix[e] <= u
       while (lo < hi) {
@@ -323,7 +390,7 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
         if (s_prefix[mid] <= u) lo = mid;
         else hi = mid - 1;
       }
-      const int local = u - s_prefix[lo], mt = local / NT;
+      const int local = u - s_prefix[lo], mt = local / p.nt;
       t.e = lo;
       t.row0 = s_off[lo] + mt * TM + rank * GM;
       t.nrows = min(GM, max(0, s_off[lo + 1] - t.row0));
@@ -331,27 +398,27 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
       t.a_mn = t.row0;
       if constexpr (BOXED) t.boxes = (t.nrows + BOX_ROWS - 1) / BOX_ROWS;
     } else {
-      const int per = KIND == SYM ? MT * (MT + 1) / 2 : MT * NT;
-      const int x = u / per;
-      int local = u - x * per, mt, nt;
+      const int x = u / p.per;
+      int local = u - x * p.per.d, mt, nt;
       if constexpr (KIND == SYM) {
         mt = 0;
         while (local >= MT - mt) local -= MT - mt++;
         nt = mt + local;
-        t.mirror = nt > mt;
       } else {
-        mt = local / NT;
+        mt = local / p.nt;
         nt = local - mt * NT;
       }
       t.e = KIND == WGRAD ? s_exp[x] : x;
       t.row0 = mt * TM + rank * GM;
-      t.nrows = min(GM, max(0, p.m_lim - t.row0));
+      t.nrows = min(GM, max(0, p.M - t.row0));
       t.col0 = nt * BN;
       t.a_mn = t.row0;
     }
     t.b_mn = t.col0 + rank * C::BROWS;
     const int k = KIND == WGRAD ? s_off[t.e + 1] - s_off[t.e] : p.K;
+    t.k0 = KIND == WGRAD ? s_off[t.e] : 0;
     t.kb = (k + GK - 1) / GK;
+    t.tail = KIND == WGRAD && k % GK != 0;
     t.last16 = (k - (t.kb - 1) * GK + UK - 1) / UK;
     return t;
   };
@@ -366,78 +433,75 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
       if (u >= total) return false;
       wt = tile_of(u);
       wkb = 0;
-      if constexpr (KIND == WGRAD) {
-        if (wt.kb > 0) {
-          acquire_map(p.maps + (size_t)wt.e * kMapBytes);
-          acquire_map(p.maps + (size_t)(p.E + wt.e) * kMapBytes);
-        }
-      }
     }
     return true;
   };
+  const bool second = warp == B_WARP;  // loads B
+  const uint32_t full0 = CTAS == 2 ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
   auto load = [&](int s) {
-    const void* ma = &p.a;
-    const void* mb = &p.b;
-    const int k = wkb * GK;
-    int ea = KIND == PRODUCT ? 0 : wt.e, eb = wt.e;
-    if constexpr (KIND == WGRAD) {
-      ma = p.maps + (size_t)wt.e * kMapBytes;
-      mb = p.maps + (size_t)(p.E + wt.e) * kMapBytes;
-      ea = eb = 0;
+    const bool upper = (second ? B : A) == UPPER;
+    const bool mn = (second ? B : A) == MN ||
+                    (upper && wkb * GK / TM < (second ? wt.b_mn : wt.a_mn) / TM);
+    const bool tail = KIND == WGRAD && wt.tail && wkb == wt.kb - 1;
+    const bool other = tail || (upper && mn);
+    const CUtensorMap* m = second ? (other ? &p.bt : &p.b) : (other ? &p.at : &p.a);
+    const int k = tail ? 0 : wt.k0 + wkb * GK;
+    const int e = KIND == WGRAD ? (tail ? wt.e : 0) : KIND == PRODUCT && !second ? 0 : wt.e;
+    const int x = second ? wt.b_mn : wt.a_mn;
+    uint8_t* d = second ? sB + s * C::B_BYTES : sA + s * C::A_BYTES;
+    const uint32_t bar = full0 + 8 * s;
+    if (!second) {  // the phase's one arrival, with the bytes of both operands (and CTAs)
+      if (CTAS == 2) {
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
+      } else {
+        mbar_arrive_expect_tx(&full[s],
+                              C::B_BYTES + (BOXED ? wt.boxes * BOX_ROWS * GK * 2 : C::A_BYTES));
+      }
     }
-    uint8_t* da = sA + s * C::A_BYTES;
-    uint8_t* db = sB + s * C::B_BYTES;
-    uint32_t bar = 0;
-    if constexpr (CTAS == 2) {
-      if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
-      bar = mapa_shared(smem_u32(&full[s]), 0);
-    } else {
-      mbar_arrive_expect_tx(&full[s],
-                            C::B_BYTES + (BOXED ? wt.boxes * BOX_ROWS * GK * 2 : C::A_BYTES));
-    }
-    auto one = [&](const void* m, uint8_t* d, int c0, int c1, int c2) {
-      if constexpr (CTAS == 2) tma_load_3d_pair(m, d, bar, c0, c1, c2);
-      else tma_load_3d(m, d, &full[s], c0, c1, c2);
+    auto one = [&](uint8_t* dst, int c0, int c1) {
+      if constexpr (CTAS == 2) tma_load_3d_pair(m, dst, bar, c0, c1, e);
+      else tma_load_3d(m, dst, bar, c0, c1, e);
     };
-    if constexpr (A_MN) {
-#pragma unroll
-      for (int j = 0; j < GM / 64; ++j) one(ma, da + j * 8192, wt.a_mn + 64 * j, k, ea);
-    } else if constexpr (BOXED) {
-      for (int j = 0; j < wt.boxes; ++j)
-        one(ma, da + j * BOX_ROWS * 128, k, wt.a_mn + j * BOX_ROWS, ea);
+    if (mn) {
+      one(d, x, k);
+      one(d + 8192, x + 64, k);
+    } else if (BOXED && !second) {
+      for (int j = 0; j < wt.boxes; ++j) one(d + j * BOX_ROWS * 128, k, x + j * BOX_ROWS);
     } else {
-      one(ma, da, k, wt.a_mn, ea);
-    }
-    if constexpr (B_MN) {
-#pragma unroll
-      for (int j = 0; j < C::BROWS / 64; ++j) one(mb, db + j * 8192, wt.b_mn + 64 * j, k, eb);
-    } else {
-      one(mb, db, k, wt.b_mn, eb);
+      one(d, k, x);
     }
     ++wkb;
     ++it;
   };
 
-  if (warp == 0) {
+  if (warp == 0 || second) {
     if (lane == 0) {
-      // ------------------------------------------------------------ producer
+      // ----------------------------------------------------------- producers
+      int s = 0;
+      uint32_t ph = 1;
       while (advance()) {
-        const int s = it % C::STAGES;
-        if (!mbar_wait_bounded(&empty[s], ((it / C::STAGES) & 1) ^ 1, abort_flag, p.status,
-                               p.limit))
-          break;
+        if (!mbar_wait_bounded(&empty[s], ph, abort_flag, p.status, p.limit)) break;
         load(s);
+        if (++s == C::STAGES) {
+          s = 0;
+          ph ^= 1;
+        }
       }
+      issued[second] = it;
       if constexpr (CTAS == 2)
-        st_shared_remote(mapa_shared(smem_u32((const void*)peer_issued), rank ^ 1), it);
+        st_shared_remote(mapa_shared(smem_u32((const void*)(issued + 2 + second)), rank ^ 1), it);
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       // ---------------------------------------------------------- MMA issuer
-      const uint32_t idesc = p.formats | (1u << 4) | ((uint32_t)A_MN << 15) |
-                             ((uint32_t)B_MN << 16) | ((uint32_t)(BN >> 3) << 17) |
-                             ((uint32_t)(TM >> 4) << 24);
-      int jt = 0, tcount = 0;
+      const uint32_t idesc0 = p.formats | (1u << 4) | ((uint32_t)(BN >> 3) << 17) |
+                              ((uint32_t)(TM >> 4) << 24);
+      // descriptors of stage 0, in both majors; a stage and a 16-deep step only add to the address
+      const uint64_t a_km = sdesc_k_major_sw128(smem_u32(sA)), a_tm = sdesc_mn_major_sw128(smem_u32(sA));
+      const uint64_t b_km = sdesc_k_major_sw128(smem_u32(sB)), b_tm = sdesc_mn_major_sw128(smem_u32(sB));
+      constexpr uint32_t KM_STEP = UK * 2 / 16, MN_STEP = UK * 128 / 16;
+      int s = 0, tcount = 0;
+      uint32_t ph = 0;
       bool aborted = false;
       for (int i = 0; i * P < total && !aborted; ++i) {
         const int u = unit_of(i);
@@ -450,26 +514,36 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
           break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
-        for (int kb = 0; kb < t.kb; ++kb, ++jt) {
-          const int s = jt % C::STAGES;
-          if (!mbar_wait_bounded(&full[s], (jt / C::STAGES) & 1, abort_flag, p.status, p.limit)) {
+        for (int kb = 0; kb < t.kb; ++kb) {
+          if (!mbar_wait_bounded(&full[s], ph, abort_flag, p.status, p.limit)) {
             aborted = true;
             break;
           }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(sA + s * C::A_BYTES);
-          const uint32_t b_addr = smem_u32(sB + s * C::B_BYTES);
-          const int steps = kb + 1 < t.kb ? GK / UK : t.last16;
-          for (int kk = 0; kk < steps; ++kk) {
+          const bool a_mn = A == MN || (A == UPPER && kb * GK / TM < t.row0 / TM);
+          const bool b_mn = B == MN || (B == UPPER && kb * GK / TM < t.col0 / TM);
+          const uint32_t idesc = idesc0 | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
+          const uint64_t da = (a_mn ? a_tm : a_km) + (uint32_t)(s * (C::A_BYTES / 16));
+          const uint64_t db = (b_mn ? b_tm : b_km) + (uint32_t)(s * (C::B_BYTES / 16));
+          const uint32_t ga = a_mn ? MN_STEP : KM_STEP, gb = b_mn ? MN_STEP : KM_STEP;
+          auto mma = [&](int kk) {
             if constexpr (CTAS == 2)
-              mma_bf16_pair(d_tmem, sdesc<A_MN>(a_addr, kk), sdesc<B_MN>(b_addr, kk), idesc,
-                            (kb > 0 || kk > 0) ? 1u : 0u);
+              mma_bf16_pair(d_tmem, da + kk * ga, db + kk * gb, idesc, kk > 0 || kb > 0 ? 1u : 0u);
             else
-              mma_bf16(d_tmem, sdesc<A_MN>(a_addr, kk), sdesc<B_MN>(b_addr, kk), idesc,
-                       (kb > 0 || kk > 0) ? 1u : 0u);
+              mma_bf16(d_tmem, da + kk * ga, db + kk * gb, idesc, kk > 0 || kb > 0 ? 1u : 0u);
+          };
+          if (kb + 1 < t.kb || t.last16 == GK / UK) {
+#pragma unroll
+            for (int kk = 0; kk < GK / UK; ++kk) mma(kk);
+          } else {
+            for (int kk = 0; kk < t.last16; ++kk) mma(kk);
           }
           if constexpr (CTAS == 2) mma_commit_pair(&empty[s], 0x3);
           else mma_commit(&empty[s]);
+          if (++s == C::STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
         }
         if (aborted) break;
         if constexpr (CTAS == 2) mma_commit_pair(&tfull[acc], 0x3);
@@ -484,9 +558,8 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
   } else {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3;  // TMEM lane quarter this warp may access
-    float* st = s_epi + q * 32 * C::EPI_LD;
-    const int elt = p.out_type == MOE_DTYPE_F32 ? 4 : 2;
-    const int c_elt = p.c_type == MOE_DTYPE_F32 ? 4 : 2;
+    const int first = (warp - 2) >> 2;
+    uint4* st = s_epi + (warp - 2) * (32 * 8);
     int tcount = 0;
     for (int i = 0; i * P < total; ++i) {
       const int u = unit_of(i);
@@ -494,7 +567,8 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
       const Tile t = tile_of(u);
       if (KIND == WGRAD && t.kb == 0 && p.c != nullptr) continue;  // nothing to add
       const int acc = tcount & 1;
-      if (t.kb > 0) {
+      const bool sums = KIND != WGRAD || t.kb > 0;
+      if (sums) {
         int ok = 1;
         if (lane == 0)
           ok = mbar_wait_bounded(&tfull[acc], (tcount >> 1) & 1, abort_flag, p.status, p.limit);
@@ -503,39 +577,54 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
         tc_fence_after();
       }
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
-      const int nrows = min(32, max(0, t.nrows - q * 32));
-      const long long row0 = t.row0 + q * 32;
+      const int nrows = min(32, t.nrows - q * 32);
       const int ncols = min(BN, p.n_lim - t.col0);
-      uint8_t* out = static_cast<uint8_t*>(p.out) + (KIND == PRODUCT ? 0 : t.e * p.es * elt);
-      const float alpha = p.alpha * (p.alpha_e ? __ldg(p.alpha_e + t.e) : 1.0f);
-      const float beta = p.beta * (p.beta_e ? __ldg(p.beta_e + t.e) : 1.0f);
       if (nrows > 0) {
-#pragma unroll 1
-        for (int c0 = 0; c0 < ncols; c0 += 32) {
-          if (t.kb > 0) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(taddr + c0, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) st[lane * 33 + j] = alpha * __uint_as_float(v[j]);
+        const int row0 = t.row0 + q * 32;
+        const long long at = (KIND == PRODUCT ? 0 : t.e * p.es) + row0 * p.ld + t.col0;
+        void* out = static_cast<uint8_t*>(p.out) + at * (p.out_type == MOE_DTYPE_F32 ? 4 : 2);
+        const int oe = KIND == PRODUCT ? 0 : t.e;
+        if constexpr (KIND == BATCH || KIND == SYM) {
+          const CUtensorMap* map = p.tma ? &p.o : nullptr;
+          const float alpha = p.alpha * (p.alpha_e ? __ldg(p.alpha_e + t.e) : 1.0f);
+          const float beta = p.beta * (p.beta_e ? __ldg(p.beta_e + t.e) : 1.0f);
+          const __half* c = static_cast<const __half*>(p.c) + t.e * p.c_es + row0 * p.c_ld + t.col0;
+          if (p.out_type == MOE_DTYPE_BF16)  // (the last step's result)
+            store_tile<MOE_DTYPE_BF16, true, false>(taddr, true, st, lane, first, map, t.col0, row0,
+                                                    oe, out, p.ld, false, nrows, ncols, c, p.c_ld,
+                                                    alpha, beta);
+          else if (p.c != nullptr)
+            store_tile<MOE_DTYPE_F16, true, false>(taddr, true, st, lane, first, map, t.col0, row0, oe,
+                                                   out, p.ld, false, nrows, ncols, c, p.c_ld, alpha,
+                                                   beta);
+          else
+            store_tile<MOE_DTYPE_F16, false, false>(taddr, true, st, lane, first, map, t.col0, row0,
+                                                    oe, out, p.ld, false, nrows, ncols, nullptr, 0,
+                                                    alpha, 0.0f);
+        } else {
+          // (a product's rows behind the expert's last belong to the next one)
+          const CUtensorMap* map = KIND == WGRAD || nrows == 32 ? &p.o : nullptr;
+          if (p.out_type == MOE_DTYPE_F32) {
+            if (KIND == WGRAD && p.c != nullptr)
+              store_tile<MOE_DTYPE_F32, false, true>(taddr, sums, st, lane, first, nullptr, 0, 0, 0,
+                                                     out, p.ld, true, nrows, ncols, out, p.ld, 1.0f,
+                                                     1.0f);
+            else
+              store_tile<MOE_DTYPE_F32, false, false>(taddr, sums, st, lane, first, map, t.col0, row0,
+                                                      oe, out, p.ld, true, nrows, ncols, nullptr, 0,
+                                                      1.0f, 0.0f);
+          } else if (p.out_type == MOE_DTYPE_BF16) {
+            store_tile<MOE_DTYPE_BF16, false, false>(taddr, sums, st, lane, first, map, t.col0, row0,
+                                                     oe, out, p.ld, true, nrows, ncols, nullptr, 0,
+                                                     1.0f, 0.0f);
           } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) st[lane * 33 + j] = 0.0f;
+            store_tile<MOE_DTYPE_F16, false, false>(taddr, sums, st, lane, first, map, t.col0, row0,
+                                                    oe, out, p.ld, true, nrows, ncols, nullptr, 0,
+                                                    1.0f, 0.0f);
           }
-          __syncwarp();
-          const int nc = min(32, ncols - c0);
-          if (KIND != PRODUCT && p.c != nullptr)
-            add_block(st, lane, static_cast<const uint8_t*>(p.c) + t.e * p.c_es * c_elt, p.c_ld,
-                      p.c_type, p.vec, beta, row0, t.col0 + c0, nrows, nc);
-          store_block(st, lane, out, p.ld, p.out_type, p.vec, p.turned, row0, t.col0 + c0, nrows,
-                      nc);
-          if (KIND == SYM && t.mirror)  // (a padded row has more columns than there are rows)
-            store_block(st, lane, out, p.ld, p.out_type, p.vec, true, row0, t.col0 + c0, nrows,
-                        min(nc, p.N - t.col0 - c0));
-          __syncwarp();
         }
       }
-      if (t.kb > 0) {
+      if (sums) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -545,6 +634,7 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
         ++tcount;
       }
     }
+    if (lane == 0) tma_stores_done();
   }
 
   tc_fence_before();
@@ -558,15 +648,15 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
   }
   if (aborted) {
     // All MMAs are complete and no role waits any more.  Copies into the last STAGES slots may
-    // still be in flight.  A stage that only one CTA of a pair has issued gets the other's
-    // bytes now, so that its barrier completes; the even CTA waits for the bytes of both.
-    if (threadIdx.x == 0) {
-      if constexpr (CTAS == 2)
-        while (it < *peer_issued && advance()) load(it % C::STAGES);
-      if (rank == 0)
-        for (int i = (it > C::STAGES ? it - C::STAGES : 0); i < it; ++i)
-          wait_drain(&full[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
-    }
+    // still be in flight.  A stage that one producer has issued and another has not gets the
+    // other's bytes now (its slot's last MMAs are complete, or the one could not have issued
+    // it), so that its barrier completes; the even CTA waits for the bytes of both.
+    const int most = max(max(issued[0], issued[1]), max(issued[2], issued[3]));
+    if ((warp == 0 || second) && lane == 0)
+      while (it < most && advance()) load(it % C::STAGES);
+    if (threadIdx.x == 0 && rank == 0)
+      for (int i = (most > C::STAGES ? most - C::STAGES : 0); i < most; ++i)
+        wait_drain(&full[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
     if constexpr (CTAS == 2) cluster_sync();  // the odd CTA's copies count on the even's barriers
   }
   if (warp == 1) {
@@ -576,48 +666,39 @@ __global__ void __launch_bounds__(192, 1) train_gemm_kernel(const __grid_constan
   }
 }
 
-// One warp makes one expert's map of one operand: the caller's map of all rows with the base
-// address and the number of rows of the expert.
-struct BaseMaps {
-  CUtensorMap a, b;
-};
-__global__ void __launch_bounds__(32)
-    wgrad_maps_kernel(const __grid_constant__ BaseMaps base, const int32_t* __restrict__ offsets,
-                      int E, int R, const uint8_t* x, long long x_bytes, const uint8_t* dy,
-                      long long dy_bytes, uint8_t* maps) {
-  __shared__ alignas(128) uint32_t m[32];
-  const bool second = blockIdx.x >= E;
-  const int e = blockIdx.x - (second ? E : 0), lane = threadIdx.x;
+// The rows of each expert's partial last k-block (fewer than 64) to tails [E][64][cols], filled up
+// with zeros to the 16 rows that an MMA reads; x's and then dy's.  TAIL_SPLIT blocks an expert.
+constexpr int TAIL_SPLIT = 8;
+__global__ void __launch_bounds__(256)
+    tails_kernel(const int32_t* __restrict__ offsets, int E, int R, const uint8_t* x,
+                 long long x_bytes, int K, const uint8_t* dy, long long dy_bytes, int N, uint4* tx,
+                 uint4* tdy) {
   pdl_wait();
   pdl_launch_dependents();
+  const int e = blockIdx.x / TAIL_SPLIT, part = blockIdx.x % TAIL_SPLIT;
   const int lo = __ldg(offsets + e), hi = __ldg(offsets + e + 1);
-  if (lo < 0 || hi <= lo || hi > R) return;  // (a bad sequence: the product reports it and reads no map)
-  m[lane] = reinterpret_cast<const uint32_t*>(second ? &base.b : &base.a)[lane];
-  __syncwarp();
-  if (lane == 0) {
-    const uint64_t addr = reinterpret_cast<uint64_t>(
-        second ? dy + (long long)lo * dy_bytes : x + (long long)lo * x_bytes);
-    asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(
-                     smem_u32(m)),
-                 "l"(addr)
-                 : "memory");
-    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(
-                     smem_u32(m)),
-                 "r"(hi - lo)
-                 : "memory");
-  }
-  __syncwarp();
-  asm volatile(
-      "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned "
-      "[%0], [%1], 128;" ::"l"(maps + (size_t)blockIdx.x * kMapBytes),
-      "r"(smem_u32(m))
-      : "memory");
+  if (lo < 0 || hi <= lo || hi > R) return;  // (a bad sequence: the product reports it and reads nothing)
+  const int rem = (hi - lo) % GK;
+  const int rows = (rem + UK - 1) / UK * UK;
+  const long long r0 = hi - rem;
+  for (int r = part; r < rows; r += TAIL_SPLIT)
+    for (int c = threadIdx.x; c < (K + N) / 8; c += blockDim.x) {
+      const bool second = c >= K / 8;
+      const int cc = second ? c - K / 8 : c;
+      const uint8_t* src = second ? dy + (r0 + r) * dy_bytes : x + (r0 + r) * x_bytes;
+      uint4* dst = second ? tdy + (long long)(e * GK + r) * (N / 8) : tx + (long long)(e * GK + r) * (K / 8);
+      dst[cc] = r < rem ? __ldg(reinterpret_cast<const uint4*>(src) + cc) : make_uint4(0, 0, 0, 0);
+    }
 }
 
-template <int CTAS, int BN, Kind KIND, bool A_MN, bool B_MN>
-cudaError_t launch(const Args& p, long long units, cudaStream_t s) {
+template <int CTAS, int BN, Kind KIND, Major A, Major B>
+cudaError_t launch(Args& p, long long units, cudaStream_t s) {
   using C = Shape<CTAS, BN>;
-  auto kern = train_gemm_kernel<CTAS, BN, KIND, A_MN, B_MN>;
+  constexpr int TM = GM * CTAS;
+  const int MT = (p.M + TM - 1) / TM;
+  p.nt = make_div((p.N + BN - 1) / BN);
+  if (KIND != PRODUCT) p.per = make_div(KIND == SYM ? MT * (MT + 1) / 2 : MT * p.nt.d);
+  auto kern = train_gemm_kernel<CTAS, BN, KIND, A, B>;
   static int cache[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -628,7 +709,7 @@ cudaError_t launch(const Args& p, long long units, cudaStream_t s) {
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = CTAS;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(192, 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   int most = dev < 64 ? cache[dev] : 0;  // CTAs resident at once
   if (most == 0) {
@@ -656,14 +737,13 @@ cudaError_t launch(const Args& p, long long units, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-uint32_t formats_of(int dtype) {  // A and B: BF16, or both FP16
-  return dtype == MOE_DTYPE_BF16 ? (1u << 7) | (1u << 10) : 0u;
+bool encode_out(CUtensorMap* m, const void* out, int type, uint64_t cols, uint64_t rows, int E,
+                long long ld, long long es) {
+  return encode_out_3d(m, out, type == MOE_DTYPE_F32, cols, rows, E, ld, es);
 }
 
-bool vec_ok(const void* out, int type, long long ld, long long es, long long n) {
-  const int per = type == MOE_DTYPE_F32 ? 4 : 8;
-  return (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ld % per == 0 && es % per == 0 &&
-         n % per == 0;
+uint32_t formats_of(int dtype) {  // A and B: BF16, or both FP16
+  return dtype == MOE_DTYPE_BF16 ? (1u << 7) | (1u << 10) : 0u;
 }
 
 }  // namespace
@@ -689,8 +769,7 @@ cudaError_t launch_product(const TrainProduct& q, cudaStream_t s) {
   p.out = q.y;
   p.ld = q.y_ld;
   p.out_type = q.y_type;
-  p.vec = vec_ok(q.y, q.y_type, q.y_ld, 0, q.N);
-  p.alpha = 1.0f;
+  if (!encode_out(&p.o, q.y, q.y_type, q.N, q.R, 1, q.y_ld, 0)) return cudaErrorInvalidValue;
   p.formats = formats_of(q.type);
   p.status = q.status;
   p.limit = q.limit;
@@ -698,76 +777,80 @@ cudaError_t launch_product(const TrainProduct& q, cudaStream_t s) {
   const long long tiles = (q.R + tm - 1) / tm + (q.E < q.R ? q.E : q.R);
   const long long units = tiles * ((q.N + bn - 1) / bn);
   if (pair)
-    return q.turned ? launch<2, 256, PRODUCT, false, false>(p, units, s)
-                    : launch<2, 256, PRODUCT, false, true>(p, units, s);
-  return q.turned ? launch<1, 128, PRODUCT, false, false>(p, units, s)
-                  : launch<1, 128, PRODUCT, false, true>(p, units, s);
+    return q.turned ? launch<2, 256, PRODUCT, KM, KM>(p, units, s)
+                    : launch<2, 256, PRODUCT, KM, MN>(p, units, s);
+  return q.turned ? launch<1, 128, PRODUCT, KM, KM>(p, units, s)
+                  : launch<1, 128, PRODUCT, KM, MN>(p, units, s);
 }
 
+size_t wgrad_tail_bytes(int E, int cols) { return (size_t)E * GK * cols * 2; }
+
 cudaError_t launch_wgrad(const TrainWgrad& q, cudaStream_t s) {
-  BaseMaps base;
-  if (!encode_16bit_3d(&base.a, q.x, q.K, q.R, 1, q.x_ld, 0, GK) ||
-      !encode_16bit_3d(&base.b, q.dy, q.N, q.R, 1, q.dy_ld, 0, GK))
-    return cudaErrorInvalidValue;
-  cudaError_t err = launch_pdl(wgrad_maps_kernel, dim3(2 * q.E), dim3(32), 0, s, base, q.offsets,
-                               q.E, q.R, static_cast<const uint8_t*>(q.x), 2 * q.x_ld,
-                               static_cast<const uint8_t*>(q.dy), 2 * q.dy_ld, q.maps);
-  if (err != cudaSuccess) return err;
   Args p = {};
-  p.maps = q.maps;
+  if (!encode_16bit_3d(&p.a, q.x, q.K, q.R, 1, q.x_ld, 0, GK) ||
+      !encode_16bit_3d(&p.b, q.dy, q.N, q.R, 1, q.dy_ld, 0, GK) ||
+      !encode_16bit_3d(&p.at, q.tail_x, q.K, GK, q.E, q.K, (uint64_t)GK * q.K, GK) ||
+      !encode_16bit_3d(&p.bt, q.tail_dy, q.N, GK, q.E, q.N, (uint64_t)GK * q.N, GK))
+    return cudaErrorInvalidValue;
+  cudaError_t err = launch_pdl(tails_kernel, dim3(q.E * TAIL_SPLIT), dim3(256), 0, s, q.offsets, q.E,
+                               q.R, static_cast<const uint8_t*>(q.x), 2 * q.x_ld, q.K,
+                               static_cast<const uint8_t*>(q.dy), 2 * q.dy_ld, q.N,
+                               static_cast<uint4*>(q.tail_x), static_cast<uint4*>(q.tail_dy));
+  if (err != cudaSuccess) return err;
   p.offsets = q.offsets;
   p.E = q.E;
   p.R = q.R;
-  p.M = p.m_lim = q.K;
+  p.M = q.K;
   p.N = p.n_lim = q.N;
   p.out = q.out;
   p.ld = q.ld;
   p.es = q.es;
   p.out_type = q.out_type;
-  p.vec = vec_ok(q.out, q.out_type, q.ld, q.es, q.N);
-  p.alpha = 1.0f;
-  if (q.accumulate) {
-    p.c = q.out;
-    p.c_ld = q.ld;
-    p.c_es = q.es;
-    p.c_type = MOE_DTYPE_F32;
-    p.beta = 1.0f;
-  }
+  if (q.accumulate) p.c = q.out;
+  if (!encode_out(&p.o, q.out, q.out_type, q.N, q.K, q.E, q.ld, q.es)) return cudaErrorInvalidValue;
   p.formats = formats_of(q.type);
   p.status = q.status;
   p.limit = q.limit;
   const bool pair = q.K > 128 && q.N > 128;
   const int t = pair ? 256 : 128;
   const long long units = (long long)q.E * ((q.K + t - 1) / t) * ((q.N + t - 1) / t);
-  return pair ? launch<2, 256, WGRAD, true, true>(p, units, s)
-              : launch<1, 128, WGRAD, true, true>(p, units, s);
+  return pair ? launch<2, 256, WGRAD, MN, MN>(p, units, s)
+              : launch<1, 128, WGRAD, MN, MN>(p, units, s);
 }
 
 cudaError_t launch_batch(const TrainBatch& q, cudaStream_t s) {
-  const int least = q.M < q.N ? q.M : q.N;
-  const bool pair = least > 128;
-  const uint32_t rows = 128;
+  const bool pair = q.pair;
   Args p = {};
-  if (!encode_16bit_3d(&p.a, q.a, q.K, q.M, q.E, q.a_ld, q.a_es, GM)) return cudaErrorInvalidValue;
-  const bool okb = q.sym ? encode_16bit_3d(&p.b, q.b, q.K, q.N, q.E, q.b_ld, q.b_es, rows)
-                         : encode_16bit_3d(&p.b, q.b, q.N, q.K, q.E, q.b_ld, q.b_es, GK);
-  if (!okb) return cudaErrorInvalidValue;
+  auto encode = [&](CUtensorMap* m, const void* x, bool mn, int mn_size, long long ld, long long es) {
+    return mn ? encode_16bit_3d(m, x, mn_size, q.K, q.E, ld, es, GK)
+              : encode_16bit_3d(m, x, q.K, mn_size, q.E, ld, es, GM);
+  };
+  const bool a_mn = q.form == TrainBatch::GRAM_COLS;
+  const bool b_mn = a_mn || q.form == TrainBatch::LEFT;
+  const bool square = q.form == TrainBatch::SQUARE;
+  if (!encode(&p.a, q.a, a_mn, q.M, q.a_ld, q.a_es) || !encode(&p.b, q.b, b_mn, q.N, q.b_ld, q.b_es))
+    return cudaErrorInvalidValue;
+  if ((square || q.form == TrainBatch::LEFT) && !encode(&p.at, q.a, true, q.M, q.a_ld, q.a_es))
+    return cudaErrorInvalidValue;
+  if ((square || q.form == TrainBatch::RIGHT) && !encode(&p.bt, q.b, true, q.N, q.b_ld, q.b_es))
+    return cudaErrorInvalidValue;
   p.E = q.E;
-  p.M = p.m_lim = q.M;
+  p.M = q.M;
   p.N = q.N;
   p.K = q.K;
   p.out = q.out;
   p.ld = q.ld;
   p.es = q.es;
   p.out_type = q.out_type;
-  p.turned = q.turned;
   // columns of a padded buffer may be written up to its row length (they hold zeros)
   p.n_lim = q.padded ? (q.N + 7) / 8 * 8 : q.N;
-  p.vec = q.padded || vec_ok(q.out, q.out_type, q.ld, q.es, q.turned ? q.M : q.N);
+  // (a TMA store ends a row with a whole 16-byte piece, whatever the map's extent)
+  p.tma = q.padded || (q.N % 8 == 0 && q.ld % 8 == 0 && (q.E == 1 || q.es % q.ld == 0));
+  if (p.tma && !encode_out(&p.o, q.out, q.out_type, p.n_lim, q.M, q.E, q.ld, q.es))
+    return cudaErrorInvalidValue;
   p.c = q.c;
   p.c_ld = q.c_ld;
   p.c_es = q.c_es;
-  p.c_type = MOE_DTYPE_F16;
   p.alpha = q.alpha;
   p.beta = q.beta;
   p.alpha_e = q.alpha_e;
@@ -777,12 +860,23 @@ cudaError_t launch_batch(const TrainBatch& q, cudaStream_t s) {
   p.limit = q.limit;
   const int t = pair ? 256 : 128;
   const long long mt = (q.M + t - 1) / t, nt = (q.N + t - 1) / t;
-  const long long units = q.E * (q.sym ? mt * (mt + 1) / 2 : mt * nt);
-  if (pair)
-    return q.sym ? launch<2, 256, SYM, false, false>(p, units, s)
-                 : launch<2, 256, BATCH, false, true>(p, units, s);
-  return q.sym ? launch<1, 128, SYM, false, false>(p, units, s)
-               : launch<1, 128, BATCH, false, true>(p, units, s);
+  const bool half = q.form != TrainBatch::LEFT && q.form != TrainBatch::RIGHT;
+  const long long units = q.E * (half ? mt * (mt + 1) / 2 : mt * nt);
+  switch (q.form) {
+    case TrainBatch::GRAM_ROWS:
+      return pair ? launch<2, 256, SYM, KM, KM>(p, units, s) : launch<1, 128, SYM, KM, KM>(p, units, s);
+    case TrainBatch::GRAM_COLS:
+      return pair ? launch<2, 256, SYM, MN, MN>(p, units, s) : launch<1, 128, SYM, MN, MN>(p, units, s);
+    case TrainBatch::SQUARE:
+      return pair ? launch<2, 256, SYM, UPPER, UPPER>(p, units, s)
+                  : launch<1, 128, SYM, UPPER, UPPER>(p, units, s);
+    case TrainBatch::LEFT:
+      return pair ? launch<2, 256, BATCH, UPPER, MN>(p, units, s)
+                  : launch<1, 128, BATCH, UPPER, MN>(p, units, s);
+    default:
+      return pair ? launch<2, 256, BATCH, KM, UPPER>(p, units, s)
+                  : launch<1, 128, BATCH, KM, UPPER>(p, units, s);
+  }
 }
 
 }  // namespace moe

@@ -131,10 +131,33 @@ cudaError_t launch_rows(const void* gu, long long gu_ld, const void* d, long lon
 }
 
 // ------------------------------------------------ start of an orthogonalisation ---
-__device__ __forceinline__ float element(const void* p, long long i, int type) {
-  if (type == MOE_DTYPE_F32) return __ldg(static_cast<const float*>(p) + i);
-  if (type == MOE_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
+// Elements c .. c + 7 of a row of n (zeros behind its end); vec: rows start on 16-byte boundaries.
+__device__ __forceinline__ void eight(const void* row, int c, int n, int type, bool vec, float (&v)[8]) {
+  if (vec && c + 8 <= n) {
+    if (type == MOE_DTYPE_F32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + c);
+      const float4 a = __ldg(p), b = __ldg(p + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c));
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = type == MOE_DTYPE_BF16 ? two<MOE_DTYPE_BF16>(w[i]) : two<MOE_DTYPE_F16>(w[i]);
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = 0.0f;
+    if (c + i < n) {
+      if (type == MOE_DTYPE_F32) v[i] = __ldg(static_cast<const float*>(row) + c + i);
+      else if (type == MOE_DTYPE_BF16) v[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(row)[c + i]);
+      else v[i] = __half2float(static_cast<const __half*>(row)[c + i]);
+    }
+  }
 }
 
 struct Squares {  // of v, and of v scaled by 2^-64 and 2^64 for where those leave FP32's range
@@ -160,16 +183,23 @@ __device__ __forceinline__ float block_sum(float v, float* sh) {
 
 // parts [E][3][nb]: the sums of squares of nb groups of rows.
 __global__ void __launch_bounds__(256)
-    squares_kernel(const void* __restrict__ m, int type, long long ld, long long es, int rows,
-                   int cols, int per, float* __restrict__ parts) {
+    squares_kernel(const uint8_t* __restrict__ m, int type, bool vec, long long ld, long long es,
+                   int rows, int cols, int per, float* __restrict__ parts) {
   __shared__ float sh[8];
   pdl_wait();
   pdl_launch_dependents();
   const int e = blockIdx.y, nb = gridDim.x;
   const int r0 = blockIdx.x * per, r1 = min(rows, r0 + per);
   Squares q = {0.0f, 0.0f, 0.0f};
-  for (int r = r0; r < r1; ++r)
-    for (int c = threadIdx.x; c < cols; c += blockDim.x) q.add(element(m, e * es + r * ld + c, type));
+  const int n = (cols + 7) / 8, elt = type == MOE_DTYPE_F32 ? 4 : 2;
+#pragma unroll 2
+  for (int i = threadIdx.x; i < n * (r1 - r0); i += blockDim.x) {
+    const int r = i / n;
+    float v[8];
+    eight(m + (e * es + (r0 + r) * ld) * elt, 8 * (i - r * n), cols, type, vec, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q.add(v[j]);
+  }
   const float a = block_sum(q.mid, sh), b = block_sum(q.big, sh), c = block_sum(q.small, sh);
   if (threadIdx.x == 0) {
     float* o = parts + ((long long)e * 3) * nb + blockIdx.x;
@@ -179,18 +209,17 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// A 64 x 64 tile of x [E][M][ldx] (M x N, ldx = N padded to 8, the padding zero) = M 2^k in FP16.
+// x [E][rows][ldx] (ldx = cols padded to 8, the padding zero) = M 2^k in FP16, `per` rows a block.
 // 2^k brings the norm to [512, 1024): the elements of a BF16 matrix stay exact, and neither a
 // product of rows nor (with eps) 1 / norm comes near FP32's ends.
 __global__ void __launch_bounds__(256)
-    scale_kernel(const void* __restrict__ m, int type, long long ld, long long es, int M, int N,
-                 int turned, int ldx, float eps, const float* __restrict__ parts, int nb,
+    scale_kernel(const uint8_t* __restrict__ m, int type, bool vec, long long ld, long long es,
+                 int rows, int cols, int per, int ldx, float eps, const float* __restrict__ parts,
                  __half* __restrict__ x, float* __restrict__ f, int E) {
   __shared__ float sh[8];
-  __shared__ float tile[64][65];
   pdl_wait();
   pdl_launch_dependents();
-  const int e = blockIdx.z;
+  const int e = blockIdx.y, nb = gridDim.x;
   float s[3];
   for (int j = 0; j < 3; ++j) {
     float v = 0.0f;
@@ -208,30 +237,26 @@ __global__ void __launch_bounds__(256)
     frexpf(norm, &ex);  // norm = r 2^ex, r in [0.5, 1)
     k = 10 - ex;
   }
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
     const float total = norm + eps;
     float v = !finite ? __int_as_float(0x7FC00000) : total > 0.0f ? ldexpf(1.0f / total, -k) : 0.0f;
     f[e] = v;
     f[E + e] = v * v;
   }
   const float s1 = ldexpf(1.0f, k / 2), s2 = ldexpf(1.0f, k - k / 2);
-  const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;  // of x
-  // read along the source's rows
-  const int lane = threadIdx.x & 63, row = threadIdx.x >> 6;
-#pragma unroll 4
-  for (int t = row; t < 64; t += 4) {
-    const int i = turned ? i0 + lane : i0 + t, j = turned ? j0 + t : j0 + lane;
-    float v = 0.0f;
-    if (i < M && j < N) v = element(m, e * es + (turned ? j * ld + i : i * ld + j), type) * s1 * s2;
-    if (turned) tile[lane][t] = v;
-    else tile[t][lane] = v;
-  }
-  __syncthreads();
-  __half* o = x + (long long)e * M * ldx;
-#pragma unroll 4
-  for (int t = row; t < 64; t += 4) {
-    const int i = i0 + t, j = j0 + lane;
-    if (i < M && j < ldx) o[(long long)i * ldx + j] = __float2half_rn(tile[t][lane]);
+  const int r0 = blockIdx.x * per, r1 = min(rows, r0 + per);
+  const int n = ldx / 8, elt = type == MOE_DTYPE_F32 ? 4 : 2;
+  uint4* o = reinterpret_cast<uint4*>(x + ((long long)e * rows + r0) * ldx);
+#pragma unroll 2
+  for (int i = threadIdx.x; i < n * (r1 - r0); i += blockDim.x) {
+    const int r = i / n;
+    float v[8];
+    eight(m + (e * es + (r0 + r) * ld) * elt, 8 * (i - r * n), cols, type, vec, v);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = pack<MOE_DTYPE_F16>(v[2 * j] * s1 * s2, v[2 * j + 1] * s1 * s2);
+    o[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -257,14 +282,15 @@ cudaError_t launch_orth_start(const void* m, int type, long long ld_m, long long
   int per = (16384 + cols - 1) / cols;  // rows a block
   if ((rows + per - 1) / per > kNormParts) per = (rows + kNormParts - 1) / kNormParts;
   const int nb = (rows + per - 1) / per;
-  cudaError_t err = launch_pdl(squares_kernel, dim3(nb, E), dim3(256), 0, s, m, type, ld_m, es_m,
+  const int elt = type == MOE_DTYPE_F32 ? 4 : 2;
+  const bool vec = ld_m * elt % 16 == 0 && (E == 1 || es_m * elt % 16 == 0);
+  const uint8_t* src = static_cast<const uint8_t*>(m);
+  cudaError_t err = launch_pdl(squares_kernel, dim3(nb, E), dim3(256), 0, s, src, type, vec, ld_m, es_m,
                                rows, cols, per, parts);
   if (err != cudaSuccess) return err;
-  const bool turned = rows > cols;
-  const int M = turned ? cols : rows, N = turned ? rows : cols, ldx = (N + 7) / 8 * 8;
-  return launch_pdl(scale_kernel, dim3((ldx + 63) / 64, (M + 63) / 64, E), dim3(256), 0, s, m, type,
-                    ld_m, es_m, M, N, turned ? 1 : 0, ldx, eps, parts, nb, static_cast<__half*>(x),
-                    f, E);
+  const int ldx = (cols + 7) / 8 * 8;
+  return launch_pdl(scale_kernel, dim3(nb, E), dim3(256), 0, s, src, type, vec, ld_m, es_m, rows, cols, per,
+                    ldx, eps, static_cast<const float*>(parts), static_cast<__half*>(x), f, E);
 }
 
 }  // namespace moe
