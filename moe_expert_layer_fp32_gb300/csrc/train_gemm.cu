@@ -99,6 +99,16 @@ struct Tile {
   int boxes;                 // A boxes of the single product form
 };
 
+// (A role's thread is elected, not named: the compiler then knows that it is the only one, and
+// issues copies and MMAs without a loop over the active lanes.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ void tma_load_3d(const void* map, void* dst, uint32_t bar, int c0, int c1,
                                             int c2) {
   asm volatile(
@@ -474,9 +484,11 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
     ++it;
   };
 
+  bool loads = false;
   if (warp == 0 || second) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ----------------------------------------------------------- producers
+      loads = true;
       int s = 0;
       uint32_t ph = 1;
       while (advance()) {
@@ -492,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
         st_shared_remote(mapa_shared(smem_u32((const void*)(issued + 2 + second)), rank ^ 1), it);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       // ---------------------------------------------------------- MMA issuer
       const uint32_t idesc0 = p.formats | (1u << 4) | ((uint32_t)(BN >> 3) << 17) |
                               ((uint32_t)(TM >> 4) << 24);
@@ -652,7 +664,7 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
     // other's bytes now (its slot's last MMAs are complete, or the one could not have issued
     // it), so that its barrier completes; the even CTA waits for the bytes of both.
     const int most = max(max(issued[0], issued[1]), max(issued[2], issued[3]));
-    if ((warp == 0 || second) && lane == 0)
+    if (loads)
       while (it < most && advance()) load(it % C::STAGES);
     if (threadIdx.x == 0 && rank == 0)
       for (int i = (most > C::STAGES ? most - C::STAGES : 0); i < most; ++i)
