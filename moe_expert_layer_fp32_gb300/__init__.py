@@ -42,6 +42,7 @@ except ImportError as _e:
             return None
 
         route_select = route_select_backward = mx4_quantize = mx4_expert_product = _decline
+        grouped_product = grouped_weight_grad = swiglu = swiglu_backward = orthogonalize = _decline
 
 MOE_OK = 0
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_MISALIGNED",
@@ -1048,6 +1049,11 @@ def grouped_product(x, offsets, w, workspace, transposed=False, dtype=None, out=
     if stream is not None:
         with _on_stream(stream):
             return grouped_product(x, offsets, w, workspace, transposed, dtype, out)
+    if out is None and isinstance(x, torch.Tensor):
+        r = _calls.grouped_product(x, offsets, w, workspace, bool(transposed),
+                                   _DTYPES.get(x.dtype if dtype is None else dtype))
+        if r is not None:
+            return _made("moe_grouped_product", r)
     E = _offsets(offsets)
     x_ld = _rows16("x", x, None, (None, None))
     R, K = x.shape
@@ -1085,6 +1091,10 @@ def grouped_weight_grad(x, dy, offsets, workspace, dtype=torch.float32, out=None
     if stream is not None:
         with _on_stream(stream):
             return grouped_weight_grad(x, dy, offsets, workspace, dtype, out, accumulate)
+    if out is None and not accumulate:
+        r = _calls.grouped_weight_grad(x, dy, offsets, workspace, _DTYPES.get(dtype))
+        if r is not None:
+            return _made("moe_grouped_weight_grad", r)
     E = _offsets(offsets)
     x_ld = _rows16("x", x, None, (None, None))
     R, K = x.shape
@@ -1125,6 +1135,9 @@ def swiglu(gate_up, row_weights=None, stream=None):
     if stream is not None:
         with _on_stream(stream):
             return swiglu(gate_up, row_weights)
+    r = _calls.swiglu(gate_up, row_weights)
+    if r is not None:
+        return _made("moe_swiglu", r)
     ld, R, I = _gate_up_args(gate_up, row_weights)
     _on_device(gate_up, row_weights)
     h = torch.empty((R, I), dtype=gate_up.dtype, device=gate_up.device)
@@ -1138,6 +1151,9 @@ def swiglu_backward(gate_up, d_h, row_weights=None, stream=None):
     if stream is not None:
         with _on_stream(stream):
             return swiglu_backward(gate_up, d_h, row_weights)
+    r = _calls.swiglu_backward(gate_up, d_h, row_weights)
+    if r is not None:
+        return _made("moe_swiglu_bwd", r)
     ld, R, I = _gate_up_args(gate_up, row_weights)
     d_ld = _rows16("d_h", d_h, gate_up.dtype, (R, I))
     _on_device(gate_up, d_h, row_weights)
@@ -1224,6 +1240,10 @@ def orthogonalize(m, workspace, coefficients=(3.4445, -4.7750, 2.0315), steps=5,
     if stream is not None:
         with _on_stream(stream):
             return orthogonalize(m, workspace, coefficients, steps, eps, scale, dtype, out)
+    if out is None and len(coefficients) == 3:
+        r = _calls.orthogonalize(m, workspace, *coefficients, steps, eps, scale, _DTYPES.get(dtype))
+        if r is not None:
+            return _made("moe_orthogonalize", r)
     if not isinstance(m, torch.Tensor) or m.dim() != 3:
         raise ValueError("m: a tensor [E, rows, cols]")
     code = _dtype("m", m)

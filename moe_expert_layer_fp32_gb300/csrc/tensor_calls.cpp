@@ -1,5 +1,6 @@
-// The tensor calls' fast path: selection, its gradient, quantisation and the 4-bit product from
-// torch tensors, for small batches, where the host's part of a call is longer than the kernel's
+// The tensor calls' fast path: selection, its gradient, quantisation, the 4-bit product and the calls
+// that train the experts, from torch tensors, for small batches, where the host's part of a call is
+// longer than the kernel's
 // (GB300's host, route_select of one token: 13 us through the interpreter and ctypes, of which
 // the launch is 4).
 //
@@ -28,6 +29,13 @@ struct Library {
   decltype(&moe_mx4_quantize) mx4_quantize = nullptr;
   decltype(&moe_mx4_packed_bytes) mx4_packed_bytes = nullptr;
   decltype(&moe_mx4_expert_product) mx4_expert_product = nullptr;
+  decltype(&moe_grouped_product) grouped_product = nullptr;
+  decltype(&moe_grouped_weight_grad) grouped_weight_grad = nullptr;
+  decltype(&moe_grouped_workspace_bytes) grouped_workspace_bytes = nullptr;
+  decltype(&moe_swiglu) swiglu = nullptr;
+  decltype(&moe_swiglu_bwd) swiglu_bwd = nullptr;
+  decltype(&moe_orthogonalize) orthogonalize = nullptr;
+  decltype(&moe_orthogonalize_workspace_bytes) orthogonalize_workspace_bytes = nullptr;
 } lib;
 
 int dtype_of(const at::Tensor& t) {
@@ -214,6 +222,144 @@ PyObject* mx4_expert_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A moe_dtype as an int, and torch's type of it.
+bool type_of(PyObject* o, int& code, at::ScalarType& type) {
+  int64_t v;
+  if (!int_of(o, v) || v > MOE_DTYPE_F16) return false;
+  code = (int)v;
+  type = v == MOE_DTYPE_F32 ? at::kFloat : v == MOE_DTYPE_BF16 ? at::kBFloat16 : at::kHalf;
+  return true;
+}
+
+bool is16(int dtype) { return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F16; }
+
+bool tensor_of(PyObject* o, at::Tensor& t) { return o != Py_None && maybe(o, t); }
+
+// (x, offsets, w, workspace, transposed, type)
+PyObject* grouped_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  at::Tensor x, off, w, ws;
+  int dt, dev, yt;
+  at::ScalarType type;
+  if (n != 6 || !matrix(a[0], x, dt, dev) || !is16(dt) || !tensor_of(a[1], off) ||
+      !tensor_of(a[2], w) || !tensor_of(a[3], ws) || !type_of(a[5], yt, type))
+    Py_RETURN_NONE;
+  if (!plain(off, at::kInt, dev, {-1}) || off.size(0) < 2 || off.size(0) > 257 ||
+      !plain(w, x.scalar_type(), dev, {off.size(0) - 1, -1, -1}) || !plain(ws, at::kByte, dev, {-1}))
+    Py_RETURN_NONE;
+  const bool turned = a[4] == Py_True;
+  const int64_t E = off.size(0) - 1, R = x.size(0), K = x.size(1), N = w.size(turned ? 1 : 2);
+  if (w.size(turned ? 2 : 1) != K || N > INT32_MAX ||
+      lib.grouped_workspace_bytes((int32_t)E, (int32_t)K, (int32_t)N) == 0)
+    Py_RETURN_NONE;
+  at::Tensor y = make({R, N}, type, dev);
+  const int r = lib.grouped_product(x.data_ptr(), K, dt, (const int32_t*)off.data_ptr(), w.data_ptr(),
+                                    w.size(2), w.size(1) * w.size(2), turned, (int32_t)R, (int32_t)K,
+                                    (int32_t)N, (int32_t)E, y.data_ptr(), N, yt, ws.data_ptr(),
+                                    (size_t)ws.size(0), current_stream(dev));
+  if (r != MOE_OK) return PyLong_FromLong(r);
+  return THPVariable_Wrap(y);
+  END_HANDLE_TH_ERRORS
+}
+
+// (x, dy, offsets, workspace, type)
+PyObject* grouped_weight_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  at::Tensor x, dy, off, ws;
+  int dt, dev, wt;
+  at::ScalarType type;
+  if (n != 5 || !matrix(a[0], x, dt, dev) || !is16(dt) || !tensor_of(a[1], dy) ||
+      !tensor_of(a[2], off) || !tensor_of(a[3], ws) || !type_of(a[4], wt, type))
+    Py_RETURN_NONE;
+  if (!plain(dy, x.scalar_type(), dev, {x.size(0), -1}) || !plain(off, at::kInt, dev, {-1}) ||
+      off.size(0) < 2 || off.size(0) > 257 || !plain(ws, at::kByte, dev, {-1}))
+    Py_RETURN_NONE;
+  const int64_t E = off.size(0) - 1, R = x.size(0), K = x.size(1), N = dy.size(1);
+  if (N > INT32_MAX || lib.grouped_workspace_bytes((int32_t)E, (int32_t)K, (int32_t)N) == 0)
+    Py_RETURN_NONE;
+  at::Tensor d = make({E, K, N}, type, dev);
+  const int r = lib.grouped_weight_grad(x.data_ptr(), K, dy.data_ptr(), N, dt,
+                                        (const int32_t*)off.data_ptr(), (int32_t)R, (int32_t)K,
+                                        (int32_t)N, (int32_t)E, d.data_ptr(), N, K * N, wt, 0,
+                                        ws.data_ptr(), (size_t)ws.size(0), current_stream(dev));
+  if (r != MOE_OK) return PyLong_FromLong(r);
+  return THPVariable_Wrap(d);
+  END_HANDLE_TH_ERRORS
+}
+
+// (gate_up, row_weights)
+PyObject* swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  at::Tensor gu, w;
+  int dt, dev;
+  if (n != 2 || !matrix(a[0], gu, dt, dev) || !is16(dt) || gu.size(1) % 16 != 0 || !maybe(a[1], w) ||
+      (w.defined() && !plain(w, at::kFloat, dev, {gu.size(0)})))
+    Py_RETURN_NONE;
+  const int64_t R = gu.size(0), I = gu.size(1) / 2;
+  at::Tensor h = make({R, I}, gu.scalar_type(), dev);
+  const int r = lib.swiglu(gu.data_ptr(), 2 * I, (const float*)ptr(w), dt, (int32_t)R, (int32_t)I,
+                           h.data_ptr(), I, current_stream(dev));
+  if (r != MOE_OK) return PyLong_FromLong(r);
+  return THPVariable_Wrap(h);
+  END_HANDLE_TH_ERRORS
+}
+
+// (gate_up, d_h, row_weights)
+PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  at::Tensor gu, d, w;
+  int dt, dev;
+  if (n != 3 || !matrix(a[0], gu, dt, dev) || !is16(dt) || gu.size(1) % 16 != 0 ||
+      !tensor_of(a[1], d) || !maybe(a[2], w) ||
+      !plain(d, gu.scalar_type(), dev, {gu.size(0), gu.size(1) / 2}) ||
+      (w.defined() && !plain(w, at::kFloat, dev, {gu.size(0)})))
+    Py_RETURN_NONE;
+  const int64_t R = gu.size(0), I = gu.size(1) / 2;
+  at::Tensor dgu = make({R, 2 * I}, gu.scalar_type(), dev), h = make({R, I}, gu.scalar_type(), dev), dw;
+  if (w.defined()) dw = make({R}, at::kFloat, dev);
+  const int r = lib.swiglu_bwd(gu.data_ptr(), 2 * I, d.data_ptr(), I, (const float*)ptr(w), dt,
+                               (int32_t)R, (int32_t)I, dgu.data_ptr(), 2 * I, h.data_ptr(), I,
+                               (float*)ptr(dw), current_stream(dev));
+  if (r != MOE_OK) return PyLong_FromLong(r);
+  return dw.defined() ? pack({dgu, h, dw}) : pack({dgu, h});
+  END_HANDLE_TH_ERRORS
+}
+
+// (m, workspace, a, b, c, steps, eps, scale, type)
+PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  at::Tensor m, ws;
+  int ot;
+  int64_t steps;
+  at::ScalarType type;
+  if (n != 9 || !tensor_of(a[0], m) || !tensor_of(a[1], ws) || !int_of(a[5], steps) ||
+      !type_of(a[8], ot, type) || !is16(ot))
+    Py_RETURN_NONE;
+  double v[5];
+  for (int i = 0; i < 5; ++i) {
+    PyObject* o = a[i < 3 ? 2 + i : 3 + i];
+    if (!PyFloat_Check(o)) Py_RETURN_NONE;
+    v[i] = PyFloat_AS_DOUBLE(o);
+  }
+  const int dt = dtype_of(m), dev = m.is_cuda() ? (int)m.get_device() : -1;
+  if (dt < 0 || dev != (int)c10::cuda::current_device() || m.dim() != 3 || !m.is_contiguous() ||
+      !plain(ws, at::kByte, dev, {-1}))
+    Py_RETURN_NONE;
+  const int64_t E = m.size(0), rows = m.size(1), cols = m.size(2);
+  if (E > 256 || rows > 16384 || cols > 16384 ||
+      lib.orthogonalize_workspace_bytes((int32_t)E, (int32_t)rows, (int32_t)cols) == 0)
+    Py_RETURN_NONE;
+  at::Tensor out = make({E, rows, cols}, type, dev);
+  const float co[3] = {(float)v[0], (float)v[1], (float)v[2]};
+  const int r = lib.orthogonalize(m.data_ptr(), dt, cols, rows * cols, (int32_t)E, (int32_t)rows,
+                                  (int32_t)cols, co, (int32_t)steps, (float)v[3], (float)v[4],
+                                  out.data_ptr(), ot, cols, rows * cols, ws.data_ptr(),
+                                  (size_t)ws.size(0), current_stream(dev));
+  if (r != MOE_OK) return PyLong_FromLong(r);
+  return THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
 // (path of the library): the package has it loaded
 PyObject* bind(PyObject*, PyObject* path) {
   const char* p = PyUnicode_AsUTF8(path);
@@ -230,6 +376,13 @@ PyObject* bind(PyObject*, PyObject* path) {
   get(lib.mx4_quantize, "moe_mx4_quantize");
   get(lib.mx4_packed_bytes, "moe_mx4_packed_bytes");
   get(lib.mx4_expert_product, "moe_mx4_expert_product");
+  get(lib.grouped_product, "moe_grouped_product");
+  get(lib.grouped_weight_grad, "moe_grouped_weight_grad");
+  get(lib.grouped_workspace_bytes, "moe_grouped_workspace_bytes");
+  get(lib.swiglu, "moe_swiglu");
+  get(lib.swiglu_bwd, "moe_swiglu_bwd");
+  get(lib.orthogonalize, "moe_orthogonalize");
+  get(lib.orthogonalize_workspace_bytes, "moe_orthogonalize_workspace_bytes");
   if (!ok) {
     PyErr_Format(PyExc_ImportError, "%s: %s", p, dlerror());
     return nullptr;
@@ -242,6 +395,11 @@ PyMethodDef methods[] = {FAST(route_select),
                          FAST(route_select_backward),
                          FAST(mx4_quantize),
                          FAST(mx4_expert_product),
+                         FAST(grouped_product),
+                         FAST(grouped_weight_grad),
+                         FAST(swiglu),
+                         FAST(swiglu_backward),
+                         FAST(orthogonalize),
                          {"bind", bind, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_calls", nullptr, -1, methods};

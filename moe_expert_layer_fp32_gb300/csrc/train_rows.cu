@@ -131,32 +131,52 @@ cudaError_t launch_rows(const void* gu, long long gu_ld, const void* d, long lon
 }
 
 // ------------------------------------------------ start of an orthogonalisation ---
-// Elements c .. c + 7 of a row of n (zeros behind its end); vec: rows start on 16-byte boundaries.
-__device__ __forceinline__ void eight(const void* row, int c, int n, int type, bool vec, float (&v)[8]) {
-  if (vec && c + 8 <= n) {
-    if (type == MOE_DTYPE_F32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + c);
-      const float4 a = __ldg(p), b = __ldg(p + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c));
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// Elements c .. c + 7 of a row of n (zeros behind its end); VEC: whole 16-byte pieces.
+template <int TYPE, bool VEC>
+__device__ __forceinline__ void eight(const uint8_t* row, int c, int n, float (&v)[8]) {
+  if constexpr (VEC && TYPE == MOE_DTYPE_F32) {
+    const float4* p = reinterpret_cast<const float4*>(row + 4 * c);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else if constexpr (VEC) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + 2 * c));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = type == MOE_DTYPE_BF16 ? two<MOE_DTYPE_BF16>(w[i]) : two<MOE_DTYPE_F16>(w[i]);
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = two<TYPE>(w[i]);
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = 0.0f;
+      if (c + i < n) {
+        if constexpr (TYPE == MOE_DTYPE_F32) v[i] = __ldg(reinterpret_cast<const float*>(row) + c + i);
+        else if constexpr (TYPE == MOE_DTYPE_BF16)
+          v[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[c + i]);
+        else v[i] = __half2float(reinterpret_cast<const __half*>(row)[c + i]);
       }
     }
-    return;
   }
+}
+
+// f(piece, its elements) for the 8-element pieces of `rows` rows of n pieces, AHEAD of a thread's
+// loaded before the first is used.
+constexpr int AHEAD = 4;
+template <int TYPE, bool VEC, typename F>
+__device__ __forceinline__ void pieces(const uint8_t* m, long long row_bytes, int rows, int n, int cols,
+                                       F f) {
+  const int total = rows * n;
+  for (int i0 = threadIdx.x; i0 < total; i0 += AHEAD * blockDim.x) {
+    float v[AHEAD][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = 0.0f;
-    if (c + i < n) {
-      if (type == MOE_DTYPE_F32) v[i] = __ldg(static_cast<const float*>(row) + c + i);
-      else if (type == MOE_DTYPE_BF16) v[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(row)[c + i]);
-      else v[i] = __half2float(static_cast<const __half*>(row)[c + i]);
+    for (int j = 0; j < AHEAD; ++j) {
+      const int i = i0 + j * blockDim.x, r = i / n;
+      if (i < total) eight<TYPE, VEC>(m + r * row_bytes, 8 * (i - r * n), cols, v[j]);
     }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (i0 + j * blockDim.x < total) f(i0 + j * blockDim.x, v[j]);
   }
 }
 
@@ -182,24 +202,22 @@ __device__ __forceinline__ float block_sum(float v, float* sh) {
 }
 
 // parts [E][3][nb]: the sums of squares of nb groups of rows.
+template <int TYPE, bool VEC>
 __global__ void __launch_bounds__(256)
-    squares_kernel(const uint8_t* __restrict__ m, int type, bool vec, long long ld, long long es,
-                   int rows, int cols, int per, float* __restrict__ parts) {
+    squares_kernel(const uint8_t* __restrict__ m, long long ld, long long es, int rows, int cols,
+                   int per, float* __restrict__ parts) {
   __shared__ float sh[8];
   pdl_wait();
   pdl_launch_dependents();
   const int e = blockIdx.y, nb = gridDim.x;
   const int r0 = blockIdx.x * per, r1 = min(rows, r0 + per);
   Squares q = {0.0f, 0.0f, 0.0f};
-  const int n = (cols + 7) / 8, elt = type == MOE_DTYPE_F32 ? 4 : 2;
-#pragma unroll 2
-  for (int i = threadIdx.x; i < n * (r1 - r0); i += blockDim.x) {
-    const int r = i / n;
-    float v[8];
-    eight(m + (e * es + (r0 + r) * ld) * elt, 8 * (i - r * n), cols, type, vec, v);
+  constexpr int ELT = TYPE == MOE_DTYPE_F32 ? 4 : 2;
+  pieces<TYPE, VEC>(m + (e * es + r0 * ld) * ELT, ld * ELT, r1 - r0, (cols + 7) / 8, cols,
+                    [&](int, const float(&v)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q.add(v[j]);
-  }
+                      for (int j = 0; j < 8; ++j) q.add(v[j]);
+                    });
   const float a = block_sum(q.mid, sh), b = block_sum(q.big, sh), c = block_sum(q.small, sh);
   if (threadIdx.x == 0) {
     float* o = parts + ((long long)e * 3) * nb + blockIdx.x;
@@ -212,9 +230,10 @@ __global__ void __launch_bounds__(256)
 // x [E][rows][ldx] (ldx = cols padded to 8, the padding zero) = M 2^k in FP16, `per` rows a block.
 // 2^k brings the norm to [512, 1024): the elements of a BF16 matrix stay exact, and neither a
 // product of rows nor (with eps) 1 / norm comes near FP32's ends.
+template <int TYPE, bool VEC>
 __global__ void __launch_bounds__(256)
-    scale_kernel(const uint8_t* __restrict__ m, int type, bool vec, long long ld, long long es,
-                 int rows, int cols, int per, int ldx, float eps, const float* __restrict__ parts,
+    scale_kernel(const uint8_t* __restrict__ m, long long ld, long long es, int rows, int cols,
+                 int per, int ldx, float eps, const float* __restrict__ parts,
                  __half* __restrict__ x, float* __restrict__ f, int E) {
   __shared__ float sh[8];
   pdl_wait();
@@ -245,19 +264,29 @@ __global__ void __launch_bounds__(256)
   }
   const float s1 = ldexpf(1.0f, k / 2), s2 = ldexpf(1.0f, k - k / 2);
   const int r0 = blockIdx.x * per, r1 = min(rows, r0 + per);
-  const int n = ldx / 8, elt = type == MOE_DTYPE_F32 ? 4 : 2;
+  constexpr int ELT = TYPE == MOE_DTYPE_F32 ? 4 : 2;
   uint4* o = reinterpret_cast<uint4*>(x + ((long long)e * rows + r0) * ldx);
-#pragma unroll 2
-  for (int i = threadIdx.x; i < n * (r1 - r0); i += blockDim.x) {
-    const int r = i / n;
-    float v[8];
-    eight(m + (e * es + (r0 + r) * ld) * elt, 8 * (i - r * n), cols, type, vec, v);
-    uint32_t w[4];
+  pieces<TYPE, VEC>(m + (e * es + r0 * ld) * ELT, ld * ELT, r1 - r0, ldx / 8, cols,
+                    [&](int i, const float(&v)[8]) {
+                      uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = pack<MOE_DTYPE_F16>(v[2 * j] * s1 * s2, v[2 * j + 1] * s1 * s2);
-    o[i] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+                      for (int j = 0; j < 4; ++j)
+                        w[j] = pack<MOE_DTYPE_F16>(v[2 * j] * s1 * s2, v[2 * j + 1] * s1 * s2);
+                      o[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    });
+}
+
+template <int TYPE, bool VEC>
+cudaError_t start(const uint8_t* m, long long ld, long long es, int E, int rows, int cols, float eps,
+                  float* parts, __half* x, float* f, cudaStream_t s) {
+  int per = (16384 + cols - 1) / cols;  // rows a block
+  if ((rows + per - 1) / per > kNormParts) per = (rows + kNormParts - 1) / kNormParts;
+  const dim3 grid((rows + per - 1) / per, E);
+  cudaError_t err = launch_pdl(squares_kernel<TYPE, VEC>, grid, dim3(256), 0, s, m, ld, es, rows, cols,
+                               per, parts);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(scale_kernel<TYPE, VEC>, grid, dim3(256), 0, s, m, ld, es, rows, cols, per,
+                    (cols + 7) / 8 * 8, eps, static_cast<const float*>(parts), x, f, E);
 }
 
 }  // namespace
@@ -279,18 +308,17 @@ cudaError_t launch_swiglu_bwd(const void* gate_up, long long gu_ld, const void* 
 cudaError_t launch_orth_start(const void* m, int type, long long ld_m, long long es_m, int E,
                               int rows, int cols, float eps, float* parts, void* x, float* f,
                               cudaStream_t s) {
-  int per = (16384 + cols - 1) / cols;  // rows a block
-  if ((rows + per - 1) / per > kNormParts) per = (rows + kNormParts - 1) / kNormParts;
-  const int nb = (rows + per - 1) / per;
-  const int elt = type == MOE_DTYPE_F32 ? 4 : 2;
-  const bool vec = ld_m * elt % 16 == 0 && (E == 1 || es_m * elt % 16 == 0);
   const uint8_t* src = static_cast<const uint8_t*>(m);
-  cudaError_t err = launch_pdl(squares_kernel, dim3(nb, E), dim3(256), 0, s, src, type, vec, ld_m, es_m,
-                               rows, cols, per, parts);
-  if (err != cudaSuccess) return err;
-  const int ldx = (cols + 7) / 8 * 8;
-  return launch_pdl(scale_kernel, dim3(nb, E), dim3(256), 0, s, src, type, vec, ld_m, es_m, rows, cols, per,
-                    ldx, eps, static_cast<const float*>(parts), static_cast<__half*>(x), f, E);
+  __half* o = static_cast<__half*>(x);
+  const int elt = type == MOE_DTYPE_F32 ? 4 : 2;
+  const bool vec = cols % 8 == 0 && ld_m * elt % 16 == 0 && (E == 1 || es_m * elt % 16 == 0);
+#define MOE_START(T)                                                                          \
+  return vec ? start<T, true>(src, ld_m, es_m, E, rows, cols, eps, parts, o, f, s)            \
+             : start<T, false>(src, ld_m, es_m, E, rows, cols, eps, parts, o, f, s)
+  if (type == MOE_DTYPE_F32) MOE_START(MOE_DTYPE_F32);
+  if (type == MOE_DTYPE_BF16) MOE_START(MOE_DTYPE_BF16);
+  MOE_START(MOE_DTYPE_F16);
+#undef MOE_START
 }
 
 }  // namespace moe
