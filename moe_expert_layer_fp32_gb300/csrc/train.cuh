@@ -10,6 +10,21 @@
 
 namespace moe {
 
+// n / d for n < 2^31 by a multiplication: m = 2^32 (2^s - d) / d + 1, s = ceil(log2 d).
+struct Div {
+  uint32_t m;
+  int s, d;
+};
+inline Div make_div(int d) {
+  Div v = {0, 0, d};
+  while ((1LL << v.s) < d) ++v.s;
+  v.m = (uint32_t)(((1ULL << 32) * ((1ULL << v.s) - d)) / d + 1);
+  return v;
+}
+__device__ __forceinline__ int operator/(int n, const Div& v) {
+  return (int)((__umulhi((uint32_t)n, v.m) + (uint32_t)n) >> v.s);
+}
+
 // A map of 16-bit elements [d2][d1][d0], rows ld and slices es elements apart, boxes of
 // 64 x box1 x 1 with 128-byte swizzle, zeros outside (moe_api.cu).
 bool encode_16bit_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2,
@@ -59,10 +74,12 @@ cudaError_t launch_wgrad(const TrainWgrad& q, cudaStream_t s);
 //   LEFT       out = A B            ~A [M, M], B [M, N]
 //   RIGHT      out = A B            A [M, N], ~B [N, N]
 // padded: out is a padded buffer too; else (LEFT, RIGHT) rows of any length.
+// c_lo, out_lo (null: without): what the rounding of c and of a padded out left, times 2048, in
+// FP16 and the same layouts; c then counts with both.
 struct TrainBatch {
   enum Form { GRAM_ROWS, GRAM_COLS, SQUARE, LEFT, RIGHT } form;
-  const void *a, *b, *c;
-  void* out;
+  const void *a, *b, *c, *c_lo;
+  void *out, *out_lo;
   int E, M, N, K, out_type;
   bool pair, padded;
   long long a_ld, a_es, b_ld, b_es, c_ld, c_es, ld, es;
@@ -82,10 +99,19 @@ cudaError_t launch_swiglu_bwd(const void* gate_up, long long gu_ld, const void* 
                               long long dgu_ld, void* h, long long h_ld, float* d_w,
                               cudaStream_t s);
 
-// First step of an orthogonalisation: x [E][rows][ld] FP16 (ld = cols padded to 8) = M 2^k, f[e] = 2^-k / (|M| + eps), f[E + e] = f[e]^2.
+// First step of an orthogonalisation: x [E][rows][ld] FP16 (ld = cols padded to 8) = M 2^k, x_lo what its rounding left, times 2048 (null: without),
+// f[e] = 2^-k / (|M| + eps), f[E + e] = f[e]^2.
 constexpr int kNormParts = 512;  // at most, partial sums of squares an expert
 cudaError_t launch_orth_start(const void* m, int type, long long ld_m, long long es_m, int E,
-                              int rows, int cols, float eps, float* parts, void* x, float* f,
+                              int rows, int cols, float eps, float* parts, void* x, void* x_lo, float* f,
                               cudaStream_t s);
+
+// The whole orthogonalisation in one kernel, a CTA a matrix (train_orth.cu): at most 128 x 256 or
+// 256 x 128.  coefficients: host.
+bool orth_small(int rows, int cols);
+cudaError_t launch_orth_small(const void* m, int type, long long ld, long long es, int E, int rows,
+                              int cols, const float* coefficients, int steps, float eps, float scale,
+                              void* out, int out_type, long long out_ld, long long out_es,
+                              int32_t* status, long long limit, cudaStream_t s);
 
 }  // namespace moe

@@ -56,24 +56,10 @@ struct Shape {
       STAGES * STAGE_BYTES + EPI_BYTES + NBAR * 8 + 48 + 2 * (kMaxE + 1) * 4;
 };
 
-// n / d for n < 2^31 by a multiplication: m = 2^32 (2^s - d) / d + 1, s = ceil(log2 d).
-struct Div {
-  uint32_t m;
-  int s, d;
-};
-Div make_div(int d) {
-  Div v = {0, 0, d};
-  while ((1LL << v.s) < d) ++v.s;
-  v.m = (uint32_t)(((1ULL << 32) * ((1ULL << v.s) - d)) / d + 1);
-  return v;
-}
-__device__ __forceinline__ int operator/(int n, const Div& v) {
-  return (int)((__umulhi((uint32_t)n, v.m) + (uint32_t)n) >> v.s);
-}
-
 struct Args {
   CUtensorMap a, b;
   CUtensorMap o;       // the output, boxes of 128 bytes x 32 rows, if tma
+  CUtensorMap o_lo;    // BATCH: what the output's rounding left, times 2048, if has_lo
   CUtensorMap at, bt;  // UPPER: the same matrix in MN-major boxes; WGRAD: the experts' tails
   const int32_t* offsets;
   int E, R, M, N, K;
@@ -81,8 +67,10 @@ struct Args {
   void* out;
   long long ld, es;
   int out_type, tma;  // (else: rows that start anywhere)
+  int has_lo;
   int n_lim;          // columns that may be stored
   const void* c;      // BATCH, SYM: FP16 rows in 16-byte pieces; WGRAD: the FP32 output
+  const void* c_lo;   // what c's rounding left, times 2048, or null
   long long c_ld, c_es;
   float alpha, beta;
   const float *alpha_e, *beta_e;  // per expert, or null
@@ -175,10 +163,12 @@ __device__ __forceinline__ uint4* piece(uint4* st, int r, int c) { return st + 8
 // registers, four whole spans an instruction.  out and c point to the rows' first element at
 // the tile's first column.
 template <int TYPE, bool ADD16, bool ADD32>
-__device__ __forceinline__ void store_tile(uint32_t taddr, bool sums, uint4* st, int lane, int first,
+__device__ __forceinline__ void store_tile(uint32_t taddr, uint4* st, int lane, int first,
                                            const CUtensorMap* map, int col0, int row0, int e,
                                            void* out, long long ld, bool vec, int nrows, int ncols,
-                                           const void* c, long long c_ld, float alpha, float beta) {
+                                           const void* c, long long c_ld, float alpha, float beta,
+                                           const CUtensorMap* map_lo = nullptr,
+                                           const void* c_lo = nullptr) {
   constexpr int COLS = TYPE == MOE_DTYPE_F32 ? 32 : 64, PER = COLS / 8;  // of a span, of a piece
   constexpr int BYTES = 128 / COLS;
 #pragma unroll 1
@@ -186,60 +176,70 @@ __device__ __forceinline__ void store_tile(uint32_t taddr, bool sums, uint4* st,
     const int cp = lane & 7, r4 = lane >> 3;  // this lane's piece and row (of four) in memory order
     const bool in = c0 + cp * PER < ncols;
     uint4 add[8];
-    if constexpr (ADD16 || ADD32) {
-      const uint8_t* src = static_cast<const uint8_t*>(c) + (size_t)(c0 + cp * PER) * BYTES;
+    auto fetch = [&](const void* from) {
+      const uint8_t* src = static_cast<const uint8_t*>(from) + (size_t)(c0 + cp * PER) * BYTES;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = 4 * i + r4;
         add[i] = in && r < nrows ? *reinterpret_cast<const uint4*>(src + r * c_ld * BYTES)
                                  : make_uint4(0, 0, 0, 0);
       }
-    }
-    uint32_t w[32];
+    };
+    uint32_t w[32], v[TYPE == MOE_DTYPE_F32 ? 1 : 64];
     if constexpr (TYPE == MOE_DTYPE_F32) {
-      if (sums) {
-        tmem_ld_32x32b_x32(taddr + c0, w);
-        tmem_ld_wait();
-      }
+      tmem_ld_32x32b_x32(taddr + c0, w);
+      tmem_ld_wait();
     } else {
-      if constexpr (ADD16) {
-        if (lane == 0) tma_stores_read();
-        __syncwarp();
+      // v = a v + b add: what was fetched in memory order reaches this lane's row through st
+      auto stage = [&]() {
 #pragma unroll
         for (int i = 0; i < 8; ++i) *piece(st, 4 * i + r4, cp) = add[i];
         __syncwarp();
-      }
-      uint32_t v[64];
-      if (sums) {
-        tmem_ld_32x32b_x32(taddr + c0, *reinterpret_cast<uint32_t(*)[32]>(v));
-        tmem_ld_32x32b_x32(taddr + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-        tmem_ld_wait();
-      }
+      };
+      auto added = [&](float a, float b) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        uint32_t a[4];
-        if constexpr (ADD16) {
+        for (int q = 0; q < 8; ++q) {
           const uint4 x = *piece(st, lane, q);
-          a[0] = x.x, a[1] = x.y, a[2] = x.z, a[3] = x.w;
-        }
+          const uint32_t h[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float lo = __uint_as_float(v[8 * q + 2 * j]), hi = __uint_as_float(v[8 * q + 2 * j + 1]);
-          if constexpr (ADD16) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a[j]));
-            lo = fmaf(alpha, lo, beta * f.x);
-            hi = fmaf(alpha, hi, beta * f.y);
-          } else {
-            lo *= alpha;
-            hi *= alpha;
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+            uint32_t *lo = &v[8 * q + 2 * j], *hi = lo + 1;
+            *lo = __float_as_uint(fmaf(a, __uint_as_float(*lo), b * f.x));
+            *hi = __float_as_uint(fmaf(a, __uint_as_float(*hi), b * f.y));
           }
-          w[4 * q + j] = pack16<TYPE>(lo, hi);
+        }
+      };
+      if constexpr (ADD16) {
+        if (c_lo != nullptr) fetch(c_lo);
+        else fetch(c);
+        if (lane == 0) tma_stores_read();
+        __syncwarp();
+        stage();
+      }
+      tmem_ld_32x32b_x32(taddr + c0, *reinterpret_cast<uint32_t(*)[32]>(v));
+      tmem_ld_32x32b_x32(taddr + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+      tmem_ld_wait();
+      if constexpr (ADD16) {
+        if (c_lo != nullptr) {
+          added(alpha, beta * (1.0f / 2048.0f));
+          fetch(c);
+          __syncwarp();
+          stage();
+          added(1.0f, beta);
+        } else {
+          added(alpha, beta);
         }
       }
-    }
-    if (!sums) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = 0;
+      for (int j = 0; j < 32; ++j) {
+        float lo = __uint_as_float(v[2 * j]), hi = __uint_as_float(v[2 * j + 1]);
+        if constexpr (!ADD16) {
+          lo *= alpha;
+          hi *= alpha;
+        }
+        w[j] = pack16<TYPE>(lo, hi);
+      }
     }
     if constexpr (!ADD16) {
       if (lane == 0) tma_stores_read();
@@ -252,6 +252,26 @@ __device__ __forceinline__ void store_tile(uint32_t taddr, bool sums, uint4* st,
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) tma_store_3d(map, st, col0 + c0, row0, e);
+      if constexpr (TYPE == MOE_DTYPE_F16 && ADD16) {
+        if (map_lo != nullptr) {
+          if (lane == 0) tma_stores_read();
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint32_t l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[4 * q + j]));
+              l[j] = pack16<TYPE>((__uint_as_float(v[8 * q + 2 * j]) - f.x) * 2048.0f,
+                                  (__uint_as_float(v[8 * q + 2 * j + 1]) - f.y) * 2048.0f);
+            }
+            *piece(st, lane, q) = make_uint4(l[0], l[1], l[2], l[3]);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) tma_store_3d(map_lo, st, col0 + c0, row0, e);
+        }
+      }
       continue;
     }
     __syncwarp();
@@ -262,10 +282,13 @@ __device__ __forceinline__ void store_tile(uint32_t taddr, bool sums, uint4* st,
         const int r = 4 * i + r4;
         uint4 x = *piece(st, r, cp);
         if constexpr (ADD32) {
-          float* p = reinterpret_cast<float*>(&x);
-          const float* y = reinterpret_cast<const float*>(&add[i]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) p[j] += y[j];
+          if (in && r < nrows) {
+            const float4 y = *reinterpret_cast<const float4*>(dst + r * ld * BYTES);
+            x.x = __float_as_uint(__uint_as_float(x.x) + y.x);
+            x.y = __float_as_uint(__uint_as_float(x.y) + y.y);
+            x.z = __float_as_uint(__uint_as_float(x.z) + y.z);
+            x.w = __float_as_uint(__uint_as_float(x.w) + y.w);
+          }
         }
         if (in && r < nrows) *reinterpret_cast<uint4*>(dst + r * ld * BYTES) = x;
       }
@@ -281,6 +304,19 @@ __device__ __forceinline__ void store_tile(uint32_t taddr, bool sums, uint4* st,
     }
     __syncwarp();
   }
+}
+
+// The same for an expert without rows: zeros.
+__device__ __forceinline__ void zero_tile(uint4* st, int lane, int first, int cols, const CUtensorMap* map,
+                                          int col0, int row0, int e, int ncols) {
+  if (lane == 0) tma_stores_read();
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 8; ++q) *piece(st, lane, q) = make_uint4(0, 0, 0, 0);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0)
+    for (int c0 = first * cols; c0 < ncols; c0 += 2 * cols) tma_store_3d(map, st, col0 + c0, row0, e);
 }
 
 template <int CTAS, int BN, Kind KIND, Major A, Major B>
@@ -600,37 +636,44 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
           const CUtensorMap* map = p.tma ? &p.o : nullptr;
           const float alpha = p.alpha * (p.alpha_e ? __ldg(p.alpha_e + t.e) : 1.0f);
           const float beta = p.beta * (p.beta_e ? __ldg(p.beta_e + t.e) : 1.0f);
-          const __half* c = static_cast<const __half*>(p.c) + t.e * p.c_es + row0 * p.c_ld + t.col0;
-          if (p.out_type == MOE_DTYPE_BF16)  // (the last step's result)
-            store_tile<MOE_DTYPE_BF16, true, false>(taddr, true, st, lane, first, map, t.col0, row0,
+          const long long c_at = t.e * p.c_es + row0 * p.c_ld + t.col0;
+          const __half* c = static_cast<const __half*>(p.c) + c_at;
+          const __half* c_lo = p.c_lo ? static_cast<const __half*>(p.c_lo) + c_at : nullptr;
+          if (KIND == BATCH && p.out_type == MOE_DTYPE_BF16)  // (the last step's result)
+            store_tile<MOE_DTYPE_BF16, true, false>(taddr, st, lane, first, map, t.col0, row0,
                                                     oe, out, p.ld, false, nrows, ncols, c, p.c_ld,
-                                                    alpha, beta);
+                                                    alpha, beta, nullptr,
+                                                    KIND == BATCH ? c_lo : nullptr);
           else if (p.c != nullptr)
-            store_tile<MOE_DTYPE_F16, true, false>(taddr, true, st, lane, first, map, t.col0, row0, oe,
+            store_tile<MOE_DTYPE_F16, true, false>(taddr, st, lane, first, map, t.col0, row0, oe,
                                                    out, p.ld, false, nrows, ncols, c, p.c_ld, alpha,
-                                                   beta);
+                                                   beta, KIND == BATCH && p.has_lo ? &p.o_lo : nullptr,
+                                                   KIND == BATCH ? c_lo : nullptr);
           else
-            store_tile<MOE_DTYPE_F16, false, false>(taddr, true, st, lane, first, map, t.col0, row0,
+            store_tile<MOE_DTYPE_F16, false, false>(taddr, st, lane, first, map, t.col0, row0,
                                                     oe, out, p.ld, false, nrows, ncols, nullptr, 0,
                                                     alpha, 0.0f);
         } else {
           // (a product's rows behind the expert's last belong to the next one)
           const CUtensorMap* map = KIND == WGRAD || nrows == 32 ? &p.o : nullptr;
-          if (p.out_type == MOE_DTYPE_F32) {
+          if (!sums) {
+            zero_tile(st, lane, first, p.out_type == MOE_DTYPE_F32 ? 32 : 64, map, t.col0, row0, oe,
+                      ncols);
+          } else if (p.out_type == MOE_DTYPE_F32) {
             if (KIND == WGRAD && p.c != nullptr)
-              store_tile<MOE_DTYPE_F32, false, true>(taddr, sums, st, lane, first, nullptr, 0, 0, 0,
-                                                     out, p.ld, true, nrows, ncols, out, p.ld, 1.0f,
+              store_tile<MOE_DTYPE_F32, false, true>(taddr, st, lane, first, nullptr, 0, 0, 0,
+                                                     out, p.ld, true, nrows, ncols, nullptr, 0, 1.0f,
                                                      1.0f);
             else
-              store_tile<MOE_DTYPE_F32, false, false>(taddr, sums, st, lane, first, map, t.col0, row0,
+              store_tile<MOE_DTYPE_F32, false, false>(taddr, st, lane, first, map, t.col0, row0,
                                                       oe, out, p.ld, true, nrows, ncols, nullptr, 0,
                                                       1.0f, 0.0f);
           } else if (p.out_type == MOE_DTYPE_BF16) {
-            store_tile<MOE_DTYPE_BF16, false, false>(taddr, sums, st, lane, first, map, t.col0, row0,
+            store_tile<MOE_DTYPE_BF16, false, false>(taddr, st, lane, first, map, t.col0, row0,
                                                      oe, out, p.ld, true, nrows, ncols, nullptr, 0,
                                                      1.0f, 0.0f);
           } else {
-            store_tile<MOE_DTYPE_F16, false, false>(taddr, sums, st, lane, first, map, t.col0, row0,
+            store_tile<MOE_DTYPE_F16, false, false>(taddr, st, lane, first, map, t.col0, row0,
                                                     oe, out, p.ld, true, nrows, ncols, nullptr, 0,
                                                     1.0f, 0.0f);
           }
@@ -860,6 +903,12 @@ cudaError_t launch_batch(const TrainBatch& q, cudaStream_t s) {
   p.tma = q.padded || (q.N % 8 == 0 && q.ld % 8 == 0 && (q.E == 1 || q.es % q.ld == 0));
   if (p.tma && !encode_out(&p.o, q.out, q.out_type, p.n_lim, q.M, q.E, q.ld, q.es))
     return cudaErrorInvalidValue;
+  if (q.out_lo != nullptr) {
+    p.has_lo = 1;
+    if (!encode_out(&p.o_lo, q.out_lo, q.out_type, p.n_lim, q.M, q.E, q.ld, q.es))
+      return cudaErrorInvalidValue;
+  }
+  p.c_lo = q.c_lo;
   p.c = q.c;
   p.c_ld = q.c_ld;
   p.c_es = q.c_es;

@@ -131,62 +131,94 @@ cudaError_t launch_rows(const void* gu, long long gu_ld, const void* d, long lon
 }
 
 // ------------------------------------------------ start of an orthogonalisation ---
-// Elements c .. c + 7 of a row of n (zeros behind its end); VEC: whole 16-byte pieces.
+// Eight elements of a row as they lie in memory, and as FP32; VEC: whole 16-byte pieces, else element
+// by element with zeros behind the row's end.
 template <int TYPE, bool VEC>
-__device__ __forceinline__ void eight(const uint8_t* row, int c, int n, float (&v)[8]) {
-  if constexpr (VEC && TYPE == MOE_DTYPE_F32) {
-    const float4* p = reinterpret_cast<const float4*>(row + 4 * c);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else if constexpr (VEC) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + 2 * c));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Eight {
+  static constexpr int ELT = TYPE == MOE_DTYPE_F32 ? 4 : 2;
+  uint4 w[VEC ? ELT / 2 : 1];
+  float f[VEC ? 1 : 8];
+  __device__ __forceinline__ void load(const uint8_t* row, int c, int n) {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = two<TYPE>(w[i]);
-      v[2 * i] = f.x, v[2 * i + 1] = f.y;
-    }
-  } else {
+      for (int i = 0; i < ELT / 2; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(row + ELT * c) + i);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = 0.0f;
-      if (c + i < n) {
-        if constexpr (TYPE == MOE_DTYPE_F32) v[i] = __ldg(reinterpret_cast<const float*>(row) + c + i);
+      for (int i = 0; i < 8; ++i) {
+        const int j = min(c + i, n - 1);
+        float v;
+        if constexpr (TYPE == MOE_DTYPE_F32) v = __ldg(reinterpret_cast<const float*>(row) + j);
         else if constexpr (TYPE == MOE_DTYPE_BF16)
-          v[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[c + i]);
-        else v[i] = __half2float(reinterpret_cast<const __half*>(row)[c + i]);
+          v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[j]);
+        else v = __half2float(reinterpret_cast<const __half*>(row)[j]);
+        f[i] = c + i < n ? v : 0.0f;
       }
     }
   }
-}
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    if constexpr (!VEC) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = f[i];
+    } else {
+      const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (TYPE == MOE_DTYPE_F32) {
+          v[2 * i] = __uint_as_float(u[2 * i]), v[2 * i + 1] = __uint_as_float(u[2 * i + 1]);
+        } else {
+          const float2 t = two<TYPE>(u[i]);
+          v[2 * i] = t.x, v[2 * i + 1] = t.y;
+        }
+      }
+    }
+  }
+};
 
 // f(piece, its elements) for the 8-element pieces of `rows` rows of n pieces, AHEAD of a thread's
 // loaded before the first is used.
 constexpr int AHEAD = 4;
 template <int TYPE, bool VEC, typename F>
-__device__ __forceinline__ void pieces(const uint8_t* m, long long row_bytes, int rows, int n, int cols,
-                                       F f) {
-  const int total = rows * n;
+__device__ __forceinline__ void pieces(const uint8_t* m, long long row_bytes, int rows, const Div& n,
+                                       int cols, F f) {
+  const int total = rows * n.d;
   for (int i0 = threadIdx.x; i0 < total; i0 += AHEAD * blockDim.x) {
-    float v[AHEAD][8];
+    Eight<TYPE, VEC> e[AHEAD];
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
-      const int i = i0 + j * blockDim.x, r = i / n;
-      if (i < total) eight<TYPE, VEC>(m + r * row_bytes, 8 * (i - r * n), cols, v[j]);
+      const int i = min(i0 + j * (int)blockDim.x, total - 1), r = i / n;
+      e[j].load(m + r * row_bytes, 8 * (i - r * n.d), cols);
     }
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-      if (i0 + j * blockDim.x < total) f(i0 + j * blockDim.x, v[j]);
+    for (int j = 0; j < AHEAD; ++j) {
+      const int i = i0 + j * (int)blockDim.x;
+      if (i < total) {
+        float v[8];
+        e[j].values(v);
+        f(i, v);
+      }
+    }
   }
 }
 
-struct Squares {  // of v, and of v scaled by 2^-64 and 2^64 for where those leave FP32's range
+// Sums of squares: pieces whose sum leaves [2^-60, 2^100] are summed scaled by 2^-64 (big) or 2^64
+// (small) instead, so that no size of matrix overflows or vanishes.
+struct Squares {
   float mid, big, small;
-  __device__ void add(float v) {
-    mid = fmaf(v, v, mid);
-    const float b = v * 0x1p-64f, t = v * 0x1p64f;
-    big = fmaf(b, b, big);
-    small = fmaf(t, t, small);
+  __device__ void add(const float (&v)[8]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
+    if (s >= 0x1p-60f && s <= 0x1p100f) {
+      mid += s;
+      return;
+    }
+    const bool tiny = s < 0x1p-60f;
+    const float by = tiny ? 0x1p64f : 0x1p-64f;
+    float t = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t = fmaf(v[j] * by, v[j] * by, t);
+    if (tiny) small += t;
+    else big += t;  // (infinities and NaN too)
   }
 };
 
@@ -205,7 +237,7 @@ __device__ __forceinline__ float block_sum(float v, float* sh) {
 template <int TYPE, bool VEC>
 __global__ void __launch_bounds__(256)
     squares_kernel(const uint8_t* __restrict__ m, long long ld, long long es, int rows, int cols,
-                   int per, float* __restrict__ parts) {
+                   int per, Div n, float* __restrict__ parts) {
   __shared__ float sh[8];
   pdl_wait();
   pdl_launch_dependents();
@@ -213,11 +245,8 @@ __global__ void __launch_bounds__(256)
   const int r0 = blockIdx.x * per, r1 = min(rows, r0 + per);
   Squares q = {0.0f, 0.0f, 0.0f};
   constexpr int ELT = TYPE == MOE_DTYPE_F32 ? 4 : 2;
-  pieces<TYPE, VEC>(m + (e * es + r0 * ld) * ELT, ld * ELT, r1 - r0, (cols + 7) / 8, cols,
-                    [&](int, const float(&v)[8]) {
-#pragma unroll
-                      for (int j = 0; j < 8; ++j) q.add(v[j]);
-                    });
+  pieces<TYPE, VEC>(m + (e * es + r0 * ld) * ELT, ld * ELT, r1 - r0, n, cols,
+                    [&](int, const float(&v)[8]) { q.add(v); });
   const float a = block_sum(q.mid, sh), b = block_sum(q.big, sh), c = block_sum(q.small, sh);
   if (threadIdx.x == 0) {
     float* o = parts + ((long long)e * 3) * nb + blockIdx.x;
@@ -233,8 +262,8 @@ __global__ void __launch_bounds__(256)
 template <int TYPE, bool VEC>
 __global__ void __launch_bounds__(256)
     scale_kernel(const uint8_t* __restrict__ m, long long ld, long long es, int rows, int cols,
-                 int per, int ldx, float eps, const float* __restrict__ parts,
-                 __half* __restrict__ x, float* __restrict__ f, int E) {
+                 int per, Div n, int ldx, float eps, const float* __restrict__ parts,
+                 __half* __restrict__ x, __half* __restrict__ x_lo, float* __restrict__ f, int E) {
   __shared__ float sh[8];
   pdl_wait();
   pdl_launch_dependents();
@@ -246,9 +275,9 @@ __global__ void __launch_bounds__(256)
     s[j] = block_sum(v, sh);
   }
   float norm;
-  if (!(s[0] <= 0x1p120f)) norm = sqrtf(s[1]) * 0x1p64f;       // (NaN too)
-  else if (s[0] < 0x1p-80f) norm = sqrtf(s[2]) * 0x1p-64f;
-  else norm = sqrtf(s[0]);
+  if (!(s[1] <= 0.0f)) norm = sqrtf(s[1] + s[0] * 0x1p-128f) * 0x1p64f;  // (NaN too)
+  else if (!(s[0] <= 0.0f)) norm = sqrtf(s[0] + s[2] * 0x1p-128f);
+  else norm = sqrtf(s[2]) * 0x1p-64f;
   int k = 0;
   const bool finite = norm <= 0x1.fffffep127f;
   if (finite && norm > 0.0f) {
@@ -265,28 +294,40 @@ __global__ void __launch_bounds__(256)
   const float s1 = ldexpf(1.0f, k / 2), s2 = ldexpf(1.0f, k - k / 2);
   const int r0 = blockIdx.x * per, r1 = min(rows, r0 + per);
   constexpr int ELT = TYPE == MOE_DTYPE_F32 ? 4 : 2;
-  uint4* o = reinterpret_cast<uint4*>(x + ((long long)e * rows + r0) * ldx);
-  pieces<TYPE, VEC>(m + (e * es + r0 * ld) * ELT, ld * ELT, r1 - r0, ldx / 8, cols,
+  const long long at = ((long long)e * rows + r0) * ldx;
+  uint4* o = reinterpret_cast<uint4*>(x + at);
+  uint4* o_lo = x_lo ? reinterpret_cast<uint4*>(x_lo + at) : nullptr;
+  pieces<TYPE, VEC>(m + (e * es + r0 * ld) * ELT, ld * ELT, r1 - r0, n, cols,
                     [&](int i, const float(&v)[8]) {
-                      uint32_t w[4];
+                      uint32_t w[4], l[4];
 #pragma unroll
-                      for (int j = 0; j < 4; ++j)
-                        w[j] = pack<MOE_DTYPE_F16>(v[2 * j] * s1 * s2, v[2 * j + 1] * s1 * s2);
+                      for (int j = 0; j < 4; ++j) {
+                        const float a = v[2 * j] * s1 * s2, b = v[2 * j + 1] * s1 * s2;
+                        w[j] = pack<MOE_DTYPE_F16>(a, b);
+                        const float2 h = two<MOE_DTYPE_F16>(w[j]);
+                        l[j] = pack<MOE_DTYPE_F16>((a - h.x) * 2048.0f, (b - h.y) * 2048.0f);
+                      }
                       o[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                      if (o_lo) o_lo[i] = make_uint4(l[0], l[1], l[2], l[3]);
                     });
 }
 
 template <int TYPE, bool VEC>
 cudaError_t start(const uint8_t* m, long long ld, long long es, int E, int rows, int cols, float eps,
-                  float* parts, __half* x, float* f, cudaStream_t s) {
-  int per = (16384 + cols - 1) / cols;  // rows a block
+                  float* parts, __half* x, __half* x_lo, float* f, cudaStream_t s) {
+  // rows a block: 32768 elements of large stacks (four rounds of loads a thread), fewer where that
+  // would leave SMs without a block (5 x 1439 x 1001 FP32: 389 against XXX us for the whole call)
+  const long long most = (long long)E * rows * cols / (8LL * device_sm_count());
+  const int elements = most < 2048 ? 2048 : most > 32768 ? 32768 : (int)most;
+  int per = (elements + cols - 1) / cols;
   if ((rows + per - 1) / per > kNormParts) per = (rows + kNormParts - 1) / kNormParts;
   const dim3 grid((rows + per - 1) / per, E);
   cudaError_t err = launch_pdl(squares_kernel<TYPE, VEC>, grid, dim3(256), 0, s, m, ld, es, rows, cols,
-                               per, parts);
+                               per, make_div((cols + 7) / 8), parts);
   if (err != cudaSuccess) return err;
   return launch_pdl(scale_kernel<TYPE, VEC>, grid, dim3(256), 0, s, m, ld, es, rows, cols, per,
-                    (cols + 7) / 8 * 8, eps, static_cast<const float*>(parts), x, f, E);
+                    make_div((cols + 7) / 8), (cols + 7) / 8 * 8, eps,
+                    static_cast<const float*>(parts), x, x_lo, f, E);
 }
 
 }  // namespace
@@ -306,15 +347,15 @@ cudaError_t launch_swiglu_bwd(const void* gate_up, long long gu_ld, const void* 
 }
 
 cudaError_t launch_orth_start(const void* m, int type, long long ld_m, long long es_m, int E,
-                              int rows, int cols, float eps, float* parts, void* x, float* f,
-                              cudaStream_t s) {
+                              int rows, int cols, float eps, float* parts, void* x, void* x_lo,
+                              float* f, cudaStream_t s) {
   const uint8_t* src = static_cast<const uint8_t*>(m);
-  __half* o = static_cast<__half*>(x);
+  __half *o = static_cast<__half*>(x), *l = static_cast<__half*>(x_lo);
   const int elt = type == MOE_DTYPE_F32 ? 4 : 2;
   const bool vec = cols % 8 == 0 && ld_m * elt % 16 == 0 && (E == 1 || es_m * elt % 16 == 0);
 #define MOE_START(T)                                                                          \
-  return vec ? start<T, true>(src, ld_m, es_m, E, rows, cols, eps, parts, o, f, s)            \
-             : start<T, false>(src, ld_m, es_m, E, rows, cols, eps, parts, o, f, s)
+  return vec ? start<T, true>(src, ld_m, es_m, E, rows, cols, eps, parts, o, l, f, s)            \
+             : start<T, false>(src, ld_m, es_m, E, rows, cols, eps, parts, o, l, f, s)
   if (type == MOE_DTYPE_F32) MOE_START(MOE_DTYPE_F32);
   if (type == MOE_DTYPE_BF16) MOE_START(MOE_DTYPE_BF16);
   MOE_START(MOE_DTYPE_F16);

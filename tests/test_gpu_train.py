@@ -218,6 +218,24 @@ def test_orthogonalize(moe, E, rows, cols, dt, out):
     assert moe.moe_read_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("E,rows,cols,rank", [(2, 300, 500, 8), (2, 500, 300, 8), (1, 128, 700, 3), (2, 260, 520, 64)])
+@pytest.mark.parametrize("dt", [F32, BF])
+def test_orthogonalize_of_low_rank(moe, E, rows, cols, rank, dt):
+    """A few rows' gradients: what rounding leaves outside their span is not lifted step by step.  The first three
+    iterates count with 22 bits in a X, so a rounding of 2^-12 (of X, A and B) is lifted by two steps at most."""
+    g = gen(rank)
+    u, v = normal(g, E, rows, rank), normal(g, E, rank, cols)
+    m = (u @ v).to(dt)  # (BF16: of full rank again, by its rounding, which belongs to the input)
+    ws = moe.orthogonalize_new_workspace(E, rows, cols)
+    x = moe.orthogonalize(m, ws)
+    want, _ = ref.orthogonalize(m)
+    norm = want.square().sum((1, 2)).sqrt()
+    # roundings of X_3 and X_4 lifted twice and once, in 2-norms of at most 1.2 sqrt(rank) + what bf16 noise adds
+    tol = 3 * 2.0 ** -12 * (3.4445 ** 2 + 3.4445 + 1) + 2.0 ** -8
+    assert ((x.double() - want).square().sum((1, 2)).sqrt() <= tol * norm).all()
+    assert moe.moe_read_device_status(ws) == 0
+
+
 def test_orthogonalize_bad_and_zero_matrices(moe):
     """Zeros stay zeros, an infinity or a NaN stays in its matrix, and sizes up to FP32's ends are no matter."""
     g = gen(1)
