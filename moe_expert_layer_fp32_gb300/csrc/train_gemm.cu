@@ -135,6 +135,10 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1,
                                              int c2) {
   asm volatile(
@@ -616,6 +620,16 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
       if (KIND == WGRAD && t.kb == 0 && p.c != nullptr) continue;  // nothing to add
       const int acc = tcount & 1;
       const bool sums = KIND != WGRAD || t.kb > 0;
+      if constexpr (KIND == BATCH) {  // this tile's rows of c move into L2 while it is multiplied
+        const int row = t.row0 + q * 32 + lane;
+        if (row < p.M) {
+          const long long at = t.e * p.c_es + row * p.c_ld;
+          for (int col = t.col0 + 64 * first; col < min(p.n_lim, t.col0 + BN); col += 128) {
+            prefetch_l2(static_cast<const __half*>(p.c) + at + col);
+            if (p.c_lo) prefetch_l2(static_cast<const __half*>(p.c_lo) + at + col);
+          }
+        }
+      }
       if (sums) {
         int ok = 1;
         if (lane == 0)
