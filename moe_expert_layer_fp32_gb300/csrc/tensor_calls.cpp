@@ -341,7 +341,8 @@ PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!PyFloat_Check(o)) Py_RETURN_NONE;
     v[i] = PyFloat_AS_DOUBLE(o);
   }
-  const int dt = dtype_of(m), dev = m.is_cuda() ? (int)m.get_device() : -1;
+  if (!m.is_cuda()) Py_RETURN_NONE;
+  const int dt = dtype_of(m), dev = (int)m.get_device();
   if (dt < 0 || dev != (int)c10::cuda::current_device() || m.dim() != 3 || !m.is_contiguous() ||
       !plain(ws, at::kByte, dev, {-1}))
     Py_RETURN_NONE;

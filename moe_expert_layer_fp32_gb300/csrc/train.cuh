@@ -46,7 +46,6 @@ struct TrainProduct {
   int32_t* status;
   long long limit;
 };
-bool product_pair_form(int E, int R);
 cudaError_t launch_product(const TrainProduct& q, cudaStream_t s);
 
 // out [E, K, N] = (or, FP32, +=) the sums over each expert's rows of x [R, K]^T dy [R, N]; R > 0.
@@ -88,6 +87,8 @@ struct TrainBatch {
   int32_t* status;
   long long limit;
 };
+// The choice of `pair` for matrices of this size.
+bool batch_pairs(int E, int rows, int cols);
 cudaError_t launch_batch(const TrainBatch& q, cudaStream_t s);
 
 // h [R, I] = w silu(gate) up of gate_up [R, 2 I] (w: [R] FP32 or null)

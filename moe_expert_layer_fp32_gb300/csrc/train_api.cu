@@ -377,7 +377,7 @@ moe_status moe_orthogonalize(const void* m, int32_t dtype, int64_t ld, int64_t e
                              dtype == MOE_DTYPE_F32 ? lo : nullptr, f, s));
   TrainBatch q = {};
   q.E = E;
-  q.pair = S > 128;
+  q.pair = batch_pairs(E, rows, cols);
   q.status = static_cast<int32_t*>(workspace);
   q.limit = wait_limit();
   for (int i = 0; i < steps; ++i) {

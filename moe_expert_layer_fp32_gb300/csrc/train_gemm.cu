@@ -22,9 +22,7 @@
 //
 // A weight gradient contracts over an expert's rows, which end anywhere.  The rows of an
 // expert's last, partial k-block are copied beforehand (tails_kernel) and filled up with zeros, so
-// another expert's rows (or infinities and NaN among them) never enter the sum.  (Tensor maps
-// that end with the expert's rows, made on the device, need a proxy fence whenever a CTA
-// changes the expert: 411 against XXX us for 64 experts of 512 rows, 2048 x 2048 FP32.)
+// another expert's rows (or infinities and NaN among them) never enter the sum.
 //
 // Bounded waits, and what happens when one runs out, as in expert_gemm.cu.
 #include "common.cuh"
@@ -817,13 +815,29 @@ uint32_t formats_of(int dtype) {  // A and B: BF16, or both FP16
 
 }  // namespace
 
-// The pair form needs many rows an expert to fill its 256-row tiles; with fewer the single form
-// loads no more than the rows there are and spreads an expert's columns over twice the CTAs.
-bool product_pair_form(int E, int R) { return (long long)R >= 128LL * E; }
+// The pair form's 256-row tiles need rows to fill them; with fewer, the single form loads no more
+// than the rows there are.  64 experts with unevenly spread rows, 2048 x 2048 BF16, pair
+// against single, at 32, 64, 96, 128, 256 and 512 rows an expert on average: 89 against 84 us, 91
+// against 86, 94 against 96, 95 against 110, 122 against 170, 200 against 298 (768 x 2048 crosses at
+// the same place).  Nor does it pay where 128 x 128 tiles do not go round the SMs once: 8 experts of
+// 256 rows, 512 x 512, 8.1 us against 6.6, 2 of 1000 rows, 1000 x 1000, 12.7 against 11.7.  Both
+// forms give a row the same bits.
+static bool product_pairs(int E, int R, int N) {
+  return (long long)R >= 96LL * E && (long long)(R / 128) * ((N + 127) / 128) > device_sm_count();
+}
+
+// The pair form of the Newton-Schulz products halves the bytes that an SM reads a product, but
+// makes tiles of twice the side: with few of them SMs stand idle and the dependent products
+// take longer.  A whole update, pair against single: 8 of 512 x 512 148 against 109 us, 8 of 384 x
+// 1024 155 against 121, 64 of 256 x 512 176 against 162, 5 of 1000 x 1440 263 against 322.
+bool batch_pairs(int E, int rows, int cols) {
+  const long long tiles = (long long)E * ((rows + 127) / 128) * ((cols + 127) / 128);
+  return (rows < cols ? rows : cols) > 256 && tiles > 2LL * device_sm_count();
+}
 
 cudaError_t launch_product(const TrainProduct& q, cudaStream_t s) {
   if (q.R == 0) return cudaSuccess;
-  const bool pair = product_pair_form(q.E, q.R);
+  const bool pair = product_pairs(q.E, q.R, q.N);
   Args p = {};
   if (!encode_16bit_3d(&p.a, q.x, q.K, q.R, 1, q.x_ld, 0, pair ? GM : BOX_ROWS))
     return cudaErrorInvalidValue;
@@ -880,6 +894,8 @@ cudaError_t launch_wgrad(const TrainWgrad& q, cudaStream_t s) {
   p.formats = formats_of(q.type);
   p.status = q.status;
   p.limit = q.limit;
+  // (the pair form's 256 x 256 tiles, unless half of one would stay empty; 8 experts of 256 rows,
+  // 512 x 512: 9.4 us against 11.1 with 128 x 128, 64 of 192 x 1024 19.1 against 17.4)
   const bool pair = q.K > 128 && q.N > 128;
   const int t = pair ? 256 : 128;
   const long long units = (long long)q.E * ((q.K + t - 1) / t) * ((q.N + t - 1) / t);

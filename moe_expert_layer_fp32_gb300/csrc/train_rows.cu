@@ -316,7 +316,7 @@ template <int TYPE, bool VEC>
 cudaError_t start(const uint8_t* m, long long ld, long long es, int E, int rows, int cols, float eps,
                   float* parts, __half* x, __half* x_lo, float* f, cudaStream_t s) {
   // rows a block: 32768 elements of large stacks (four rounds of loads a thread), fewer where that
-  // would leave SMs without a block (5 x 1439 x 1001 FP32: 389 against XXX us for the whole call)
+  // would leave SMs with fewer than eight blocks
   const long long most = (long long)E * rows * cols / (8LL * device_sm_count());
   const int elements = most < 2048 ? 2048 : most > 32768 ? 32768 : (int)most;
   int per = (elements + cols - 1) / cols;
