@@ -543,7 +543,7 @@ moe_status moe_mx4_layer_fwd(const void* x, const float* w_router, const float* 
  * rows of adjacent elements, ld elements apart and starting on 16-byte boundaries
  * (ld * element size a multiple of 16); stacks of E matrices es elements apart, es a
  * multiple of ld.  K, N, H and I are multiples of 8, at most 32768 (I: 16384);
- * 1 <= E <= 256.  offsets [E+1] int32 as moe_load_stats writes them: expert e has the
+ * 1 <= E <= 256, R <= 2^31 - 512.  offsets [E+1] int32 as moe_load_stats writes them: expert e has the
  * rows [offsets[e], offsets[e+1]).  Offsets that are not a non-decreasing sequence
  * from 0 to R are flagged (MOE_ERR_DEVICE_CHECK) and no output is written.
  * Workspaces as moe_workspace_bytes describes them (status word first). */
@@ -563,8 +563,7 @@ moe_status moe_grouped_product(const void* x, int64_t x_ld, int32_t dtype, const
                                int32_t y_dtype, void* workspace, size_t ws_bytes, void* stream);
 
 /* Gradient of the product for the weights: d_w[e, k, n] = sum over the rows r of expert
- * e of x[r, k] * dy[r, n], in an order that the rows' number fixes; 0 for an expert
- * without rows.
+ * e of x[r, k] * dy[r, n], in ascending order of the rows; 0 for an expert without rows.
  *   x [R, K], dy [R, N] of dtype; d_w [E, K, N] of w_dtype (any moe_dtype)
  *   accumulate nonzero (FP32 only): d_w += instead (an expert without rows is not
  *   touched). */
@@ -621,10 +620,13 @@ size_t moe_orthogonalize_workspace_bytes(int32_t E, int32_t rows, int32_t cols);
  * -4.7750, 2.0315 with five steps bring singular values above about 0.002 of the norm
  * to between 0.7 and 1.2.  A zero matrix gives zeros; one with an infinity or a NaN gives NaN,
  * and the others' results do not depend on it.
- * X and the products are held in FP16 (times 1024; |X| stays near 1) between steps and
- * summed in FP32: see the error of each step's rounding where singular values are far
- * below the others: a step lifts them, and the rounding noise beside them, a times.
- * Out may be m. */
+ * X, A = X X^T and B = b A + c A A are held in FP16 (times 1024) between the products and
+ * summed in FP32.  A step lifts small singular values a times, and with them what the
+ * roundings left beside them; the first three iterates (up to 128 x 256, either way
+ * round: all) therefore keep what their rounding left, which counts in a X.  Measured
+ * against 64 bits, before the rounding of out: about 0.001 (relative 2-norm) for momenta of
+ * full rank, 0.002 for rank 8 of 500 x 720.  Coefficients that let |X| grow past 60 overflow
+ * FP16.  out may be m. */
 moe_status moe_orthogonalize(const void* m, int32_t dtype, int64_t ld, int64_t es, int32_t E,
                              int32_t rows, int32_t cols, const float* coefficients, int32_t steps,
                              float eps, float scale, void* out, int32_t out_dtype, int64_t out_ld,

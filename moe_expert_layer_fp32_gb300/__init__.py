@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) top-k routed MoE feed-forward layer forward.
+"""GB300 (sm_103a) top-k routed MoE feed-forward layer: forward pass, 4-bit experts, and the
+operators that train its router and experts.
 
 Thin binding over the C ABI in ``include/moe.h`` (``libmoe_gb300.so``): the
 functions below carry the same names and only marshal arguments (torch tensors

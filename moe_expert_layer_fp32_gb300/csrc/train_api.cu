@@ -46,9 +46,10 @@ moe_status check_grouped(int E, int K, int N) {
   if (E > kMaxE || K % 8 != 0 || N % 8 != 0 || K > 32768 || N > 32768) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
-// Rows of a product: its tiles are numbered in 32 bits.
+// Rows of a product: a tile may end 256 rows behind them, and tiles are numbered in 32 bits.
 moe_status check_rows(long long R, int E, int N) {
   if (R < 0) return MOE_ERR_INVALID_ARG;
+  if (R > (1LL << 31) - 512) return MOE_ERR_UNSUPPORTED;
   return (R / 128 + E + 1) * ((N + 127) / 128) >= (1LL << 30) ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 

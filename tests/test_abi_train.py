@@ -41,6 +41,7 @@ def test_product(moe):  # noqa: F811
     refused(moe, "INVALID_ARG", lambda: f(R=-1))
     refused(moe, "UNSUPPORTED", lambda: f(R=2 ** 31 - 1, N=32768, wl=32768, we=64 * 32768, yl=32768,
                                           ws=(WS[0], 1 << 40)))
+    refused(moe, "UNSUPPORTED", lambda: f(R=2 ** 31 - 511))
     refused(moe, "UNSUPPORTED", lambda: f(K=60))
     refused(moe, "UNSUPPORTED", lambda: f(N=124))
     refused(moe, "UNSUPPORTED", lambda: f(E=257))
