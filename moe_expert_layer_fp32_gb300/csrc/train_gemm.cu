@@ -40,19 +40,16 @@ constexpr int GM = 128, GK = 64, UK = 16;
 constexpr int EPI_WARPS = 8, B_WARP = 2 + EPI_WARPS, THREADS = 32 * (B_WARP + 1);
 constexpr int BOX_ROWS = 16;  // A boxes of the single form of a product
 
-// SLABS: 4096-byte blocks of an epilogue warp.  With two, one is filled while TMA reads the other;
-// the weight gradient, whose tiles come fastest and are the largest (FP32), takes them for a stage.
-template <int CTAS, int BN, int SLABS_>
+template <int CTAS, int BN>
 struct Shape {
-  static constexpr int SLABS = SLABS_;
-  static constexpr int STAGES = SLABS == 2 ? 5 : 6;
+  static constexpr int STAGES = 6;
   static constexpr int A_BYTES = GM * GK * 2;
   static constexpr int BROWS = BN / CTAS;  // of B in this CTA
   static constexpr int B_BYTES = BROWS * GK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int NBAR = 2 * STAGES + 2 + 2 + 1;
-  static constexpr int EPI_BYTES = EPI_WARPS * SLABS * 32 * 128;
+  static constexpr int EPI_BYTES = EPI_WARPS * 32 * 128;
   static constexpr int SMEM_BYTES =
       STAGES * STAGE_BYTES + EPI_BYTES + NBAR * 8 + 48 + 2 * (kMaxE + 1) * 4;
 };
@@ -149,10 +146,9 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// All of this thread's stores but the last N have read their shared memory (done: and are performed).
-template <int N = 0>
+// This thread's stores have read their shared memory (all: and are performed).
 __device__ __forceinline__ void tma_stores_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 __device__ __forceinline__ void tma_stores_done() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -168,8 +164,8 @@ __device__ __forceinline__ uint4* piece(uint4* st, int r, int c) { return st + 8
 // ends), else (an expert's last rows, sums added to the output, rows that start anywhere) through
 // registers, four whole spans an instruction.  out and c point to the rows' first element at
 // the tile's first column.
-template <int TYPE, bool ADD16, bool ADD32, int SLABS = 1>
-__device__ __forceinline__ void store_tile(uint32_t taddr, uint4* slabs, int& turn, int lane, int first,
+template <int TYPE, bool ADD16, bool ADD32>
+__device__ __forceinline__ void store_tile(uint32_t taddr, uint4* st, int lane, int first,
                                            const CUtensorMap* map, int col0, int row0, int e,
                                            void* out, long long ld, bool vec, int nrows, int ncols,
                                            const void* c, long long c_ld, float alpha, float beta,
@@ -177,7 +173,6 @@ __device__ __forceinline__ void store_tile(uint32_t taddr, uint4* slabs, int& tu
                                            const void* c_lo = nullptr) {
   constexpr int COLS = TYPE == MOE_DTYPE_F32 ? 32 : 64, PER = COLS / 8;  // of a span, of a piece
   constexpr int BYTES = 128 / COLS;
-  uint4* st = slabs;
 #pragma unroll 1
   for (int c0 = first * COLS; c0 < ncols; c0 += 2 * COLS) {
     const int cp = lane & 7, r4 = lane >> 3;  // this lane's piece and row (of four) in memory order
@@ -249,11 +244,7 @@ __device__ __forceinline__ void store_tile(uint32_t taddr, uint4* slabs, int& tu
       }
     }
     if constexpr (!ADD16) {
-      if constexpr (SLABS == 2) {  // the slab that was not the last one's
-        turn ^= 1;
-        st = slabs + turn * (32 * 8);
-      }
-      if (lane == 0) tma_stores_read<SLABS - 1>();
+      if (lane == 0) tma_stores_read();
       __syncwarp();
     }
 #pragma unroll
@@ -318,10 +309,8 @@ __device__ __forceinline__ void store_tile(uint32_t taddr, uint4* slabs, int& tu
 }
 
 // The same for an expert without rows: zeros.
-__device__ __forceinline__ void zero_tile(uint4* slabs, int& turn, int lane, int first, int cols, const CUtensorMap* map,
+__device__ __forceinline__ void zero_tile(uint4* st, int lane, int first, int cols, const CUtensorMap* map,
                                           int col0, int row0, int e, int ncols) {
-  turn ^= 1;
-  uint4* st = slabs + turn * (32 * 8);
   if (lane == 0) tma_stores_read();
   __syncwarp();
 #pragma unroll
@@ -334,7 +323,7 @@ __device__ __forceinline__ void zero_tile(uint4* slabs, int& turn, int lane, int
 
 template <int CTAS, int BN, Kind KIND, Major A, Major B>
 __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_constant__ Args p) {
-  using C = Shape<CTAS, BN, KIND == WGRAD ? 2 : 1>;
+  using C = Shape<CTAS, BN>;
   constexpr int TM = GM * CTAS;
   constexpr bool BOXED = KIND == PRODUCT && CTAS == 1;
   extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's period; there is no other)
@@ -620,8 +609,7 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3;  // TMEM lane quarter this warp may access
     const int first = (warp - 2) >> 2;
-    uint4* st = s_epi + (warp - 2) * (32 * 8 * C::SLABS);
-    int turn = 0;
+    uint4* st = s_epi + (warp - 2) * (32 * 8);
     int tcount = 0;
     for (int i = 0; i * P < total; ++i) {
       const int u = unit_of(i);
@@ -664,40 +652,40 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
           const __half* c = static_cast<const __half*>(p.c) + c_at;
           const __half* c_lo = p.c_lo ? static_cast<const __half*>(p.c_lo) + c_at : nullptr;
           if (KIND == BATCH && p.out_type == MOE_DTYPE_BF16)  // (the last step's result)
-            store_tile<MOE_DTYPE_BF16, true, false>(taddr, st, turn, lane, first, map, t.col0, row0,
+            store_tile<MOE_DTYPE_BF16, true, false>(taddr, st, lane, first, map, t.col0, row0,
                                                     oe, out, p.ld, false, nrows, ncols, c, p.c_ld,
                                                     alpha, beta, nullptr,
                                                     KIND == BATCH ? c_lo : nullptr);
           else if (p.c != nullptr)
-            store_tile<MOE_DTYPE_F16, true, false>(taddr, st, turn, lane, first, map, t.col0, row0, oe,
+            store_tile<MOE_DTYPE_F16, true, false>(taddr, st, lane, first, map, t.col0, row0, oe,
                                                    out, p.ld, false, nrows, ncols, c, p.c_ld, alpha,
                                                    beta, KIND == BATCH && p.has_lo ? &p.o_lo : nullptr,
                                                    KIND == BATCH ? c_lo : nullptr);
           else
-            store_tile<MOE_DTYPE_F16, false, false>(taddr, st, turn, lane, first, map, t.col0, row0,
+            store_tile<MOE_DTYPE_F16, false, false>(taddr, st, lane, first, map, t.col0, row0,
                                                     oe, out, p.ld, false, nrows, ncols, nullptr, 0,
                                                     alpha, 0.0f);
         } else {
           // (a product's rows behind the expert's last belong to the next one)
           const CUtensorMap* map = KIND == WGRAD || nrows == 32 ? &p.o : nullptr;
-          if (KIND == WGRAD && !sums) {
-            zero_tile(st, turn, lane, first, p.out_type == MOE_DTYPE_F32 ? 32 : 64, map, t.col0, row0, oe,
+          if (!sums) {
+            zero_tile(st, lane, first, p.out_type == MOE_DTYPE_F32 ? 32 : 64, map, t.col0, row0, oe,
                       ncols);
           } else if (p.out_type == MOE_DTYPE_F32) {
             if (KIND == WGRAD && p.c != nullptr)
-              store_tile<MOE_DTYPE_F32, false, true>(taddr, st, turn, lane, first, nullptr, 0, 0, 0,
+              store_tile<MOE_DTYPE_F32, false, true>(taddr, st, lane, first, nullptr, 0, 0, 0,
                                                      out, p.ld, true, nrows, ncols, nullptr, 0, 1.0f,
                                                      1.0f);
             else
-              store_tile<MOE_DTYPE_F32, false, false, C::SLABS>(taddr, st, turn, lane, first, map, t.col0, row0,
+              store_tile<MOE_DTYPE_F32, false, false>(taddr, st, lane, first, map, t.col0, row0,
                                                       oe, out, p.ld, true, nrows, ncols, nullptr, 0,
                                                       1.0f, 0.0f);
           } else if (p.out_type == MOE_DTYPE_BF16) {
-            store_tile<MOE_DTYPE_BF16, false, false, C::SLABS>(taddr, st, turn, lane, first, map, t.col0, row0,
+            store_tile<MOE_DTYPE_BF16, false, false>(taddr, st, lane, first, map, t.col0, row0,
                                                      oe, out, p.ld, true, nrows, ncols, nullptr, 0,
                                                      1.0f, 0.0f);
           } else {
-            store_tile<MOE_DTYPE_F16, false, false, C::SLABS>(taddr, st, turn, lane, first, map, t.col0, row0,
+            store_tile<MOE_DTYPE_F16, false, false>(taddr, st, lane, first, map, t.col0, row0,
                                                     oe, out, p.ld, true, nrows, ncols, nullptr, 0,
                                                     1.0f, 0.0f);
           }
@@ -772,7 +760,7 @@ __global__ void __launch_bounds__(256)
 
 template <int CTAS, int BN, Kind KIND, Major A, Major B>
 cudaError_t launch(Args& p, long long units, cudaStream_t s) {
-  using C = Shape<CTAS, BN, KIND == WGRAD ? 2 : 1>;
+  using C = Shape<CTAS, BN>;
   constexpr int TM = GM * CTAS;
   const int MT = (p.M + TM - 1) / TM;
   p.nt = make_div((p.N + BN - 1) / BN);
