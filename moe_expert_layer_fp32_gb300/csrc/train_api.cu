@@ -177,7 +177,7 @@ constexpr int kMaxSteps = 64;
 // left, which counts in a X only: later steps lift a rounding there up to a times each, and B X
 // does not lift it (B vanishes where the singular values do).  Without: an error of 0.041 for rank
 // 8 of 500 x 720, 0.0021 for full-rank momenta; three kept 0.0024 and 0.0008, all five 0.0003 and
-// 0.0009, at a read and a write of X more each.
+// 0.0009, at a read and a write of X more each (64 x 1024 x 2048 BF16: 2183 us without, 2250 with).
 constexpr int kKeepLow = 3;
 
 bool orth_sizes(int E, int rows, int cols) {

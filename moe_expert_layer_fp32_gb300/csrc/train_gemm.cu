@@ -24,6 +24,20 @@
 // expert's last, partial k-block are copied beforehand (tails_kernel) and filled up with zeros, so
 // another expert's rows (or infinities and NaN among them) never enter the sum.
 //
+// What bounds it.  Few rows: the weights' bytes (512 rows of 64 experts, 1024 x 2048: 43.9 us, 6.2 TB/s,
+// 91% of the copy rate).  Many rows: the tensor pipe, 90% busy at 131072 rows of 128 experts, 2048 x
+// 1536 (516 us alone under the profiler, 608 among others under the power cap; full 256-row tiles
+// would be 12% fewer).  Weight gradients: the FP32 output's way out beside the short contractions
+// (512 rows an expert, 2048 x 2048: 271 us, 4.95 TB/s, tensor pipe 49%).  Chains of Newton-Schulz
+// products: 70-83% of the tensor pipe at 64 x 1024 x 2048, the rest is each kernel's first and last
+// tile.
+//
+// What it took: a k-block of the pair form is 512 cycles of MMA, so everything that a role's thread
+// does for one has to stay under that.  Descriptors made anew for each MMA cost the issuing thread
+// more (product of 64 x 512 rows 208 us, made once 192), and so did four copies of a weight
+// gradient's stage from one thread (450 us, from two 351); the roles' threads are elected, so that
+// copies and MMAs are issued without a loop over active lanes (128 x 1024 rows: 480 against 456).
+//
 // Bounded waits, and what happens when one runs out, as in expert_gemm.cu.
 #include "common.cuh"
 #include "kernels.cuh"
