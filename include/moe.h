@@ -638,7 +638,7 @@ moe_status moe_orthogonalize(const void* m, int32_t dtype, int64_t ld, int64_t e
 moe_status moe_read_device_status(void* workspace, int32_t* status_out, void* stream);
 
 /* Diagnostics: the limit, in SM clock cycles, of every bounded wait inside the
- * grouped GEMM kernels and the router of at most eight tokens (whose rows then get
+ * grouped GEMM kernels, the orthogonalisation and the router of at most eight tokens (whose rows then get
  * index -1 and weight 0) of calls launched afterwards (process-wide; cycles <= 0
  * restores the default of 4e9, about 2 s).  A wait that runs out records
  * MOE_ERR_TIMEOUT in the workspace status word; the kernel then waits for its own

@@ -1058,8 +1058,8 @@ def grouped_product(x, offsets, w, workspace, transposed=False, dtype=None, out=
     E = _offsets(offsets)
     x_ld = _rows16("x", x, None, (None, None))
     R, K = x.shape
-    if w.dim() != 3:
-        raise ValueError(f"w: [E, K, N] or [E, N, K], not {tuple(w.shape)}")
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w: a tensor [E, K, N] or [E, N, K]")
     N = w.shape[1] if transposed else w.shape[2]
     w_ld, w_es = _stack("w", w, x.dtype, (E, N, K) if transposed else (E, K, N))
     _buffer("workspace", workspace)
@@ -1189,8 +1189,8 @@ def expert_ffn_backward(x_perm, offsets, w_gate_up, w_down, d_y, workspace, row_
     E = _offsets(offsets)
     _rows16("x_perm", x_perm, None, (None, None))
     dt, (R, H) = x_perm.dtype, x_perm.shape
-    if w_gate_up.dim() != 3 or w_gate_up.shape[2] % 2:
-        raise ValueError(f"w_gate_up: [E, H, 2 I], not {tuple(w_gate_up.shape)}")
+    if not isinstance(w_gate_up, torch.Tensor) or w_gate_up.dim() != 3 or w_gate_up.shape[2] % 2:
+        raise ValueError("w_gate_up: a tensor [E, H, 2 I]")
     I = w_gate_up.shape[2] // 2
     for name, t, shape in (("x_perm", x_perm, (R, H)), ("d_y", d_y, (R, H)),
                            ("w_gate_up", w_gate_up, (E, H, 2 * I)), ("w_down", w_down, (E, I, H)),

@@ -136,6 +136,21 @@ def test_rows_do_not_depend_on_the_others(moe):
     assert torch.equal(y, torch.cat([whole[:5], whole[1000:1007], whole[1900:1950]]))
 
 
+def test_256_experts(moe):
+    """As many experts as there may be, most of them with a row or two or none, one with many."""
+    g, K, N, E = gen(13), 72, 200, 256
+    counts = [(7 * e) % 3 for e in range(E)]
+    counts[200] = 900
+    off, R = offsets_of(counts), sum(counts)
+    ws = moe.grouped_new_workspace(E, K, N)
+    x, dy, w = normal(g, R, K, dtype=BF), normal(g, R, N, dtype=BF), normal(g, E, K, N, dtype=BF)
+    ref.close(moe.grouped_product(x, off, w, ws, dtype=F32), ref.product(x, off, w), K, ref.product(x.abs(), off, w.abs()))
+    d = moe.grouped_weight_grad(x, dy, off, ws)
+    ref.close(d, ref.weight_grad(x, dy, off), 900, ref.weight_grad(x.abs(), dy.abs(), off))
+    assert all(not d[e].any() for e in range(E) if counts[e] == 0)
+    assert moe.moe_read_device_status(ws) == 0
+
+
 def test_bad_offsets_are_flagged(moe):
     g, K, N, R = gen(11), 64, 128, 40
     x, dy, w = normal(g, R, K, dtype=BF), normal(g, R, N, dtype=BF), normal(g, 3, K, N, dtype=BF)
@@ -205,7 +220,8 @@ def updates(g, E, rows, cols, dtype, low=None):
 
 @pytest.mark.parametrize("E,rows,cols", [(1, 1, 1), (2, 1, 9), (2, 9, 1), (3, 8, 8), (2, 33, 65), (2, 65, 33), (3, 128, 128),
                                          (2, 128, 256), (2, 129, 200), (2, 200, 129), (2, 256, 512), (2, 511, 513),
-                                         (1, 1000, 700), (40, 40, 24)])
+                                         (1, 1000, 700), (40, 40, 24), (2, 1, 1000), (2, 1000, 1), (2, 5, 300),
+                                         (1, 3000, 40), (256, 9, 300), (1, 257, 257)])
 @pytest.mark.parametrize("dt,out", [(F32, BF), (BF, BF), (HF, HF)])
 def test_orthogonalize(moe, E, rows, cols, dt, out):
     m = updates(gen(rows + cols), E, rows, cols, dt)
