@@ -6,9 +6,11 @@
 // X stays in registers in FP32 (a thread has half a row, 128 columns); what the tensor cores
 // read (X, A, B) goes to shared memory in FP16 times 1024, in rows of 128 bytes with the
 // 128-byte swizzle.  The same image of X serves both products: its rows as the K-major operands of
-// X X^T, and as the MN-major operand of B X.  Everything waits on everything in a step, so the
-// time is that of 3 x steps dependent products with their barriers (about 1.2 us each) and of the
-// way in and out (18 us), not of bytes or operations: 36 us for 8 matrices of 128 x 256, five steps.
+// X X^T, and as the MN-major operand of B X.  B's diagonal, its largest values, stays in FP32 and joins
+// a (its rounding is most of the error of these sizes).  Everything waits on everything in a step, so the
+// time is that of 3 x steps dependent products with their barriers (about 1.6 us each) and of the
+// way in and out (18 us), not of bytes or operations: 41 us for 8 matrices of 128 x 256, five steps
+// (36 with the diagonal in FP16).
 // The chain of kernels for larger matrices (train_gemm.cu) takes 17 launches and 78 us for them.
 #include "common.cuh"
 #include "kernels.cuh"
@@ -21,7 +23,7 @@ namespace {
 constexpr int S = 128, L = 256;  // rows and columns held (zeros behind the matrix's own)
 constexpr int OFF_X = 0, OFF_A = (L / 64) * S * 128, OFF_B = OFF_A + (S / 64) * S * 128;
 constexpr int OFF_END = OFF_B + (S / 64) * S * 128;
-constexpr int SMEM = OFF_END + 128;
+constexpr int OFF_DIAG = OFF_END + 128, SMEM = OFF_DIAG + S * 4;
 constexpr int G_COL = 0, Q_COL = 128, Y_COL = 256, TMEM_COLS = 512;
 constexpr int HALF = L / 2;
 constexpr float HELD = 1024.0f;
@@ -56,6 +58,7 @@ __global__ void __launch_bounds__(256, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* sums = reinterpret_cast<float*>(tmem_slot + 2);  // 3 x 8 (and the largest)
+  float* diagonal = reinterpret_cast<float*>(smem + OFF_DIAG);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = 32 * (warp & 3) + lane, h = warp >> 2;  // this thread's row of X, and half of it
   const bool turned = rows > cols;
@@ -213,6 +216,12 @@ __global__ void __launch_bounds__(256, 1)
         g[32 * t + j] = fmaf(c / (HELD * HELD), __uint_as_float(v[j]), b * g[32 * t + j]);
     }
 #pragma unroll
+    for (int j = 0; j < 64; ++j)
+      if (64 * h + j == r) {
+        diagonal[r] = g[j];
+        g[j] = 0.0f;
+      }
+#pragma unroll
     for (int q = 0; q < 8; ++q) {
       uint32_t w[4];
 #pragma unroll
@@ -226,6 +235,7 @@ __global__ void __launch_bounds__(256, 1)
       }
     });
     if (!ok) break;
+    const float ad = a + diagonal[r];
 #pragma unroll
     for (int t = 0; t < HALF / 32; ++t) {
       uint32_t v[32];
@@ -233,7 +243,7 @@ __global__ void __launch_bounds__(256, 1)
       tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        x[32 * t + j] = fmaf(a, x[32 * t + j], __uint_as_float(v[j]) * (1.0f / (HELD * HELD)));
+        x[32 * t + j] = fmaf(ad, x[32 * t + j], __uint_as_float(v[j]) * (1.0f / (HELD * HELD)));
     }
   }
 
