@@ -364,7 +364,7 @@ struct PairCfg {
   static constexpr int NBAR = 2 * STAGES + 2 + 2 + 1;
   static constexpr int EPI_LD = 36;
   static constexpr int EPI_BYTES = 4 * 32 * EPI_LD * 4;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + NBAR * 8 + 16 +
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + NBAR * 8 + 24 +
                                     3 * (kMaxE + 1) * 4;
 };
 
@@ -419,7 +419,8 @@ __global__ void __launch_bounds__(192, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* peer_abort = abort_flag + 1;   // the other CTA's flag, and the k-blocks that it
   volatile int* peer_issued = abort_flag + 2;  // has issued: written by it at its end
-  int* s_prefix = reinterpret_cast<int*>(tmem_slot + 4);
+  volatile int* committed = abort_flag + 3;    // k-blocks and accumulators committed, by the issuer
+  int* s_prefix = reinterpret_cast<int*>(tmem_slot + 6);
   int* s_off = s_prefix + (kMaxE + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -449,6 +450,7 @@ __global__ void __launch_bounds__(192, 1)
     *abort_flag = 0;
     *peer_abort = 0;
     *peer_issued = 0;
+    committed[0] = committed[1] = 0;
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);   // the even CTA's producer; bytes from both CTAs
       mbar_init(&empty[s], 1);  // the pair MMA's commit, multicast
@@ -495,6 +497,11 @@ __global__ void __launch_bounds__(192, 1)
           load(s, w, kb);
         }
       }
+      // the last k-blocks' commits arrive in this CTA, the odd one too: it does not leave before
+      // (the epilogue has waited for every accumulator's)
+      for (int i = (it > C::STAGES ? it - C::STAGES : 0); i < it && !aborted; ++i)
+        aborted = !mbar_wait_bounded(&empty[i % C::STAGES], (i / C::STAGES) & 1, abort_flag, status,
+                                     spin_limit);
       st_shared_remote(mapa_shared(smem_u32((const void*)peer_issued), rank ^ 1), it);
     }
   } else if (warp == 1) {
@@ -533,6 +540,10 @@ __global__ void __launch_bounds__(192, 1)
       // every MMA this thread issued completes before tensor memory is released
       mma_commit_pair(mma_done, 0x1);
       wait_drain(mma_done, 0, kSpinLimitCycles);
+      committed[0] = it;
+      committed[1] = tcount;
+      for (int i = 0; i < 2; ++i)
+        st_shared_remote(mapa_shared(smem_u32((const void*)(committed + i)), 1), i ? tcount : it);
     }
   } else {
     // -------------------------------------------------------------- epilogue
@@ -568,8 +579,14 @@ __global__ void __launch_bounds__(192, 1)
     // All MMAs are complete and no role waits any more.  Copies into the last STAGES slots
     // may still be in flight.  A stage that only one CTA has issued gets the other's bytes
     // now (its slot's last MMAs are complete, or the one could not have issued it), so
-    // that its barrier completes; the even CTA waits for the bytes of both.
+    // that its barrier completes; the even CTA waits for the bytes of both.  A role that gave
+    // up did not wait for the commits that arrive in its CTA: thread 0 does.
     if (threadIdx.x == 0) {
+      const int blocks = committed[0], tiles = committed[1];
+      for (int i = (blocks > C::STAGES ? blocks - C::STAGES : 0); i < blocks; ++i)
+        wait_drain(&empty[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
+      for (int i = (tiles > 2 ? tiles - 2 : 0); i < tiles; ++i)
+        wait_drain(&tfull[i & 1], (i >> 1) & 1, kSpinLimitCycles);
       for (; it < *peer_issued; ++it) {
         const int kb = it % KB;
         load(it % C::STAGES,

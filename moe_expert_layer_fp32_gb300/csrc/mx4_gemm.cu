@@ -66,7 +66,7 @@ struct MxCfg {
   static constexpr int ACC_COLS = TILE_ROWS;
   static constexpr int SF_COL = 2 * ACC_COLS;                // first scale column
   static constexpr int SMEM_BYTES =
-      1024 + STAGES * STAGE_BYTES + NBAR * 8 + 16 + (int)sizeof(Mx4Tables) + 16;
+      1024 + STAGES * STAGE_BYTES + NBAR * 8 + 32 + (int)sizeof(Mx4Tables) + 16;
   static_assert(ROW_OFF % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzled images: 1024 bytes");
   static_assert(SF_COL + 48 <= TMEM_COLS, "scale columns");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* peer_abort = abort_flag + 1;   // pair: the other CTA's flag and the k-blocks
   volatile int* peer_issued = abort_flag + 2;  // that it has issued, written by it at its end
-  Mx4Tables& tb = *reinterpret_cast<Mx4Tables*>(tmem_slot + 4);
+  volatile int* committed = abort_flag + 3;    // k-blocks and accumulators that the issuer has committed
+  Mx4Tables& tb = *reinterpret_cast<Mx4Tables*>(tmem_slot + 8);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int NT = N / kMx4WTile;
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     *peer_abort = 0;
     *peer_issued = 0;
+    committed[0] = committed[1] = 0;
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);                            // the (even) producer; all bytes
       mbar_init(&empty[s], 1);                           // the MMA's commit
@@ -292,6 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_l2(rimg + nx.row_img + (size_t)kb * nx.rows16 * 128, nx.rows16 * 128);
         }
       }
+      // the last k-blocks' commits arrive in this CTA, the odd one too: it does not leave before
+      // (the epilogue has waited for every accumulator's)
+      for (int i = (it > C::STAGES ? it - C::STAGES : 0); i < it && !aborted; ++i)
+        aborted = !mbar_wait_bounded(&empty[i % C::STAGES], (i / C::STAGES) & 1, abort_flag, status,
+                                     spin_limit);
       issued = it;
       if constexpr (PAIR) st_shared_remote(mapa_shared(smem_u32((const void*)peer_issued), rank ^ 1), it);
     }
@@ -356,6 +363,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (PAIR) mma_commit_pair(mma_done, 0x1);
       else mma_commit(mma_done);
       wait_drain(mma_done, 0, kSpinLimitCycles);
+      committed[0] = it;
+      committed[1] = tcount;
+      if constexpr (PAIR)
+        for (int i = 0; i < 2; ++i)
+          st_shared_remote(mapa_shared(smem_u32((const void*)(committed + i)), 1), i ? tcount : it);
     }
     __syncwarp();
   } else {
@@ -413,7 +425,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // still be in flight (of a unit that no MMA took: whoever gave up, the producer need not
     // have noticed).  A stage that only one CTA of a pair has issued gets the other's bytes now
     // (its slot's last MMAs are complete, or the one could not have issued it), so that its barrier
-    // completes; the even CTA waits for the bytes of both.
+    // completes; the even CTA waits for the bytes of both.  A role that gave up did not wait for
+    // the commits that arrive in its CTA: thread 0 does.
+    if (threadIdx.x == 0) {
+      const int blocks = committed[0], tiles = committed[1];
+      for (int i = (blocks > C::STAGES ? blocks - C::STAGES : 0); i < blocks; ++i)
+        wait_drain(&empty[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
+      for (int i = (tiles > 2 ? tiles - 2 : 0); i < tiles; ++i)
+        wait_drain(&tfull[i & 1], (i >> 1) & 1, kSpinLimitCycles);
+    }
     if (issued >= 0) {
       int n = issued;
       if constexpr (PAIR) {

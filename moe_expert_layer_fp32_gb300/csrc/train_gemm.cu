@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
   volatile int* issued = abort_flag + 2;  // k-blocks issued of A and B here, and by the other CTA
   int* s_total = reinterpret_cast<int*>(tmem_slot + 7);
   int* s_bad = s_total + 1;
+  volatile int* committed = s_bad + 1;  // k-blocks and accumulators that the issuer has committed
   int* s_off = reinterpret_cast<int*>(tmem_slot + 12);
   int* s_prefix = s_off + (kMaxE + 1);  // PRODUCT: first unit of an expert
   int* s_exp = s_prefix;                // WGRAD: experts by falling number of rows
@@ -369,6 +370,7 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
     *abort_flag = 0;
     *peer_abort = 0;
     for (int i = 0; i < 4; ++i) issued[i] = 0;
+    committed[0] = committed[1] = 0;
     *s_bad = (smem_u32(smem) & 1023u) != 0;  // (never: asked for above)
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -543,14 +545,21 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
       loads = true;
       int s = 0;
       uint32_t ph = 1;
+      bool ok = true;
       while (advance()) {
-        if (!mbar_wait_bounded(&empty[s], ph, abort_flag, p.status, p.limit)) break;
+        ok = mbar_wait_bounded(&empty[s], ph, abort_flag, p.status, p.limit);
+        if (!ok) break;
         load(s);
         if (++s == C::STAGES) {
           s = 0;
           ph ^= 1;
         }
       }
+      // the last k-blocks' commits arrive in this CTA, the odd one too: it does not leave before
+      // (the epilogue has waited for every accumulator's)
+      for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it && ok; ++i)
+        ok = mbar_wait_bounded(&empty[i % C::STAGES], (i / C::STAGES) & 1, abort_flag, p.status,
+                               p.limit);
       issued[second] = it;
       if constexpr (CTAS == 2)
         st_shared_remote(mapa_shared(smem_u32((const void*)(issued + 2 + second)), rank ^ 1), it);
@@ -564,7 +573,7 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
       const uint64_t a_km = sdesc_k_major_sw128(smem_u32(sA)), a_tm = sdesc_mn_major_sw128(smem_u32(sA));
       const uint64_t b_km = sdesc_k_major_sw128(smem_u32(sB)), b_tm = sdesc_mn_major_sw128(smem_u32(sB));
       constexpr uint32_t KM_STEP = UK * 2 / 16, MN_STEP = UK * 128 / 16;
-      int s = 0, tcount = 0;
+      int s = 0, tcount = 0, blocks = 0;
       uint32_t ph = 0;
       bool aborted = false;
       for (int i = 0; i * P < total && !aborted; ++i) {
@@ -604,6 +613,7 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
           }
           if constexpr (CTAS == 2) mma_commit_pair(&empty[s], 0x3);
           else mma_commit(&empty[s]);
+          ++blocks;
           if (++s == C::STAGES) {
             s = 0;
             ph ^= 1;
@@ -618,6 +628,11 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
       if constexpr (CTAS == 2) mma_commit_pair(mma_done, 0x1);
       else mma_commit(mma_done);
       wait_drain(mma_done, 0, kSpinLimitCycles);
+      committed[0] = blocks;
+      committed[1] = tcount;
+      if constexpr (CTAS == 2)
+        for (int i = 0; i < 2; ++i)
+          st_shared_remote(mapa_shared(smem_u32((const void*)(committed + i)), 1), i ? tcount : blocks);
     }
   } else {
     // -------------------------------------------------------------- epilogue
@@ -732,7 +747,15 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
     // still be in flight.  A stage that one producer has issued and another has not gets the
     // other's bytes now (its slot's last MMAs are complete, or the one could not have issued
     // it), so that its barrier completes; the even CTA waits for the bytes of both.
+    // A role that gave up did not wait for the commits that arrive in its CTA: thread 0 does.
     const int most = max(max(issued[0], issued[1]), max(issued[2], issued[3]));
+    if (threadIdx.x == 0) {
+      const int blocks = committed[0], tiles = committed[1];
+      for (int i = (blocks > C::STAGES ? blocks - C::STAGES : 0); i < blocks; ++i)
+        wait_drain(&empty[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
+      for (int i = (tiles > 2 ? tiles - 2 : 0); i < tiles; ++i)
+        wait_drain(&tfull[i & 1], (i >> 1) & 1, kSpinLimitCycles);
+    }
     if (loads)
       while (it < most && advance()) load(it % C::STAGES);
     if (threadIdx.x == 0 && rank == 0)
