@@ -94,11 +94,17 @@ cudaError_t launch_batch(const TrainBatch& q, cudaStream_t s);
 // h [R, I] = w silu(gate) up of gate_up [R, 2 I] (w: [R] FP32 or null)
 cudaError_t launch_swiglu(const void* gate_up, long long gu_ld, const float* w, int type, int R,
                           int I, void* h, long long h_ld, cudaStream_t s);
-// its gradient for d [R, I]; h (w silu(gate) up) and d_w [R] may be null
+// its gradient for d [R, I]; h (w silu(gate) up) and d_w [R] may be null.  offsets [E + 1] (null:
+// not looked at): nothing is written if they are not a sequence from 0 to R.
 cudaError_t launch_swiglu_bwd(const void* gate_up, long long gu_ld, const void* d, long long d_ld,
                               const float* w, int type, int R, int I, void* d_gate_up,
                               long long dgu_ld, void* h, long long h_ld, float* d_w,
-                              cudaStream_t s);
+                              const int32_t* offsets, int E, cudaStream_t s);
+
+// A grouped call without rows: offsets [E + 1] other than zeros are flagged, else (out not null) the E
+// slices of rows x cols elements of elt bytes become zeros (rows of whole 16-byte pieces).
+cudaError_t launch_no_rows(const int32_t* offsets, int E, int32_t* status, void* out, int elt, int rows,
+                           int cols, long long ld, long long es, cudaStream_t s);
 
 // First step of an orthogonalisation: x [E][rows][ld] FP16 (ld = cols padded to 8) = M 2^k, x_lo what its rounding left, times 2048 (null: without),
 // f[e] = 2^-k / (|M| + eps), f[E + e] = f[e]^2.

@@ -82,23 +82,14 @@ GroupedLayout grouped_layout(int E, int K, int N) {
   return L;
 }
 
-moe_status zero_stack(void* out, int dtype, int E, long long rows, long long cols, long long ld,
-                      long long es, cudaStream_t s) {
-  const size_t b = bytes_of(dtype);
-  if (es == rows * ld || E == 1) {
-    MOE_CUDA(cudaMemset2DAsync(out, ld * b, 0, cols * b, (size_t)E * rows, s));
-    return MOE_OK;
-  }
-  for (int e = 0; e < E; ++e)
-    MOE_CUDA(cudaMemset2DAsync(static_cast<uint8_t*>(out) + e * es * b, ld * b, 0, cols * b, rows,
-                               s));
-  return MOE_OK;
-}
-
 moe_status do_product(const void* x, long long x_ld, int type, const int32_t* offsets,
                       const void* w, long long w_ld, long long w_es, bool turned, int R, int K,
                       int N, int E, void* y, long long y_ld, int y_type, void* ws,
                       cudaStream_t s) {
+  if (R == 0) {
+    MOE_CUDA(launch_no_rows(offsets, E, static_cast<int32_t*>(ws), nullptr, 0, 0, 0, 0, 0, s));
+    return MOE_OK;
+  }
   TrainProduct q;
   q.x = x;
   q.offsets = offsets;
@@ -124,7 +115,11 @@ moe_status do_product(const void* x, long long x_ld, int type, const int32_t* of
 moe_status do_wgrad(const void* x, long long x_ld, const void* dy, long long dy_ld, int type,
                     const int32_t* offsets, int R, int K, int N, int E, void* out, long long ld,
                     long long es, int out_type, bool accumulate, void* ws, cudaStream_t s) {
-  if (R == 0) return accumulate ? MOE_OK : zero_stack(out, out_type, E, K, N, ld, es, s);
+  if (R == 0) {
+    MOE_CUDA(launch_no_rows(offsets, E, static_cast<int32_t*>(ws), accumulate ? nullptr : out,
+                            bytes_of(out_type), K, N, ld, es, s));
+    return MOE_OK;
+  }
   TrainWgrad q;
   q.x = x;
   q.dy = dy;
@@ -275,7 +270,7 @@ moe_status moe_swiglu_bwd(const void* gate_up, int64_t gate_up_ld, const void* d
   if (d_row_w != nullptr) MOE_TRY(validate_ptr(d_row_w));
   MOE_TRY(validate_device());
   MOE_CUDA(launch_swiglu_bwd(gate_up, gate_up_ld, d_h, d_ld, row_w, dtype, R, I, d_gate_up,
-                             d_gate_up_ld, h, h_ld, d_row_w, as_stream(stream)));
+                             d_gate_up_ld, h, h_ld, d_row_w, nullptr, 0, as_stream(stream)));
   return MOE_OK;
 }
 
@@ -319,7 +314,7 @@ moe_status moe_expert_ffn_bwd(const void* x_perm, const int32_t* offsets, const 
   MOE_TRY(do_product(d_y, H, dtype, offsets, w_down, H, (long long)H * I, true, R, H, I, E, d_h, I,
                      dtype, ws, s));
   MOE_CUDA(launch_swiglu_bwd(gate_up, 2 * I, d_h, I, row_w, dtype, R, I, dgu, 2 * I,
-                             d_w_down ? h : nullptr, I, d_row_w, s));
+                             d_w_down ? h : nullptr, I, d_row_w, offsets, E, s));
   if (d_w_down != nullptr)
     MOE_TRY(do_wgrad(h, I, d_y, H, dtype, offsets, R, I, H, E, d_w_down, H, (long long)H * I,
                      d_w_dtype, accumulate != 0, ws, s));

@@ -52,13 +52,27 @@ __device__ __forceinline__ void swiglu_bwd_pair(uint32_t g, uint32_t u, uint32_t
 // (513 x 1024: 5.4 us, the host's launch and two allocations).
 constexpr int PIECES = 3, ROW_WARPS = 8;
 
+// Whether offsets [E + 1] are a non-decreasing sequence from 0 to R: the same answer in every thread of
+// the block.
+__device__ __forceinline__ bool block_sequence(const int32_t* __restrict__ offsets, int E, int R) {
+  int bad = 0;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    const int a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
+    bad |= b < a || (e == 0 && a != 0) || (e == E - 1 && b != R);
+  }
+  return !__syncthreads_or(bad);
+}
+
 template <int TYPE, bool BWD>
 __global__ void __launch_bounds__(32 * ROW_WARPS)
     swiglu_kernel(const uint8_t* __restrict__ gu, long long gu_ld, const uint8_t* __restrict__ d,
                   long long d_ld, const float* __restrict__ w, int R, int I, uint8_t* dgu,
-                  long long dgu_ld, uint8_t* h, long long h_ld, float* d_w) {
+                  long long dgu_ld, uint8_t* h, long long h_ld, float* d_w,
+                  const int32_t* __restrict__ offsets, int E) {
   pdl_wait();
   pdl_launch_dependents();
+  // (bad offsets: the product that d comes from wrote nothing)
+  if (BWD && offsets && !block_sequence(offsets, E, R)) return;
   const int lane = threadIdx.x & 31;
   for (long long r = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5); r < R;
        r += (long long)gridDim.x * ROW_WARPS) {
@@ -120,7 +134,8 @@ __global__ void __launch_bounds__(32 * ROW_WARPS)
 template <bool BWD>
 cudaError_t launch_rows(const void* gu, long long gu_ld, const void* d, long long d_ld,
                         const float* w, int type, int R, int I, void* dgu, long long dgu_ld,
-                        void* h, long long h_ld, float* d_w, cudaStream_t s) {
+                        void* h, long long h_ld, float* d_w, const int32_t* offsets, int E,
+                        cudaStream_t s) {
   if (R == 0) return cudaSuccess;
   const long long need = ((long long)R + ROW_WARPS - 1) / ROW_WARPS;
   const long long most = 8LL * device_sm_count();
@@ -129,7 +144,24 @@ cudaError_t launch_rows(const void* gu, long long gu_ld, const void* d, long lon
                                      : swiglu_kernel<MOE_DTYPE_F16, BWD>;
   return launch_pdl(kern, grid, dim3(32 * ROW_WARPS), 0, s, static_cast<const uint8_t*>(gu), gu_ld,
                     static_cast<const uint8_t*>(d), d_ld, w, R, I, static_cast<uint8_t*>(dgu),
-                    dgu_ld, static_cast<uint8_t*>(h), h_ld, d_w);
+                    dgu_ld, static_cast<uint8_t*>(h), h_ld, d_w, offsets, E);
+}
+
+__global__ void __launch_bounds__(256)
+    no_rows_kernel(const int32_t* __restrict__ offsets, int E, int32_t* status, uint8_t* out, int elt,
+                   int rows, int pieces, long long ld, long long es) {
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!block_sequence(offsets, E, 0)) {
+    if (threadIdx.x == 0) flag_error(status, MOE_ERR_DEVICE_CHECK);
+    return;
+  }
+  if (out == nullptr) return;
+  for (long long i = blockIdx.x; i < (long long)E * rows; i += gridDim.x) {
+    const long long e = i / rows, r = i - e * rows;
+    uint4* row = reinterpret_cast<uint4*>(out + (e * es + r * ld) * elt);
+    for (int c = threadIdx.x; c < pieces; c += blockDim.x) row[c] = make_uint4(0, 0, 0, 0);
+  }
 }
 
 // ------------------------------------------------ start of an orthogonalisation ---
@@ -338,15 +370,22 @@ cudaError_t start(const uint8_t* m, long long ld, long long es, int E, int rows,
 cudaError_t launch_swiglu(const void* gate_up, long long gu_ld, const float* w, int type, int R,
                           int I, void* h, long long h_ld, cudaStream_t s) {
   return launch_rows<false>(gate_up, gu_ld, nullptr, 0, w, type, R, I, nullptr, 0, h, h_ld, nullptr,
-                            s);
+                            nullptr, 0, s);
 }
 
 cudaError_t launch_swiglu_bwd(const void* gate_up, long long gu_ld, const void* d, long long d_ld,
                               const float* w, int type, int R, int I, void* d_gate_up,
                               long long dgu_ld, void* h, long long h_ld, float* d_w,
-                              cudaStream_t s) {
+                              const int32_t* offsets, int E, cudaStream_t s) {
   return launch_rows<true>(gate_up, gu_ld, d, d_ld, w, type, R, I, d_gate_up, dgu_ld, h, h_ld, d_w,
-                           s);
+                           offsets, E, s);
+}
+
+cudaError_t launch_no_rows(const int32_t* offsets, int E, int32_t* status, void* out, int elt, int rows,
+                           int cols, long long ld, long long es, cudaStream_t s) {
+  const long long need = out ? (long long)E * rows : 1, most = 8LL * device_sm_count();
+  return launch_pdl(no_rows_kernel, dim3((unsigned)(need < most ? need : most)), dim3(256), 0, s, offsets,
+                    E, status, static_cast<uint8_t*>(out), elt, rows, cols * elt / 16, ld, es);
 }
 
 cudaError_t launch_orth_start(const void* m, int type, long long ld_m, long long es_m, int E,
