@@ -53,6 +53,12 @@ enum Major { KM, MN, UPPER };  // UPPER: a symmetric matrix of which the upper t
 constexpr int GM = 128, GK = 64, UK = 16;
 constexpr int EPI_WARPS = 8, B_WARP = 2 + EPI_WARPS, THREADS = 32 * (B_WARP + 1);
 constexpr int BOX_ROWS = 16;  // A boxes of the single form of a product
+// k-blocks whose products one accumulator sums.  The tensor cores' addition drops up to 2^-23 of the
+// running sum at each step of sixteen products, always towards zero, so that an error grows with the
+// contraction (relative 2-norm, K = N = 256, random signs / one sign: 4096 rows 4.4e-6 / 1.4e-5, 131072
+// 1.5e-4 / 8.2e-4).  Longer sums are taken apart, and the parts added in FP32 by the epilogue.  (Not
+// in BATCH and SYM: at their longest, 16384, the error is a third of the rounding to FP16 behind them.)
+constexpr int SEG = 64;
 
 template <int CTAS, int BN>
 struct Shape {
@@ -95,6 +101,7 @@ struct Tile {
   int e, row0, nrows, col0;  // output rows [row0, row0 + nrows) of this CTA, first column
   int a_mn, b_mn;            // this CTA's first A row and B row (or column) of the maps
   int k0, kb, last16;        // first k (WGRAD: row), k-blocks, and 16-deep steps of the last
+  int segs;                  // parts of the sum, SEG k-blocks each
   bool tail;                 // WGRAD: the last k-block is the expert's tail
   int boxes;                 // A boxes of the single product form
 };
@@ -145,6 +152,22 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) {
@@ -335,11 +358,32 @@ __device__ __forceinline__ void zero_tile(uint4* st, int lane, int first, int co
     for (int c0 = first * cols; c0 < ncols; c0 += 2 * cols) tma_store_3d(map, st, col0 + c0, row0, e);
 }
 
+// Adds the accumulator at `part` to the one at `sum`, the columns that store_tile() gives this warp.
+template <int COLS>
+__device__ __forceinline__ void add_part(uint32_t sum, uint32_t part, int first, int ncols) {
+#pragma unroll 1
+  for (int c0 = first * COLS; c0 < ncols; c0 += 2 * COLS) {
+#pragma unroll 1
+    for (int c = c0; c < c0 + COLS; c += 32) {
+      uint32_t a[32], b[32];
+      tmem_ld_32x32b_x32(sum + c, a);
+      tmem_ld_32x32b_x32(part + c, b);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        a[j] = __float_as_uint(__uint_as_float(a[j]) + __uint_as_float(b[j]));
+      tmem_st_32x32b_x32(sum + c, a);
+    }
+  }
+  tmem_st_wait();
+}
+
 template <int CTAS, int BN, Kind KIND, Major A, Major B>
 __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_constant__ Args p) {
   using C = Shape<CTAS, BN>;
   constexpr int TM = GM * CTAS;
   constexpr bool BOXED = KIND == PRODUCT && CTAS == 1;
+  constexpr bool PARTS = KIND == PRODUCT || KIND == WGRAD;
   extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's period; there is no other)
   uint8_t* sA = smem;
   uint8_t* sB = smem + C::STAGES * C::A_BYTES;
@@ -356,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
   volatile int* issued = abort_flag + 2;  // k-blocks issued of A and B here, and by the other CTA
   int* s_total = reinterpret_cast<int*>(tmem_slot + 7);
   int* s_bad = s_total + 1;
-  volatile int* committed = s_bad + 1;  // k-blocks and accumulators that the issuer has committed
+  volatile int* committed = s_bad + 1;  // by the issuer: k-blocks, uses of either accumulator
   int* s_off = reinterpret_cast<int*>(tmem_slot + 12);
   int* s_prefix = s_off + (kMaxE + 1);  // PRODUCT: first unit of an expert
   int* s_exp = s_prefix;                // WGRAD: experts by falling number of rows
@@ -370,7 +414,7 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
     *abort_flag = 0;
     *peer_abort = 0;
     for (int i = 0; i < 4; ++i) issued[i] = 0;
-    committed[0] = committed[1] = 0;
+    for (int i = 0; i < 3; ++i) committed[i] = 0;
     *s_bad = (smem_u32(smem) & 1023u) != 0;  // (never: asked for above)
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -484,6 +528,7 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
     t.kb = (k + GK - 1) / GK;
     t.tail = KIND == WGRAD && k % GK != 0;
     t.last16 = (k - (t.kb - 1) * GK + UK - 1) / UK;
+    t.segs = PARTS ? (t.kb + SEG - 1) / SEG : 1;
     return t;
   };
   // the k-blocks of this CTA's units, in order
@@ -573,7 +618,8 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
       const uint64_t a_km = sdesc_k_major_sw128(smem_u32(sA)), a_tm = sdesc_mn_major_sw128(smem_u32(sA));
       const uint64_t b_km = sdesc_k_major_sw128(smem_u32(sB)), b_tm = sdesc_mn_major_sw128(smem_u32(sB));
       constexpr uint32_t KM_STEP = UK * 2 / 16, MN_STEP = UK * 128 / 16;
-      int s = 0, tcount = 0, blocks = 0;
+      int s = 0, acc0 = 0, blocks = 0;
+      int uses[2] = {0, 0};  // of either accumulator
       uint32_t ph = 0;
       bool aborted = false;
       for (int i = 0; i * P < total && !aborted; ++i) {
@@ -581,71 +627,100 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
         if (u >= total) break;
         const Tile t = tile_of(u);
         if (t.kb == 0) continue;
-        const int acc = tcount & 1;
-        if (!mbar_wait_bounded(&tempty[acc], ((tcount >> 1) & 1) ^ 1, abort_flag, p.status,
-                               p.limit))
-          break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * BN;
-        for (int kb = 0; kb < t.kb; ++kb) {
-          if (!mbar_wait_bounded(&full[s], ph, abort_flag, p.status, p.limit)) {
+        // a sum's first part stays where it is, the others pass through the other accumulator
+        for (int seg = 0; seg < t.segs && !aborted; ++seg) {
+          const int acc = seg == 0 ? acc0 : acc0 ^ 1;
+          const int used = acc ? uses[1] : uses[0];
+          if (!mbar_wait_bounded(&tempty[acc], (used & 1) ^ 1, abort_flag, p.status, p.limit)) {
             aborted = true;
             break;
           }
           tc_fence_after();
-          const bool a_mn = A == MN || (A == UPPER && kb * GK / TM < t.row0 / TM);
-          const bool b_mn = B == MN || (B == UPPER && kb * GK / TM < t.col0 / TM);
-          const uint32_t idesc = idesc0 | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
-          const uint64_t da = (a_mn ? a_tm : a_km) + (uint32_t)(s * (C::A_BYTES / 16));
-          const uint64_t db = (b_mn ? b_tm : b_km) + (uint32_t)(s * (C::B_BYTES / 16));
-          const uint32_t ga = a_mn ? MN_STEP : KM_STEP, gb = b_mn ? MN_STEP : KM_STEP;
-          auto mma = [&](int kk) {
-            if constexpr (CTAS == 2)
-              mma_bf16_pair(d_tmem, da + kk * ga, db + kk * gb, idesc, kk > 0 || kb > 0 ? 1u : 0u);
-            else
-              mma_bf16(d_tmem, da + kk * ga, db + kk * gb, idesc, kk > 0 || kb > 0 ? 1u : 0u);
-          };
-          if (kb + 1 < t.kb || t.last16 == GK / UK) {
+          const uint32_t d_tmem = tmem_base + acc * BN;
+          const int kb0 = PARTS ? seg * SEG : 0, kb1 = PARTS ? min(t.kb, kb0 + SEG) : t.kb;
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait_bounded(&full[s], ph, abort_flag, p.status, p.limit)) {
+              aborted = true;
+              break;
+            }
+            tc_fence_after();
+            const bool a_mn = A == MN || (A == UPPER && kb * GK / TM < t.row0 / TM);
+            const bool b_mn = B == MN || (B == UPPER && kb * GK / TM < t.col0 / TM);
+            const uint32_t idesc = idesc0 | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
+            const uint64_t da = (a_mn ? a_tm : a_km) + (uint32_t)(s * (C::A_BYTES / 16));
+            const uint64_t db = (b_mn ? b_tm : b_km) + (uint32_t)(s * (C::B_BYTES / 16));
+            const uint32_t ga = a_mn ? MN_STEP : KM_STEP, gb = b_mn ? MN_STEP : KM_STEP;
+            auto mma = [&](int kk) {
+              const uint32_t more = kk > 0 || kb > kb0 ? 1u : 0u;
+              if constexpr (CTAS == 2)
+                mma_bf16_pair(d_tmem, da + kk * ga, db + kk * gb, idesc, more);
+              else
+                mma_bf16(d_tmem, da + kk * ga, db + kk * gb, idesc, more);
+            };
+            if (kb + 1 < t.kb || t.last16 == GK / UK) {
 #pragma unroll
-            for (int kk = 0; kk < GK / UK; ++kk) mma(kk);
-          } else {
-            for (int kk = 0; kk < t.last16; ++kk) mma(kk);
+              for (int kk = 0; kk < GK / UK; ++kk) mma(kk);
+            } else {
+              for (int kk = 0; kk < t.last16; ++kk) mma(kk);
+            }
+            if constexpr (CTAS == 2) mma_commit_pair(&empty[s], 0x3);
+            else mma_commit(&empty[s]);
+            ++blocks;
+            if (++s == C::STAGES) {
+              s = 0;
+              ph ^= 1;
+            }
           }
-          if constexpr (CTAS == 2) mma_commit_pair(&empty[s], 0x3);
-          else mma_commit(&empty[s]);
-          ++blocks;
-          if (++s == C::STAGES) {
-            s = 0;
-            ph ^= 1;
-          }
+          if (aborted) break;
+          if constexpr (CTAS == 2) mma_commit_pair(&tfull[acc], 0x3);
+          else mma_commit(&tfull[acc]);
+          if (acc) ++uses[1];
+          else ++uses[0];
         }
-        if (aborted) break;
-        if constexpr (CTAS == 2) mma_commit_pair(&tfull[acc], 0x3);
-        else mma_commit(&tfull[acc]);
-        ++tcount;
+        acc0 ^= 1;
       }
       // every MMA this thread issued completes before tensor memory is released
       if constexpr (CTAS == 2) mma_commit_pair(mma_done, 0x1);
       else mma_commit(mma_done);
       wait_drain(mma_done, 0, kSpinLimitCycles);
-      committed[0] = blocks;
-      committed[1] = tcount;
-      if constexpr (CTAS == 2)
-        for (int i = 0; i < 2; ++i)
-          st_shared_remote(mapa_shared(smem_u32((const void*)(committed + i)), 1), i ? tcount : blocks);
+      const int done[3] = {blocks, uses[0], uses[1]};
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        committed[i] = done[i];
+        if constexpr (CTAS == 2)
+          st_shared_remote(mapa_shared(smem_u32((const void*)(committed + i)), 1), done[i]);
+      }
     }
   } else {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3;  // TMEM lane quarter this warp may access
     const int first = (warp - 2) >> 2;
     uint4* st = s_epi + (warp - 2) * (32 * 8);
-    int tcount = 0;
+    int tcount = 0, odd = 0;  // PARTS, bit a of odd: the next use of accumulator a is an odd one
+    // the next use's products of accumulator a are there
+    auto ready = [&](int a) {
+      int ok = 1;
+      if (lane == 0)
+        ok = mbar_wait_bounded(&tfull[a], (PARTS ? odd >> a : tcount >> 1) & 1, abort_flag, p.status,
+                               p.limit);
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (PARTS) odd ^= 1 << a;
+      tc_fence_after();
+      return ok != 0;
+    };
+    auto release = [&](int a) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CTAS == 2) mbar_arrive_remote(mapa_shared(smem_u32(&tempty[a]), 0));
+        else mbar_arrive(&tempty[a]);
+      }
+    };
     for (int i = 0; i * P < total; ++i) {
       const int u = unit_of(i);
       if (u >= total) break;
       const Tile t = tile_of(u);
       if (KIND == WGRAD && t.kb == 0 && p.c != nullptr) continue;  // nothing to add
-      const int acc = tcount & 1;
       const bool sums = KIND != WGRAD || t.kb > 0;
       if constexpr (KIND == BATCH) {  // this tile's rows of c move into L2 while it is multiplied
         const int row = t.row0 + q * 32 + lane;
@@ -657,17 +732,24 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
           }
         }
       }
-      if (sums) {
-        int ok = 1;
-        if (lane == 0)
-          ok = mbar_wait_bounded(&tfull[acc], (tcount >> 1) & 1, abort_flag, p.status, p.limit);
-        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-        if (!ok) break;
-        tc_fence_after();
-      }
+      const int acc = tcount & 1;
+      if (sums && !ready(acc)) break;
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
       const int nrows = min(32, t.nrows - q * 32);
       const int ncols = min(BN, p.n_lim - t.col0);
+      if constexpr (PARTS) {
+        bool ok = true;
+        for (int seg = 1; seg < t.segs && ok; ++seg) {
+          ok = ready(acc ^ 1);
+          if (ok && nrows > 0) {
+            const uint32_t part = acc ? taddr - BN : taddr + BN;
+            if (p.out_type == MOE_DTYPE_F32) add_part<32>(taddr, part, first, ncols);
+            else add_part<64>(taddr, part, first, ncols);
+          }
+          if (ok) release(acc ^ 1);
+        }
+        if (!ok) break;
+      }
       if (nrows > 0) {
         const int row0 = t.row0 + q * 32;
         const long long at = (KIND == PRODUCT ? 0 : t.e * p.es) + row0 * p.ld + t.col0;
@@ -721,12 +803,7 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
         }
       }
       if (sums) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CTAS == 2) mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
-          else mbar_arrive(&tempty[acc]);
-        }
+        release(acc);
         ++tcount;
       }
     }
@@ -750,11 +827,11 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
     // A role that gave up did not wait for the commits that arrive in its CTA: thread 0 does.
     const int most = max(max(issued[0], issued[1]), max(issued[2], issued[3]));
     if (threadIdx.x == 0) {
-      const int blocks = committed[0], tiles = committed[1];
+      const int blocks = committed[0];
       for (int i = (blocks > C::STAGES ? blocks - C::STAGES : 0); i < blocks; ++i)
         wait_drain(&empty[i % C::STAGES], (i / C::STAGES) & 1, kSpinLimitCycles);
-      for (int i = (tiles > 2 ? tiles - 2 : 0); i < tiles; ++i)
-        wait_drain(&tfull[i & 1], (i >> 1) & 1, kSpinLimitCycles);
+      for (int a = 0; a < 2; ++a)
+        if (committed[1 + a] > 0) wait_drain(&tfull[a], (committed[1 + a] - 1) & 1, kSpinLimitCycles);
     }
     if (loads)
       while (it < most && advance()) load(it % C::STAGES);
