@@ -168,12 +168,14 @@ OrthLayout orth_layout(int E, int rows, int cols) {
 }
 constexpr float kHeld = 1024.0f;  // X, A and B are held in FP16 times this
 constexpr int kMaxSteps = 64;
-// The first iterates (M itself, if FP32, and the next ones) also keep what their rounding to FP16
-// left, which counts in a X only: later steps lift a rounding there up to a times each, and B X
-// does not lift it (B vanishes where the singular values do).  Without: an error of 0.041 for rank
-// 8 of 500 x 720, 0.0021 for full-rank momenta; three kept 0.0024 and 0.0008, all five 0.0003 and
-// 0.0009, at a read and a write of X more each (64 x 1024 x 2048 BF16: 2183 us without, 2250 with).
-constexpr int kKeepLow = 3;
+// The iterates (M itself, if FP32, and the next ones) also keep what their rounding to FP16 left,
+// which counts in a X only: later steps lift a rounding there up to a times each, and B X does not
+// lift it (B vanishes where the singular values do).  The last two need not (a rounding of
+// theirs is lifted twice at most).  Without: an error of 0.041 for rank 8 of 500 x 720,
+// 0.0021 for full-rank momenta; three kept 0.0024 and 0.0008, all five 0.0003 and 0.0009, at a read
+// and a write of X more each (64 x 1024 x 2048 BF16: 2183 us without, 2250 with).  Three kept of ten
+// steps: 1.8 for rank 8 of 300 x 500, eight 0.022 (FP32 throughout 0.021).
+inline int keep_low(int steps) { return steps > 5 ? steps - 2 : 3; }
 
 bool orth_sizes(int E, int rows, int cols) {
   return E > 0 && rows > 0 && cols > 0 && E <= kMaxE && rows <= 16384 && cols <= 16384;
@@ -376,6 +378,7 @@ moe_status moe_orthogonalize(const void* m, int32_t dtype, int64_t ld, int64_t e
   q.pair = batch_pairs(E, rows, cols);
   q.status = static_cast<int32_t*>(workspace);
   q.limit = wait_limit();
+  const int keep = keep_low(steps);
   for (int i = 0; i < steps; ++i) {
     const bool first = i == 0, last = i == steps - 1;
     const float held = first ? 1.0f : kHeld;  // x holds X times this (the first: X / f_e)
@@ -419,7 +422,7 @@ moe_status moe_orthogonalize(const void* m, int32_t dtype, int64_t ld, int64_t e
     q.M = rows;
     q.N = cols;
     q.c = x;
-    q.c_lo = i < kKeepLow && (i > 0 || dtype == MOE_DTYPE_F32) ? lo : nullptr;
+    q.c_lo = i < keep && (i > 0 || dtype == MOE_DTYPE_F32) ? lo : nullptr;
     q.c_ld = lx;
     q.c_es = xs;
     q.alpha = next / (held * kHeld);
@@ -427,7 +430,7 @@ moe_status moe_orthogonalize(const void* m, int32_t dtype, int64_t ld, int64_t e
     q.alpha_e = q.beta_e = first ? f : nullptr;
     q.padded = !last;
     q.out = last ? out : x1;
-    q.out_lo = last || i + 1 >= kKeepLow ? nullptr : lo1;
+    q.out_lo = last || i + 1 >= keep ? nullptr : lo1;
     q.ld = last ? out_ld : lx;
     q.es = last ? out_es : xs;
     q.out_type = last ? out_dtype : MOE_DTYPE_F16;

@@ -6,8 +6,11 @@
 // X stays in registers in FP32 (a thread has half a row, 128 columns); what the tensor cores
 // read (X, A, B) goes to shared memory in FP16 times 1024, in rows of 128 bytes with the
 // 128-byte swizzle.  The same image of X serves both products: its rows as the K-major operands of
-// X X^T, and as the MN-major operand of B X.  B's diagonal, its largest values, stays in FP32 and joins
-// a (its rounding is most of the error of these sizes).  Everything waits on everything in a step, so the
+// X X^T, and as the MN-major operand of B X.  What the rounding of B's diagonal, its largest values,
+// left joins a in FP32 (it is most of the error of these sizes).  The diagonal itself multiplies the
+// rounded X as the rest of B does: what X's rounding leaves outside of X's span then stays of second order
+// in B X, where one part of B on X unrounded brings it in at first order (the whole diagonal there: rank
+// 8 of 128 x 256 was 0.1 off after eight steps, each of which lifts it a times).  Everything waits on everything in a step, so the
 // time is that of 3 x steps dependent products with their barriers (about 1.6 us each) and of the
 // way in and out (18 us), not of bytes or operations: 41 us for 8 matrices of 128 x 256, five steps
 // (36 with the diagonal in FP16).
@@ -218,8 +221,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
     for (int j = 0; j < 64; ++j)
       if (64 * h + j == r) {
-        diagonal[r] = g[j];
-        g[j] = 0.0f;
+        diagonal[r] = g[j] - __half2float(__float2half_rn(g[j] * HELD)) * (1.0f / HELD);
       }
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
