@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(256, 1)
   const float norm = sqrtf(sq) + eps * s1 * s2;
   const float inv = !(norm <= 0x1.fffffep127f) && !(eps * s1 * s2 > 0x1.fffffep127f)
                         ? __int_as_float(0x7FC00000)  // NaN or an infinity in M
-                        : (norm > 0.0f ? 1.0f / norm : 0.0f);
+                        : (sq > 0.0f ? 1.0f / norm : 0.0f);  // (sq at least 1, or M is zero)
 #pragma unroll
   for (int j = 0; j < HALF; ++j) x[j] *= inv;
 

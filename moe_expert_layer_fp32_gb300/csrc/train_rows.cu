@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(256)
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     const float total = norm + eps;
-    float v = !finite ? __int_as_float(0x7FC00000) : total > 0.0f ? ldexpf(1.0f / total, -k) : 0.0f;
+    float v = !finite ? __int_as_float(0x7FC00000) : norm > 0.0f ? ldexpf(1.0f / total, -k) : 0.0f;
     f[e] = v;
     f[E + e] = v * v;
   }
