@@ -1,5 +1,5 @@
 // Row-wise operators that train the experts: SwiGLU and its gradient, and the first step of an
-// orthogonalisation (norm, scaling and, for tall matrices, transposition).
+// orthogonalisation (norm and scaling).
 #include "common.cuh"
 #include "kernels.cuh"
 #include "pdl.cuh"
@@ -234,20 +234,23 @@ __device__ __forceinline__ void pieces(const uint8_t* m, long long row_bytes, in
   }
 }
 
-// Sums of squares: pieces whose sum leaves [2^-60, 2^100] are summed scaled by 2^-64 (big) or 2^64
-// (small) instead, so that no size of matrix overflows or vanishes.
+// Sums of squares: pieces whose sum leaves [2^-80, 2^100] are summed from values times 2^-80 (big) or
+// 2^88 (small) instead, so that no finite matrix of up to 2^28 elements overflows (mid at most 2^125, big
+// 2^(2 (128 - 80) + 28), small 2^(-80 + 2 * 88 + 25)) and the smallest value's square, 2^(2 (88 - 149)), is no
+// subnormal number.
+constexpr int kBig = -80, kSmall = 88;
 struct Squares {
   float mid, big, small;
   __device__ void add(const float (&v)[8]) {
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
-    if (s >= 0x1p-60f && s <= 0x1p100f) {
+    if (s >= 0x1p-80f && s <= 0x1p100f) {
       mid += s;
       return;
     }
-    const bool tiny = s < 0x1p-60f;
-    const float by = tiny ? 0x1p64f : 0x1p-64f;
+    const bool tiny = s < 0x1p-80f;
+    const float by = tiny ? 0x1p88f : 0x1p-80f;
     float t = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) t = fmaf(v[j] * by, v[j] * by, t);
@@ -292,8 +295,9 @@ __global__ void __launch_bounds__(256)
 }
 
 // x [E][rows][ldx] (ldx = cols padded to 8, the padding zero) = M 2^k in FP16, `per` rows a block.
-// 2^k brings the norm to [512, 1024): the elements of a BF16 matrix stay exact, and neither a
-// product of rows nor (with eps) 1 / norm comes near FP32's ends.
+// 2^k brings the norm to [512, 1024): elements of a BF16 matrix stay exact down to 2^-24 of the norm
+// (below they are rounded to a multiple of 2^-33 of it at most), and neither a product of rows nor (with
+// eps) 1 / norm comes near FP32's ends.
 template <int TYPE, bool VEC>
 __global__ void __launch_bounds__(256)
     scale_kernel(const uint8_t* __restrict__ m, long long ld, long long es, int rows, int cols,
@@ -309,20 +313,27 @@ __global__ void __launch_bounds__(256)
     for (int i = threadIdx.x; i < nb; i += blockDim.x) v += parts[((long long)e * 3 + j) * nb + i];
     s[j] = block_sum(v, sh);
   }
-  float norm;
-  if (!(s[1] <= 0.0f)) norm = sqrtf(s[1] + s[0] * 0x1p-128f) * 0x1p64f;  // (NaN too)
-  else if (!(s[0] <= 0.0f)) norm = sqrtf(s[0] + s[2] * 0x1p-128f);
-  else norm = sqrtf(s[2]) * 0x1p-64f;
-  int k = 0;
-  const bool finite = norm <= 0x1.fffffep127f;
-  if (finite && norm > 0.0f) {
-    int ex;
-    frexpf(norm, &ex);  // norm = r 2^ex, r in [0.5, 1)
-    k = 10 - ex;
+  float root;  // |M| 2^by, which FP32 holds whatever |M| is
+  int by = 0;
+  if (!(s[1] <= 0.0f)) {  // (NaN too)
+    root = sqrtf(ldexpf(s[0], 2 * kBig) + s[1]);
+    by = kBig;
+  } else if (!(s[0] <= 0.0f)) {
+    root = sqrtf(s[0] + ldexpf(s[2], -2 * kSmall));
+  } else {
+    root = sqrtf(s[2]);
+    by = kSmall;
+  }
+  int k = 0, ex = 0;
+  const bool finite = root <= 0x1.fffffep127f;
+  if (finite && root > 0.0f) {
+    frexpf(root, &ex);  // root = r 2^ex, r in [0.5, 1)
+    k = 10 - ex + by;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    const float total = norm + eps;
-    float v = !finite ? __int_as_float(0x7FC00000) : norm > 0.0f ? ldexpf(1.0f / total, -k) : 0.0f;
+    // 2^-k / (|M| + eps), as 1 / (|M| 2^k + eps 2^k)
+    const float norm = ldexpf(root, 10 - ex);
+    float v = !finite ? __int_as_float(0x7FC00000) : root > 0.0f ? 1.0f / (norm + ldexpf(eps, k)) : 0.0f;
     f[e] = v;
     f[E + e] = v * v;
   }
