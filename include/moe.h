@@ -631,7 +631,7 @@ size_t moe_orthogonalize_workspace_bytes(int32_t E, int32_t rows, int32_t cols);
  * 0.02: what FP32's sums leave outside of a low-rank matrix's span is lifted too, about a^steps 2^-23
  * (ten steps in FP32 throughout: 0.02).  Values of X below 2^-24 lose bits and those below 2^-45
  * vanish, which shows where |M_e| is far below eps.  Coefficients that let |X| grow past 60 overflow
- * FP16.  out may be m. */
+ * FP16.  out may be m, or overlap it in any way. */
 moe_status moe_orthogonalize(const void* m, int32_t dtype, int64_t ld, int64_t es, int32_t E,
                              int32_t rows, int32_t cols, const float* coefficients, int32_t steps,
                              float eps, float scale, void* out, int32_t out_dtype, int64_t out_ld,

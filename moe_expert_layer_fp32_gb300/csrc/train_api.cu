@@ -177,6 +177,18 @@ constexpr int kMaxSteps = 64;
 // steps: 1.8 for rank 8 of 300 x 500, eight 0.022 (FP32 throughout 0.021).
 inline int keep_low(int steps) { return steps > 5 ? steps - 2 : 3; }
 
+// Whether result e may lie in bytes of another matrix than e, whose CTA of the one-kernel form may not
+// have read it yet.  (The chain of kernels writes out in its last launch.)
+bool orth_crosses(const void* m, int dtype, long long ld, long long es, const void* out, long long out_ld,
+                  long long out_es, int E, int rows, int cols) {
+  const int b = bytes_of(dtype);
+  if (E == 1 || (m == out && b == 2 && ld == out_ld && es == out_es)) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(m), o = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t a_end = a + ((E - 1) * es + (rows - 1) * ld + cols) * b;
+  const uintptr_t o_end = o + ((E - 1) * out_es + (rows - 1) * out_ld + cols) * 2;
+  return a < o_end && o < a_end;
+}
+
 bool orth_sizes(int E, int rows, int cols) {
   return E > 0 && rows > 0 && cols > 0 && E <= kMaxE && rows <= 16384 && cols <= 16384;
 }
@@ -356,7 +368,8 @@ moe_status moe_orthogonalize(const void* m, int32_t dtype, int64_t ld, int64_t e
   MOE_TRY(check_workspace(workspace, ws_bytes, L.total));
   MOE_TRY(validate_device());
   cudaStream_t s = as_stream(stream);
-  if (orth_small(rows, cols)) {
+  if (orth_small(rows, cols) &&
+      !orth_crosses(m, dtype, ld, es, out, out_ld, out_es, E, rows, cols)) {
     MOE_CUDA(launch_orth_small(m, dtype, ld, es, E, rows, cols, coefficients, steps, eps, scale, out,
                                out_dtype, out_ld, out_es, static_cast<int32_t*>(workspace),
                                wait_limit(), s));

@@ -15,6 +15,8 @@
 // way in and out (18 us), not of bytes or operations: 41 us for 8 matrices of 128 x 256, five steps
 // (36 with the diagonal in FP16).
 // The chain of kernels for larger matrices (train_gemm.cu) takes 17 launches and 78 us for them.
+// A CTA writes its result while others may not have read their matrices yet, so that an out which
+// lies in other matrices' bytes goes to the chain.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "pdl.cuh"
