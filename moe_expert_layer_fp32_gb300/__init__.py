@@ -678,8 +678,14 @@ def _rows(name, t, cols=None):
     return t.stride(0)
 
 
+def _tensor(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: a tensor, not {type(t).__name__}")
+    return t
+
+
 def _dense(name, t, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if _tensor(name, t).dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise ValueError(f"{name}: a dense {dtype} tensor of shape {tuple(shape)}, not "
                          f"{t.dtype} {tuple(t.shape)} strides {t.stride()}")
     return t
@@ -687,9 +693,7 @@ def _dense(name, t, dtype, shape):
 
 def _buffer(name, t, nbytes=None, of=""):
     """A dense tensor of any type; of exactly nbytes, if given."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: a tensor, not {type(t).__name__}")
-    if not t.is_contiguous():
+    if not _tensor(name, t).is_contiguous():
         raise ValueError(f"{name}: a dense tensor, not strides {t.stride()}")
     n = t.numel() * t.element_size()
     if nbytes is not None and n != nbytes:
@@ -1001,8 +1005,7 @@ def mx4_layer_forward(x, w_router, bias, packed_gate_up, packed_down, d, workspa
 # (as the calls above: not part of autograd; a training step calls the gradients itself)
 def _stack(name, t, dtype, shape):
     """(row stride, matrix stride) of a 3D tensor of rows of adjacent elements."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: a tensor, not {type(t).__name__}")
+    _tensor(name, t)
     if (dtype is not None and t.dtype != dtype) or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: a {dtype} tensor of shape {tuple(shape)}, not {t.dtype} "
                          f"{tuple(t.shape)}")
@@ -1018,8 +1021,7 @@ def _stack(name, t, dtype, shape):
 
 def _rows16(name, t, dtype, shape):
     """Row stride of a 2D tensor of this 16-bit type and shape."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: a tensor, not {type(t).__name__}")
+    _tensor(name, t)
     if t.dtype not in (torch.bfloat16, torch.float16) or (dtype is not None and t.dtype != dtype):
         raise TypeError(f"{name}: {dtype or 'bfloat16 or float16'}, not {t.dtype}")
     if t.dim() != 2 or any(w is not None and n != w for n, w in zip(t.shape, shape)):
@@ -1072,7 +1074,7 @@ def grouped_product(x, offsets, w, workspace, transposed=False, dtype=None, out=
             raise MoEError("moe_grouped_product", 2)
         out, y_ld = torch.empty((R, N), dtype=dtype, device=x.device), N
     else:
-        _on_device(x, offsets, w, workspace, out)
+        _on_device(x, offsets, w, workspace, _tensor("out", out))
         if dtype not in (None, out.dtype):
             raise TypeError(f"out: {dtype}, not {out.dtype}")
         _dtype("out", out)
@@ -1112,7 +1114,7 @@ def grouped_weight_grad(x, dy, offsets, workspace, dtype=torch.float32, out=None
             raise MoEError("moe_grouped_weight_grad", 2)
         out, w_ld, w_es = torch.empty((E, K, N), dtype=dtype, device=x.device), N, K * N
     else:
-        _on_device(x, dy, offsets, workspace, out)
+        _on_device(x, dy, offsets, workspace, _tensor("out", out))
         _dtype("out", out)
         w_ld, w_es = _stack("out", out, None, (E, K, N))
     moe_grouped_weight_grad(x, x_ld, dy, dy_ld, _DTYPES[x.dtype], offsets, R, K, N, E, out, w_ld,
@@ -1262,7 +1264,7 @@ def orthogonalize(m, workspace, coefficients=(3.4445, -4.7750, 2.0315), steps=5,
         _on_device(m, workspace)
         out, o_ld, o_es = torch.empty((E, rows, cols), dtype=dtype, device=m.device), cols, rows * cols
     else:
-        if out.dtype not in (torch.bfloat16, torch.float16):
+        if _tensor("out", out).dtype not in (torch.bfloat16, torch.float16):
             raise TypeError(f"out: bfloat16 or float16, not {out.dtype}")
         _on_device(m, workspace, out)
         o_ld, o_es = _stack("out", out, None, m.shape)
