@@ -1031,6 +1031,15 @@ def _rows16(name, t, dtype, shape):
     return _rows(name, t)
 
 
+def _grouped_limits(name, R, E, K, N, widest=None):
+    """The library's limits on grouped calls, before anything of that size is allocated.  widest: the widest
+    product of the call, if not N."""
+    n = N if widest is None else widest
+    if (moe_grouped_workspace_bytes(E, K, N) == 0 or R > (1 << 31) - 512
+            or (R // 128 + E + 1) * ((n + 127) // 128) >= 1 << 30):
+        raise MoEError(name, 2)
+
+
 def _offsets(offsets):
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError("offsets: a tensor [E + 1]")
@@ -1070,8 +1079,7 @@ def grouped_product(x, offsets, w, workspace, transposed=False, dtype=None, out=
         dtype = x.dtype if dtype is None else dtype
         if dtype not in _DTYPES:
             raise TypeError(f"y: float32, bfloat16 or float16, not {dtype}")
-        if moe_grouped_workspace_bytes(E, K, N) == 0:
-            raise MoEError("moe_grouped_product", 2)
+        _grouped_limits("moe_grouped_product", R, E, K, N)
         out, y_ld = torch.empty((R, N), dtype=dtype, device=x.device), N
     else:
         _on_device(x, offsets, w, workspace, _tensor("out", out))
@@ -1110,8 +1118,7 @@ def grouped_weight_grad(x, dy, offsets, workspace, dtype=torch.float32, out=None
         _on_device(x, dy, offsets, workspace)
         if dtype not in _DTYPES:
             raise TypeError(f"d_w: float32, bfloat16 or float16, not {dtype}")
-        if moe_grouped_workspace_bytes(E, K, N) == 0:
-            raise MoEError("moe_grouped_weight_grad", 2)
+        _grouped_limits("moe_grouped_weight_grad", R, E, K, N)
         out, w_ld, w_es = torch.empty((E, K, N), dtype=dtype, device=x.device), N, K * N
     else:
         _on_device(x, dy, offsets, workspace, _tensor("out", out))
@@ -1127,6 +1134,8 @@ def _gate_up_args(gate_up, row_weights):
     R, n = gate_up.shape
     if n % 2:
         raise ValueError(f"gate_up: [R, 2 I], not {tuple(gate_up.shape)}")
+    if n // 2 % 8 or n // 2 > 1 << 24:
+        raise MoEError("moe_swiglu", 2)
     if row_weights is not None:
         _dense("row_weights", row_weights, torch.float32, (R,))
     return ld, R, n // 2
@@ -1215,6 +1224,7 @@ def expert_ffn_backward(x_perm, offsets, w_gate_up, w_down, d_y, workspace, row_
     _on_device(x_perm, offsets, w_gate_up, w_down, d_y, workspace, row_weights, gate_up, *given)
     if moe_expert_ffn_bwd_workspace_bytes(R, H, I, E) == 0:
         raise MoEError("moe_expert_ffn_bwd", 2)
+    _grouped_limits("moe_expert_ffn_bwd", R, E, H, I, max(H, 2 * I))
     dev = x_perm.device
     d_x = torch.empty((R, H), dtype=d_x_dtype, device=dev)
     if d_w_gate_up is None:

@@ -235,6 +235,14 @@ bool is16(int dtype) { return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F16;
 
 bool tensor_of(PyObject* o, at::Tensor& t) { return o != Py_None && maybe(o, t); }
 
+// Whether a grouped call's sizes are within the library's limits.  (Others: the Python path refuses
+// them before it allocates.)
+bool grouped_sizes(int64_t R, int64_t E, int64_t K, int64_t N) {
+  return N <= INT32_MAX && R <= (1LL << 31) - 512 &&
+         lib.grouped_workspace_bytes((int32_t)E, (int32_t)K, (int32_t)N) != 0 &&
+         (R / 128 + E + 1) * ((N + 127) / 128) < (1LL << 30);
+}
+
 // (x, offsets, w, workspace, transposed, type)
 PyObject* grouped_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -249,9 +257,7 @@ PyObject* grouped_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   const bool turned = a[4] == Py_True;
   const int64_t E = off.size(0) - 1, R = x.size(0), K = x.size(1), N = w.size(turned ? 1 : 2);
-  if (w.size(turned ? 2 : 1) != K || N > INT32_MAX ||
-      lib.grouped_workspace_bytes((int32_t)E, (int32_t)K, (int32_t)N) == 0)
-    Py_RETURN_NONE;
+  if (w.size(turned ? 2 : 1) != K || !grouped_sizes(R, E, K, N)) Py_RETURN_NONE;
   at::Tensor y = make({R, N}, type, dev);
   const int r = lib.grouped_product(x.data_ptr(), K, dt, (const int32_t*)off.data_ptr(), w.data_ptr(),
                                     w.size(2), w.size(1) * w.size(2), turned, (int32_t)R, (int32_t)K,
@@ -275,8 +281,7 @@ PyObject* grouped_weight_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
       off.size(0) < 2 || off.size(0) > 257 || !plain(ws, at::kByte, dev, {-1}))
     Py_RETURN_NONE;
   const int64_t E = off.size(0) - 1, R = x.size(0), K = x.size(1), N = dy.size(1);
-  if (N > INT32_MAX || lib.grouped_workspace_bytes((int32_t)E, (int32_t)K, (int32_t)N) == 0)
-    Py_RETURN_NONE;
+  if (!grouped_sizes(R, E, K, N)) Py_RETURN_NONE;
   at::Tensor d = make({E, K, N}, type, dev);
   const int r = lib.grouped_weight_grad(x.data_ptr(), K, dy.data_ptr(), N, dt,
                                         (const int32_t*)off.data_ptr(), (int32_t)R, (int32_t)K,
@@ -292,7 +297,7 @@ PyObject* swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   at::Tensor gu, w;
   int dt, dev;
-  if (n != 2 || !matrix(a[0], gu, dt, dev) || !is16(dt) || gu.size(1) % 16 != 0 || !maybe(a[1], w) ||
+  if (n != 2 || !matrix(a[0], gu, dt, dev) || !is16(dt) || gu.size(1) % 16 != 0 || gu.size(1) > (2 << 24) || !maybe(a[1], w) ||
       (w.defined() && !plain(w, at::kFloat, dev, {gu.size(0)})))
     Py_RETURN_NONE;
   const int64_t R = gu.size(0), I = gu.size(1) / 2;
@@ -310,7 +315,7 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   at::Tensor gu, d, w;
   int dt, dev;
   if (n != 3 || !matrix(a[0], gu, dt, dev) || !is16(dt) || gu.size(1) % 16 != 0 ||
-      !tensor_of(a[1], d) || !maybe(a[2], w) ||
+      gu.size(1) > (2 << 24) || !tensor_of(a[1], d) || !maybe(a[2], w) ||
       !plain(d, gu.scalar_type(), dev, {gu.size(0), gu.size(1) / 2}) ||
       (w.defined() && !plain(w, at::kFloat, dev, {gu.size(0)})))
     Py_RETURN_NONE;

@@ -1,4 +1,5 @@
-"""Arguments of the training calls that are no tensors.  CPU only: every refusal comes before anything is launched."""
+"""Arguments of the training calls that are no tensors, and sizes past the limits.  CPU only: every refusal comes before
+anything is allocated or launched."""
 import pytest
 import torch
 
@@ -28,3 +29,33 @@ def test_no_tensors(moe, bad, monkeypatch):  # noqa: F811
             lambda: moe.expert_ffn_backward(x, off, wgu, wd, x, ws, d_w_down=bad)):
         with pytest.raises(TypeError, match="a tensor, not"):
             call()
+
+
+def test_sizes_are_refused_before_an_allocation(moe, monkeypatch):  # noqa: F811
+    """(Outputs of these sizes would take terabytes, or the input's bytes once more.)"""
+    monkeypatch.setattr(moe, "_on_device", lambda *t: None)
+    make = torch.empty
+    bf = lambda *s: make(s, dtype=torch.bfloat16, device="meta")  # noqa: E731
+    off, ws, rows = torch.zeros(2, dtype=torch.int32), torch.zeros(1024, dtype=torch.uint8), 2 ** 31 - 511
+    calls = [lambda: moe.grouped_product(bf(rows, 8), off, bf(1, 8, 8), ws),
+             lambda: moe.grouped_product(bf(2 ** 29, 8), off, bf(1, 8, 32768), ws),     # rows, but too many tiles
+             lambda: moe.grouped_product(bf(2 ** 29, 8), off, bf(1, 32768, 8), ws, transposed=True),
+             lambda: moe.grouped_product(bf(4, 12), off, bf(1, 12, 8), ws),
+             lambda: moe.grouped_weight_grad(bf(rows, 8), bf(rows, 8), off, ws),
+             lambda: moe.grouped_weight_grad(bf(2 ** 29, 32768), bf(2 ** 29, 32768), off, ws),
+             lambda: moe.expert_ffn_backward(bf(rows, 8), off, bf(1, 8, 16), bf(1, 8, 8), bf(rows, 8), ws),
+             lambda: moe.expert_ffn_backward(bf(2 ** 29, 8), off, bf(1, 8, 32768), bf(1, 16384, 8), bf(2 ** 29, 8), ws),
+             lambda: moe.swiglu(bf(3, 2 ** 25 + 16)),
+             lambda: moe.swiglu(bf(3, 24)),
+             lambda: moe.swiglu_backward(bf(3, 2 ** 25 + 16), bf(3, 2 ** 24 + 8)),
+             lambda: moe.orthogonalize(bf(1, 16385, 8), ws),
+             lambda: moe.orthogonalize(bf(257, 8, 8), ws)]
+
+    def allocates(*a, **k):
+        raise AssertionError("allocated")
+
+    monkeypatch.setattr(torch, "empty", allocates)
+    for call in calls:
+        with pytest.raises(moe.MoEError) as e:
+            call()
+        assert moe.STATUS[e.value.code] == "MOE_ERR_UNSUPPORTED"
