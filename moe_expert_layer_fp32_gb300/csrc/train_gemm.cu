@@ -942,12 +942,25 @@ static bool product_pairs(int E, int R, int N) {
 }
 
 // The pair form of the Newton-Schulz products halves the bytes that an SM reads a product, but
-// makes tiles of twice the side: with few of them SMs stand idle and the dependent products
-// take longer.  A whole update, pair against single: 8 of 512 x 512 148 against 109 us, 8 of 384 x
-// 1024 155 against 121, 64 of 256 x 512 176 against 162, 5 of 1000 x 1440 263 against 322.
+// makes tiles of twice the side.  A product takes as many turns of the SMs as its tiles need, a pair's
+// twice as long as a single CTA's, and a single CTA's turn costs a quarter more for its bytes; a step
+// is the Gram product over the long side, its square over the short one (both upper tiles only), and the
+// product over the short side.  Of 48 stacks between 256 and 4096 this takes the slower form for seven, by
+// 3% on average (13% at worst: 16 of 512 x 512, 152 us against 135).  Whole updates, pair against single:
+// 8 of 512 x 512 143 against 101 us, 64 of 300 x 520 290 against 250, 8 of 1024 x 1024 264 against 238, 5 of
+// 1439 x 1001 250 against 315, 64 of 768 x 2048 1429 against 1504, 64 of 1024 x 2048 2206 against 2525.  Both
+// forms give the same bits.
 bool batch_pairs(int E, int rows, int cols) {
-  const long long tiles = (long long)E * ((rows + 127) / 128) * ((cols + 127) / 128);
-  return (rows < cols ? rows : cols) > 256 && tiles > 2LL * device_sm_count();
+  const long long S = rows < cols ? rows : cols, L = rows < cols ? cols : rows;
+  if (S <= 256) return false;
+  auto step = [&](int tile, int at_once) {
+    const long long s = (S + tile - 1) / tile, l = (L + tile - 1) / tile;
+    const long long half = (E * s * (s + 1) / 2 + at_once - 1) / at_once;
+    const long long whole = (E * s * l + at_once - 1) / at_once;
+    return (L + S) * half + S * whole;
+  };
+  const int sms = device_sm_count();
+  return 4 * 2 * step(256, sms / 2) <= 5 * step(128, sms);
 }
 
 cudaError_t launch_product(const TrainProduct& q, cudaStream_t s) {
@@ -981,6 +994,24 @@ cudaError_t launch_product(const TrainProduct& q, cudaStream_t s) {
                   : launch<1, 128, PRODUCT, KM, MN>(p, units, s);
 }
 
+static long long wgrad_units(const TrainWgrad& q, int t) {
+  return (long long)q.E * ((q.K + t - 1) / t) * ((q.N + t - 1) / t);
+}
+
+// The pair form's 256 x 256 tiles need rows to multiply, three turns of the SMs to go round, and not much
+// more than a quarter of them may be empty.  With few rows an expert the output's way out is the time:
+// FP32 leaves single CTAs as fast, and 16 bits the pairs faster once there are many tiles.  64 unevenly
+// loaded experts, BF16 in, pair against single, FP32 and BF16 out: 16 rows each, 768 x 2048 81.4 / 52.6
+// against 81.1 / 60.7 us, 192 x 1024 19.1 / 17.9 against 17.1 / 17.3; 128 rows, 768 x 2048 93.2 / 56.4 against 87.4 /
+// 66.1; 512 rows, 768 x 2048 112 / 88 against 144 / 112, 192 x 1024 32.2 / 28.1 against 34.0 / 29.9, 384 x 384 26.4 / 22.9
+// against 21.9 / 18.6, 192 x 192 15.0 / 14.7 against 13.5 / 13.3; 8 experts of 2048 rows, 1024 x 1024 31.6 / 29.1 against
+// 38.0 / 35.1, 512 x 512 22.5 / 22.3 against 17.2 / 17.1.  Both forms give the same bits.
+static bool wgrad_pairs(const TrainWgrad& q) {
+  const long long single = wgrad_units(q, 128), sms = device_sm_count();
+  if (single <= 3 * sms || 5 * 4 * wgrad_units(q, 256) > 7 * single) return false;
+  return (long long)q.R >= 256LL * q.E || (q.out_type != MOE_DTYPE_F32 && single > 24 * sms);
+}
+
 size_t wgrad_tail_bytes(int E, int cols) { return (size_t)E * GK * cols * 2; }
 
 cudaError_t launch_wgrad(const TrainWgrad& q, cudaStream_t s) {
@@ -1009,11 +1040,9 @@ cudaError_t launch_wgrad(const TrainWgrad& q, cudaStream_t s) {
   p.formats = formats_of(q.type);
   p.status = q.status;
   p.limit = q.limit;
-  // (the pair form's 256 x 256 tiles, unless half of one would stay empty; 8 experts of 256 rows,
-  // 512 x 512: 9.4 us against 11.1 with 128 x 128, 64 of 192 x 1024 19.1 against 17.4)
-  const bool pair = q.K > 128 && q.N > 128;
+  const bool pair = wgrad_pairs(q);
   const int t = pair ? 256 : 128;
-  const long long units = (long long)q.E * ((q.K + t - 1) / t) * ((q.N + t - 1) / t);
+  const long long units = wgrad_units(q, t);
   return pair ? launch<2, 256, WGRAD, MN, MN>(p, units, s)
               : launch<1, 128, WGRAD, MN, MN>(p, units, s);
 }
