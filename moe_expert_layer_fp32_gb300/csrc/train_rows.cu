@@ -49,8 +49,12 @@ __device__ __forceinline__ void swiglu_bwd_pair(uint32_t g, uint32_t u, uint32_t
 
 // A warp a row, 16-byte pieces; PIECES of a lane's are loaded before the first is used.  Bound by its
 // bytes: three values in and three out, 131072 x 768 BF16 in 183.8 us, 6.58 TB/s, 97% of the copy rate
-// (513 x 1024: 5.4 us, the host's launch and two allocations).
-constexpr int PIECES = 3, ROW_WARPS = 8;
+// (513 x 1024: 5.4 us, the host's launch and two allocations).  One piece where a row has few, whose
+// lanes would else wait with the rest of a group empty, four in long rows, whose warps have little else
+// under way; gradient / forward of 2^20 x 100 BF16 values, by 1, 2, 3 and 4 pieces: rows of 256 196/99,
+// 232/123, 267/120, 271/123 us; of 768 191/97, 199/112, 192/101, 194/96; of 1408 191/97, 197/119, 196/98, 198/98; of
+// 2048 202/102, 195/113, 191/104, 195/100; of 8192 198/120, 193/97, 197/101, 193/97.
+constexpr int ROW_WARPS = 8, LONG_ROW = 2048;
 
 // Whether offsets [E + 1] are a non-decreasing sequence from 0 to R: the same answer in every thread of
 // the block.
@@ -63,7 +67,7 @@ __device__ __forceinline__ bool block_sequence(const int32_t* __restrict__ offse
   return !__syncthreads_or(bad);
 }
 
-template <int TYPE, bool BWD>
+template <int TYPE, bool BWD, int PIECES>
 __global__ void __launch_bounds__(32 * ROW_WARPS)
     swiglu_kernel(const uint8_t* __restrict__ gu, long long gu_ld, const uint8_t* __restrict__ d,
                   long long d_ld, const float* __restrict__ w, int R, int I, uint8_t* dgu,
@@ -140,8 +144,9 @@ cudaError_t launch_rows(const void* gu, long long gu_ld, const void* d, long lon
   const long long need = ((long long)R + ROW_WARPS - 1) / ROW_WARPS;
   const long long most = 8LL * device_sm_count();
   const dim3 grid((unsigned)(need < most ? need : most));
-  auto kern = type == MOE_DTYPE_BF16 ? swiglu_kernel<MOE_DTYPE_BF16, BWD>
-                                     : swiglu_kernel<MOE_DTYPE_F16, BWD>;
+  const bool bf16 = type == MOE_DTYPE_BF16;
+  auto kern = I < LONG_ROW ? (bf16 ? swiglu_kernel<MOE_DTYPE_BF16, BWD, 1> : swiglu_kernel<MOE_DTYPE_F16, BWD, 1>)
+                           : (bf16 ? swiglu_kernel<MOE_DTYPE_BF16, BWD, 4> : swiglu_kernel<MOE_DTYPE_F16, BWD, 4>);
   return launch_pdl(kern, grid, dim3(32 * ROW_WARPS), 0, s, static_cast<const uint8_t*>(gu), gu_ld,
                     static_cast<const uint8_t*>(d), d_ld, w, R, I, static_cast<uint8_t*>(dgu),
                     dgu_ld, static_cast<uint8_t*>(h), h_ld, d_w, offsets, E);
