@@ -721,6 +721,7 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
       if (u >= total) break;
       const Tile t = tile_of(u);
       if (KIND == WGRAD && t.kb == 0 && p.c != nullptr) continue;  // nothing to add
+      const int acc = tcount & 1;
       const bool sums = KIND != WGRAD || t.kb > 0;
       if constexpr (KIND == BATCH) {  // this tile's rows of c move into L2 while it is multiplied
         const int row = t.row0 + q * 32 + lane;
@@ -732,8 +733,9 @@ __global__ void __launch_bounds__(THREADS, 1) train_gemm_kernel(const __grid_con
           }
         }
       }
-      const int acc = tcount & 1;
-      if (sums && !ready(acc)) break;
+      if (sums) {
+        if (!ready(acc)) break;
+      }
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
       const int nrows = min(32, t.nrows - q * 32);
       const int ncols = min(BN, p.n_lim - t.col0);
