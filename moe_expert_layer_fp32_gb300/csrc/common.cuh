@@ -37,6 +37,16 @@ __device__ __forceinline__ float silu_f32(float g) {
   return __fdividef(g, __fadd_rn(1.0f, __expf(-g)));
 }
 
+// One thread of a whole warp.  A role's thread is elected, not named: the compiler then knows that it
+// is the only one, and issues copies and MMAs without a loop over the active lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

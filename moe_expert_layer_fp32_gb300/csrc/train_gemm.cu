@@ -106,16 +106,6 @@ struct Tile {
   int boxes;                 // A boxes of the single product form
 };
 
-// (A role's thread is elected, not named: the compiler then knows that it is the only one, and
-// issues copies and MMAs without a loop over the active lanes.)
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, P;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
 __device__ __forceinline__ void tma_load_3d(const void* map, void* dst, uint32_t bar, int c0, int c1,
                                             int c2) {
   asm volatile(

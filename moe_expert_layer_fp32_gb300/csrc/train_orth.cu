@@ -159,9 +159,7 @@ __global__ void __launch_bounds__(256, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 0 && ok) {
-      uint32_t p;
-      asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
-      if (p) {
+      if (elect_one()) {
         issue();
         mma_commit(bar);
       }
