@@ -539,7 +539,10 @@ moe_status moe_mx4_layer_fwd(const void* x, const float* w_router, const float* 
  * orthogonalised updates.
  *
  * dtype is MOE_DTYPE_BF16 or MOE_DTYPE_F16, the type of both operands of a product;
- * products are exact, sums FP32, and a 16-bit output is rounded once.  Matrices have
+ * products are exact, sums FP32, and a 16-bit output is rounded once.  A sum loses up to 2^-23 of its
+ * running value at every step of sixteen products; parts of 4096 products are added separately, so that
+ * its error (relative 2-norm, measured) is 1.0e-6 at 1024 products, 4.4e-6 from 4096 on, 1.4e-5 if all
+ * products have one sign.  Outputs do not overlap inputs or one another, but where it is said.  Matrices have
  * rows of adjacent elements, ld elements apart and starting on 16-byte boundaries
  * (ld * element size a multiple of 16); stacks of E matrices es elements apart, es a
  * multiple of ld.  K, N, H and I are multiples of 8, at most 32768 (I: 16384);
@@ -574,7 +577,8 @@ moe_status moe_grouped_weight_grad(const void* x, int64_t x_ld, const void* dy, 
                                    size_t ws_bytes, void* stream);
 
 /* h[r, i] = row_w[r] * silu(gate_up[r, i]) * gate_up[r, I + i], one rounding (row_w NULL:
- * 1).  gate_up [R, 2 I], h [R, I] of dtype. */
+ * 1) of a value within 2^-23 (8 + 2 |gate|), by the special-function unit's exponential.
+ * gate_up [R, 2 I], h [R, I] of dtype. */
 moe_status moe_swiglu(const void* gate_up, int64_t gate_up_ld, const float* row_w, int32_t dtype,
                       int32_t R, int32_t I, void* h, int64_t h_ld, void* stream);
 

@@ -1056,8 +1056,8 @@ def grouped_new_workspace(E, K, N, device="cuda") -> torch.Tensor:
 def grouped_product(x, offsets, w, workspace, transposed=False, dtype=None, out=None, stream=None):
     """y [R, N] (fp32, bf16 or fp16; default: x's type): the rows x [R, K] (bf16 or fp16) of each
     expert (offsets [E+1] int32) times its matrix of w [E, K, N], or w [E, N, K] if transposed,
-    of x's type.  out: written instead of a new tensor.  Not part of autograd: the gradients are
-    this call with the other `transposed`, and grouped_weight_grad."""
+    of x's type.  out: written instead of a new tensor (no bytes of the inputs).  Not part of autograd:
+    the gradients are this call with the other `transposed`, and grouped_weight_grad."""
     if stream is not None:
         with _on_stream(stream):
             return grouped_product(x, offsets, w, workspace, transposed, dtype, out)

@@ -24,11 +24,11 @@
 // expert's last, partial k-block are copied beforehand (tails_kernel) and filled up with zeros, so
 // another expert's rows (or infinities and NaN among them) never enter the sum.
 //
-// What bounds it.  Few rows: the weights' bytes (512 rows of 64 experts, 1024 x 2048: 43.9 us, 6.2 TB/s,
-// 91% of the copy rate).  Many rows: the tensor pipe, 90% busy at 131072 rows of 128 experts, 2048 x
-// 1536 (516 us alone under the profiler, 608 among others under the power cap; full 256-row tiles
+// What bounds it.  Few rows: the weights' bytes (512 rows of 64 experts, 1024 x 2048: 44.3 us, 6.2 TB/s,
+// 91% of the copy rate).  Many rows: the tensor pipe, 94% active at 131072 rows of 128 experts, 2048 x
+// 1536 (532 us alone under the profiler, 608 among others under the power cap; full 256-row tiles
 // would be 12% fewer).  Weight gradients: the FP32 output's way out beside the short contractions
-// (512 rows an expert, 2048 x 2048: 271 us, 4.95 TB/s, tensor pipe 49%).  Chains of Newton-Schulz
+// (512 rows an expert, 2048 x 2048: 273 us, 4.92 TB/s, tensor pipe 49%).  Chains of Newton-Schulz
 // products: 70-83% of the tensor pipe at 64 x 1024 x 2048, the rest is each kernel's first and last
 // tile.
 //
@@ -56,7 +56,8 @@ constexpr int BOX_ROWS = 16;  // A boxes of the single form of a product
 // k-blocks whose products one accumulator sums.  The tensor cores' addition drops up to 2^-23 of the
 // running sum at each step of sixteen products, always towards zero, so that an error grows with the
 // contraction (relative 2-norm, K = N = 256, random signs / one sign: 4096 rows 4.4e-6 / 1.4e-5, 131072
-// 1.5e-4 / 8.2e-4).  Longer sums are taken apart, and the parts added in FP32 by the epilogue.  (Not
+// 1.5e-4 / 8.2e-4).  Longer sums are taken apart, and the parts added in FP32 by the epilogue, while the
+// MMAs wait (65536 rows, 2048 x 2048 FP32: 158 -> 162 us; parts half as long would double both).  (Not
 // in BATCH and SYM: at their longest, 16384, the error is a third of the rounding to FP16 behind them.)
 constexpr int SEG = 64;
 

@@ -11,9 +11,9 @@
 // rounded X as the rest of B does: what X's rounding leaves outside of X's span then stays of second order
 // in B X, where one part of B on X unrounded brings it in at first order (the whole diagonal there: rank
 // 8 of 128 x 256 was 0.1 off after eight steps, each of which lifts it a times).  Everything waits on everything in a step, so the
-// time is that of 3 x steps dependent products with their barriers (about 1.6 us each) and of the
-// way in and out (18 us), not of bytes or operations: 41 us for 8 matrices of 128 x 256, five steps
-// (36 with the diagonal in FP16).
+// time is that of 3 x steps dependent products with their barriers (about 1.4 us each) and of the
+// way in and out (18 us), not of bytes or operations: 38.6 us for 8 matrices of 128 x 256, five steps
+// (36 without the diagonal's rest).
 // The chain of kernels for larger matrices (train_gemm.cu) takes 17 launches and 78 us for them.
 // A CTA writes its result while others may not have read their matrices yet, so that an out which
 // lies in other matrices' bytes goes to the chain.
